@@ -138,6 +138,15 @@ typedef struct tide_plan tide_plan;
  * same exact value once and so gives the same bits. */
 #define TIDE_F_AVG 0x4u
 
+/* Flag, tide_block_mm_dw only: add the product to what `dw` holds (in fp32,
+ * then one rounding to dw's type) instead of overwriting it, for gradients
+ * summed over micro-batches. */
+#define TIDE_F_ACCUMULATE 0x40u
+
+/* Flag, tide_block_dequant and tide_block_unshard only: write fp16 (the exact
+ * value rounded once, to infinity past 65504).  Excludes TIDE_F_OUT_BF16. */
+#define TIDE_F_OUT_F16 0x80u
+
 /* ---------------------------------------------------------------------- */
 /* Plan (host only; makes no HIP call).                                    */
 /* ---------------------------------------------------------------------- */
@@ -298,6 +307,113 @@ tide_status tide_rs_slots(const tide_plan *plan, int32_t rank, const void *const
  *   use one stream. */
 tide_status tide_rs_noalloc(const tide_plan *plan, int32_t rank, const void *const *grads,
                             void *out, uint32_t flags, int32_t max_workgroups, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Matrices in 8-bit blocks: an 8-bit gather of the sharded weights, 8-bit */
+/* activation checkpoints, and the products of a linear layer over both.   */
+/* ---------------------------------------------------------------------- */
+
+/* Format.  A row-major matrix [R, C] is held as
+ *   codes   [R, Cp] bytes, Cp = tide_block_cols(C)       = C rounded up to 128
+ *   scales  [R, Sp] bytes, Sp = tide_block_scale_cols(C) = Cp/128 rounded up to 4
+ * and element (r, c) is e4m3(codes[r*Cp + c]) * 2^(scales[r*Sp + c/128] - 127).
+ * A block is 128 columns of one row (the last one of a row may be shorter), so
+ * a dim-0 shard boundary never cuts a block.  e4m3 has a sign, 4 exponent and 3
+ * fraction bits, largest value 448, NaN 0x7f and 0xff, no infinity.  With
+ * a = max|x| over the finite values of a block, its exponent e is the smallest
+ * integer with a <= 448 * 2^e, kept within [-117, 119] (0 if a = 0), its scale
+ * byte e + 127, and each code the e4m3 number nearest to x * 2^-e, ties to
+ * even; |x * 2^-e| above 448 (only if a > 448 * 2^119) becomes 448.  An infinity
+ * or a NaN becomes NaN and leaves the rest of its block as it is.  Codes past
+ * column C are 0, scale bytes past the last block 127.  Every finite value of
+ * the format is a bf16 number: reading it back is exact in bf16 and fp32.
+ * Operands given to the calls below hold scale bytes of 10..246 and those
+ * zeros, as tide_block_quant and tide_block_shard write them.
+ *
+ * codes have to be 16-byte aligned and scales 4-byte aligned.  Sizes are at
+ * least 0 and below 2^31; a size of 0 is a matrix without elements.  These
+ * calls keep nothing on the device or the host between calls, allocate
+ * nothing and may be captured into a graph at any time.  Errors and streams
+ * as for tide_rs; the current device has to be the one that holds the data. */
+
+/* Cp and Sp for C columns (-1 if C < 0). */
+int64_t tide_block_cols(int64_t cols);
+int64_t tide_block_scale_cols(int64_t cols);
+
+/* Write x [rows, cols] (bf16; fp16 or fp32 by TIDE_F_GRAD_F16 / _F32) in 8-bit
+ * blocks.  Any element alignment of x; 16-byte aligned x with cols a multiple
+ * of 8 takes the vector path.  The outputs may not overlap x or each other. */
+tide_status tide_block_quant(const void *x, int64_t rows, int64_t cols, void *codes,
+                             void *scales, uint32_t flags, void *stream);
+
+/* Write the values of 8-bit blocks to out [rows, cols]: fp32, or bf16 or fp16
+ * by TIDE_F_OUT_BF16 / TIDE_F_OUT_F16. */
+tide_status tide_block_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                               void *out, uint32_t flags, void *stream);
+
+/* A plan for gathering n of `plan`'s parameters in 8-bit blocks: select[j]
+ * (host array, no index twice) names the j-th.  Parameter i is taken as the
+ * matrix [dim0_i, inner_i].  The new plan has the same world and 2n parameters
+ * of 4-byte words, with align 4: number j is [dim0, Cp/4], the codes, and
+ * number n + j is [dim0, Sp/4], the scales, of matrix select[j].  It is used
+ * like any other plan with elem_bytes 4 - tide_ag with it places a gathered
+ * buffer of N*S words into whole codes and scales - and by the two calls
+ * below.  It does not refer to `plan` afterwards; free it with
+ * tide_plan_destroy. */
+tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int32_t *select,
+                                    tide_plan **out_plan);
+
+/* Rank `rank`'s fp32 master shard -> its 8-bit rank block.
+ *   plan    a plan from tide_plan_create_blocks
+ *   master  rank `rank`'s block of the source plan (its S floats, 4-byte aligned)
+ *   block   plan's S words (tide_plan_shard_numel), 16-byte aligned, e.g. block
+ *           `rank` of the gathered buffer; must not overlap master.  Padding
+ *           rows are written as rows of zeros, alignment gaps are not written.
+ *   flags   0 */
+tide_status tide_block_shard(const tide_plan *plan, int32_t rank, const float *master,
+                             void *block, uint32_t flags, void *stream);
+
+/* N gathered 8-bit rank blocks -> the full matrices in bf16, fp16 or fp32, with
+ * no 8-bit copy in between.
+ *   gathered  N*S words, rank-major, 16-byte aligned
+ *   params    host array of n device pointers to [dim0, inner] matrices in the
+ *             order of `select` (NULL allowed for one without elements),
+ *             element-aligned; no overlaps
+ *   flags     TIDE_F_OUT_BF16, TIDE_F_OUT_F16 or neither (fp32) */
+tide_status tide_block_unshard(const tide_plan *plan, const void *gathered, void *const *params,
+                               uint32_t flags, void *stream);
+
+/* The products of a linear layer with weights W [n, k] and input X [m, k] in
+ * 8-bit blocks and the output's gradient dY [m, n] in bf16 (2-byte aligned):
+ *   tide_block_mm     out[m, n] = X W^T        (the forward pass)
+ *   tide_block_mm_dx  dx[m, k]  = dY W         (the input's gradient)
+ *   tide_block_mm_dw  dw[n, k]  = dY^T X       (the weights' gradient)
+ * All matrices are row-major without gaps.  The output is fp32, or bf16 with
+ * TIDE_F_OUT_BF16; it must not overlap an operand.  Sums are held in fp32.
+ * Products are exact, except in tide_block_mm with a bf16 output and more than
+ * 64 rows: the 8-bit matrix instruction there adds 128 products at a time with
+ * fewer bits (an error of about 2e-5 of the result's norm on normal data,
+ * against 2e-3 of the rounding to bf16).  Results do not depend on timing: the
+ * same call gives the same bits.  An empty sum gives zeros.
+ *   workspace  device memory of tide_block_workspace() bytes, 16-byte aligned,
+ *              used during the call only; with fewer bytes (NULL and 0) the
+ *              call runs without cutting its sum into pieces, which is slower
+ *              where the output is small and the sum long, and may round
+ *              differently. */
+tide_status tide_block_mm(const void *x_codes, const void *x_scales, int64_t m,
+                          const void *w_codes, const void *w_scales, int64_t n, int64_t k,
+                          void *out, uint32_t flags, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+tide_status tide_block_mm_dx(const void *dy, int64_t m, int64_t n, const void *w_codes,
+                             const void *w_scales, int64_t k, void *dx, uint32_t flags,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+tide_status tide_block_mm_dw(const void *dy, int64_t m, int64_t n, const void *x_codes,
+                             const void *x_scales, int64_t k, void *dw, uint32_t flags,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that the product `op` (0 mm, 1 mm_dx, 2 mm_dw) uses for
+ * these sizes and flags; 0 if none, -1 for a bad argument. */
+int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics.                                                            */

@@ -6,6 +6,7 @@ kernels of libtide.so.  PyTorch supplies device memory and streams.
     plan = Plan(shapes, world)                  # tide_plan_create
     rs(plan, rank, grads, out)                  # tide_rs  (TIDE-RS)
     ag(plan, rank_src, params)                  # tide_ag  (TIDE-AG placement)
+    y = block_linear(x, w, grad=dw)             # a linear layer in 8-bit blocks (blocks.py)
 
 TIDE-RS and TIDE-AG are described in "FSDP通信终局：TIDE零拷贝集合通信优化"
 (kongchang.com), §"TIDE的设计思路：布局感知的零拷贝通信".
@@ -372,3 +373,9 @@ __all__ = ["Plan", "PointerTable", "TideError", "SMALL_FOOTPRINT", "COPY_ENGINE"
            "GRAD_F16", "GRAD_F32", "OUT_BF16", "grad_table",
            "ag_tables", "slot_table",
            "rs", "rs_noalloc", "ag", "pack", "rs_slots", "lib"]
+
+from .blocks import (Blocks, BlockPlan, block_dequant, block_linear, block_mm,  # noqa: E402
+                     block_mm_dw, block_mm_dx, block_quant, block_shard, block_unshard)
+
+__all__ += ["Blocks", "BlockPlan", "block_quant", "block_dequant", "block_mm", "block_mm_dx",
+            "block_mm_dw", "block_linear", "block_shard", "block_unshard"]

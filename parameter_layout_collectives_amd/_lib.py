@@ -26,6 +26,17 @@ SIGNATURES = {
     "tide_pack": (_i32, [_p, _p, _p, _i32, _u32, _i32, _p]),
     "tide_rs_slots": (_i32, [_p, _i32, _p, _p, _u32, _i32, _p]),
     "tide_rs_noalloc": (_i32, [_p, _i32, _p, _p, _u32, _i32, _p]),
+    "tide_block_cols": (_i64, [_i64]),
+    "tide_block_scale_cols": (_i64, [_i64]),
+    "tide_block_quant": (_i32, [_p, _i64, _i64, _p, _p, _u32, _p]),
+    "tide_block_dequant": (_i32, [_p, _p, _i64, _i64, _p, _u32, _p]),
+    "tide_plan_create_blocks": (_i32, [_p, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_p)]),
+    "tide_block_shard": (_i32, [_p, _i32, _p, _p, _u32, _p]),
+    "tide_block_unshard": (_i32, [_p, _p, _p, _u32, _p]),
+    "tide_block_mm": (_i32, [_p, _p, _i64, _p, _p, _i64, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_block_mm_dx": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_block_mm_dw": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_block_workspace": (_i64, [_i32, _i64, _i64, _i64, _u32]),
     "tide_last_error": (ctypes.c_char_p, []),
     "tide_status_string": (ctypes.c_char_p, [_i32]),
 }

@@ -1,0 +1,366 @@
+"""Matrices in 8-bit blocks: the 8-bit gather of an FSDP unit's weights, 8-bit
+activation checkpoints, and the products of a linear layer over both.
+
+    q = block_quant(x)                       # x [m, k] -> Blocks (the checkpoint)
+    x = block_dequant(q)                     # ... and back
+    y = block_mm(q, w)                       # y [m, n] = x w^T, both in blocks
+    dx = block_mm_dx(dy, w)                  # dx [m, k] = dy w
+    dw = block_mm_dw(dy, q)                  # dw [n, k] = dy^T x
+    y = block_linear(x, w, grad=dw)          # all of it through autograd
+
+    plan = BlockPlan(Plan(shapes, world))    # gather matrices in 8 bits
+    block_shard(plan, rank, master, gathered[rank])
+    ag(plan, gathered, plan.views(weights))  # -> Blocks for the products, or
+    block_unshard(plan, gathered, params)    # -> full tensors
+
+The format (e4m3 codes, one power of two per 128 columns of a row), the
+arguments and the errors are documented in include/tide.h.  An FSDP unit that
+gathers its weights this way moves half the bytes of a bf16 all-gather
+("FSDP通信终局：TIDE零拷贝集合通信优化", §"FSDP2通信开销的根源": the all-gather's
+bytes are part of every step).
+
+The calls run on PyTorch's current stream of the tensors' device; outputs and
+workspaces that they make come from PyTorch's allocator, so they may be
+captured into a graph.
+"""
+import contextlib
+import ctypes
+
+import torch
+
+from . import GRAD_F16, GRAD_F32, OUT_BF16, Plan, PointerTable, _check, _numel
+from ._lib import lib
+
+BLOCK = 128            # columns of a block
+ACCUMULATE = 0x40
+OUT_F16 = 0x80
+
+_IN_FLAG = {torch.bfloat16: 0, torch.float16: GRAD_F16, torch.float32: GRAD_F32}
+_OUT_FLAG = {torch.float32: 0, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}
+_MM, _DX, _DW = 0, 1, 2
+
+
+def _code_cols(cols):
+    return -(-cols // BLOCK) * BLOCK
+
+
+def _scale_cols(cols):
+    return -(-cols // (4 * BLOCK)) * 4
+
+
+def _launch(device):
+    """(context that makes `device` current, its current stream's handle)."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), stream
+    return torch.cuda.device(device), stream
+
+
+def _matrix(t, what, dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} is {t.dtype}, expected one of "
+                        f"{', '.join(str(d).replace('torch.', '') for d in dtypes)}")
+    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 2-D device tensor")
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+
+
+class Blocks:
+    """A matrix [rows, cols] in 8-bit blocks.
+
+    codes: [rows, cols rounded up to 128], float8_e4m3fn or uint8.
+    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "device", "_ptrs")
+
+    def __init__(self, codes, scales, cols):
+        _matrix(codes, "codes", (torch.float8_e4m3fn, torch.uint8))
+        _matrix(scales, "scales", (torch.uint8, torch.float8_e8m0fnu))
+        self.cols = int(cols)
+        self.rows = codes.shape[0]
+        self.device = codes.device
+        _same_device(codes.device, scales)
+        if self.cols < 0 or codes.shape[1] != _code_cols(self.cols) \
+                or tuple(scales.shape) != (self.rows, _scale_cols(self.cols)):
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
+                             f"hold {self.rows} rows of {self.cols} columns")
+        self.codes, self.scales = codes, scales
+        self._ptrs = ctypes.c_void_p(codes.data_ptr()), ctypes.c_void_p(scales.data_ptr())
+
+    @classmethod
+    def empty(cls, rows, cols, device="cuda"):
+        return cls(torch.empty(rows, _code_cols(cols), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(rows, _scale_cols(cols), dtype=torch.uint8, device=device), cols)
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+
+def _out(out, shape, dtype, dtypes, device, what):
+    """`out` checked, or a new tensor."""
+    if out is None:
+        if dtype not in dtypes:
+            raise TypeError(f"{what} cannot be {dtype}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    _matrix(out, what, dtypes)
+    _same_device(device, out)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    return out
+
+
+def block_quant(x, out=None):
+    """x [rows, cols] (bf16, fp16 or fp32) in 8-bit blocks: `out` or new Blocks."""
+    _matrix(x, "x", tuple(_IN_FLAG))
+    rows, cols = x.shape
+    if out is None:
+        out = Blocks.empty(rows, cols, x.device)
+    elif out.shape != (rows, cols):
+        raise ValueError(f"out holds {out.shape}, x is {(rows, cols)}")
+    _same_device(x.device, out)
+    ctx, stream = _launch(x.device)
+    with ctx:
+        _check(lib().tide_block_quant(ctypes.c_void_p(x.data_ptr()), rows, cols, *out._ptrs,
+                                      _IN_FLAG[x.dtype], stream))
+    return out
+
+
+def block_dequant(q, out=None, dtype=torch.bfloat16):
+    """The values of 8-bit blocks: in `out`, or in a new tensor of `dtype`."""
+    out = _out(out, q.shape, dtype, tuple(_OUT_FLAG), q.device, "out")
+    ctx, stream = _launch(q.device)
+    with ctx:
+        _check(lib().tide_block_dequant(*q._ptrs, q.rows, q.cols, ctypes.c_void_p(out.data_ptr()),
+                                        _OUT_FLAG[out.dtype], stream))
+    return out
+
+
+def _workspace(op, m, n, k, flags, device):
+    size = lib().tide_block_workspace(op, m, n, k, flags)
+    if size <= 0:
+        return None, None, 0
+    buf = torch.empty(size, dtype=torch.uint8, device=device)
+    return buf, ctypes.c_void_p(buf.data_ptr()), size
+
+
+_PRODUCT_TYPES = (torch.bfloat16, torch.float32)
+
+
+def block_mm(x, w, out=None, dtype=torch.bfloat16):
+    """x w^T for x [m, k] and w [n, k] in 8-bit blocks: [m, n] in bf16 or fp32."""
+    if x.cols != w.cols:
+        raise ValueError(f"x has {x.cols} columns, w has {w.cols}")
+    _same_device(x.device, w)
+    out = _out(out, (x.rows, w.rows), dtype, _PRODUCT_TYPES, x.device, "out")
+    flags = _OUT_FLAG[out.dtype]
+    ctx, stream = _launch(x.device)
+    with ctx:
+        keep, ptr, size = _workspace(_MM, x.rows, w.rows, x.cols, flags, x.device)
+        _check(lib().tide_block_mm(*x._ptrs, x.rows, *w._ptrs, w.rows, w.cols,
+                                   ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    return out
+
+
+def block_mm_dx(dy, w, out=None, dtype=torch.bfloat16):
+    """dy w for dy [m, n] in bf16 and w [n, k] in 8-bit blocks: [m, k] in bf16 or fp32."""
+    _matrix(dy, "dy", (torch.bfloat16,))
+    if dy.shape[1] != w.rows:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w has {w.rows} rows")
+    _same_device(dy.device, w)
+    m, n = dy.shape
+    out = _out(out, (m, w.cols), dtype, _PRODUCT_TYPES, dy.device, "out")
+    flags = _OUT_FLAG[out.dtype]
+    ctx, stream = _launch(dy.device)
+    with ctx:
+        keep, ptr, size = _workspace(_DX, m, n, w.cols, flags, dy.device)
+        _check(lib().tide_block_mm_dx(ctypes.c_void_p(dy.data_ptr()), m, n, *w._ptrs, w.cols,
+                                      ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    return out
+
+
+def block_mm_dw(dy, x, out=None, dtype=torch.bfloat16, accumulate=False):
+    """dy^T x for dy [m, n] in bf16 and the checkpoint x [m, k] in 8-bit blocks:
+    [n, k] in bf16 or fp32; with accumulate, added to what `out` holds."""
+    _matrix(dy, "dy", (torch.bfloat16,))
+    if dy.shape[0] != x.rows:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x has {x.rows}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs an out to add to")
+    _same_device(dy.device, x)
+    m, n = dy.shape
+    out = _out(out, (n, x.cols), dtype, _PRODUCT_TYPES, dy.device, "out")
+    flags = _OUT_FLAG[out.dtype] | (ACCUMULATE if accumulate else 0)
+    ctx, stream = _launch(dy.device)
+    with ctx:
+        keep, ptr, size = _workspace(_DW, m, n, x.cols, flags, dy.device)
+        _check(lib().tide_block_mm_dw(ctypes.c_void_p(dy.data_ptr()), m, n, *x._ptrs, x.cols,
+                                      ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    return out
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, anchor, w, dtype, grad, accumulate):
+        q = block_quant(x)
+        ctx.save_for_backward(q.codes, q.scales, w.codes, w.scales)
+        ctx.cols, ctx.x_dtype, ctx.grad, ctx.accumulate = w.cols, x.dtype, grad, accumulate
+        return block_mm(q, w, dtype=dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        qc, qs, wc, ws = ctx.saved_tensors
+        dy = dy.to(torch.bfloat16).contiguous()
+        dx = None
+        if ctx.needs_input_grad[0]:
+            half = ctx.x_dtype == torch.float16
+            dx = block_mm_dx(dy, Blocks(wc, ws, ctx.cols),
+                             dtype=torch.float32 if half else ctx.x_dtype)
+            dx = dx.to(ctx.x_dtype) if half else dx
+        if ctx.grad is not None:
+            block_mm_dw(dy, Blocks(qc, qs, ctx.cols), out=ctx.grad, accumulate=ctx.accumulate)
+        return dx, None, None, None, None, None
+
+
+def block_linear(x, w, dtype=None, grad=None, accumulate=False):
+    """A linear layer: x [..., k] times w [n, k] (8-bit blocks) -> [..., n].
+
+    x (bf16, fp16 or fp32, contiguous) becomes 8-bit blocks, which are all that
+    is kept of it for the backward pass.  dtype: the output's, bf16 or fp32
+    (default: fp32 for an fp32 x, else bf16).
+    The backward pass takes the output's gradient in bf16, returns x's gradient
+    in x's dtype, treating the rounding of x to 8 bits as the identity, and
+    writes the weights' gradient to `grad` ([n, k], bf16 or fp32; as the
+    reduce-scatter takes it), or adds it there with accumulate.  Without `grad`
+    the weights are frozen.  w's blocks must hold the same values in the
+    backward pass as in the forward pass."""
+    if x.shape[-1] != w.cols:
+        raise ValueError(f"x has {x.shape[-1]} columns, w has {w.cols}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if dtype is None:
+        dtype = torch.float32 if x.dtype == torch.float32 else torch.bfloat16
+    if grad is not None:
+        _out(grad, w.shape, None, _PRODUCT_TYPES, w.device, "grad")
+    lead = x.shape[:-1]
+    if x.dim() != 2:
+        x = x.reshape(_numel(lead), w.cols)
+    if torch.is_grad_enabled() and (x.requires_grad or grad is not None):
+        # With an x that needs no gradient, this empty leaf is what makes
+        # autograd run the backward pass, and with it the weights' gradient.
+        anchor = torch.empty(0, requires_grad=True) if grad is not None else None
+        y = _Linear.apply(x, anchor, w, dtype, grad, accumulate)
+    else:
+        y = block_mm(block_quant(x), w, dtype=dtype)
+    return y if len(lead) == 1 else y.view(*lead, w.rows)
+
+
+def _words(t):
+    """The int32 view of a contiguous byte matrix (its row length divides by 4)."""
+    if t.numel() == 0:
+        return torch.empty(t.shape[0], t.shape[1] // 4, dtype=torch.int32, device=t.device)
+    return t.view(torch.int32)
+
+
+class BlockPlan(Plan):
+    """The plan of an 8-bit gather of `plan`'s matrices (tide_plan_create_blocks).
+
+    select: indices of plan's parameters, by default all 2-D ones.  Its own
+    parameters are the codes and then the scales of the selected matrices in
+    int32 words, so ag(plan, gathered, plan.views(blocks)) places them."""
+
+    def __init__(self, plan, select=None):
+        self._h = None
+        if select is None:
+            select = [i for i, s in enumerate(plan.shapes) if len(s) == 2]
+        self.select = [int(i) for i in select]
+        n = len(self.select)
+        arr = (ctypes.c_int32 * max(n, 1))(*self.select)
+        h = ctypes.c_void_p()
+        self._destroy = lib().tide_plan_destroy
+        _check(lib().tide_plan_create_blocks(plan.handle, n, arr, ctypes.byref(h)))
+        self._h = h
+        self.world = plan.world
+        self.matrices = []
+        for i in self.select:
+            s = plan.shapes[i]
+            self.matrices.append((s[0] if s else 1, _numel(s[1:])))
+        self.shapes = [(d, _code_cols(c) // 4) for d, c in self.matrices] + \
+                      [(d, _scale_cols(c) // 4) for d, c in self.matrices]
+        self.P = 2 * n
+        self.S = int(lib().tide_plan_shard_numel(h))
+        self.source_S = plan.S
+        self._sig = (self.world, tuple(self.shapes), self.S)
+
+    def empty(self, device="cuda"):
+        """A gathered buffer [world, S] of int32 words."""
+        return torch.empty(self.world, self.S, dtype=torch.int32, device=device)
+
+    def blocks(self, device="cuda"):
+        """One (uninitialised) Blocks per matrix, for ag() to place into."""
+        return [Blocks.empty(d, c, device) for d, c in self.matrices]
+
+    def views(self, blocks):
+        """The int32 views of a list of Blocks that ag() takes as parameters."""
+        if [b.shape for b in blocks] != self.matrices:
+            raise ValueError("need one Blocks per matrix, of its shape")
+        return [_words(b.codes) for b in blocks] + [_words(b.scales) for b in blocks]
+
+
+def block_shard(plan, rank, master, block):
+    """Rank `rank`'s fp32 master shard (source_S elements) -> its 8-bit rank
+    block (plan.S int32 words, e.g. a row of plan.empty())."""
+    if master.dtype != torch.float32 or not master.is_cuda or not master.is_contiguous() \
+            or master.numel() != plan.source_S:
+        raise ValueError(f"master must be a contiguous float32 device tensor of "
+                         f"{plan.source_S} elements")
+    if block.dtype != torch.int32 or not block.is_cuda or not block.is_contiguous() \
+            or block.numel() != plan.S:
+        raise ValueError(f"block must be a contiguous int32 device tensor of {plan.S} elements")
+    _same_device(master.device, block)
+    ctx, stream = _launch(master.device)
+    with ctx:
+        _check(lib().tide_block_shard(plan.handle, int(rank), ctypes.c_void_p(master.data_ptr()),
+                                      ctypes.c_void_p(block.data_ptr()), 0, stream))
+
+
+def _check_unshard(plan, params, device):
+    dtype = params[0].dtype
+    if dtype not in _OUT_FLAG:
+        raise TypeError(f"params must be bfloat16, float16 or float32, got {dtype}")
+    for j, (t, s) in enumerate(zip(params, plan.matrices)):
+        if t.dtype != dtype or t.device != device or not t.is_contiguous() \
+                or t.numel() != s[0] * s[1]:
+            raise ValueError(f"params[{j}] must be a contiguous {dtype} tensor on {device} with "
+                             f"{s[0] * s[1]} elements")
+
+
+def block_unshard(plan, gathered, params):
+    """Gathered 8-bit rank blocks (plan.empty()) -> full tensors.
+
+    params: one tensor per matrix of the plan, all bf16, all fp16 or all fp32,
+    or a PointerTable of them."""
+    if gathered.dtype != torch.int32 or not gathered.is_cuda or not gathered.is_contiguous() \
+            or gathered.numel() != plan.world * plan.S:
+        raise ValueError(f"gathered must be a contiguous int32 device tensor of "
+                         f"{plan.world * plan.S} elements")
+    if not isinstance(params, PointerTable):
+        params = PointerTable(params)
+    params.check_len(len(plan.matrices), "block_unshard")
+    device = gathered.device
+    params._ensure(plan, "block_unshard", lambda: _check_unshard(plan, params.tensors, device))
+    _same_device(device, params.tensors[0])
+    ctx, stream = _launch(device)
+    with ctx:
+        _check(lib().tide_block_unshard(plan.handle, ctypes.c_void_p(gathered.data_ptr()),
+                                        params.array, _OUT_FLAG[params.tensors[0].dtype], stream))
+
+
+__all__ = ["Blocks", "BlockPlan", "block_quant", "block_dequant", "block_mm", "block_mm_dx",
+           "block_mm_dw", "block_linear", "block_shard", "block_unshard"]

@@ -24,7 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtide.so")
 
-SOURCES = ["plan.cpp", "runtime.hip", "kernels.hip", "noalloc.hip"]
+SOURCES = ["plan.cpp", "block_args.cpp", "runtime.hip", "kernels.hip", "noalloc.hip",
+           "block_cast.hip", "block_mm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

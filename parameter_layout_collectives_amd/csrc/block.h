@@ -1,0 +1,75 @@
+// Matrices in 8-bit blocks: the format, the checks of its entry points
+// (block_args.cpp, host only) and the launches (block_cast.hip, block_mm.hip).
+//
+// A matrix [R, C] is held as codes [R, Cp] (e4m3 bytes, Cp = C rounded up to
+// 128) and scales [R, Sp] (e8m0 bytes, one per 128 columns, rounded up to 4):
+// element (r, c) is e4m3(codes[r, c]) * 2^(scales[r, c / 128] - 127).  Blocks
+// lie inside one row, so a dim-0 shard boundary never cuts one.
+#pragma once
+
+#include "internal.h"
+
+namespace tide {
+
+constexpr int64_t kBlockCols = 128;
+inline int64_t block_cols(int64_t c) { return (c + kBlockCols - 1) / kBlockCols * kBlockCols; }
+inline int64_t block_count(int64_t c) { return (c + kBlockCols - 1) / kBlockCols; }
+inline int64_t block_scale_cols(int64_t c) { return (block_count(c) + 3) / 4 * 4; }
+
+// Element types that become 8-bit blocks or come back from them.
+enum ElemType { kElemBf16 = 0, kElemF16 = 1, kElemF32 = 2 };
+inline ElemType in_type(uint32_t flags) {
+    return (flags & TIDE_F_GRAD_F32) ? kElemF32 : (flags & TIDE_F_GRAD_F16) ? kElemF16 : kElemBf16;
+}
+inline ElemType out_type(uint32_t flags) {
+    return (flags & TIDE_F_OUT_BF16) ? kElemBf16 : (flags & TIDE_F_OUT_F16) ? kElemF16 : kElemF32;
+}
+inline int elem_size(ElemType t) { return t == kElemF32 ? 4 : 2; }
+
+// The three products.  Each is out[i, j] = sum over c of I(i, c) * J(c, j),
+// with J always in 8-bit blocks:
+//   kMm    i = token, j = row of W, c = column: I = X (blocks), J = W
+//   kMmDx  i = token, j = column of W, c = row of W: I = dY (bf16), J = W
+//   kMmDw  i = row of W, j = column, c = token: I = dY transposed, J = X
+enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
+
+// The card's compute units (a product's tiles are counted against them), the
+// most rows the skinny kernel takes, and the bounds of a split sum.
+constexpr int64_t kCus = 256;
+constexpr int64_t kSkinnyRows = 64;
+constexpr int64_t kMinSplitSteps = 4;
+constexpr int64_t kMaxSplits = 16;
+
+// How a product runs: the kernel, and into how many pieces its sum is cut.
+enum MmKernel { kMmEight, kMmWide, kMmSkinny };
+struct MmChoice {
+    MmKernel kernel;
+    int tile;            // 256 or 128 rows and columns of the output per workgroup
+    int splits;          // pieces of the sum (1: no workspace)
+    int64_t chunk;       // steps of the sum in one piece
+    int64_t workspace;   // bytes
+};
+MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool may_split);
+
+tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
+                              const void *scales, uint32_t flags);
+tide_status check_block_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                                const void *out, uint32_t flags);
+tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *master,
+                              const void *block, uint32_t flags);
+tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void *const *params,
+                                uint32_t flags);
+
+// Operands of a product as its entry point got them: `a` is X's codes or dY.
+struct MmArgs {
+    const void *a, *a_scales;
+    const void *b, *b_scales;
+    int64_t M, N, K;
+    void *out;
+    void *workspace;
+    int64_t workspace_bytes;
+    uint32_t flags;
+};
+tide_status check_mm(MmOp op, const char *name, const MmArgs &g);
+
+}  // namespace tide

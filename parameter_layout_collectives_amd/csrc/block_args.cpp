@@ -1,0 +1,286 @@
+// Host side of the 8-bit block operators: block plans, argument checks and
+// the choice of a product's kernel.  Makes no HIP call.
+#include <algorithm>
+#include <new>
+
+#include "block.h"
+
+namespace tide {
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;   // rows and columns of a product or a block matrix
+
+struct Bytes {
+    uintptr_t lo, hi;
+};
+Bytes bytes_of(const void *p, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, a + static_cast<uintptr_t>(n)};
+}
+bool overlap(const Bytes &a, const Bytes &b) { return a.lo < b.hi && b.lo < a.hi; }
+bool misaligned(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+tide_status bad(const char *name, const char *what) {
+    return fail(TIDE_E_INVALID, std::string(name) + ": " + what);
+}
+
+tide_status check_flags(const char *name, uint32_t flags, uint32_t known) {
+    if (flags & ~known) return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": unknown flag bits");
+    if ((flags & TIDE_F_GRAD_F16) && (flags & TIDE_F_GRAD_F32))
+        return bad(name, "TIDE_F_GRAD_F16 and TIDE_F_GRAD_F32 both set");
+    if ((flags & TIDE_F_OUT_BF16) && (flags & TIDE_F_OUT_F16))
+        return bad(name, "TIDE_F_OUT_BF16 and TIDE_F_OUT_F16 both set");
+    return TIDE_OK;
+}
+
+tide_status check_dims(const char *name, int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return bad(name, "negative size");
+    if (rows >= kMaxDim || cols >= kMaxDim) return bad(name, "a size of 2^31 or more");
+    // the products' byte offsets then fit int64 with room to spare
+    if (rows && block_cols(cols) > (int64_t(1) << 60) / rows) return bad(name, "sizes overflow");
+    return TIDE_OK;
+}
+
+// A matrix in 8-bit blocks: both pointers present and aligned for the widest
+// loads the kernels make of them.
+tide_status check_blocks(const char *name, const char *which, const void *codes,
+                         const void *scales) {
+    if (!codes) return bad(name, (std::string(which) + " codes are NULL").c_str());
+    if (!scales) return bad(name, (std::string(which) + " scales are NULL").c_str());
+    if (misaligned(codes, 16))
+        return bad(name, (std::string(which) + " codes are not 16-byte aligned").c_str());
+    if (misaligned(scales, 4))
+        return bad(name, (std::string(which) + " scales are not 4-byte aligned").c_str());
+    return TIDE_OK;
+}
+
+tide_status check_block_plan(const char *name, const tide_plan *bp) {
+    if (!bp) return bad(name, "plan is NULL");
+    if (!bp->nblk) return bad(name, "not a plan of tide_plan_create_blocks");
+    return TIDE_OK;
+}
+
+}  // namespace
+
+tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
+                              const void *scales, uint32_t flags) {
+    const char *name = "tide_block_quant";
+    tide_status st = check_flags(name, flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32);
+    if (st == TIDE_OK) st = check_dims(name, rows, cols);
+    if (st != TIDE_OK || rows == 0 || cols == 0) return st;
+    const int es = elem_size(in_type(flags));
+    if (!x) return bad(name, "x is NULL");
+    if (misaligned(x, es)) return bad(name, "x is not aligned to its element size");
+    st = check_blocks(name, "the output's", codes, scales);
+    if (st != TIDE_OK) return st;
+    const Bytes in = bytes_of(x, rows * cols * es), c = bytes_of(codes, rows * block_cols(cols)),
+                s = bytes_of(scales, rows * block_scale_cols(cols));
+    if (overlap(in, c) || overlap(in, s) || overlap(c, s))
+        return bad(name, "an output overlaps the input or the other output");
+    return TIDE_OK;
+}
+
+tide_status check_block_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                                const void *out, uint32_t flags) {
+    const char *name = "tide_block_dequant";
+    tide_status st = check_flags(name, flags, TIDE_F_OUT_BF16 | TIDE_F_OUT_F16);
+    if (st == TIDE_OK) st = check_dims(name, rows, cols);
+    if (st != TIDE_OK || rows == 0 || cols == 0) return st;
+    st = check_blocks(name, "the input's", codes, scales);
+    if (st != TIDE_OK) return st;
+    const int es = elem_size(out_type(flags));
+    if (!out) return bad(name, "out is NULL");
+    if (misaligned(out, es)) return bad(name, "out is not aligned to its element size");
+    const Bytes o = bytes_of(out, rows * cols * es);
+    if (overlap(o, bytes_of(codes, rows * block_cols(cols))) ||
+        overlap(o, bytes_of(scales, rows * block_scale_cols(cols))))
+        return bad(name, "out overlaps the input");
+    return TIDE_OK;
+}
+
+tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *master,
+                              const void *block, uint32_t flags) {
+    const char *name = "tide_block_shard";
+    tide_status st = check_block_plan(name, bp);
+    if (st != TIDE_OK) return st;
+    if (rank < 0 || rank >= bp->N)
+        return fail(TIDE_E_INVALID, std::string(name) + ": rank " + std::to_string(rank) +
+                                        " outside [0, " + std::to_string(bp->N) + ")");
+    st = check_flags(name, flags, 0);
+    if (st != TIDE_OK || bp->S == 0) return st;
+    if (!master) return bad(name, "master is NULL");
+    if (misaligned(master, 4)) return bad(name, "master is not aligned to its element size");
+    if (!block) return bad(name, "block is NULL");
+    if (misaligned(block, 16)) return bad(name, "block is not 16-byte aligned");
+    if (overlap(bytes_of(master, bp->blk_S * 4), bytes_of(block, bp->S * 4)))
+        return bad(name, "block overlaps master");
+    return TIDE_OK;
+}
+
+tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void *const *params,
+                                uint32_t flags) {
+    const char *name = "tide_block_unshard";
+    tide_status st = check_block_plan(name, bp);
+    if (st != TIDE_OK) return st;
+    st = check_flags(name, flags, TIDE_F_OUT_BF16 | TIDE_F_OUT_F16);
+    if (st != TIDE_OK || bp->psi == 0) return st;
+    if (!gathered) return bad(name, "gathered is NULL");
+    if (misaligned(gathered, 16)) return bad(name, "gathered is not 16-byte aligned");
+    if (!params) return bad(name, "params array is NULL");
+    const int es = elem_size(out_type(flags));
+    const Bytes src = bytes_of(gathered, bp->S * 4 * bp->N);
+    std::vector<Bytes> dst;
+    try {
+        dst.reserve(bp->nblk);
+    } catch (const std::bad_alloc &) {
+        return fail(TIDE_E_NOMEM, std::string(name) + ": out of host memory");
+    }
+    for (int32_t j = 0; j < bp->nblk; j++) {
+        const int64_t n = bp->d0[j] * bp->blk_inner[j];
+        if (n == 0) continue;
+        const std::string which = "params[" + std::to_string(j) + "]";
+        if (!params[j]) return bad(name, (which + " is NULL").c_str());
+        if (misaligned(params[j], es))
+            return bad(name, (which + " is not aligned to its element size").c_str());
+        dst.push_back(bytes_of(params[j], n * es));
+        if (overlap(dst.back(), src))
+            return bad(name, (which + " overlaps the gathered buffer").c_str());
+    }
+    std::sort(dst.begin(), dst.end(), [](const Bytes &a, const Bytes &b) { return a.lo < b.lo; });
+    for (size_t k = 1; k < dst.size(); k++)
+        if (overlap(dst[k - 1], dst[k])) return bad(name, "a destination overlaps another");
+    return TIDE_OK;
+}
+
+tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
+    const uint32_t known =
+        TIDE_F_OUT_BF16 | (op == kMmDw ? static_cast<uint32_t>(TIDE_F_ACCUMULATE) : 0u);
+    tide_status st = check_flags(name, g.flags, known);
+    if (st != TIDE_OK) return st;
+    if (g.M < 0 || g.N < 0 || g.K < 0) return bad(name, "negative size");
+    for (int64_t rows : {g.M, g.N})
+        for (int64_t cols : {g.N, g.K})
+            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
+    if (g.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
+    if (g.workspace_bytes > 0 && !g.workspace) return bad(name, "workspace is NULL");
+    if (g.workspace && misaligned(g.workspace, 16))
+        return bad(name, "workspace is not 16-byte aligned");
+    const int64_t orows = op == kMmDw ? g.N : g.M, ocols = op == kMm ? g.N : g.K;
+    const int64_t sum = op == kMm ? g.K : op == kMmDx ? g.N : g.M;
+    if (orows == 0 || ocols == 0) return TIDE_OK;
+    const int es = elem_size(out_type(g.flags));
+    if (!g.out) return bad(name, "out is NULL");
+    if (misaligned(g.out, es)) return bad(name, "out is not aligned to its element size");
+    const Bytes out = bytes_of(g.out, orows * ocols * es);
+    const Bytes wsp = bytes_of(g.workspace, g.workspace ? g.workspace_bytes : 0);
+    if (overlap(out, wsp)) return bad(name, "out overlaps the workspace");
+    if (sum == 0) return TIDE_OK;
+    // a: X in blocks [M, K] (kMm) or dY [M, N]; b: W [N, K] or X [M, K] in blocks
+    Bytes in[4];
+    int n = 0;
+    if (op == kMm) {
+        st = check_blocks(name, "x's", g.a, g.a_scales);
+        in[n++] = bytes_of(g.a, g.M * block_cols(g.K));
+        in[n++] = bytes_of(g.a_scales, g.M * block_scale_cols(g.K));
+    } else {
+        if (!g.a) return bad(name, "dy is NULL");
+        if (misaligned(g.a, 2)) return bad(name, "dy is not aligned to its element size");
+        in[n++] = bytes_of(g.a, g.M * g.N * 2);
+    }
+    if (st == TIDE_OK) st = check_blocks(name, op == kMmDw ? "x's" : "w's", g.b, g.b_scales);
+    if (st != TIDE_OK) return st;
+    const int64_t brows = op == kMmDw ? g.M : g.N;
+    in[n++] = bytes_of(g.b, brows * block_cols(g.K));
+    in[n++] = bytes_of(g.b_scales, brows * block_scale_cols(g.K));
+    for (int k = 0; k < n; k++) {
+        if (overlap(out, in[k])) return bad(name, "out overlaps an operand");
+        if (overlap(wsp, in[k])) return bad(name, "the workspace overlaps an operand");
+    }
+    return TIDE_OK;
+}
+
+MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool may_split) {
+    MmChoice c;
+    const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
+    const int64_t sum = op == kMm ? K : op == kMmDx ? N : M;
+    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16);
+    c.kernel = op == kMm && M <= kSkinnyRows ? kMmSkinny : eight ? kMmEight : kMmWide;
+    const int64_t step = eight ? 128 : 64;
+    const int64_t steps = (sum + step - 1) / step;
+    auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };
+    c.tile = tiles(256) >= kCus * 3 / 4 ? 256 : 128;
+    c.splits = 1;
+    c.chunk = steps;
+    c.workspace = 0;
+    if (c.kernel == kMmSkinny || !may_split) return c;
+    const int64_t t = tiles(c.tile), full = kCus * (c.tile == 256 ? 1 : 2);
+    if (t * 2 <= full && steps >= 2 * kMinSplitSteps) {
+        int64_t s = std::min(full / t, steps / kMinSplitSteps);
+        s = std::min<int64_t>(s, kMaxSplits);
+        c.chunk = (steps + s - 1) / s;
+        c.splits = static_cast<int>((steps + c.chunk - 1) / c.chunk);
+        if (c.splits > 1) c.workspace = rows * cols * 4 * c.splits;
+    }
+    return c;
+}
+
+}  // namespace tide
+
+using tide::bad;
+using tide::fail;
+
+extern "C" {
+
+int64_t tide_block_cols(int64_t cols) { return cols < 0 ? -1 : tide::block_cols(cols); }
+
+int64_t tide_block_scale_cols(int64_t cols) {
+    return cols < 0 ? -1 : tide::block_scale_cols(cols);
+}
+
+tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int32_t *select,
+                                    tide_plan **out_plan) {
+    const char *name = "tide_plan_create_blocks";
+    if (!out_plan) return bad(name, "out_plan is NULL");
+    *out_plan = nullptr;
+    if (!plan) return bad(name, "plan is NULL");
+    if (plan->nblk) return bad(name, "plan is a block plan itself");
+    if (n < 1 || n > plan->P) return bad(name, "n outside [1, nparams]");
+    if (!select) return bad(name, "select is NULL");
+    try {
+        std::vector<int64_t> d0(2 * static_cast<size_t>(n)), words(d0.size()), off(n), inner(n);
+        std::vector<char> seen(plan->P, 0);
+        for (int32_t j = 0; j < n; j++) {
+            const int32_t i = select[j];
+            if (i < 0 || i >= plan->P) return bad(name, "select holds an index out of range");
+            if (seen[i]) return bad(name, "select holds an index twice");
+            seen[i] = 1;
+            const tide_status st = tide::check_dims(name, plan->d0[i], plan->inner[i]);
+            if (st != TIDE_OK) return st;
+            d0[j] = d0[n + j] = plan->d0[i];
+            words[j] = tide::block_cols(plan->inner[i]) / 4;
+            words[n + j] = tide::block_scale_cols(plan->inner[i]) / 4;
+            off[j] = plan->off[i];
+            inner[j] = plan->inner[i];
+        }
+        // offsets at multiples of 4 words: every segment starts 16-byte aligned
+        tide_plan *p = nullptr;
+        const tide_status st =
+            tide_plan_create(plan->N, 2 * n, d0.data(), words.data(), 4, &p);
+        if (st != TIDE_OK) return st;
+        p->nblk = n;
+        p->blk_S = plan->S;
+        p->blk_off.swap(off);
+        p->blk_inner.swap(inner);
+        *out_plan = p;
+    } catch (const std::bad_alloc &) {
+        return fail(TIDE_E_NOMEM, std::string(name) + ": out of host memory");
+    }
+    return TIDE_OK;
+}
+
+int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {
+    if (op < 0 || op > 2 || m < 0 || n < 0 || k < 0) return -1;
+    return tide::mm_choose(static_cast<tide::MmOp>(op), m, n, k, flags, true).workspace;
+}
+
+}  // extern "C"

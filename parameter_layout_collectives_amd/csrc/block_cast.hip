@@ -1,0 +1,493 @@
+// Kernels that write and read matrices in 8-bit blocks, and their entry
+// points: tide_block_quant / tide_block_dequant (the activation checkpoint)
+// and tide_block_shard / tide_block_unshard (the 8-bit gather of sharded
+// weights).
+//
+// For a block x[0..127] of one row, with a = max|x| over its finite values:
+//   e = the smallest integer with a <= 448 * 2^e, kept in [-117, 119], 0 if a = 0
+//   code = the e4m3 number nearest to x * 2^-e, ties to even; |x * 2^-e| is cut
+//          at 448 (only a > 448 * 2^119 gets there); inf and NaN become NaN
+// A power of two as scale makes both directions exact but for the one rounding
+// to e4m3: the scaling moves the exponent alone, and code * 2^e is a bf16
+// number, since e4m3 has 4 significant bits and the bounds on e keep it normal.
+// (Within 2^e of 448 itself, a quarter of an octave of e4m3 is left unused for
+// some blocks, against a fp32 scale; its relative rounding error is the same.)
+//
+// All four move bytes with little arithmetic, so HBM bounds them: 16 lanes
+// share a block, 8 elements each (two 16-byte loads of fp32, one of bf16), and
+// each 16-lane group has kUnroll blocks in flight.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "block.h"
+
+namespace tide {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kLanes = 256;                        // lanes of a workgroup
+constexpr int kGroup = 16;                         // lanes that share a block
+constexpr int kGroups = kLanes / kGroup;           // blocks a workgroup handles at a time
+constexpr int kUnroll = 4;                         // blocks in flight per group
+constexpr int kChunk = kGroups * kUnroll;          // blocks a workgroup handles in all
+
+// 8 consecutive elements as fp32.  `vec`: the first one is 16-byte aligned
+// and all `n` asked for are whole vectors (n is 0 or 8 then).
+template <int ET>
+__device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = 0.0f;
+    if (n <= 0) return;
+    if (ET == kElemF32) {
+        const float *f = reinterpret_cast<const float *>(p);
+        if (vec) {
+            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f));
+            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f + 4));
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+        } else {
+            for (int i = 0; i < 8; i++)
+                if (i < n) v[i] = f[i];
+        }
+        return;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (vec) {
+        const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = a[i];
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) w[i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t h = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
+        v[i] = ET == kElemBf16
+                   ? __uint_as_float(h << 16)
+                   : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(h)));
+    }
+}
+
+// The largest value over the 16 lanes of a row (DPP rotations by 8, 4, 2, 1).
+__device__ __forceinline__ uint32_t max16(uint32_t u) {
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x128, 0xf, 0xf, false)));
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x124, 0xf, 0xf, false)));
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x122, 0xf, 0xf, false)));
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x121, 0xf, 0xf, false)));
+    return u;
+}
+
+// One lane's 8 values -> 8 codes; the block's scale byte is the same in all
+// 16 lanes.  Patterns of |x| order like the values, so the maximum is taken on
+// them as integers.
+__device__ __forceinline__ u32x2 encode8(const float *v, uint32_t *scale) {
+    uint32_t top = 0;
+    bool odd = false;                     // an inf or a NaN among the 8
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+        const bool finite = u < 0x7f800000u;
+        odd |= !finite;
+        top = max(top, finite ? u : 0u);
+    }
+    top = max16(top);
+    // a = m * 2^k with 1 <= m < 2: a <= 448 * 2^e = 1.75 * 2^(8+e) from
+    // e = k - 8 on if m <= 1.75, else from k - 7 on
+    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = top == 0 ? 0 : min(119, max(-117, e));
+    *scale = static_cast<uint32_t>(e + 127);
+    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(v[i] * s, -448.0f, 448.0f);
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+    u32x2 c = {static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if ((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u) {
+                const uint32_t m = 0xffu << (8 * (i & 3)), nan = 0x7fu << (8 * (i & 3));
+                if (i < 4)
+                    c.x = (c.x & ~m) | nan;
+                else
+                    c.y = (c.y & ~m) | nan;
+            }
+    }
+    return c;
+}
+
+// What a run of rows of one matrix is, for the kernels below.
+struct Rows {
+    int64_t src;          // first element of the rows in the source (or destination)
+    int64_t codes;        // byte of the first code row, from the block's start
+    int64_t scales;       // byte of the first scale row
+    int64_t rows, real;   // rows to write, and of them rows that exist in the source
+    int64_t cols;
+    uint32_t nb;          // blocks in a row
+    uint32_t wg0;         // first workgroup that works on it
+};
+
+// Reads blocks [first, first + kChunk) of `d` (row-major), encodes and stores
+// them.  The last block of a row also fills the row's spare scale bytes.
+template <int ET>
+__device__ __forceinline__ void encode_chunk(const Rows &d, int64_t first, const char *src,
+                                             char *codes, char *scales, bool vec) {
+    constexpr int ES = ET == kElemF32 ? 4 : 2;
+    const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
+    const int64_t units = d.rows * d.nb;
+    const int64_t row0 = first / d.nb;                      // uniform
+    const uint32_t b0 = static_cast<uint32_t>(first - row0 * d.nb);
+    const int64_t cp = static_cast<int64_t>(d.nb) * kBlockCols, sp = (d.nb + 3) / 4 * 4;
+    float v[kUnroll][8];
+    int64_t row[kUnroll];
+    uint32_t blk[kUnroll];
+#pragma unroll
+    for (int q = 0; q < kUnroll; q++) {
+        const uint32_t i = b0 + q * kGroups + group;        // < nb + kChunk
+        row[q] = row0 + i / d.nb;
+        blk[q] = i % d.nb;
+        const int64_t c = static_cast<int64_t>(blk[q]) * kBlockCols + lane * 8;
+        const bool there = first + q * kGroups + group < units && row[q] < d.real;
+        const int64_t left = d.cols - c;
+        load8<ET>(src + (row[q] * d.cols + c) * ES,
+                  there ? static_cast<int>(left < 8 ? left : 8) : 0, vec, v[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kUnroll; q++) {
+        uint32_t scale;
+        const u32x2 c = encode8(v[q], &scale);
+        if (first + q * kGroups + group >= units) continue;
+        *reinterpret_cast<u32x2 *>(codes + row[q] * cp + static_cast<int64_t>(blk[q]) * kBlockCols +
+                                   lane * 8) = c;
+        char *s = scales + row[q] * sp + blk[q];
+        if (lane == 0) *s = static_cast<char>(scale);
+        if (blk[q] == d.nb - 1 && lane > 0 && blk[q] + lane < sp) s[lane] = 127;
+    }
+}
+
+template <int ET>
+__global__ __launch_bounds__(kLanes) void quant_kernel(const char *__restrict__ x, int64_t rows,
+                                                       int64_t cols, char *__restrict__ codes,
+                                                       char *__restrict__ scales, int vec) {
+    const Rows d{0, 0, 0, rows, rows, cols,
+                 static_cast<uint32_t>((cols + kBlockCols - 1) / kBlockCols), 0};
+    encode_chunk<ET>(d, static_cast<int64_t>(blockIdx.x) * kChunk, x, codes, scales, vec != 0);
+}
+
+// 8 codes of one block -> the output type, stored at p.
+template <int ET>
+__device__ __forceinline__ void decode8(u32x2 c, uint32_t scale, char *p, int n, bool vec) {
+    const float s = __uint_as_float(scale << 23);            // scale bytes are 10..246
+    bf16x2 h[4];
+    h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, s, false);
+    h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, s, true);
+    h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, s, false);
+    h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, s, true);
+    if (ET == kElemF32) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = static_cast<float>(h[i / 2][i & 1]);
+        if (vec) {
+            f32x4 *o = reinterpret_cast<f32x4 *>(p);
+            __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, o);
+            __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, o + 1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < n) reinterpret_cast<float *>(p)[i] = v[i];
+        }
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (ET == kElemBf16) {
+            w[i] = __builtin_bit_cast(uint32_t, h[i]);
+        } else {   // fp16: bf16 -> fp32 is exact, then one rounding (to inf past 65504)
+            const f16x2 f = {static_cast<_Float16>(static_cast<float>(h[i][0])),
+                             static_cast<_Float16>(static_cast<float>(h[i][1]))};
+            w[i] = __builtin_bit_cast(uint32_t, f);
+        }
+    }
+    if (vec) {
+        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4 *>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n)
+                reinterpret_cast<uint16_t *>(p)[i] =
+                    static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Blocks [first, first + kChunk) of a matrix of `rows` rows; row r's codes and
+// scales are found by at(r, &codes, &scales).
+template <int ET, class At>
+__device__ __forceinline__ void decode_chunk(int64_t rows, int64_t cols, uint32_t nb, int64_t first,
+                                             At at, char *out, bool vec) {
+    constexpr int ES = ET == kElemF32 ? 4 : 2;
+    const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
+    const int64_t units = rows * nb;
+    const int64_t row0 = first / nb;
+    const uint32_t b0 = static_cast<uint32_t>(first - row0 * nb);
+    u32x2 c[kUnroll];
+    uint32_t scale[kUnroll];
+    char *o[kUnroll];
+    int n[kUnroll];
+#pragma unroll
+    for (int q = 0; q < kUnroll; q++) {
+        const uint32_t i = b0 + q * kGroups + group;
+        const int64_t row = row0 + i / nb;
+        const uint32_t blk = i % nb;
+        const int64_t col = static_cast<int64_t>(blk) * kBlockCols + lane * 8;
+        const int64_t left = cols - col;
+        n[q] = first + q * kGroups + group < units ? static_cast<int>(left < 8 ? left : 8) : 0;
+        o[q] = out + (row * cols + col) * ES;
+        if (n[q] > 0) {
+            const char *codes, *scales;
+            at(row, &codes, &scales);
+            c[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(codes + col));
+            scale[q] = static_cast<uint8_t>(scales[blk]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kUnroll; q++)
+        if (n[q] > 0) decode8<ET>(c[q], scale[q], o[q], n[q], vec);
+}
+
+template <int ET>
+__global__ __launch_bounds__(kLanes) void dequant_kernel(const char *__restrict__ codes,
+                                                         const char *__restrict__ scales,
+                                                         int64_t rows, int64_t cols,
+                                                         char *__restrict__ out, int vec) {
+    const uint32_t nb = static_cast<uint32_t>((cols + kBlockCols - 1) / kBlockCols);
+    const int64_t cp = static_cast<int64_t>(nb) * kBlockCols, sp = (nb + 3) / 4 * 4;
+    decode_chunk<ET>(rows, cols, nb, static_cast<int64_t>(blockIdx.x) * kChunk,
+                     [=](int64_t r, const char **c, const char **s) {
+                         *c = codes + r * cp;
+                         *s = scales + r * sp;
+                     },
+                     out, vec != 0);
+}
+
+// A unit's matrices travel as kernel arguments (no table in device memory, so
+// nothing to allocate, upload or keep for a captured launch): as many per
+// launch as fit 4 KB.
+constexpr int kPerLaunch = 56;
+struct ShardArgs {
+    Rows m[kPerLaunch];
+    int n;
+};
+struct UnshardArgs {
+    Rows m[kPerLaunch];             // rows = the matrix's rows, real = rows per rank
+    int n;
+};
+static_assert(sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
+
+// The matrix that workgroup `wg` works on: the last one with wg0 <= wg.
+template <class A>
+__device__ __forceinline__ int matrix_of(const A &a, uint32_t wg) {
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.m[mid].wg0 <= wg)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *__restrict__ master,
+                                                       char *__restrict__ block, int aligned) {
+    const Rows d = a.m[matrix_of(a, blockIdx.x)];
+    const bool vec = aligned && d.src % 4 == 0 && d.cols % 8 == 0;
+    encode_chunk<kElemF32>(d, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
+                           master + d.src * 4, block + d.codes, block + d.scales, vec);
+}
+
+// `src` of a matrix holds its destination's address here; row r lies in rank
+// block r / c at row r % c.
+template <int ET>
+__global__ __launch_bounds__(kLanes) void unshard_kernel(UnshardArgs a,
+                                                         const char *__restrict__ gathered,
+                                                         int64_t rank_bytes) {
+    const Rows d = a.m[matrix_of(a, blockIdx.x)];
+    char *out = reinterpret_cast<char *>(d.src);
+    const bool vec = d.src % 16 == 0 && d.cols % 8 == 0;
+    const int64_t cp = static_cast<int64_t>(d.nb) * kBlockCols, sp = (d.nb + 3) / 4 * 4;
+    const int64_t c = d.real;
+    decode_chunk<ET>(d.rows, d.cols, d.nb, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
+                     [=](int64_t r, const char **codes, const char **scales) {
+                         const int64_t rank = r / c, in = r - rank * c;
+                         const char *b = gathered + rank * rank_bytes;
+                         *codes = b + d.codes + in * cp;
+                         *scales = b + d.scales + in * sp;
+                     },
+                     out, vec);
+}
+
+// A launch counts its lanes in 32 bits.
+constexpr int64_t kMaxGrid = 0xffffffffll / kLanes;
+
+int64_t chunks(int64_t units) { return (units + kChunk - 1) / kChunk; }
+
+tide_status too_many(const char *name) {
+    return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
+}
+
+// Launches `launch(args, grid)` over the plan's matrices, kPerLaunch at a time;
+// `fill(j, &rows)` describes matrix j, with rows.rows = 0 for nothing to do.
+template <class Args, class Fill, class Launch>
+tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Launch launch) {
+    int32_t j = 0;
+    while (j < bp->nblk) {
+        Args a;
+        a.n = 0;
+        int64_t grid = 0;
+        for (; j < bp->nblk && a.n < kPerLaunch; j++) {
+            Rows r;
+            fill(j, &r);
+            const int64_t units = r.rows * r.nb;
+            if (units == 0) continue;
+            if (grid + chunks(units) > kMaxGrid) break;
+            r.wg0 = static_cast<uint32_t>(grid);
+            grid += chunks(units);
+            a.m[a.n++] = r;
+        }
+        if (a.n == 0) {
+            if (j < bp->nblk) return too_many(name);
+            break;
+        }
+        launch(a, static_cast<unsigned>(grid));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
+    }
+    return TIDE_OK;
+}
+
+uint32_t blocks_of(int64_t cols) { return static_cast<uint32_t>(block_count(cols)); }
+
+}  // namespace
+}  // namespace tide
+
+using namespace tide;
+
+extern "C" tide_status tide_block_quant(const void *x, int64_t rows, int64_t cols, void *codes,
+                                        void *scales, uint32_t flags, void *stream) {
+    tide_status st = check_block_quant(x, rows, cols, codes, scales, flags);
+    if (st != TIDE_OK) return st;
+    if (rows && cols) {
+        const int64_t grid = chunks(rows * block_count(cols));
+        if (grid > kMaxGrid) return too_many("tide_block_quant");
+        const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && cols % 8 == 0;
+        const dim3 g(static_cast<unsigned>(grid)), b(kLanes);
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        const char *in = static_cast<const char *>(x);
+        char *c = static_cast<char *>(codes), *sc = static_cast<char *>(scales);
+        switch (in_type(flags)) {
+            case kElemBf16: quant_kernel<kElemBf16><<<g, b, 0, s>>>(in, rows, cols, c, sc, vec); break;
+            case kElemF16: quant_kernel<kElemF16><<<g, b, 0, s>>>(in, rows, cols, c, sc, vec); break;
+            case kElemF32: quant_kernel<kElemF32><<<g, b, 0, s>>>(in, rows, cols, c, sc, vec); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return hip_fail("tide_block_quant: kernel launch", e);
+    }
+    clear_error();
+    return TIDE_OK;
+}
+
+extern "C" tide_status tide_block_dequant(const void *codes, const void *scales, int64_t rows,
+                                          int64_t cols, void *out, uint32_t flags, void *stream) {
+    tide_status st = check_block_dequant(codes, scales, rows, cols, out, flags);
+    if (st != TIDE_OK) return st;
+    if (rows && cols) {
+        const int64_t grid = chunks(rows * block_count(cols));
+        if (grid > kMaxGrid) return too_many("tide_block_dequant");
+        const int vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && cols % 8 == 0;
+        const dim3 g(static_cast<unsigned>(grid)), b(kLanes);
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        const char *c = static_cast<const char *>(codes), *sc = static_cast<const char *>(scales);
+        char *o = static_cast<char *>(out);
+        switch (out_type(flags)) {
+            case kElemBf16: dequant_kernel<kElemBf16><<<g, b, 0, s>>>(c, sc, rows, cols, o, vec); break;
+            case kElemF16: dequant_kernel<kElemF16><<<g, b, 0, s>>>(c, sc, rows, cols, o, vec); break;
+            case kElemF32: dequant_kernel<kElemF32><<<g, b, 0, s>>>(c, sc, rows, cols, o, vec); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return hip_fail("tide_block_dequant: kernel launch", e);
+    }
+    clear_error();
+    return TIDE_OK;
+}
+
+extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, const float *master,
+                                        void *block, uint32_t flags, void *stream) {
+    tide_status st = check_block_shard(plan, rank, master, block, flags);
+    if (st != TIDE_OK) return st;
+    const int aligned = reinterpret_cast<uintptr_t>(master) % 16 == 0;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = over_matrices<ShardArgs>(
+        "tide_block_shard", plan,
+        [&](int32_t j, Rows *r) {
+            const int64_t c = plan->c[j], d0 = plan->d0[j];
+            *r = Rows{plan->blk_off[j],
+                      plan->off[j] * 4,
+                      plan->off[plan->nblk + j] * 4,
+                      c,
+                      std::min(c, std::max<int64_t>(0, d0 - rank * c)),
+                      plan->blk_inner[j],
+                      blocks_of(plan->blk_inner[j]),
+                      0};
+        },
+        [&](const ShardArgs &a, unsigned grid) {
+            shard_kernel<<<dim3(grid), dim3(kLanes), 0, s>>>(
+                a, reinterpret_cast<const char *>(master), static_cast<char *>(block), aligned);
+        });
+    if (st == TIDE_OK) clear_error();
+    return st;
+}
+
+extern "C" tide_status tide_block_unshard(const tide_plan *plan, const void *gathered,
+                                          void *const *params, uint32_t flags, void *stream) {
+    tide_status st = check_block_unshard(plan, gathered, params, flags);
+    if (st != TIDE_OK) return st;
+    const ElemType t = out_type(flags);
+    const int64_t rank_bytes = plan->S * 4;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const char *g = static_cast<const char *>(gathered);
+    st = over_matrices<UnshardArgs>(
+        "tide_block_unshard", plan,
+        [&](int32_t j, Rows *r) {
+            *r = Rows{static_cast<int64_t>(reinterpret_cast<uintptr_t>(params[j])),
+                      plan->off[j] * 4,
+                      plan->off[plan->nblk + j] * 4,
+                      plan->d0[j],
+                      plan->c[j],
+                      plan->blk_inner[j],
+                      blocks_of(plan->blk_inner[j]),
+                      0};
+        },
+        [&](const UnshardArgs &a, unsigned grid) {
+            const dim3 gr(grid), b(kLanes);
+            switch (t) {
+                case kElemBf16: unshard_kernel<kElemBf16><<<gr, b, 0, s>>>(a, g, rank_bytes); break;
+                case kElemF16: unshard_kernel<kElemF16><<<gr, b, 0, s>>>(a, g, rank_bytes); break;
+                case kElemF32: unshard_kernel<kElemF32><<<gr, b, 0, s>>>(a, g, rank_bytes); break;
+            }
+        });
+    if (st == TIDE_OK) clear_error();
+    return st;
+}

@@ -1,0 +1,657 @@
+// Matrix products over 8-bit blocks, and their entry points:
+//   tide_block_mm      Y[m, n]  = sum over k of X[m, k] W[n, k]
+//   tide_block_mm_dx   dX[m, k] = sum over n of dY[m, n] W[n, k]
+//   tide_block_mm_dw   dW[n, k] = sum over m of dY[m, n] X[m, k]
+// with X and W the values of their 8-bit blocks and dY in bf16.
+//
+// All three are out[i, j] = sum over c of I(i, c) J(c, j).  J is the 8-bit
+// operand whose index runs along the output's rows in memory; it takes the
+// matrix instruction's row side, so that a lane's 4 results are neighbours in
+// memory.  Sums are held in fp32.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "block.h"
+
+namespace tide {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+#define LDS_AS __attribute__((address_space(3)))
+
+struct MmLaunch {
+    const char *a, *as;          // I: X's codes and scales, or dY
+    const char *b, *bs;          // J: codes and scales
+    char *out;
+    float *partial;              // splits x [rows, cols] sums, or null
+    int64_t rows, cols, sum;     // of the output, and the length of the sum
+    int64_t a_pitch, as_pitch;   // bytes between rows
+    int64_t b_pitch, bs_pitch;
+    int64_t chunk;               // steps of the sum per split
+    int tr, tc;                  // tiles along rows and columns
+    int out_bf16, accumulate, aligned;
+};
+
+// Workgroup `id` of tr x tc tiles -> its tile.  IDs go to the 8 XCDs in turn
+// and each XCD has its own L2: every XCD takes one contiguous run of tiles, and
+// within it 8 tile rows advance together, so that the tiles an XCD works on at
+// one time share their operands' rows.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tr, uint32_t tc, uint32_t *r,
+                                        uint32_t *c) {
+    const uint32_t n = tr * tc, q = n / 8, rm = n % 8, x = id % 8;
+    const uint32_t v = x * q + min(x, rm) + id / 8;
+    const uint32_t per = 8 * tc, g = v / per, in = v - g * per;
+    const uint32_t h = min(8u, tr - 8 * g);
+    *r = 8 * g + in % h;
+    *c = in / h;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+}
+
+// Stores 4 neighbouring results of one output row (n of them exist).
+__device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t col, f32x4 v) {
+    const int64_t left = p.cols - col;
+    if (row >= p.rows || left <= 0) return;
+    const int64_t at = row * p.cols + col;
+    if (p.partial) {
+        float *o = p.partial + at + static_cast<int64_t>(blockIdx.y) * p.rows * p.cols;
+        if (left >= 4 && (p.cols & 3) == 0)
+            *reinterpret_cast<f32x4 *>(o) = v;
+        else
+            for (int i = 0; i < 4; i++)
+                if (i < left) o[i] = v[i];
+        return;
+    }
+    if (p.out_bf16) {
+        __bf16 *o = reinterpret_cast<__bf16 *>(p.out) + at;
+        if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+            if (p.accumulate) {
+                const bf16x4 old = *reinterpret_cast<const bf16x4 *>(o);
+                for (int i = 0; i < 4; i++) v[i] += static_cast<float>(old[i]);
+            }
+            *reinterpret_cast<u32x2 *>(o) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+        } else {
+            for (int i = 0; i < 4; i++)
+                if (i < left)
+                    o[i] = static_cast<__bf16>(p.accumulate ? static_cast<float>(o[i]) + v[i] : v[i]);
+        }
+        return;
+    }
+    float *o = reinterpret_cast<float *>(p.out) + at;
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+        if (p.accumulate) v += *reinterpret_cast<const f32x4 *>(o);
+        *reinterpret_cast<f32x4 *>(o) = v;
+    } else {
+        for (int i = 0; i < 4; i++)
+            if (i < left) o[i] = p.accumulate ? o[i] + v[i] : v[i];
+    }
+}
+
+// Adds the splits' sums in split order.
+__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ partial, int splits,
+                                                   int64_t n, char *__restrict__ out, int out_bf16,
+                                                   int accumulate) {
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 1024) {
+        const int m = static_cast<int>(min(n - i, static_cast<int64_t>(4)));
+        for (int e = 0; e < m; e++) {
+            float s = partial[i + e];
+            for (int q = 1; q < splits; q++) s += partial[q * n + i + e];
+            if (out_bf16) {
+                __bf16 *o = reinterpret_cast<__bf16 *>(out) + i + e;
+                *o = static_cast<__bf16>(accumulate ? static_cast<float>(*o) + s : s);
+            } else {
+                float *o = reinterpret_cast<float *>(out) + i + e;
+                *o = accumulate ? *o + s : s;
+            }
+        }
+    }
+}
+
+// An empty sum: zeros.
+__global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        if (es == 4)
+            reinterpret_cast<float *>(out)[i] = 0.0f;
+        else
+            reinterpret_cast<uint16_t *>(out)[i] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Y = X W^T with the 8-bit matrix instruction (bf16 output)
+// ---------------------------------------------------------------------------
+//
+// One step of the sum is one block of 128 columns: the scaled instruction
+// (16 x 16 x 128) takes both operands' e8m0 scales, so a block's scale costs no
+// arithmetic.  Its sums of 128 products keep fewer bits than fp32 (1.6e-5 of
+// the result's norm on normal data); the bf16 output's own rounding is 100
+// times that, and an fp32 output takes the kernel below, whose products are
+// exact.
+//
+// A T x T tile of the output per workgroup, WI x WJ waves.  A row's 128 codes
+// are 8 chunks of 16 bytes; chunk h of row r lies at h ^ (r & 7) in LDS, so the
+// 16 lanes that read one chunk of 16 rows touch all banks.  Operand k-order
+// inside a step is free as long as both sides agree: a lane reads chunks g and
+// g + 4 (g = lane / 16).  Two buffers: the next step's codes travel to registers
+// while this one is multiplied.
+template <int T, int WI, int WJ>
+__global__ __launch_bounds__(WI * WJ * 64) void eight_kernel(MmLaunch p) {
+    constexpr int NT = WI * WJ * 64;
+    constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
+    constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
+    __shared__ __attribute__((aligned(16))) char lds[2][2][T * 128];   // [buffer][operand]
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int wi = wave / WJ, wj = wave % WJ;
+    uint32_t tr, tc;
+    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
+    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
+    const int64_t steps = (p.sum + 127) / 128;
+    const int64_t s0 = blockIdx.y * p.chunk, s1 = min(s0 + p.chunk, steps);
+
+    // Rows past the operand's end re-read its last row; their results are not stored.
+    const char *ga[SLOTS], *gb[SLOTS];
+    int at[SLOTS];
+#pragma unroll
+    for (int q = 0; q < SLOTS; q++) {
+        const int s = t + q * NT, row = s >> 3, h = s & 7;
+        ga[q] = p.a + min(i0 + row, p.rows - 1) * p.a_pitch + s0 * 128 + h * 16;
+        gb[q] = p.b + min(j0 + row, p.cols - 1) * p.b_pitch + s0 * 128 + h * 16;
+        at[q] = row * 128 + ((h ^ (row & 7)) << 4);
+    }
+    const char *sa[FI], *sb[FJ];
+#pragma unroll
+    for (int f = 0; f < FI; f++)
+        sa[f] = p.as + min(i0 + wi * (T / WI) + f * 16 + r16, p.rows - 1) * p.as_pitch;
+#pragma unroll
+    for (int f = 0; f < FJ; f++)
+        sb[f] = p.bs + min(j0 + wj * (T / WJ) + f * 16 + r16, p.cols - 1) * p.bs_pitch;
+
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int x = 0; x < FI; x++)
+#pragma unroll
+        for (int y = 0; y < FJ; y++) acc[x][y] = f32x4{0, 0, 0, 0};
+
+    u32x4 va[SLOTS], vb[SLOTS];
+    auto load = [&]() {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) {
+            va[q] = *reinterpret_cast<const u32x4 *>(ga[q]);
+            vb[q] = *reinterpret_cast<const u32x4 *>(gb[q]);
+            ga[q] += 128;
+            gb[q] += 128;
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) {
+            *reinterpret_cast<u32x4 *>(&lds[buf][0][at[q]]) = va[q];
+            *reinterpret_cast<u32x4 *>(&lds[buf][1][at[q]]) = vb[q];
+        }
+    };
+    const int fa = (wi * (T / WI) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
+    const int fb = (wj * (T / WJ) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
+    auto frag = [&](const char *base, int at0, int f) {
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(base + at0 + f * 2048);
+        const u32x4 hi = *reinterpret_cast<const u32x4 *>(base + (at0 ^ 64) + f * 2048);
+        return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+                     static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+                     static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+    };
+    if (s0 < s1) {
+        load();
+        put(0);
+    }
+    __syncthreads();
+    for (int64_t s = s0; s < s1; s++) {
+        const int buf = static_cast<int>(s - s0) & 1;
+        if (s + 1 < s1) load();
+        int ca[FI], cb[FJ];
+#pragma unroll
+        for (int f = 0; f < FI; f++) ca[f] = static_cast<uint8_t>(sa[f][s]);
+#pragma unroll
+        for (int f = 0; f < FJ; f++) cb[f] = static_cast<uint8_t>(sb[f][s]);
+        i32x8 bj[FJ];
+#pragma unroll
+        for (int f = 0; f < FJ; f++) bj[f] = frag(lds[buf][1], fb, f);
+#pragma unroll
+        for (int x = 0; x < FI; x++) {
+            const i32x8 ai = frag(lds[buf][0], fa, x);
+#pragma unroll
+            for (int y = 0; y < FJ; y++)
+                acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    bj[y], ai, acc[x][y], 0, 0, 0, cb[y], 0, ca[x]);
+        }
+        if (s + 1 < s1) put(buf ^ 1);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int x = 0; x < FI; x++)
+#pragma unroll
+        for (int y = 0; y < FJ; y++)
+            store4(p, i0 + wi * (T / WI) + x * 16 + r16, j0 + wj * (T / WJ) + y * 16 + g * 4,
+                   acc[x][y]);
+}
+
+// ---------------------------------------------------------------------------
+// Products with bf16 factors
+// ---------------------------------------------------------------------------
+//
+// 8-bit operands become bf16 on their way into LDS (exactly: code * 2^e is a
+// bf16 number), so every product of the bf16 instruction is exact and only the
+// fp32 sums round.  This is the kernel where a scale cannot go into the matrix
+// instruction, because it changes along the sum (dX and dW: one scale per row
+// of W or X and 128 columns, summed over rows), and for fp32 outputs.
+//
+// A step of the sum is 64 values.  LDS layouts of an operand's tile:
+//   along   (sum index contiguous in memory): T rows of 64 bf16, 8 chunks of 16
+//           bytes, chunk h of row r at h ^ (r & 7)
+//   across  (sum index is the memory row): 64 rows of T bf16; a wave's 16 lanes
+//           read 4 rows x 32 bytes with the transposing read, which hands each
+//           lane 4 values along the sum.  The 32-byte piece h of row c lies at
+//           h ^ ((c & 3) | (c >> 1 & 4)), so the rows of a read fall into
+//           different banks.
+enum Mode { kBf16Along, kBf16Across, kCodesAlong, kCodesAcross };
+
+__device__ __forceinline__ constexpr bool is_across(Mode m) {
+    return m == kBf16Across || m == kCodesAcross;
+}
+__device__ __forceinline__ constexpr bool is_codes(Mode m) {
+    return m == kCodesAlong || m == kCodesAcross;
+}
+
+__device__ __forceinline__ int swz_across(int c) { return (c & 3) | ((c >> 1) & 4); }
+
+// One operand's way from memory to LDS, for a T-wide tile and NT threads.
+// `count` is the operand's extent along the tile (output rows or columns, codes
+// count whole blocks), `sum` the length of the sum.
+template <Mode M, int T, int NT, bool ALIGNED>
+struct Stage {
+    static constexpr int EL = is_codes(M) ? 16 : 8;        // values in 16 bytes
+    static constexpr int SLOTS = T * 64 / EL / NT;         // 16-byte loads per thread
+    static constexpr int PER = is_across(M) ? T / EL : 64 / EL;   // slots in a memory row
+    u32x4 v[SLOTS];
+    uint32_t scale[is_codes(M) ? SLOTS : 1];
+
+    // Slot q of this thread: memory row (of the tile) and first value in it.
+    static __device__ __forceinline__ int row(int t, int q) { return (t + q * NT) / PER; }
+    static __device__ __forceinline__ int first(int t, int q) { return (t + q * NT) % PER * EL; }
+
+    __device__ __forceinline__ void load(const char *base, int64_t pitch, const char *scales,
+                                         int64_t spitch, int64_t at0, int64_t count, int64_t c0,
+                                         int64_t sum, int t) {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) {
+            // (mrow, mcol): place in the operand's memory; both must exist
+            const int64_t mrow = (is_across(M) ? c0 : at0) + row(t, q);
+            const int64_t mcol = (is_across(M) ? at0 : c0) + first(t, q);
+            const int64_t nrow = is_across(M) ? sum : count, ncol = is_across(M) ? count : sum;
+            v[q] = u32x4{0, 0, 0, 0};
+            if (is_codes(M)) scale[q] = 0;
+            if (mrow >= nrow || mcol >= ncol) continue;
+            if (is_codes(M)) {
+                // codes past the last column are zeros up to the end of the block
+                v[q] = *reinterpret_cast<const u32x4 *>(base + mrow * pitch + mcol);
+                scale[q] = static_cast<uint8_t>(scales[mrow * spitch + (mcol >> 7)]);
+            } else if (ALIGNED) {
+                v[q] = *reinterpret_cast<const u32x4 *>(base + mrow * pitch + mcol * 2);
+            } else {
+                const uint16_t *h =
+                    reinterpret_cast<const uint16_t *>(base + mrow * pitch + mcol * 2);
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (mcol + i < ncol) v[q][i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+            }
+        }
+    }
+
+    static __device__ __forceinline__ int lds_at(int r, int chunk) {   // 16-byte chunk of row r
+        if (is_across(M)) return r * T * 2 + ((((chunk >> 1) ^ swz_across(r)) << 1 | (chunk & 1)) << 4);
+        return r * 128 + ((chunk ^ (r & 7)) << 4);
+    }
+
+    __device__ __forceinline__ void put(char *lds, int t) const {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) {
+            const int r = row(t, q), ch = first(t, q) / 8;
+            if (!is_codes(M)) {
+                *reinterpret_cast<u32x4 *>(lds + lds_at(r, ch)) = v[q];
+                continue;
+            }
+            const float s = __uint_as_float(scale[q] << 23);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                u32x4 w;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const uint32_t c = v[q][2 * h + i];
+                    w[2 * i] = __builtin_bit_cast(
+                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
+                    w[2 * i + 1] = __builtin_bit_cast(
+                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
+                }
+                *reinterpret_cast<u32x4 *>(lds + lds_at(r, ch + h)) = w;
+            }
+        }
+    }
+
+    // The 16 x 32 fragment of tile rows (or columns) [at, at + 16), sum values
+    // [32 kk, 32 kk + 32): lane (r16, g) holds value 8 g + 0..7 of line r16.
+    static __device__ __forceinline__ bf16x8 frag(const char *lds, int at, int kk, int lane) {
+        const int r16 = lane & 15, g = lane >> 4;
+        if (!is_across(M))
+            return *reinterpret_cast<const bf16x8 *>(lds + lds_at(at + r16, kk * 4 + g));
+        union {
+            i16x4 h[2];
+            bf16x8 v;
+        } u;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int c = kk * 32 + g * 8 + h * 4 + (r16 >> 2);
+            const int off = lds_at(c, at / 8 + ((r16 & 3) >> 1)) + (r16 & 1) * 8;
+            u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)(lds + off));
+        }
+        return u.v;
+    }
+};
+
+template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
+__global__ __launch_bounds__(WI * WJ * 64) void wide_kernel(MmLaunch p) {
+    constexpr int NT = WI * WJ * 64;
+    constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
+    typedef Stage<MI, T, NT, ALIGNED> SI;
+    typedef Stage<MJ, T, NT, true> SJ;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][T * 128];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int wi = wave / WJ, wj = wave % WJ;
+    uint32_t tr, tc;
+    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
+    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
+    const int64_t steps = (p.sum + 63) / 64;
+    const int64_t s0 = blockIdx.y * p.chunk, s1 = min(s0 + p.chunk, steps);
+    // Codes exist up to the end of their last block.
+    const int64_t cols = is_across(MJ) ? (p.cols + 127) & ~static_cast<int64_t>(127) : p.cols;
+    const int64_t isum = is_codes(MI) ? (p.sum + 127) & ~static_cast<int64_t>(127) : p.sum;
+    const int64_t jsum = MJ == kCodesAlong ? (p.sum + 127) & ~static_cast<int64_t>(127) : p.sum;
+
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int x = 0; x < FI; x++)
+#pragma unroll
+        for (int y = 0; y < FJ; y++) acc[x][y] = f32x4{0, 0, 0, 0};
+
+    SI si;
+    SJ sj;
+    auto load = [&](int64_t s) {
+        si.load(p.a, p.a_pitch, p.as, p.as_pitch, i0, p.rows, s * 64, isum, t);
+        sj.load(p.b, p.b_pitch, p.bs, p.bs_pitch, j0, cols, s * 64, jsum, t);
+    };
+    if (s0 < s1) {
+        load(s0);
+        si.put(lds[0][0], t);
+        sj.put(lds[0][1], t);
+    }
+    __syncthreads();
+    for (int64_t s = s0; s < s1; s++) {
+        const int buf = static_cast<int>(s - s0) & 1;
+        if (s + 1 < s1) load(s + 1);
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            bf16x8 bj[FJ];
+#pragma unroll
+            for (int y = 0; y < FJ; y++)
+                bj[y] = SJ::frag(lds[buf][1], wj * (T / WJ) + y * 16, kk, lane);
+#pragma unroll
+            for (int x = 0; x < FI; x++) {
+                const bf16x8 ai = SI::frag(lds[buf][0], wi * (T / WI) + x * 16, kk, lane);
+#pragma unroll
+                for (int y = 0; y < FJ; y++)
+                    acc[x][y] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj[y], ai, acc[x][y], 0, 0, 0);
+            }
+        }
+        if (s + 1 < s1) {
+            si.put(lds[buf ^ 1][0], t);
+            sj.put(lds[buf ^ 1][1], t);
+        }
+        __syncthreads();
+    }
+    const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < FI; x++)
+#pragma unroll
+        for (int y = 0; y < FJ; y++)
+            store4(p, i0 + wi * (T / WI) + x * 16 + r16, j0 + wj * (T / WJ) + y * 16 + g * 4,
+                   acc[x][y]);
+}
+
+// ---------------------------------------------------------------------------
+// Y = X W^T for few rows of X
+// ---------------------------------------------------------------------------
+//
+// W's bytes bound it: each workgroup takes 16 rows of W and all rows of X (MT
+// groups of 16), its waves cut the sum at multiples of 512 columns (4 blocks:
+// one 4-byte load of scales) and join through LDS in wave order.  Codes go from
+// memory to registers as 16-byte loads, become bf16 there (exactly) and enter
+// the bf16 instruction; the k-order inside a load is the same on both sides.
+constexpr int kSkinnyWaves = 8;
+
+template <int MT>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
+    __shared__ __attribute__((aligned(16))) f32x4 part[kSkinnyWaves][MT][64];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t nb = (p.sum + 127) / 128;
+    const int64_t wrow = min(j0 + r16, p.cols - 1);
+    const char *w = p.b + wrow * p.b_pitch + g * 16;
+    const char *ws = p.bs + wrow * p.bs_pitch;
+    const char *x[MT], *xs[MT];
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+        const int64_t row = min(static_cast<int64_t>(m * 16 + r16), p.rows - 1);
+        x[m] = p.a + row * p.a_pitch + g * 16;
+        xs[m] = p.as + row * p.as_pitch;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; m++) acc[m] = f32x4{0, 0, 0, 0};
+    auto widen = [](u32x4 c, int h, float s) {
+        union {
+            bf16x2 p[4];
+            bf16x8 v;
+        } u;
+        u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h], s, false);
+        u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h], s, true);
+        u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h + 1], s, false);
+        u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h + 1], s, true);
+        return u.v;
+    };
+    for (int64_t b = wave * 4; b < nb; b += kSkinnyWaves * 4) {
+        const int n = static_cast<int>(min(nb - b, static_cast<int64_t>(4)));
+        const uint32_t wsc = *reinterpret_cast<const uint32_t *>(ws + b);
+        uint32_t xsc[MT];
+#pragma unroll
+        for (int m = 0; m < MT; m++) xsc[m] = *reinterpret_cast<const uint32_t *>(xs[m] + b);
+        u32x4 wv[4][2];
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            if (q < n) {
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    wv[q][h] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x4 *>(w + (b + q) * 128 + h * 64));
+            }
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            if (q >= n) continue;
+            const float sw = __uint_as_float((wsc >> (8 * q) & 0xffu) << 23);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                u32x4 xv[MT];
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+                    xv[m] = *reinterpret_cast<const u32x4 *>(x[m] + (b + q) * 128 + h * 64);
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const bf16x8 wf = widen(wv[q][h], e, sw);
+#pragma unroll
+                    for (int m = 0; m < MT; m++) {
+                        const float sx = __uint_as_float((xsc[m] >> (8 * q) & 0xffu) << 23);
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            wf, widen(xv[m], e, sx), acc[m], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; m++) part[wave][m][lane] = acc[m];
+    __syncthreads();
+    for (int i = t; i < MT * 64; i += kSkinnyWaves * 64) {
+        const int m = i / 64, l = i % 64;
+        f32x4 s = part[0][m][l];
+#pragma unroll
+        for (int q = 1; q < kSkinnyWaves; q++) s += part[q][m][l];
+        store4(p, m * 16 + (l & 15), j0 + (l >> 4) * 4, s);
+    }
+}
+
+template <Mode MI, Mode MJ>
+void launch_wide(const MmLaunch &p, int tile, dim3 grid, hipStream_t s) {
+    if (tile == 256) {
+        if (p.aligned)
+            wide_kernel<MI, MJ, 256, 2, 4, true><<<grid, dim3(512), 0, s>>>(p);
+        else
+            wide_kernel<MI, MJ, 256, 2, 4, false><<<grid, dim3(512), 0, s>>>(p);
+    } else {
+        if (p.aligned)
+            wide_kernel<MI, MJ, 128, 2, 2, true><<<grid, dim3(256), 0, s>>>(p);
+        else
+            wide_kernel<MI, MJ, 128, 2, 2, false><<<grid, dim3(256), 0, s>>>(p);
+    }
+}
+
+tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
+    tide_status st = check_mm(op, name, a);
+    if (st != TIDE_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    MmLaunch p = {};
+    p.rows = op == kMmDw ? a.N : a.M;
+    p.cols = op == kMm ? a.N : a.K;
+    p.sum = op == kMm ? a.K : op == kMmDx ? a.N : a.M;
+    if (p.rows == 0 || p.cols == 0) {
+        clear_error();
+        return TIDE_OK;
+    }
+    const int64_t n = p.rows * p.cols;
+    p.out = static_cast<char *>(a.out);
+    p.out_bf16 = (a.flags & TIDE_F_OUT_BF16) != 0;
+    p.accumulate = (a.flags & TIDE_F_ACCUMULATE) != 0;
+    const unsigned flat = static_cast<unsigned>(std::min<int64_t>((n + 1023) / 1024, kCus * 8));
+    if (p.sum == 0) {
+        if (!p.accumulate) {
+            zero_kernel<<<dim3(flat), dim3(256), 0, s>>>(p.out, n, p.out_bf16 ? 2 : 4);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return hip_fail("tide_block_mm: zeros", e);
+        }
+        clear_error();
+        return TIDE_OK;
+    }
+    MmChoice c = mm_choose(op, a.M, a.N, a.K, a.flags, true);
+    if (c.workspace > a.workspace_bytes) c = mm_choose(op, a.M, a.N, a.K, a.flags, false);
+    p.a = static_cast<const char *>(a.a);
+    p.as = static_cast<const char *>(a.a_scales);
+    p.b = static_cast<const char *>(a.b);
+    p.bs = static_cast<const char *>(a.b_scales);
+    p.a_pitch = op == kMm ? block_cols(a.K) : a.N * 2;
+    p.as_pitch = block_scale_cols(a.K);
+    p.b_pitch = block_cols(a.K);
+    p.bs_pitch = block_scale_cols(a.K);
+    p.aligned = op == kMm || (reinterpret_cast<uintptr_t>(a.a) % 16 == 0 && a.N % 8 == 0);
+    p.chunk = c.chunk;
+    if (c.splits > 1) p.partial = static_cast<float *>(a.workspace);
+    const int64_t tr = (p.rows + c.tile - 1) / c.tile, tc = (p.cols + c.tile - 1) / c.tile;
+    if (tr * tc > 0xffffffffll / 512 || (p.cols + 15) / 16 > 0xffffffffll / 512)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
+    p.tr = static_cast<int>(tr);
+    p.tc = static_cast<int>(tc);
+    const dim3 grid(static_cast<unsigned>(tr * tc), static_cast<unsigned>(c.splits));
+    if (c.kernel == kMmSkinny) {
+        const dim3 g(static_cast<unsigned>((p.cols + 15) / 16)), b(kSkinnyWaves * 64);
+        if (p.rows <= 16)
+            skinny_kernel<1><<<g, b, 0, s>>>(p);
+        else if (p.rows <= 32)
+            skinny_kernel<2><<<g, b, 0, s>>>(p);
+        else
+            skinny_kernel<4><<<g, b, 0, s>>>(p);
+    } else if (c.kernel == kMmEight) {
+        if (c.tile == 256)
+            eight_kernel<256, 2, 4><<<grid, dim3(512), 0, s>>>(p);
+        else
+            eight_kernel<128, 2, 2><<<grid, dim3(256), 0, s>>>(p);
+    } else if (op == kMm) {
+        launch_wide<kCodesAlong, kCodesAlong>(p, c.tile, grid, s);
+    } else if (op == kMmDx) {
+        launch_wide<kBf16Along, kCodesAcross>(p, c.tile, grid, s);
+    } else {
+        launch_wide<kBf16Across, kCodesAcross>(p, c.tile, grid, s);
+    }
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && c.splits > 1) {
+        join_kernel<<<dim3(flat), dim3(256), 0, s>>>(p.partial, c.splits, n, p.out, p.out_bf16,
+                                                     p.accumulate);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
+    clear_error();
+    return TIDE_OK;
+}
+
+}  // namespace
+}  // namespace tide
+
+using namespace tide;
+
+extern "C" tide_status tide_block_mm(const void *x_codes, const void *x_scales, int64_t m,
+                                     const void *w_codes, const void *w_scales, int64_t n,
+                                     int64_t k, void *out, uint32_t flags, void *workspace,
+                                     int64_t workspace_bytes, void *stream) {
+    return run_mm(kMm, "tide_block_mm",
+                  MmArgs{x_codes, x_scales, w_codes, w_scales, m, n, k, out, workspace,
+                         workspace_bytes, flags},
+                  stream);
+}
+
+extern "C" tide_status tide_block_mm_dx(const void *dy, int64_t m, int64_t n, const void *w_codes,
+                                        const void *w_scales, int64_t k, void *dx, uint32_t flags,
+                                        void *workspace, int64_t workspace_bytes, void *stream) {
+    return run_mm(kMmDx, "tide_block_mm_dx",
+                  MmArgs{dy, nullptr, w_codes, w_scales, m, n, k, dx, workspace, workspace_bytes,
+                         flags},
+                  stream);
+}
+
+extern "C" tide_status tide_block_mm_dw(const void *dy, int64_t m, int64_t n, const void *x_codes,
+                                        const void *x_scales, int64_t k, void *dw, uint32_t flags,
+                                        void *workspace, int64_t workspace_bytes, void *stream) {
+    return run_mm(kMmDw, "tide_block_mm_dw",
+                  MmArgs{dy, nullptr, x_codes, x_scales, m, n, k, dw, workspace, workspace_bytes,
+                         flags},
+                  stream);
+}

@@ -78,6 +78,13 @@ struct tide_plan {
     std::vector<tide::ParamDesc> desc;
     std::vector<tide::Tile> rs_tiles, rs_tiles_small, ag_tiles, ag_tiles_small;
     std::vector<tide::Tile> pack_tiles, pack_tiles_small;
+    // A block plan (tide_plan_create_blocks): its parameters j and nblk + j are
+    // the codes and the scales, in 4-byte words, of a parameter [d0, blk_inner[j]]
+    // whose fp32 shard lies at blk_off[j] of a source rank block of blk_S
+    // elements.  nblk = 0: an ordinary plan.
+    int32_t nblk = 0;
+    int64_t blk_S = 0;
+    std::vector<int64_t> blk_off, blk_inner;
     mutable std::mutex mu;
     mutable std::vector<tide::DeviceState *> devs;
 };
