@@ -203,7 +203,8 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     MmChoice c;
     const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
     const int64_t sum = op == kMm ? K : op == kMmDx ? N : M;
-    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16);
+    // The 8-bit kernel addresses a tile's rows with 32 bits.
+    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16) && K <= (1 << 22);
     c.kernel = op == kMm && M <= kSkinnyRows ? kMmSkinny : eight ? kMmEight : kMmWide;
     const int64_t step = eight ? 128 : 64;
     const int64_t steps = (sum + step - 1) / step;
@@ -217,7 +218,7 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     if (t * 2 <= full && steps >= 2 * kMinSplitSteps) {
         int64_t s = std::min(full / t, steps / kMinSplitSteps);
         s = std::min<int64_t>(s, kMaxSplits);
-        c.chunk = (steps + s - 1) / s;
+        c.chunk = ((steps + s - 1) / s + 3) / 4 * 4;   // scale bytes are read in fours
         c.splits = static_cast<int>((steps + c.chunk - 1) / c.chunk);
         if (c.splits > 1) c.workspace = rows * cols * 4 * c.splits;
     }

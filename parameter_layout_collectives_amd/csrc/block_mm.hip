@@ -148,104 +148,140 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // inside a step is free as long as both sides agree: a lane reads chunks g and
 // g + 4 (g = lane / 16).  Two buffers: the next step's codes travel to registers
 // while this one is multiplied.
+// Buffer descriptor of `bytes` bytes at p: loads past its end give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, static_cast<int>(bytes),
+                                             0x00020000);
+}
+
 template <int T, int WI, int WJ>
-__global__ __launch_bounds__(WI * WJ * 64) void eight_kernel(MmLaunch p) {
-    constexpr int NT = WI * WJ * 64;
-    constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
-    constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
-    __shared__ __attribute__((aligned(16))) char lds[2][2][T * 128];   // [buffer][operand]
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int r16 = lane & 15, g = lane >> 4;
-    const int wi = wave / WJ, wj = wave % WJ;
-    uint32_t tr, tc;
-    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
-    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
-    const int64_t steps = (p.sum + 127) / 128;
-    const int64_t s0 = blockIdx.y * p.chunk, s1 = min(s0 + p.chunk, steps);
+struct Eight {
+    static constexpr int NT = WI * WJ * 64;
+    static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
+    static constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
+    static constexpr int BUF = 2 * T * 128;                    // bytes of one buffer
 
-    // Rows past the operand's end re-read its last row; their results are not stored.
-    const char *ga[SLOTS], *gb[SLOTS];
-    int at[SLOTS];
-#pragma unroll
-    for (int q = 0; q < SLOTS; q++) {
-        const int s = t + q * NT, row = s >> 3, h = s & 7;
-        ga[q] = p.a + min(i0 + row, p.rows - 1) * p.a_pitch + s0 * 128 + h * 16;
-        gb[q] = p.b + min(j0 + row, p.cols - 1) * p.b_pitch + s0 * 128 + h * 16;
-        at[q] = row * 128 + ((h ^ (row & 7)) << 4);
-    }
-    const char *sa[FI], *sb[FJ];
-#pragma unroll
-    for (int f = 0; f < FI; f++)
-        sa[f] = p.as + min(i0 + wi * (T / WI) + f * 16 + r16, p.rows - 1) * p.as_pitch;
-#pragma unroll
-    for (int f = 0; f < FJ; f++)
-        sb[f] = p.bs + min(j0 + wj * (T / WJ) + f * 16 + r16, p.cols - 1) * p.bs_pitch;
-
+    __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
+    uint32_t va, vb;             // this thread's first slot in the operands
+    uint32_t qa, qb;             // bytes from one slot to the next (uniform)
+    uint32_t vsa, vsb, fsa, fsb; // the same for scales and fragments
+    int wave, fa, fb;
     f32x4 acc[FI][FJ];
-#pragma unroll
-    for (int x = 0; x < FI; x++)
-#pragma unroll
-        for (int y = 0; y < FJ; y++) acc[x][y] = f32x4{0, 0, 0, 0};
+    int ca[FI], cb[FJ];          // 4 steps' scale bytes of the lane's rows
 
-    u32x4 va[SLOTS], vb[SLOTS];
-    auto load = [&]() {
+    // Both operands' codes of step s -> buffer `to`.
+    __device__ __forceinline__ void fetch(LDS_AS char *__restrict__ to, uint32_t s) {
 #pragma unroll
         for (int q = 0; q < SLOTS; q++) {
-            va[q] = *reinterpret_cast<const u32x4 *>(ga[q]);
-            vb[q] = *reinterpret_cast<const u32x4 *>(gb[q]);
-            ga[q] += 128;
-            gb[q] += 128;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)(to + (wave + q * (NT / 64)) * 1024),
+                                                     16, va, q * qa + s * 128, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (LDS_AS void *)(to + T * 128 + (wave + q * (NT / 64)) * 1024), 16, vb,
+                q * qb + s * 128, 0, 0);
         }
-    };
-    auto put = [&](int buf) {
+    }
+    __device__ __forceinline__ void scales(uint32_t s) {
 #pragma unroll
-        for (int q = 0; q < SLOTS; q++) {
-            *reinterpret_cast<u32x4 *>(&lds[buf][0][at[q]]) = va[q];
-            *reinterpret_cast<u32x4 *>(&lds[buf][1][at[q]]) = vb[q];
-        }
-    };
-    const int fa = (wi * (T / WI) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
-    const int fb = (wj * (T / WJ) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
-    auto frag = [&](const char *base, int at0, int f) {
-        const u32x4 lo = *reinterpret_cast<const u32x4 *>(base + at0 + f * 2048);
-        const u32x4 hi = *reinterpret_cast<const u32x4 *>(base + (at0 ^ 64) + f * 2048);
+        for (int f = 0; f < FI; f++)
+            ca[f] = __builtin_amdgcn_raw_buffer_load_b32(rsa, vsa, f * fsa + s, 0);
+#pragma unroll
+        for (int f = 0; f < FJ; f++)
+            cb[f] = __builtin_amdgcn_raw_buffer_load_b32(rsb, vsb, f * fsb + s, 0);
+    }
+    static __device__ __forceinline__ i32x8 frag(const LDS_AS char *lo_at,
+                                                 const LDS_AS char *hi_at) {
+        const u32x4 lo = *reinterpret_cast<const LDS_AS u32x4 *>(lo_at);
+        const u32x4 hi = *reinterpret_cast<const LDS_AS u32x4 *>(hi_at);
         return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
                      static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
                      static_cast<int>(hi[2]), static_cast<int>(hi[3])};
-    };
-    if (s0 < s1) {
-        load();
-        put(0);
     }
-    __syncthreads();
-    for (int64_t s = s0; s < s1; s++) {
-        const int buf = static_cast<int>(s - s0) & 1;
-        if (s + 1 < s1) load();
-        int ca[FI], cb[FJ];
+    // Multiplies the step in `from` while step `next` travels to `to`.  Chunk
+    // g + 4 of a row lies 64 bytes from chunk g, up or down.
+    __device__ __forceinline__ void step(const LDS_AS char *__restrict__ from,
+                                         LDS_AS char *__restrict__ to, uint32_t next) {
+        fetch(to, next);
+        const LDS_AS char *a0 = from + fa, *a1 = from + (fa ^ 64);
+        const LDS_AS char *b0 = from + T * 128 + fb, *b1 = from + T * 128 + (fb ^ 64);
+        i32x8 bj[FJ], ai[2];
 #pragma unroll
-        for (int f = 0; f < FI; f++) ca[f] = static_cast<uint8_t>(sa[f][s]);
-#pragma unroll
-        for (int f = 0; f < FJ; f++) cb[f] = static_cast<uint8_t>(sb[f][s]);
-        i32x8 bj[FJ];
-#pragma unroll
-        for (int f = 0; f < FJ; f++) bj[f] = frag(lds[buf][1], fb, f);
+        for (int y = 0; y < FJ; y++) bj[y] = frag(b0 + y * 2048, b1 + y * 2048);
+        ai[0] = frag(a0, a1);
 #pragma unroll
         for (int x = 0; x < FI; x++) {
-            const i32x8 ai = frag(lds[buf][0], fa, x);
+            if (x + 1 < FI) ai[(x + 1) & 1] = frag(a0 + (x + 1) * 2048, a1 + (x + 1) * 2048);
 #pragma unroll
             for (int y = 0; y < FJ; y++)
                 acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    bj[y], ai, acc[x][y], 0, 0, 0, cb[y], 0, ca[x]);
+                    bj[y], ai[x & 1], acc[x][y], 0, 0, 0, cb[y], 0, ca[x]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (s + 1 < s1) put(buf ^ 1);
-        __syncthreads();
     }
+};
+
+template <int T, int WI, int WJ>
+__global__ __launch_bounds__(WI * WJ * 64, T == 256 ? 2 : 1) void eight_kernel(MmLaunch p) {
+    typedef Eight<T, WI, WJ> E;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * E::BUF];
+    const int t = threadIdx.x, lane = t & 63;
+    const int r16 = lane & 15, g = lane >> 4;
+    uint32_t tr, tc;
+    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
+    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
+    const uint32_t nb = static_cast<uint32_t>((p.sum + 127) / 128);
+    const uint32_t s0 = static_cast<uint32_t>(blockIdx.y * p.chunk);
+    const uint32_t s1 = min(s0 + static_cast<uint32_t>(p.chunk), nb);
+    const uint32_t pa = static_cast<uint32_t>(p.a_pitch), ps = static_cast<uint32_t>(p.as_pitch);
+    const uint32_t ni = static_cast<uint32_t>(min(p.rows - i0, static_cast<int64_t>(T)));
+    const uint32_t nj = static_cast<uint32_t>(min(p.cols - j0, static_cast<int64_t>(T)));
+
+    E e;
+    e.wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wi = e.wave / WJ, wj = e.wave % WJ;
+    e.ra = buffer_of(p.a + i0 * pa, ni * pa);
+    e.rb = buffer_of(p.b + j0 * pa, nj * pa);
+    // A wave's load fills 8 rows of 8 chunks: LDS chunk c of row r is chunk
+    // c ^ (r & 7) of memory.
+    e.va = e.vb = (t >> 3) * pa + ((t & 7) ^ (t >> 3 & 7)) * 16;
+    e.qa = e.qb = E::NT / 8 * pa;
+    e.rsa = buffer_of(p.as + (i0 + wi * (T / WI)) * ps,
+                      ni > wi * (T / WI) ? (ni - wi * (T / WI)) * ps : 0);
+    e.rsb = buffer_of(p.bs + (j0 + wj * (T / WJ)) * ps,
+                      nj > wj * (T / WJ) ? (nj - wj * (T / WJ)) * ps : 0);
+    e.vsa = e.vsb = r16 * ps;
+    e.fsa = e.fsb = 16 * ps;
+    e.fa = (wi * (T / WI) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
+    e.fb = (wj * (T / WJ) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
 #pragma unroll
-    for (int x = 0; x < FI; x++)
+    for (int x = 0; x < E::FI; x++)
 #pragma unroll
-        for (int y = 0; y < FJ; y++)
+        for (int y = 0; y < E::FJ; y++) e.acc[x][y] = f32x4{0, 0, 0, 0};
+
+    LDS_AS char *const b0 = (LDS_AS char *)lds;
+    // The step after the last one is fetched too (bytes that nothing uses, in
+    // bounds by the descriptors), which keeps branches out of the loop.
+    if (s0 < s1) e.fetch(b0, s0);
+    uint32_t at = 0;
+    for (uint32_t s = s0; s < s1; s++) {
+        if (((s - s0) & 3) == 0) {
+            e.scales(s);
+        } else {
+#pragma unroll
+            for (int f = 0; f < E::FI; f++) e.ca[f] = static_cast<uint32_t>(e.ca[f]) >> 8;
+#pragma unroll
+            for (int f = 0; f < E::FJ; f++) e.cb[f] = static_cast<uint32_t>(e.cb[f]) >> 8;
+        }
+        __syncthreads();
+        e.step(b0 + at, b0 + (at ^ E::BUF), s + 1);
+        at ^= E::BUF;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < E::FI; x++)
+#pragma unroll
+        for (int y = 0; y < E::FJ; y++)
             store4(p, i0 + wi * (T / WI) + x * 16 + r16, j0 + wj * (T / WJ) + y * 16 + g * 4,
-                   acc[x][y]);
+                   e.acc[x][y]);
 }
 
 // ---------------------------------------------------------------------------
