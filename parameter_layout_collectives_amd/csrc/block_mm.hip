@@ -14,6 +14,11 @@
 
 #include "block.h"
 
+#ifndef EWI
+#define EWI 2
+#define EWJ 4
+#define ERING 2
+#endif
 namespace tide {
 namespace {
 
@@ -154,75 +159,128 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint3
                                              0x00020000);
 }
 
-template <int T, int WI, int WJ>
+// Every wave's loads into LDS have landed and every wave's reads of LDS are
+// done.  __syncthreads() alone need not wait for loads into LDS: the compiler
+// counts them for reads that may alias, which the buffers' __restrict__ denies.
+__device__ __forceinline__ void landed() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0); the other counters as they are
+    __syncthreads();
+}
+
+template <int T, int WI, int WJ, int RING>
 struct Eight {
-    static constexpr int NT = WI * WJ * 64;
+    static constexpr int NT = WI * WJ * 64, NW = WI * WJ;
     static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
     static constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
-    static constexpr int BUF = 2 * T * 128;                    // bytes of one buffer
+    static constexpr int SCALES = 2 * T * 128;                 // where a buffer's scale words start
+    static constexpr int BUF = SCALES + 2 * T * 4;             // bytes of one buffer
+    static constexpr int SLOADS = 2 * T / NT;                  // scale words per thread
+    static_assert(FI % RING == 0, "a step starts at ring entry 0");
 
     __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-    uint32_t va, vb;             // this thread's first slot in the operands
-    uint32_t qa, qb;             // bytes from one slot to the next (uniform)
-    uint32_t vsa, vsb, fsa, fsb; // the same for scales and fragments
-    int wave, fa, fb;
+    uint32_t vc, vs;             // this thread's first code slot, and its scale words' row
+    uint32_t pitch, spitch;
+    int wave, fa, fb, sa, sb;    // fragments and their scale words, in a buffer
     f32x4 acc[FI][FJ];
-    int ca[FI], cb[FJ];          // 4 steps' scale bytes of the lane's rows
 
-    // Both operands' codes of step s -> buffer `to`.
-    __device__ __forceinline__ void fetch(LDS_AS char *__restrict__ to, uint32_t s) {
+    // Step s's codes and scale words -> buffer `to`.
+    __device__ __forceinline__ void fetch(LDS_AS char *to, uint32_t s) const {
 #pragma unroll
         for (int q = 0; q < SLOTS; q++) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)(to + (wave + q * (NT / 64)) * 1024),
-                                                     16, va, q * qa + s * 128, 0, 0);
+            LDS_AS char *at = to + (wave + q * NW) * 1024;
+            const uint32_t off = q * (NT / 8) * pitch + s * 128;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)at, 16, vc, off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void *)(at + T * 128), 16, vc, off,
+                                                     0, 0);
+        }
+        // words 0 .. T-1 are the tile's rows of I, T .. 2T-1 those of J
+#pragma unroll
+        for (int q = 0; q < SLOADS; q++) {
+            const int w = wave + q * NW, half = T / 64;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb, (LDS_AS void *)(to + T * 128 + (wave + q * (NT / 64)) * 1024), 16, vb,
-                q * qb + s * 128, 0, 0);
+                w < half ? rsa : rsb, (LDS_AS void *)(to + SCALES + w * 256), 4, vs,
+                (w < half ? w : w - half) * 64 * spitch + (s & ~3u), 0, 0);
         }
     }
-    __device__ __forceinline__ void scales(uint32_t s) {
-#pragma unroll
-        for (int f = 0; f < FI; f++)
-            ca[f] = __builtin_amdgcn_raw_buffer_load_b32(rsa, vsa, f * fsa + s, 0);
-#pragma unroll
-        for (int f = 0; f < FJ; f++)
-            cb[f] = __builtin_amdgcn_raw_buffer_load_b32(rsb, vsb, f * fsb + s, 0);
-    }
-    static __device__ __forceinline__ i32x8 frag(const LDS_AS char *lo_at,
-                                                 const LDS_AS char *hi_at) {
-        const u32x4 lo = *reinterpret_cast<const LDS_AS u32x4 *>(lo_at);
-        const u32x4 hi = *reinterpret_cast<const LDS_AS u32x4 *>(hi_at);
+    static __device__ __forceinline__ i32x8 frag(const LDS_AS char *at, int lo_at) {
+        // chunk g + 4 of a row lies 64 bytes from chunk g, up or down
+        const u32x4 lo = *reinterpret_cast<const LDS_AS u32x4 *>(at + lo_at);
+        const u32x4 hi = *reinterpret_cast<const LDS_AS u32x4 *>(at + (lo_at ^ 64));
         return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
                      static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
                      static_cast<int>(hi[2]), static_cast<int>(hi[3])};
     }
-    // Multiplies the step in `from` while step `next` travels to `to`.  Chunk
-    // g + 4 of a row lies 64 bytes from chunk g, up or down.
-    __device__ __forceinline__ void step(const LDS_AS char *__restrict__ from,
-                                         LDS_AS char *__restrict__ to, uint32_t next) {
-        fetch(to, next);
-        const LDS_AS char *a0 = from + fa, *a1 = from + (fa ^ 64);
-        const LDS_AS char *b0 = from + T * 128 + fb, *b1 = from + T * 128 + (fb ^ 64);
-        i32x8 bj[FJ], ai[2];
+    struct Rows {                // the J side of one step
+        i32x8 v[FJ];
+        int scale[FJ];
+    };
+    struct Line {                // one fragment of the I side
+        i32x8 v;
+        int scale;
+    };
+    __device__ __forceinline__ void rows(Rows &r, const LDS_AS char *b, uint32_t s) const {
 #pragma unroll
-        for (int y = 0; y < FJ; y++) bj[y] = frag(b0 + y * 2048, b1 + y * 2048);
-        ai[0] = frag(a0, a1);
+        for (int y = 0; y < FJ; y++) {
+            r.v[y] = frag(b + T * 128 + y * 2048, fb);
+            r.scale[y] = *reinterpret_cast<const LDS_AS uint8_t *>(b + SCALES + sb + y * 64 + (s & 3));
+        }
+    }
+    __device__ __forceinline__ void line(Line &l, const LDS_AS char *b, int x, uint32_t s) const {
+        l.v = frag(b + x * 2048, fa);
+        l.scale = *reinterpret_cast<const LDS_AS uint8_t *>(b + SCALES + sa + x * 64 + (s & 3));
+    }
+    __device__ __forceinline__ void multiply(int x, const Line &l, const Rows &r) {
+#pragma unroll
+        for (int y = 0; y < FJ; y++)
+            acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                r.v[y], l.v, acc[x][y], 0, 0, 0, r.scale[y], 0, l.scale);
+    }
+    // Step s, whose first RING - 1 lines and J rows are in registers: reads the
+    // rest from `here`; once nothing of it is left to read, step s + 2 starts
+    // travelling there and the first reads of step s + 1 from `there` begin,
+    // under the multiplications that remain.
+    __device__ __forceinline__ void step(Line *l, const Rows &r, Rows &next, LDS_AS char *here,
+                                         const LDS_AS char *there, uint32_t s) {
 #pragma unroll
         for (int x = 0; x < FI; x++) {
-            if (x + 1 < FI) ai[(x + 1) & 1] = frag(a0 + (x + 1) * 2048, a1 + (x + 1) * 2048);
-#pragma unroll
-            for (int y = 0; y < FJ; y++)
-                acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    bj[y], ai[x & 1], acc[x][y], 0, 0, 0, cb[y], 0, ca[x]);
+            constexpr int D = RING - 1;
+            if (x + D < FI) line(l[(x + D) % RING], here, x + D, s);
+            if (x + D == FI) {
+                landed();
+                fetch(here, s + 2);
+                rows(next, there, s + 1);
+            }
+            if (x + D >= FI) line(l[(x + D) % RING], there, x + D - FI, s + 1);
+            multiply(x, l[x % RING], r);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+    __device__ __forceinline__ void run(LDS_AS char *__restrict__ b0, LDS_AS char *__restrict__ b1,
+                                        uint32_t s0, uint32_t s1) {
+        fetch(b0, s0);
+        fetch(b1, s0 + 1);
+        landed();
+        Line l[RING];
+        Rows r0, r1;
+        rows(r0, b0, s0);
+#pragma unroll
+        for (int x = 0; x < RING - 1; x++) line(l[x], b0, x, s0);
+        uint32_t s = s0;
+        // What lies past the last step is fetched and read as well (in bounds by
+        // the descriptors, used by nothing), which keeps branches out of the loop.
+        for (; s + 1 < s1; s += 2) {
+            step(l, r0, r1, b0, b1, s);
+            step(l, r1, r0, b1, b0, s + 1);
+        }
+        if (s < s1) step(l, r0, r1, b0, b1, s);
+        landed();         // no load may still be on its way to LDS at the end
+    }
 };
 
-template <int T, int WI, int WJ>
-__global__ __launch_bounds__(WI * WJ * 64, T == 256 ? 2 : 1) void eight_kernel(MmLaunch p) {
-    typedef Eight<T, WI, WJ> E;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * E::BUF];
+template <int T, int WI, int WJ, int RING>
+__global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
+    typedef Eight<T, WI, WJ, RING> E;
+    __shared__ __attribute__((aligned(1024))) char lds[2][E::BUF];
     const int t = threadIdx.x, lane = t & 63;
     const int r16 = lane & 15, g = lane >> 4;
     uint32_t tr, tc;
@@ -231,51 +289,31 @@ __global__ __launch_bounds__(WI * WJ * 64, T == 256 ? 2 : 1) void eight_kernel(M
     const uint32_t nb = static_cast<uint32_t>((p.sum + 127) / 128);
     const uint32_t s0 = static_cast<uint32_t>(blockIdx.y * p.chunk);
     const uint32_t s1 = min(s0 + static_cast<uint32_t>(p.chunk), nb);
-    const uint32_t pa = static_cast<uint32_t>(p.a_pitch), ps = static_cast<uint32_t>(p.as_pitch);
     const uint32_t ni = static_cast<uint32_t>(min(p.rows - i0, static_cast<int64_t>(T)));
     const uint32_t nj = static_cast<uint32_t>(min(p.cols - j0, static_cast<int64_t>(T)));
 
     E e;
+    e.pitch = static_cast<uint32_t>(p.a_pitch);
+    e.spitch = static_cast<uint32_t>(p.as_pitch);
     e.wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wi = e.wave / WJ, wj = e.wave % WJ;
-    e.ra = buffer_of(p.a + i0 * pa, ni * pa);
-    e.rb = buffer_of(p.b + j0 * pa, nj * pa);
+    e.ra = buffer_of(p.a + i0 * e.pitch, ni * e.pitch);
+    e.rb = buffer_of(p.b + j0 * e.pitch, nj * e.pitch);
+    e.rsa = buffer_of(p.as + i0 * e.spitch, ni * e.spitch);
+    e.rsb = buffer_of(p.bs + j0 * e.spitch, nj * e.spitch);
     // A wave's load fills 8 rows of 8 chunks: LDS chunk c of row r is chunk
     // c ^ (r & 7) of memory.
-    e.va = e.vb = (t >> 3) * pa + ((t & 7) ^ (t >> 3 & 7)) * 16;
-    e.qa = e.qb = E::NT / 8 * pa;
-    e.rsa = buffer_of(p.as + (i0 + wi * (T / WI)) * ps,
-                      ni > wi * (T / WI) ? (ni - wi * (T / WI)) * ps : 0);
-    e.rsb = buffer_of(p.bs + (j0 + wj * (T / WJ)) * ps,
-                      nj > wj * (T / WJ) ? (nj - wj * (T / WJ)) * ps : 0);
-    e.vsa = e.vsb = r16 * ps;
-    e.fsa = e.fsb = 16 * ps;
+    e.vc = (t >> 3) * e.pitch + ((t & 7) ^ (t >> 3 & 7)) * 16;
+    e.vs = lane * e.spitch;
     e.fa = (wi * (T / WI) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
     e.fb = (wj * (T / WJ) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
+    e.sa = (wi * (T / WI) + r16) * 4;
+    e.sb = (T + wj * (T / WJ) + r16) * 4;
 #pragma unroll
     for (int x = 0; x < E::FI; x++)
 #pragma unroll
         for (int y = 0; y < E::FJ; y++) e.acc[x][y] = f32x4{0, 0, 0, 0};
-
-    LDS_AS char *const b0 = (LDS_AS char *)lds;
-    // The step after the last one is fetched too (bytes that nothing uses, in
-    // bounds by the descriptors), which keeps branches out of the loop.
-    if (s0 < s1) e.fetch(b0, s0);
-    uint32_t at = 0;
-    for (uint32_t s = s0; s < s1; s++) {
-        if (((s - s0) & 3) == 0) {
-            e.scales(s);
-        } else {
-#pragma unroll
-            for (int f = 0; f < E::FI; f++) e.ca[f] = static_cast<uint32_t>(e.ca[f]) >> 8;
-#pragma unroll
-            for (int f = 0; f < E::FJ; f++) e.cb[f] = static_cast<uint32_t>(e.cb[f]) >> 8;
-        }
-        __syncthreads();
-        e.step(b0 + at, b0 + (at ^ E::BUF), s + 1);
-        at ^= E::BUF;
-    }
-    __syncthreads();
+    e.run((LDS_AS char *)lds[0], (LDS_AS char *)lds[1], s0, s1);
 #pragma unroll
     for (int x = 0; x < E::FI; x++)
 #pragma unroll
@@ -638,9 +676,9 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
             skinny_kernel<4><<<g, b, 0, s>>>(p);
     } else if (c.kernel == kMmEight) {
         if (c.tile == 256)
-            eight_kernel<256, 2, 4><<<grid, dim3(512), 0, s>>>(p);
+            eight_kernel<256, EWI, EWJ, ERING><<<grid, dim3(EWI * EWJ * 64), 0, s>>>(p);
         else
-            eight_kernel<128, 2, 2><<<grid, dim3(256), 0, s>>>(p);
+            eight_kernel<128, 2, 2, 2><<<grid, dim3(256), 0, s>>>(p);
     } else if (op == kMm) {
         launch_wide<kCodesAlong, kCodesAlong>(p, c.tile, grid, s);
     } else if (op == kMmDx) {
