@@ -19,6 +19,9 @@
 #define EWJ 4
 #define ERING 2
 #endif
+#ifndef WRING
+#define WRING 2
+#endif
 namespace tide {
 namespace {
 
@@ -351,167 +354,273 @@ __device__ __forceinline__ constexpr bool is_codes(Mode m) {
 
 __device__ __forceinline__ int swz_across(int c) { return (c & 3) | ((c >> 1) & 4); }
 
-// One operand's way from memory to LDS, for a T-wide tile and NT threads.
-// `count` is the operand's extent along the tile (output rows or columns, codes
-// count whole blocks), `sum` the length of the sum.
+// One operand's way from memory to LDS, for a T-wide tile and NT threads, 16
+// bytes at a time: fetch() asks for a step's bytes, put() stores one slot of
+// them.  What lies outside the operand (rows or columns past its end) comes as
+// zeros, by the buffer's bounds or by an offset beyond them, so nothing from
+// there enters a sum.
 template <Mode M, int T, int NT, bool ALIGNED>
 struct Stage {
     static constexpr int EL = is_codes(M) ? 16 : 8;        // values in 16 bytes
-    static constexpr int SLOTS = T * 64 / EL / NT;         // 16-byte loads per thread
+    static constexpr int ES = is_codes(M) ? 1 : 2;
+    static constexpr int SLOTS = T * 64 / EL / NT;         // slots per thread
     static constexpr int PER = is_across(M) ? T / EL : 64 / EL;   // slots in a memory row
+    static constexpr int ROWS = NT / PER;                  // memory rows from one slot to the next
+    static constexpr uint32_t OUTSIDE = 0x80000000u;       // past every buffer's end
+
+    const char *base, *sbase;    // along: the tile's first row; across: the operand
+    int64_t lines;               // memory rows from there on
+    int64_t sum;                 // length of the sum (codes along: whole blocks)
+    int64_t at0;                 // across: the tile's first column
+    uint32_t pitch, spitch;
+    uint32_t off, soff;          // this thread's first slot
+    int have;                    // across: values of the slot's row from its first one on
+    int first;                   // first value of the slot
+    int put_at;
     u32x4 v[SLOTS];
     uint32_t scale[is_codes(M) ? SLOTS : 1];
 
-    // Slot q of this thread: memory row (of the tile) and first value in it.
-    static __device__ __forceinline__ int row(int t, int q) { return (t + q * NT) / PER; }
-    static __device__ __forceinline__ int first(int t, int q) { return (t + q * NT) % PER * EL; }
+    __device__ __forceinline__ void init(const char *p, const char *s, int64_t pitch_,
+                                         int64_t spitch_, int64_t at, int64_t count, int64_t sum_,
+                                         int t) {
+        pitch = static_cast<uint32_t>(pitch_);
+        spitch = static_cast<uint32_t>(spitch_);
+        const int row = t / PER;
+        first = t % PER * EL;
+        off = row * pitch + first * ES;
+        soff = row * spitch;
+        sum = sum_;
+        at0 = at;
+        put_at = lds_at(row, first / 8);
+        if (is_across(M)) {
+            base = p;
+            sbase = s;
+            lines = sum_;
+            const int64_t left = count - at - first;
+            have = static_cast<int>(max(min(left, static_cast<int64_t>(EL)), static_cast<int64_t>(0)));
+            if (have == 0) off = OUTSIDE;
+            soff += first / kBlockCols;
+        } else {
+            base = p + at * pitch_;
+            sbase = s + at * spitch_;
+            lines = min(count - at, static_cast<int64_t>(T));
+        }
+    }
 
-    __device__ __forceinline__ void load(const char *base, int64_t pitch, const char *scales,
-                                         int64_t spitch, int64_t at0, int64_t count, int64_t c0,
-                                         int64_t sum, int t) {
+    __device__ __forceinline__ void fetch(int64_t s) {
+        // Memory rows [row, row + n) from column byte col (scale byte scol) on.
+        const int64_t row = is_across(M) ? s * 64 : 0;
+        const int64_t n = is_across(M) ? min(lines - row, static_cast<int64_t>(64)) : lines;
+        const int64_t col = (is_across(M) ? at0 : s * 64) * ES;
+        const int64_t scol = (is_across(M) ? at0 : s * 64) / kBlockCols;
+        uint32_t at = off;
+        int there = have;
+        if (!is_across(M)) {
+            there = static_cast<int>(min(sum - s * 64, static_cast<int64_t>(64))) - first;
+            if (there <= 0) at = OUTSIDE;
+        }
+        const int64_t bytes = n > 0 ? n * pitch - col : 0, sbytes = n > 0 ? n * spitch - scol : 0;
+        const __amdgpu_buffer_rsrc_t r =
+            buffer_of(base + row * pitch + col, static_cast<uint32_t>(max(bytes, static_cast<int64_t>(0))));
 #pragma unroll
         for (int q = 0; q < SLOTS; q++) {
-            // (mrow, mcol): place in the operand's memory; both must exist
-            const int64_t mrow = (is_across(M) ? c0 : at0) + row(t, q);
-            const int64_t mcol = (is_across(M) ? at0 : c0) + first(t, q);
-            const int64_t nrow = is_across(M) ? sum : count, ncol = is_across(M) ? count : sum;
-            v[q] = u32x4{0, 0, 0, 0};
-            if (is_codes(M)) scale[q] = 0;
-            if (mrow >= nrow || mcol >= ncol) continue;
-            if (is_codes(M)) {
-                // codes past the last column are zeros up to the end of the block
-                v[q] = *reinterpret_cast<const u32x4 *>(base + mrow * pitch + mcol);
-                scale[q] = static_cast<uint8_t>(scales[mrow * spitch + (mcol >> 7)]);
-            } else if (ALIGNED) {
-                v[q] = *reinterpret_cast<const u32x4 *>(base + mrow * pitch + mcol * 2);
+            if (is_codes(M) || ALIGNED) {
+                v[q] = __builtin_amdgcn_raw_buffer_load_b128(r, at, q * ROWS * pitch, 0);
             } else {
-                const uint16_t *h =
-                    reinterpret_cast<const uint16_t *>(base + mrow * pitch + mcol * 2);
+                v[q] = u32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (mcol + i < ncol) v[q][i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+                for (int i = 0; i < 8; i++) {
+                    const uint32_t h = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+                        r, i < there ? at + 2 * i : OUTSIDE, q * ROWS * pitch, 0));
+                    v[q][i / 2] |= h << (16 * (i & 1));
+                }
             }
+        }
+        if (is_codes(M)) {
+            const __amdgpu_buffer_rsrc_t rs = buffer_of(
+                sbase + row * spitch + scol, static_cast<uint32_t>(max(sbytes, static_cast<int64_t>(0))));
+#pragma unroll
+            for (int q = 0; q < SLOTS; q++)
+                scale[q] = static_cast<uint8_t>(
+                    __builtin_amdgcn_raw_buffer_load_b8(rs, soff, q * ROWS * spitch, 0));
         }
     }
 
     static __device__ __forceinline__ int lds_at(int r, int chunk) {   // 16-byte chunk of row r
-        if (is_across(M)) return r * T * 2 + ((((chunk >> 1) ^ swz_across(r)) << 1 | (chunk & 1)) << 4);
+        if (is_across(M))
+            return r * T * 2 + ((((chunk >> 1) ^ swz_across(r)) << 1 | (chunk & 1)) << 4);
         return r * 128 + ((chunk ^ (r & 7)) << 4);
     }
 
-    __device__ __forceinline__ void put(char *lds, int t) const {
+    __device__ __forceinline__ void put(LDS_AS char *lds, int q) const {
+        // Slot q lies ROWS rows further: a multiple of 16, which leaves the
+        // swizzles as they are (along, rows step by more than 8).
+        static_assert(ROWS % 16 == 0, "slots keep their swizzle");
+        LDS_AS char *to = lds + put_at + q * ROWS * (is_across(M) ? T * 2 : 128);
+        if (!is_codes(M)) {
+            *reinterpret_cast<LDS_AS u32x4 *>(to) = v[q];
+            return;
+        }
+        const float s = __uint_as_float(scale[q] << 23);
+        // the slot's first chunk is an even one: its other half is 16 bytes away,
+        // up or (along, where the swizzle moves single chunks) down
+        const int half = is_across(M) ? 16 : (put_at ^ 16) - put_at;
 #pragma unroll
-        for (int q = 0; q < SLOTS; q++) {
-            const int r = row(t, q), ch = first(t, q) / 8;
-            if (!is_codes(M)) {
-                *reinterpret_cast<u32x4 *>(lds + lds_at(r, ch)) = v[q];
-                continue;
+        for (int h = 0; h < 2; h++) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const uint32_t c = v[q][2 * h + i];
+                w[2 * i] = __builtin_bit_cast(
+                    uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
+                w[2 * i + 1] = __builtin_bit_cast(
+                    uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
             }
-            const float s = __uint_as_float(scale[q] << 23);
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                u32x4 w;
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const uint32_t c = v[q][2 * h + i];
-                    w[2 * i] = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
-                    w[2 * i + 1] = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
-                }
-                *reinterpret_cast<u32x4 *>(lds + lds_at(r, ch + h)) = w;
-            }
+            *reinterpret_cast<LDS_AS u32x4 *>(h == 0 ? to : to + half) = w;
         }
     }
 
     // The 16 x 32 fragment of tile rows (or columns) [at, at + 16), sum values
-    // [32 kk, 32 kk + 32): lane (r16, g) holds value 8 g + 0..7 of line r16.
-    static __device__ __forceinline__ bf16x8 frag(const char *lds, int at, int kk, int lane) {
+    // [32 kk, 32 kk + 32): lane (r16, g) holds values 8 g + 0..7 of line r16.
+    static __device__ __forceinline__ bf16x8 frag(const LDS_AS char *lds, int at, int kk, int lane) {
         const int r16 = lane & 15, g = lane >> 4;
         if (!is_across(M))
-            return *reinterpret_cast<const bf16x8 *>(lds + lds_at(at + r16, kk * 4 + g));
+            return *reinterpret_cast<const LDS_AS bf16x8 *>(
+                lds + (at + r16) * 128 + (((g ^ (r16 & 7)) << 4) ^ (kk << 6)));
         union {
             i16x4 h[2];
             bf16x8 v;
         } u;
+        const int c = g * 8 + (r16 >> 2);        // swz_across is the same for all kk and h
+        const LDS_AS char *p = lds + lds_at(c, at / 8 + ((r16 & 3) >> 1)) + (r16 & 1) * 8;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int c = kk * 32 + g * 8 + h * 4 + (r16 >> 2);
-            const int off = lds_at(c, at / 8 + ((r16 & 3) >> 1)) + (r16 & 1) * 8;
-            u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)(lds + off));
-        }
+        for (int h = 0; h < 2; h++)
+            u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (LDS_AS i16x4 *)(p + (kk * 32 + h * 4) * T * 2));
         return u.v;
     }
 };
 
+// As in the 8-bit kernel, the next step's first fragments are read under this
+// step's last multiplications.  A step is two halves of 32 values; its 2 FI
+// lines (a fragment of I each) run through the J fragments of their half.
+// While step s is multiplied from one buffer, step s + 1 goes from registers
+// to the other, and then step s + 2 is asked for.
 template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
-__global__ __launch_bounds__(WI * WJ * 64) void wide_kernel(MmLaunch p) {
-    constexpr int NT = WI * WJ * 64;
-    constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
+struct Wide {
+    static constexpr int NT = WI * WJ * 64;
+    static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
+    static constexpr int RING = WRING, D = RING - 1, LINES = 2 * FI;
+    static constexpr int HALF = T * 128;                   // bytes of one operand's tile
     typedef Stage<MI, T, NT, ALIGNED> SI;
     typedef Stage<MJ, T, NT, true> SJ;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][T * 128];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int wi = wave / WJ, wj = wave % WJ;
+    static constexpr int PUTS = SI::SLOTS + SJ::SLOTS;
+    static_assert(LINES % RING == 0, "a step starts at ring entry 0");
+
+    SI si;
+    SJ sj;
+    int lane, wi, wj;
+    f32x4 acc[FI][FJ];
+
+    __device__ __forceinline__ void put(LDS_AS char *to, int q) const {
+        if (q < SI::SLOTS)
+            si.put(to, q);
+        else
+            sj.put(to + HALF, q - SI::SLOTS);
+    }
+    __device__ __forceinline__ bf16x8 line(const LDS_AS char *b, int n) const {
+        return SI::frag(b, wi * (T / WI) + n % FI * 16, n / FI, lane);
+    }
+    __device__ __forceinline__ void rows(bf16x8 *r, const LDS_AS char *b, int kk) const {
+#pragma unroll
+        for (int y = 0; y < FJ; y++) r[y] = SJ::frag(b + HALF, wj * (T / WJ) + y * 16, kk, lane);
+    }
+    __device__ __forceinline__ void step(bf16x8 *l, bf16x8 (*r)[FJ], LDS_AS char *here,
+                                         LDS_AS char *there, int64_t s) {
+        rows(r[1], here, 1);
+#pragma unroll
+        for (int n = 0; n < LINES; n++) {
+            if (n + D < LINES) l[(n + D) % RING] = line(here, n + D);
+            // the stores, spread over the second half's lines before the barrier:
+            // their loads had half a step to arrive
+            constexpr int FROM = LINES / 2 - 1, TO = LINES - D - 1;
+#pragma unroll
+            for (int q = 0; q < PUTS; q++)
+                if (n == FROM + q * (TO - FROM) / PUTS) put(there, q);
+            if (n == TO) {
+                si.fetch(s + 2);
+                sj.fetch(s + 2);
+            }
+            if (n + D == LINES) {
+                __syncthreads();
+                rows(r[0], there, 0);
+            }
+            if (n + D >= LINES) l[(n + D) % RING] = line(there, n + D - LINES);
+#pragma unroll
+            for (int y = 0; y < FJ; y++)
+                acc[n % FI][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    r[n / FI][y], l[n % RING], acc[n % FI][y], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __device__ __forceinline__ void run(LDS_AS char *b0, LDS_AS char *b1, int64_t s0, int64_t s1) {
+        si.fetch(s0);
+        sj.fetch(s0);
+#pragma unroll
+        for (int q = 0; q < PUTS; q++) put(b0, q);
+        si.fetch(s0 + 1);
+        sj.fetch(s0 + 1);
+        __syncthreads();
+        bf16x8 l[RING], r[2][FJ];
+        rows(r[0], b0, 0);
+#pragma unroll
+        for (int n = 0; n < D; n++) l[n] = line(b0, n);
+        int64_t s = s0;
+        // Steps past the last one are fetched as zeros or as values that nothing
+        // uses, which keeps branches out of the loop.
+        for (; s + 1 < s1; s += 2) {
+            step(l, r, b0, b1, s);
+            step(l, r, b1, b0, s + 1);
+        }
+        if (s < s1) step(l, r, b0, b1, s);
+    }
+};
+
+template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
+__global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
+    typedef Wide<MI, MJ, T, WI, WJ, ALIGNED> K;
+    __shared__ __attribute__((aligned(1024))) char lds[2][2 * K::HALF];
+    const int t = threadIdx.x, lane = t & 63;
     uint32_t tr, tc;
     tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
     const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
     const int64_t steps = (p.sum + 63) / 64;
     const int64_t s0 = blockIdx.y * p.chunk, s1 = min(s0 + p.chunk, steps);
     // Codes exist up to the end of their last block.
-    const int64_t cols = is_across(MJ) ? (p.cols + 127) & ~static_cast<int64_t>(127) : p.cols;
-    const int64_t isum = is_codes(MI) ? (p.sum + 127) & ~static_cast<int64_t>(127) : p.sum;
-    const int64_t jsum = MJ == kCodesAlong ? (p.sum + 127) & ~static_cast<int64_t>(127) : p.sum;
+    const int64_t whole = static_cast<int64_t>(127);
+    const int64_t cols = MJ == kCodesAcross ? (p.cols + whole) & ~whole : p.cols;
+    const int64_t isum = MI == kCodesAlong ? (p.sum + whole) & ~whole : p.sum;
+    const int64_t jsum = MJ == kCodesAlong ? (p.sum + whole) & ~whole : p.sum;
 
-    f32x4 acc[FI][FJ];
+    K k;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    k.lane = lane;
+    k.wi = wave / WJ;
+    k.wj = wave % WJ;
+    k.si.init(p.a, p.as, p.a_pitch, p.as_pitch, i0, p.rows, isum, t);
+    k.sj.init(p.b, p.bs, p.b_pitch, p.bs_pitch, j0, cols, jsum, t);
 #pragma unroll
-    for (int x = 0; x < FI; x++)
+    for (int x = 0; x < K::FI; x++)
 #pragma unroll
-        for (int y = 0; y < FJ; y++) acc[x][y] = f32x4{0, 0, 0, 0};
-
-    SI si;
-    SJ sj;
-    auto load = [&](int64_t s) {
-        si.load(p.a, p.a_pitch, p.as, p.as_pitch, i0, p.rows, s * 64, isum, t);
-        sj.load(p.b, p.b_pitch, p.bs, p.bs_pitch, j0, cols, s * 64, jsum, t);
-    };
-    if (s0 < s1) {
-        load(s0);
-        si.put(lds[0][0], t);
-        sj.put(lds[0][1], t);
-    }
-    __syncthreads();
-    for (int64_t s = s0; s < s1; s++) {
-        const int buf = static_cast<int>(s - s0) & 1;
-        if (s + 1 < s1) load(s + 1);
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            bf16x8 bj[FJ];
-#pragma unroll
-            for (int y = 0; y < FJ; y++)
-                bj[y] = SJ::frag(lds[buf][1], wj * (T / WJ) + y * 16, kk, lane);
-#pragma unroll
-            for (int x = 0; x < FI; x++) {
-                const bf16x8 ai = SI::frag(lds[buf][0], wi * (T / WI) + x * 16, kk, lane);
-#pragma unroll
-                for (int y = 0; y < FJ; y++)
-                    acc[x][y] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj[y], ai, acc[x][y], 0, 0, 0);
-            }
-        }
-        if (s + 1 < s1) {
-            si.put(lds[buf ^ 1][0], t);
-            sj.put(lds[buf ^ 1][1], t);
-        }
-        __syncthreads();
-    }
+        for (int y = 0; y < K::FJ; y++) k.acc[x][y] = f32x4{0, 0, 0, 0};
+    k.run((LDS_AS char *)lds[0], (LDS_AS char *)lds[1], s0, s1);
     const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int x = 0; x < FI; x++)
+    for (int x = 0; x < K::FI; x++)
 #pragma unroll
-        for (int y = 0; y < FJ; y++)
-            store4(p, i0 + wi * (T / WI) + x * 16 + r16, j0 + wj * (T / WJ) + y * 16 + g * 4,
-                   acc[x][y]);
+        for (int y = 0; y < K::FJ; y++)
+            store4(p, i0 + k.wi * (T / WI) + x * 16 + r16, j0 + k.wj * (T / WJ) + y * 16 + g * 4,
+                   k.acc[x][y]);
 }
 
 // ---------------------------------------------------------------------------
