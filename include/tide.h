@@ -388,7 +388,8 @@ tide_status tide_block_unshard(const tide_plan *plan, const void *gathered, void
  *   tide_block_mm     out[m, n] = X W^T        (the forward pass)
  *   tide_block_mm_dx  dx[m, k]  = dY W         (the input's gradient)
  *   tide_block_mm_dw  dw[n, k]  = dY^T X       (the weights' gradient)
- * All matrices are row-major without gaps.  The output is fp32, or bf16 with
+ * All matrices are row-major without gaps; n and k may be at most 2^22
+ * (TIDE_E_UNSUPPORTED above).  The output is fp32, or bf16 with
  * TIDE_F_OUT_BF16; it must not overlap an operand.  Sums are held in fp32.
  * Products are exact, except in tide_block_mm with a bf16 output and more than
  * 64 rows: the 8-bit matrix instruction there adds 128 products at a time with

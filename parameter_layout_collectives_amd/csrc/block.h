@@ -49,7 +49,9 @@ struct MmChoice {
     int64_t chunk;       // steps of the sum in one piece
     int64_t workspace;   // bytes
 };
-MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool may_split);
+// aligned: dY's rows can be loaded in 16-byte pieces.
+MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
+                   bool may_split);
 
 tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
                               const void *scales, uint32_t flags);

@@ -8,7 +8,9 @@
 namespace tide {
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 31;   // rows and columns of a product or a block matrix
+constexpr int64_t kMaxDim = int64_t(1) << 31;   // rows and columns of a block matrix
+constexpr int64_t kMaxLine = int64_t(1) << 22;  // n and k of a product: its kernels address the
+                                                // rows of a tile, 2 * 2^22 bytes each, in 32 bits
 
 struct Bytes {
     uintptr_t lo, hi;
@@ -161,6 +163,8 @@ tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
     for (int64_t rows : {g.M, g.N})
         for (int64_t cols : {g.N, g.K})
             if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
+    if (g.N > kMaxLine || g.K > kMaxLine)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
     if (g.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
     if (g.workspace_bytes > 0 && !g.workspace) return bad(name, "workspace is NULL");
     if (g.workspace && misaligned(g.workspace, 16))
@@ -199,17 +203,17 @@ tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
     return TIDE_OK;
 }
 
-MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool may_split) {
+MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
+                   bool may_split) {
     MmChoice c;
     const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
     const int64_t sum = op == kMm ? K : op == kMmDx ? N : M;
-    // The 8-bit kernel addresses a tile's rows with 32 bits.
-    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16) && K <= (1 << 22);
+    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16);
     c.kernel = op == kMm && M <= kSkinnyRows ? kMmSkinny : eight ? kMmEight : kMmWide;
     const int64_t step = eight ? 128 : 64;
     const int64_t steps = (sum + step - 1) / step;
     auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };
-    c.tile = tiles(256) >= kCus * 3 / 4 ? 256 : 128;
+    c.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256 : 128;
     c.splits = 1;
     c.chunk = steps;
     c.workspace = 0;
@@ -281,7 +285,12 @@ tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int3
 
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {
     if (op < 0 || op > 2 || m < 0 || n < 0 || k < 0) return -1;
-    return tide::mm_choose(static_cast<tide::MmOp>(op), m, n, k, flags, true).workspace;
+    // whichever way dY is aligned
+    int64_t most = 0;
+    for (bool aligned : {false, true})
+        most = std::max(most, tide::mm_choose(static_cast<tide::MmOp>(op), m, n, k, flags, aligned,
+                                              true).workspace);
+    return most;
 }
 
 }  // extern "C"

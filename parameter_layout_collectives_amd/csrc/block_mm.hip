@@ -19,9 +19,6 @@
 #define EWJ 4
 #define ERING 2
 #endif
-#ifndef WRING
-#define WRING 2
-#endif
 namespace tide {
 namespace {
 
@@ -50,6 +47,12 @@ struct MmLaunch {
     int out_bf16, accumulate, aligned;
 };
 
+// A value that is the same in all lanes, in a scalar register: 64-bit minima
+// and divisions run in vector registers and would drag what follows there.
+__device__ __forceinline__ uint32_t uniform(int64_t v) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+}
+
 // Workgroup `id` of tr x tc tiles -> its tile.  IDs go to the 8 XCDs in turn
 // and each XCD has its own L2: every XCD takes one contiguous run of tiles, and
 // within it 8 tile rows advance together, so that the tiles an XCD works on at
@@ -60,8 +63,8 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tr, uint32_t tc, u
     const uint32_t v = x * q + min(x, rm) + id / 8;
     const uint32_t per = 8 * tc, g = v / per, in = v - g * per;
     const uint32_t h = min(8u, tr - 8 * g);
-    *r = 8 * g + in % h;
-    *c = in / h;
+    *r = uniform(8 * g + in % h);
+    *c = uniform(in / h);
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -156,17 +159,21 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // inside a step is free as long as both sides agree: a lane reads chunks g and
 // g + 4 (g = lane / 16).  Two buffers: the next step's codes travel to registers
 // while this one is multiplied.
-// Buffer descriptor of `bytes` bytes at p: loads past its end give zeros.
+// Buffer descriptor of `bytes` bytes at p (the same in all lanes): loads past
+// its end give zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, static_cast<int>(bytes),
                                              0x00020000);
 }
 
-// Every wave's loads into LDS have landed and every wave's reads of LDS are
-// done.  __syncthreads() alone need not wait for loads into LDS: the compiler
-// counts them for reads that may alias, which the buffers' __restrict__ denies.
+// Every wave's loads into LDS have landed, but for the LATER loads it has asked
+// for since (loads return in order), and every wave's reads of LDS are done.
+// __syncthreads() alone need not wait for loads into LDS: the compiler counts
+// them for reads that may alias, which the buffers' __restrict__ denies.
+template <int LATER = 0>
 __device__ __forceinline__ void landed() {
-    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0); the other counters as they are
+    static_assert(LATER < 16, "the counter's low bits");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | LATER);   // vmcnt(LATER); the other counters as they are
     __syncthreads();
 }
 
@@ -292,8 +299,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
     const uint32_t nb = static_cast<uint32_t>((p.sum + 127) / 128);
     const uint32_t s0 = static_cast<uint32_t>(blockIdx.y * p.chunk);
     const uint32_t s1 = min(s0 + static_cast<uint32_t>(p.chunk), nb);
-    const uint32_t ni = static_cast<uint32_t>(min(p.rows - i0, static_cast<int64_t>(T)));
-    const uint32_t nj = static_cast<uint32_t>(min(p.cols - j0, static_cast<int64_t>(T)));
+    const uint32_t ni = uniform(min(p.rows - i0, static_cast<int64_t>(T)));
+    const uint32_t nj = uniform(min(p.cols - j0, static_cast<int64_t>(T)));
 
     E e;
     e.pitch = static_cast<uint32_t>(p.a_pitch);
@@ -345,14 +352,31 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
 //           different banks.
 enum Mode { kBf16Along, kBf16Across, kCodesAlong, kCodesAcross };
 
-__device__ __forceinline__ constexpr bool is_across(Mode m) {
+__host__ __device__ constexpr bool is_across(Mode m) {
     return m == kBf16Across || m == kCodesAcross;
 }
-__device__ __forceinline__ constexpr bool is_codes(Mode m) {
+__host__ __device__ constexpr bool is_codes(Mode m) {
     return m == kCodesAlong || m == kCodesAcross;
 }
 
 __device__ __forceinline__ int swz_across(int c) { return (c & 3) | ((c >> 1) & 4); }
+
+// 16 bytes per lane from r + at + off straight into LDS, from `to` on.  The
+// builtin for it would make the compiler wait for the load before the next
+// transposing read of LDS, of whatever buffer: it cannot tell that they do not
+// meet.  An asm statement is not counted, which is safe: its only output is
+// LDS, for which landed() waits, and loads return in order, so a wait for a
+// counted load is at worst longer than needed.
+__device__ __forceinline__ void direct_load(__amdgpu_buffer_rsrc_t r, LDS_AS char *to, uint32_t at,
+                                            uint32_t off) {
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)));
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+        :
+        : "s"(lds), "v"(at), "s"(r), "s"(off)
+        : "memory", "m0");
+}
 
 // One operand's way from memory to LDS, for a T-wide tile and NT threads, 16
 // bytes at a time: fetch() asks for a step's bytes, put() stores one slot of
@@ -367,12 +391,16 @@ struct Stage {
     static constexpr int PER = is_across(M) ? T / EL : 64 / EL;   // slots in a memory row
     static constexpr int ROWS = NT / PER;                  // memory rows from one slot to the next
     static constexpr uint32_t OUTSIDE = 0x80000000u;       // past every buffer's end
+    // bf16 whose 16-byte pieces are aligned goes straight into LDS: there a
+    // wave's lanes fill consecutive pieces, so the swizzle picks the source.
+    static constexpr bool DIRECT = !is_codes(M) && ALIGNED;
 
     const char *base, *sbase;    // along: the tile's first row; across: the operand
-    int64_t lines;               // memory rows from there on
-    int64_t sum;                 // length of the sum (codes along: whole blocks)
-    int64_t at0;                 // across: the tile's first column
     uint32_t pitch, spitch;
+    uint32_t lines;              // along: the tile's memory rows; across: those left of the sum
+    int end;                     // along: values left of the sum from the slot's next one on
+    uint32_t at0, sat0;          // across: bytes before the tile in a row
+    uint32_t next;               // first value of the sum not yet asked for
     uint32_t off, soff;          // this thread's first slot
     int have;                    // across: values of the slot's row from its first one on
     int first;                   // first value of the slot
@@ -380,69 +408,86 @@ struct Stage {
     u32x4 v[SLOTS];
     uint32_t scale[is_codes(M) ? SLOTS : 1];
 
-    __device__ __forceinline__ void init(const char *p, const char *s, int64_t pitch_,
+    // The tile's lines [at, at + T) of `count`, from step s0 on.  Sums are
+    // below 2^31 and rows at most 2^23 bytes long, so the bytes of T rows fit
+    // 32 bits.
+    __device__ __forceinline__ void init(const char *p, const char *sp, int64_t pitch_,
                                          int64_t spitch_, int64_t at, int64_t count, int64_t sum_,
-                                         int t) {
+                                         uint32_t s0, int t) {
         pitch = static_cast<uint32_t>(pitch_);
         spitch = static_cast<uint32_t>(spitch_);
         const int row = t / PER;
         first = t % PER * EL;
+        // the swizzles are their own inverses
+        if (DIRECT) first = lds_at(row, t % PER) / 16 % PER * 8;
         off = row * pitch + first * ES;
         soff = row * spitch;
-        sum = sum_;
-        at0 = at;
         put_at = lds_at(row, first / 8);
+        next = s0 * 64;
+        end = static_cast<int>(sum_) - static_cast<int>(next) - first;
+        base = p;
+        sbase = sp;
         if (is_across(M)) {
-            base = p;
-            sbase = s;
-            lines = sum_;
-            const int64_t left = count - at - first;
-            have = static_cast<int>(max(min(left, static_cast<int64_t>(EL)), static_cast<int64_t>(0)));
-            if (have == 0) off = OUTSIDE;
+            at0 = static_cast<uint32_t>(at * ES);
+            sat0 = static_cast<uint32_t>(at / kBlockCols);
+            lines = static_cast<uint32_t>(sum_) - next;
+            have = static_cast<int>(min(count - at - first, static_cast<int64_t>(EL)));
+            if (have <= 0) off = OUTSIDE;
             soff += first / kBlockCols;
         } else {
-            base = p + at * pitch_;
-            sbase = s + at * spitch_;
-            lines = min(count - at, static_cast<int64_t>(T));
+            base += at * pitch_;
+            sbase += at * spitch_;
+            lines = uniform(min(count - at, static_cast<int64_t>(T)));
         }
     }
 
-    __device__ __forceinline__ void fetch(int64_t s) {
-        // Memory rows [row, row + n) from column byte col (scale byte scol) on.
-        const int64_t row = is_across(M) ? s * 64 : 0;
-        const int64_t n = is_across(M) ? min(lines - row, static_cast<int64_t>(64)) : lines;
-        const int64_t col = (is_across(M) ? at0 : s * 64) * ES;
-        const int64_t scol = (is_across(M) ? at0 : s * 64) / kBlockCols;
+    // Asks for the next step, into registers or straight into `lds`.  Past the
+    // last one: for nothing, by the bounds.
+    __device__ __forceinline__ void fetch(LDS_AS char *lds, int wave) {
+        // across: 64 memory rows from row `next`, from column byte at0 on;
+        // along: all of the tile's rows, from value `next` on
+        const char *p = base, *sp = sbase;
+        uint32_t n = lines, skip = 0, sskip = 0;
         uint32_t at = off;
         int there = have;
-        if (!is_across(M)) {
-            there = static_cast<int>(min(sum - s * 64, static_cast<int64_t>(64))) - first;
+        if (is_across(M)) {
+            p += static_cast<uint64_t>(next) * pitch;
+            sp += static_cast<uint64_t>(next) * spitch;
+            n = min(lines, 64u);
+            lines -= n;
+            skip = at0;
+            sskip = sat0;
+        } else {
+            skip = next * ES;
+            sskip = next / kBlockCols;
+            there = end;
             if (there <= 0) at = OUTSIDE;
+            end -= 64;
         }
-        const int64_t bytes = n > 0 ? n * pitch - col : 0, sbytes = n > 0 ? n * spitch - scol : 0;
-        const __amdgpu_buffer_rsrc_t r =
-            buffer_of(base + row * pitch + col, static_cast<uint32_t>(max(bytes, static_cast<int64_t>(0))));
+        next += 64;
+        const __amdgpu_buffer_rsrc_t r = buffer_of(p, n * pitch);
 #pragma unroll
         for (int q = 0; q < SLOTS; q++) {
-            if (is_codes(M) || ALIGNED) {
-                v[q] = __builtin_amdgcn_raw_buffer_load_b128(r, at, q * ROWS * pitch, 0);
+            if (DIRECT) {
+                direct_load(r, lds + (wave + q * (NT / 64)) * 1024, at, q * ROWS * pitch + skip);
+            } else if (is_codes(M)) {
+                v[q] = __builtin_amdgcn_raw_buffer_load_b128(r, at, q * ROWS * pitch + skip, 0);
             } else {
                 v[q] = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const uint32_t h = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
-                        r, i < there ? at + 2 * i : OUTSIDE, q * ROWS * pitch, 0));
+                        r, i < there ? at + 2 * i : OUTSIDE, q * ROWS * pitch + skip, 0));
                     v[q][i / 2] |= h << (16 * (i & 1));
                 }
             }
         }
         if (is_codes(M)) {
-            const __amdgpu_buffer_rsrc_t rs = buffer_of(
-                sbase + row * spitch + scol, static_cast<uint32_t>(max(sbytes, static_cast<int64_t>(0))));
+            const __amdgpu_buffer_rsrc_t rs = buffer_of(sp, n * spitch);
 #pragma unroll
             for (int q = 0; q < SLOTS; q++)
                 scale[q] = static_cast<uint8_t>(
-                    __builtin_amdgcn_raw_buffer_load_b8(rs, soff, q * ROWS * spitch, 0));
+                    __builtin_amdgcn_raw_buffer_load_b8(rs, soff, q * ROWS * spitch + sskip, 0));
         }
     }
 
@@ -505,57 +550,72 @@ struct Stage {
 // step's last multiplications.  A step is two halves of 32 values; its 2 FI
 // lines (a fragment of I each) run through the J fragments of their half.
 // While step s is multiplied from one buffer, step s + 1 goes from registers
-// to the other, and then step s + 2 is asked for.
+// to the other (or is on its way there directly); step s + 2 is asked for once
+// the barrier has freed registers and buffer.
 template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
 struct Wide {
     static constexpr int NT = WI * WJ * 64;
     static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
-    static constexpr int RING = WRING, D = RING - 1, LINES = 2 * FI;
-    static constexpr int HALF = T * 128;                   // bytes of one operand's tile
+    static constexpr int RING = 4, D = RING - 1, LINES = 2 * FI;
+    static constexpr int TILE = T * 128;                   // bytes of one operand's tile
     typedef Stage<MI, T, NT, ALIGNED> SI;
     typedef Stage<MJ, T, NT, true> SJ;
-    static constexpr int PUTS = SI::SLOTS + SJ::SLOTS;
+    static constexpr int JLOADS = 2 * SJ::SLOTS;           // codes and scales
+    static constexpr int IPUTS = SI::DIRECT ? 0 : SI::SLOTS, PUTS = IPUTS + SJ::SLOTS;
     static_assert(LINES % RING == 0, "a step starts at ring entry 0");
 
     SI si;
     SJ sj;
-    int lane, wi, wj;
+    int lane, wave, wi, wj;
     f32x4 acc[FI][FJ];
 
-    __device__ __forceinline__ void put(LDS_AS char *to, int q) const {
-        if (q < SI::SLOTS)
-            si.put(to, q);
+    // A buffer: I's tile and J's.  All four tiles are separate objects to the
+    // compiler (run()'s __restrict__), so that reads and stores of one do not
+    // wait for loads that travel to another.
+    __device__ __forceinline__ void fetch(LDS_AS char *ti, LDS_AS char *tj) {
+        sj.fetch(tj, wave);      // first: its registers are waited for first
+        si.fetch(ti, wave);
+    }
+    __device__ __forceinline__ void put(LDS_AS char *ti, LDS_AS char *tj, int q) const {
+        if (q < IPUTS)
+            si.put(ti, q);
         else
-            sj.put(to + HALF, q - SI::SLOTS);
+            sj.put(tj, q - IPUTS);
     }
     __device__ __forceinline__ bf16x8 line(const LDS_AS char *b, int n) const {
         return SI::frag(b, wi * (T / WI) + n % FI * 16, n / FI, lane);
     }
     __device__ __forceinline__ void rows(bf16x8 *r, const LDS_AS char *b, int kk) const {
 #pragma unroll
-        for (int y = 0; y < FJ; y++) r[y] = SJ::frag(b + HALF, wj * (T / WJ) + y * 16, kk, lane);
+        for (int y = 0; y < FJ; y++) r[y] = SJ::frag(b, wj * (T / WJ) + y * 16, kk, lane);
     }
-    __device__ __forceinline__ void step(bf16x8 *l, bf16x8 (*r)[FJ], LDS_AS char *here,
-                                         LDS_AS char *there, int64_t s) {
-        rows(r[1], here, 1);
+    // LAST: nothing is left to ask for.
+    template <bool LAST>
+    __device__ __forceinline__ void step(bf16x8 *l, bf16x8 (*r)[FJ], LDS_AS char *here_i,
+                                         LDS_AS char *here_j, LDS_AS char *there_i,
+                                         LDS_AS char *there_j) {
+        rows(r[1], here_j, 1);
 #pragma unroll
         for (int n = 0; n < LINES; n++) {
-            if (n + D < LINES) l[(n + D) % RING] = line(here, n + D);
+            if (n + D < LINES) l[(n + D) % RING] = line(here_i, n + D);
             // the stores, spread over the second half's lines before the barrier:
             // their loads had half a step to arrive
             constexpr int FROM = LINES / 2 - 1, TO = LINES - D - 1;
 #pragma unroll
             for (int q = 0; q < PUTS; q++)
-                if (n == FROM + q * (TO - FROM) / PUTS) put(there, q);
-            if (n == TO) {
-                si.fetch(s + 2);
-                sj.fetch(s + 2);
+                if (!LAST && n == FROM + q * (TO - FROM) / PUTS) put(there_i, there_j, q);
+            if (!LAST && n == TO) sj.fetch(here_j, wave);
+            if (!LAST && n == TO && !SI::DIRECT) si.fetch(here_i, wave);
+            if (!LAST && n + D == LINES) {
+                if (SI::DIRECT) {
+                    landed<JLOADS>();
+                    si.fetch(here_i, wave);
+                } else {
+                    __syncthreads();
+                }
+                rows(r[0], there_j, 0);
             }
-            if (n + D == LINES) {
-                __syncthreads();
-                rows(r[0], there, 0);
-            }
-            if (n + D >= LINES) l[(n + D) % RING] = line(there, n + D - LINES);
+            if (!LAST && n + D >= LINES) l[(n + D) % RING] = line(there_i, n + D - LINES);
 #pragma unroll
             for (int y = 0; y < FJ; y++)
                 acc[n % FI][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -563,33 +623,33 @@ struct Wide {
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __device__ __forceinline__ void run(LDS_AS char *b0, LDS_AS char *b1, int64_t s0, int64_t s1) {
-        si.fetch(s0);
-        sj.fetch(s0);
+    __device__ __forceinline__ void run(LDS_AS char *__restrict__ i0, LDS_AS char *__restrict__ i1,
+                                        LDS_AS char *__restrict__ j0, LDS_AS char *__restrict__ j1,
+                                        uint32_t steps) {
+        fetch(i0, j0);
 #pragma unroll
-        for (int q = 0; q < PUTS; q++) put(b0, q);
-        si.fetch(s0 + 1);
-        sj.fetch(s0 + 1);
-        __syncthreads();
+        for (int q = 0; q < PUTS; q++) put(i0, j0, q);
+        fetch(i1, j1);
+        landed();
         bf16x8 l[RING], r[2][FJ];
-        rows(r[0], b0, 0);
+        rows(r[0], j0, 0);
 #pragma unroll
-        for (int n = 0; n < D; n++) l[n] = line(b0, n);
-        int64_t s = s0;
-        // Steps past the last one are fetched as zeros or as values that nothing
-        // uses, which keeps branches out of the loop.
-        for (; s + 1 < s1; s += 2) {
-            step(l, r, b0, b1, s);
-            step(l, r, b1, b0, s + 1);
+        for (int n = 0; n < D; n++) l[n] = line(i0, n);
+        // Past the last step zeros are fetched, or values that nothing uses,
+        // which keeps branches out of the loop.
+        for (; steps > 1; steps -= 2) {
+            step<false>(l, r, i0, j0, i1, j1);
+            step<false>(l, r, i1, j1, i0, j0);
         }
-        if (s < s1) step(l, r, b0, b1, s);
+        if (steps) step<true>(l, r, i0, j0, i1, j1);
+        landed();                // no load may still be on its way to LDS at the end
     }
 };
 
 template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
 __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
     typedef Wide<MI, MJ, T, WI, WJ, ALIGNED> K;
-    __shared__ __attribute__((aligned(1024))) char lds[2][2 * K::HALF];
+    __shared__ __attribute__((aligned(1024))) char lds[4 * K::TILE];
     const int t = threadIdx.x, lane = t & 63;
     uint32_t tr, tc;
     tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
@@ -603,17 +663,20 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
     const int64_t jsum = MJ == kCodesAlong ? (p.sum + whole) & ~whole : p.sum;
 
     K k;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    k.wave = __builtin_amdgcn_readfirstlane(t >> 6);
     k.lane = lane;
-    k.wi = wave / WJ;
-    k.wj = wave % WJ;
-    k.si.init(p.a, p.as, p.a_pitch, p.as_pitch, i0, p.rows, isum, t);
-    k.sj.init(p.b, p.bs, p.b_pitch, p.bs_pitch, j0, cols, jsum, t);
+    k.wi = k.wave / WJ;
+    k.wj = k.wave % WJ;
+    k.si.init(p.a, p.as, p.a_pitch, p.as_pitch, i0, p.rows, isum, uniform(s0), t);
+    k.sj.init(p.b, p.bs, p.b_pitch, p.bs_pitch, j0, cols, jsum, uniform(s0), t);
 #pragma unroll
     for (int x = 0; x < K::FI; x++)
 #pragma unroll
         for (int y = 0; y < K::FJ; y++) k.acc[x][y] = f32x4{0, 0, 0, 0};
-    k.run((LDS_AS char *)lds[0], (LDS_AS char *)lds[1], s0, s1);
+    // I's two buffers, then J's: one address and constant offsets (below 64 KB)
+    // reach both buffers of an operand.
+    LDS_AS char *const b = (LDS_AS char *)lds;
+    k.run(b, b + K::TILE, b + 2 * K::TILE, b + 3 * K::TILE, uniform(s1 - s0));
     const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int x = 0; x < K::FI; x++)
@@ -717,17 +780,12 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
 
 template <Mode MI, Mode MJ>
 void launch_wide(const MmLaunch &p, int tile, dim3 grid, hipStream_t s) {
-    if (tile == 256) {
-        if (p.aligned)
-            wide_kernel<MI, MJ, 256, 2, 4, true><<<grid, dim3(512), 0, s>>>(p);
-        else
-            wide_kernel<MI, MJ, 256, 2, 4, false><<<grid, dim3(512), 0, s>>>(p);
-    } else {
-        if (p.aligned)
-            wide_kernel<MI, MJ, 128, 2, 2, true><<<grid, dim3(256), 0, s>>>(p);
-        else
-            wide_kernel<MI, MJ, 128, 2, 2, false><<<grid, dim3(256), 0, s>>>(p);
-    }
+    if (tile == 256)
+        wide_kernel<MI, MJ, 256, 2, 4, true><<<grid, dim3(512), 0, s>>>(p);
+    else if (is_codes(MI) || p.aligned)
+        wide_kernel<MI, MJ, 128, 2, 2, true><<<grid, dim3(256), 0, s>>>(p);
+    else
+        wide_kernel<MI, MJ, 128, 2, 2, is_codes(MI)><<<grid, dim3(256), 0, s>>>(p);
 }
 
 tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
@@ -756,8 +814,10 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
         clear_error();
         return TIDE_OK;
     }
-    MmChoice c = mm_choose(op, a.M, a.N, a.K, a.flags, true);
-    if (c.workspace > a.workspace_bytes) c = mm_choose(op, a.M, a.N, a.K, a.flags, false);
+    p.aligned = op == kMm || (reinterpret_cast<uintptr_t>(a.a) % 16 == 0 && a.N % 8 == 0);
+    MmChoice c = mm_choose(op, a.M, a.N, a.K, a.flags, p.aligned, true);
+    if (c.workspace > a.workspace_bytes)
+        c = mm_choose(op, a.M, a.N, a.K, a.flags, p.aligned, false);
     p.a = static_cast<const char *>(a.a);
     p.as = static_cast<const char *>(a.a_scales);
     p.b = static_cast<const char *>(a.b);
@@ -766,7 +826,6 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
     p.as_pitch = block_scale_cols(a.K);
     p.b_pitch = block_cols(a.K);
     p.bs_pitch = block_scale_cols(a.K);
-    p.aligned = op == kMm || (reinterpret_cast<uintptr_t>(a.a) % 16 == 0 && a.N % 8 == 0);
     p.chunk = c.chunk;
     if (c.splits > 1) p.partial = static_cast<float *>(a.workspace);
     const int64_t tr = (p.rows + c.tile - 1) / c.tile, tc = (p.cols + c.tile - 1) / c.tile;

@@ -103,6 +103,8 @@ COMMON = [
     (dict(k=-1), E_INVALID, "negative"),
     (dict(m=1 << 31), E_INVALID, "2^31"),
     (dict(k=1 << 31), E_INVALID, "2^31"),
+    (dict(n=(1 << 22) + 1), E_UNSUPPORTED, "2^22"),
+    (dict(k=(1 << 22) + 1), E_UNSUPPORTED, "2^22"),
     (dict(flags=0x80), E_UNSUPPORTED, "flag"),
     (dict(flags=0x1), E_UNSUPPORTED, "flag"),
     (dict(out=0), E_INVALID, "out is NULL"),
