@@ -14,11 +14,6 @@
 
 #include "block.h"
 
-#ifndef EWI
-#define EWI 2
-#define EWJ 4
-#define ERING 2
-#endif
 namespace tide {
 namespace {
 
@@ -26,6 +21,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -177,15 +173,19 @@ __device__ __forceinline__ void landed() {
     __syncthreads();
 }
 
-template <int T, int WI, int WJ, int RING>
+template <int T, int WI, int WJ>
 struct Eight {
     static constexpr int NT = WI * WJ * 64, NW = WI * WJ;
     static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
     static constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
-    static constexpr int SCALES = 2 * T * 128;                 // where a buffer's scale words start
-    static constexpr int BUF = SCALES + 2 * T * 4;             // bytes of one buffer
+    static constexpr int TILE = T * 128;                       // bytes of an operand's codes
+    static constexpr int WORDS = 2 * T * 4;                    // and of both operands' scale words
+    static constexpr int LDS = 4 * TILE + 2 * WORDS;
     static constexpr int SLOADS = 2 * T / NT;                  // scale words per thread
-    static_assert(FI % RING == 0, "a step starts at ring entry 0");
+    // I's fragments (lines) go through a ring of registers, D ahead of the
+    // multiplications.
+    static constexpr int RING = 2, D = RING - 1;
+    static_assert(FI % RING == 0 && SLOTS <= FI, "a step starts at ring entry 0");
 
     __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
     uint32_t vc, vs;             // this thread's first code slot, and its scale words' row
@@ -193,22 +193,21 @@ struct Eight {
     int wave, fa, fb, sa, sb;    // fragments and their scale words, in a buffer
     f32x4 acc[FI][FJ];
 
-    // Step s's codes and scale words -> buffer `to`.
-    __device__ __forceinline__ void fetch(LDS_AS char *to, uint32_t s) const {
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) {
-            LDS_AS char *at = to + (wave + q * NW) * 1024;
-            const uint32_t off = q * (NT / 8) * pitch + s * 128;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)at, 16, vc, off, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void *)(at + T * 128), 16, vc, off,
-                                                     0, 0);
-        }
+    // Part q of step s's codes (and with the last one the scale words) -> a
+    // buffer (I's codes, J's, words).
+    __device__ __forceinline__ void fetch(LDS_AS char *ta, LDS_AS char *tb, LDS_AS char *tw,
+                                          uint32_t s, int q) const {
+        const int at = (wave + q * NW) * 1024;
+        const uint32_t off = q * (NT / 8) * pitch + s * 128;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)(ta + at), 16, vc, off, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void *)(tb + at), 16, vc, off, 0, 0);
+        if (q < SLOTS - 1) return;
         // words 0 .. T-1 are the tile's rows of I, T .. 2T-1 those of J
 #pragma unroll
-        for (int q = 0; q < SLOADS; q++) {
-            const int w = wave + q * NW, half = T / 64;
+        for (int k = 0; k < SLOADS; k++) {
+            const int w = wave + k * NW, half = T / 64;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                w < half ? rsa : rsb, (LDS_AS void *)(to + SCALES + w * 256), 4, vs,
+                w < half ? rsa : rsb, (LDS_AS void *)(tw + w * 256), 4, vs,
                 (w < half ? w : w - half) * 64 * spitch + (s & ~3u), 0, 0);
         }
     }
@@ -228,16 +227,18 @@ struct Eight {
         i32x8 v;
         int scale;
     };
-    __device__ __forceinline__ void rows(Rows &r, const LDS_AS char *b, uint32_t s) const {
+    __device__ __forceinline__ void rows(Rows &r, const LDS_AS char *b, const LDS_AS char *w,
+                                         uint32_t s) const {
 #pragma unroll
         for (int y = 0; y < FJ; y++) {
-            r.v[y] = frag(b + T * 128 + y * 2048, fb);
-            r.scale[y] = *reinterpret_cast<const LDS_AS uint8_t *>(b + SCALES + sb + y * 64 + (s & 3));
+            r.v[y] = frag(b + y * 2048, fb);
+            r.scale[y] = *reinterpret_cast<const LDS_AS uint8_t *>(w + sb + y * 64 + (s & 3));
         }
     }
-    __device__ __forceinline__ void line(Line &l, const LDS_AS char *b, int x, uint32_t s) const {
-        l.v = frag(b + x * 2048, fa);
-        l.scale = *reinterpret_cast<const LDS_AS uint8_t *>(b + SCALES + sa + x * 64 + (s & 3));
+    __device__ __forceinline__ void line(Line &l, const LDS_AS char *a, const LDS_AS char *w, int x,
+                                         uint32_t s) const {
+        l.v = frag(a + x * 2048, fa);
+        l.scale = *reinterpret_cast<const LDS_AS uint8_t *>(w + sa + x * 64 + (s & 3));
     }
     __device__ __forceinline__ void multiply(int x, const Line &l, const Rows &r) {
 #pragma unroll
@@ -245,52 +246,59 @@ struct Eight {
             acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 r.v[y], l.v, acc[x][y], 0, 0, 0, r.scale[y], 0, l.scale);
     }
-    // Step s, whose first RING - 1 lines and J rows are in registers: reads the
-    // rest from `here`; once nothing of it is left to read, step s + 2 starts
-    // travelling there and the first reads of step s + 1 from `there` begin,
-    // under the multiplications that remain.
-    __device__ __forceinline__ void step(Line *l, const Rows &r, Rows &next, LDS_AS char *here,
-                                         const LDS_AS char *there, uint32_t s) {
+    // Step s, whose first D lines and J rows are in registers: reads the rest from
+    // its buffer (h*); once nothing of it is left to read, the first reads of step
+    // s + 1 from the other (t*) begin under the multiplications that remain, and
+    // step s + 2 starts travelling to h*.  Loads go out a part at a time: a burst
+    // of them would hold up the reads behind it (issued in order, 16 cycles of the
+    // address path each, 64 a step and workgroup).
+    template <bool LAST>
+    __device__ __forceinline__ void step(Line *l, const Rows &r, Rows &next, LDS_AS char *ha,
+                                         LDS_AS char *hb, LDS_AS char *hw, LDS_AS char *ta,
+                                         LDS_AS char *tb, LDS_AS char *tw, uint32_t s) {
 #pragma unroll
         for (int x = 0; x < FI; x++) {
-            constexpr int D = RING - 1;
-            if (x + D < FI) line(l[(x + D) % RING], here, x + D, s);
-            if (x + D == FI) {
+            if (x + D < FI) line(l[(x + D) % RING], ha, hw, x + D, s);
+            if (!LAST && x + D == FI) {
                 landed();
-                fetch(here, s + 2);
-                rows(next, there, s + 1);
+                rows(next, tb, tw, s + 1);
             }
-            if (x + D >= FI) line(l[(x + D) % RING], there, x + D - FI, s + 1);
+            if (!LAST && x + D >= FI) line(l[(x + D) % RING], ta, tw, x + D - FI, s + 1);
+            if (!LAST && x < SLOTS - 1) fetch(ta, tb, tw, s + 1, x + 1);
             multiply(x, l[x % RING], r);
+            if (!LAST && x == FI - 1) fetch(ha, hb, hw, s + 2, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __device__ __forceinline__ void run(LDS_AS char *__restrict__ b0, LDS_AS char *__restrict__ b1,
+    __device__ __forceinline__ void run(LDS_AS char *__restrict__ a0, LDS_AS char *__restrict__ a1,
+                                        LDS_AS char *__restrict__ b0, LDS_AS char *__restrict__ b1,
+                                        LDS_AS char *__restrict__ w0, LDS_AS char *__restrict__ w1,
                                         uint32_t s0, uint32_t s1) {
-        fetch(b0, s0);
-        fetch(b1, s0 + 1);
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) fetch(a0, b0, w0, s0, q);
+        fetch(a1, b1, w1, s0 + 1, 0);
         landed();
         Line l[RING];
         Rows r0, r1;
-        rows(r0, b0, s0);
+        rows(r0, b0, w0, s0);
 #pragma unroll
-        for (int x = 0; x < RING - 1; x++) line(l[x], b0, x, s0);
+        for (int x = 0; x < D; x++) line(l[x], a0, w0, x, s0);
         uint32_t s = s0;
         // What lies past the last step is fetched and read as well (in bounds by
         // the descriptors, used by nothing), which keeps branches out of the loop.
         for (; s + 1 < s1; s += 2) {
-            step(l, r0, r1, b0, b1, s);
-            step(l, r1, r0, b1, b0, s + 1);
+            step<false>(l, r0, r1, a0, b0, w0, a1, b1, w1, s);
+            step<false>(l, r1, r0, a1, b1, w1, a0, b0, w0, s + 1);
         }
-        if (s < s1) step(l, r0, r1, b0, b1, s);
-        landed();         // no load may still be on its way to LDS at the end
+        if (s < s1) step<true>(l, r0, r1, a0, b0, w0, a1, b1, w1, s);
+        landed();                // no load may still be on its way to LDS at the end
     }
 };
 
-template <int T, int WI, int WJ, int RING>
+template <int T, int WI, int WJ>
 __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
-    typedef Eight<T, WI, WJ, RING> E;
-    __shared__ __attribute__((aligned(1024))) char lds[2][E::BUF];
+    typedef Eight<T, WI, WJ> E;
+    __shared__ __attribute__((aligned(1024))) char lds[E::LDS];
     const int t = threadIdx.x, lane = t & 63;
     const int r16 = lane & 15, g = lane >> 4;
     uint32_t tr, tc;
@@ -323,7 +331,10 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
     for (int x = 0; x < E::FI; x++)
 #pragma unroll
         for (int y = 0; y < E::FJ; y++) e.acc[x][y] = f32x4{0, 0, 0, 0};
-    e.run((LDS_AS char *)lds[0], (LDS_AS char *)lds[1], s0, s1);
+    // An operand's two buffers lie side by side: one address and constant offsets
+    // (below 64 KB) reach both.
+    LDS_AS char *const b = (LDS_AS char *)lds, *const w = b + 4 * E::TILE;
+    e.run(b, b + E::TILE, b + 2 * E::TILE, b + 3 * E::TILE, w, w + E::WORDS, s0, s1);
 #pragma unroll
     for (int x = 0; x < E::FI; x++)
 #pragma unroll
@@ -562,7 +573,9 @@ struct Wide {
     typedef Stage<MJ, T, NT, true> SJ;
     static constexpr int JLOADS = 2 * SJ::SLOTS;           // codes and scales
     static constexpr int IPUTS = SI::DIRECT ? 0 : SI::SLOTS, PUTS = IPUTS + SJ::SLOTS;
-    static_assert(LINES % RING == 0, "a step starts at ring entry 0");
+    static_assert(LINES % RING == 0 && D <= FI,
+                  "a step starts at ring entry 0, and its first half is over when the next "
+                  "step's J fragments replace it");
 
     SI si;
     SJ sj;
@@ -844,9 +857,9 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
             skinny_kernel<4><<<g, b, 0, s>>>(p);
     } else if (c.kernel == kMmEight) {
         if (c.tile == 256)
-            eight_kernel<256, EWI, EWJ, ERING><<<grid, dim3(EWI * EWJ * 64), 0, s>>>(p);
+            eight_kernel<256, 2, 4><<<grid, dim3(512), 0, s>>>(p);
         else
-            eight_kernel<128, 2, 2, 2><<<grid, dim3(256), 0, s>>>(p);
+            eight_kernel<128, 2, 2><<<grid, dim3(256), 0, s>>>(p);
     } else if (op == kMm) {
         launch_wide<kCodesAlong, kCodesAlong>(p, c.tile, grid, s);
     } else if (op == kMmDx) {
