@@ -412,8 +412,18 @@ tide_status tide_block_mm_dw(const void *dy, int64_t m, int64_t n, const void *x
                              const void *x_scales, int64_t k, void *dw, uint32_t flags,
                              void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Bytes of workspace that the product `op` (0 mm, 1 mm_dx, 2 mm_dw) uses for
- * these sizes and flags; 0 if none, -1 for a bad argument. */
+/* tide_block_quant of x [m, k] (bf16; fp16 or fp32 by TIDE_F_GRAD_F16 / _F32;
+ * any element alignment) and tide_block_mm in one call, with the same result,
+ * for a layer that keeps no checkpoint (serving): in one launch for few rows,
+ * else through blocks in the workspace, which has to hold
+ * tide_block_workspace(3, ...) bytes for them (TIDE_E_INVALID with less than
+ * the blocks need). */
+tide_status tide_block_linear(const void *x, int64_t m, int64_t k, const void *w_codes,
+                              const void *w_scales, int64_t n, void *out, uint32_t flags,
+                              void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that the call `op` (0 mm, 1 mm_dx, 2 mm_dw, 3 linear) uses
+ * for these sizes and flags; 0 if none, -1 for a bad argument. */
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags);
 
 /* ---------------------------------------------------------------------- */

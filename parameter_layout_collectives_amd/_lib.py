@@ -36,6 +36,7 @@ SIGNATURES = {
     "tide_block_mm": (_i32, [_p, _p, _i64, _p, _p, _i64, _i64, _p, _u32, _p, _i64, _p]),
     "tide_block_mm_dx": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
     "tide_block_mm_dw": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_block_linear": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
     "tide_block_workspace": (_i64, [_i32, _i64, _i64, _i64, _u32]),
     "tide_last_error": (ctypes.c_char_p, []),
     "tide_status_string": (ctypes.c_char_p, [_i32]),

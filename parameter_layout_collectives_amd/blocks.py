@@ -23,7 +23,6 @@ The calls run on PyTorch's current stream of the tensors' device; outputs and
 workspaces that they make come from PyTorch's allocator, so they may be
 captured into a graph.
 """
-import contextlib
 import ctypes
 
 import torch
@@ -37,7 +36,8 @@ OUT_F16 = 0x80
 
 _IN_FLAG = {torch.bfloat16: 0, torch.float16: GRAD_F16, torch.float32: GRAD_F32}
 _OUT_FLAG = {torch.float32: 0, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}
-_MM, _DX, _DW = 0, 1, 2
+_IN_TYPES, _OUT_TYPES = tuple(_IN_FLAG), tuple(_OUT_FLAG)
+_MM, _DX, _DW, _LINEAR = 0, 1, 2, 3
 
 
 def _code_cols(cols):
@@ -48,12 +48,20 @@ def _scale_cols(cols):
     return -(-cols // (4 * BLOCK)) * 4
 
 
-def _launch(device):
-    """(context that makes `device` current, its current stream's handle)."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), stream
-    return torch.cuda.device(device), stream
+# The handle of a device's current stream (a public call makes a Stream object
+# for it, which costs as much as the rest of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        _check(fn(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _raw_stream(index)))
 
 
 def _matrix(t, what, dtypes):
@@ -90,12 +98,16 @@ class Blocks:
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
                              f"hold {self.rows} rows of {self.cols} columns")
         self.codes, self.scales = codes, scales
-        self._ptrs = ctypes.c_void_p(codes.data_ptr()), ctypes.c_void_p(scales.data_ptr())
+        self._ptrs = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
-        return cls(torch.empty(rows, _code_cols(cols), dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(rows, _scale_cols(cols), dtype=torch.uint8, device=device), cols)
+        self = object.__new__(cls)          # right by construction: no checks
+        self.codes = torch.empty((rows, _code_cols(cols)), dtype=torch.float8_e4m3fn, device=device)
+        self.scales = torch.empty((rows, _scale_cols(cols)), dtype=torch.uint8, device=device)
+        self.rows, self.cols, self.device = rows, cols, self.codes.device
+        self._ptrs = self.codes.data_ptr(), self.scales.data_ptr()
+        return self
 
     @property
     def shape(self):
@@ -117,27 +129,23 @@ def _out(out, shape, dtype, dtypes, device, what):
 
 def block_quant(x, out=None):
     """x [rows, cols] (bf16, fp16 or fp32) in 8-bit blocks: `out` or new Blocks."""
-    _matrix(x, "x", tuple(_IN_FLAG))
+    _matrix(x, "x", _IN_TYPES)
     rows, cols = x.shape
     if out is None:
         out = Blocks.empty(rows, cols, x.device)
     elif out.shape != (rows, cols):
         raise ValueError(f"out holds {out.shape}, x is {(rows, cols)}")
     _same_device(x.device, out)
-    ctx, stream = _launch(x.device)
-    with ctx:
-        _check(lib().tide_block_quant(ctypes.c_void_p(x.data_ptr()), rows, cols, *out._ptrs,
-                                      _IN_FLAG[x.dtype], stream))
+    _call(x.device, lib().tide_block_quant, x.data_ptr(), rows, cols, *out._ptrs,
+          _IN_FLAG[x.dtype])
     return out
 
 
 def block_dequant(q, out=None, dtype=torch.bfloat16):
     """The values of 8-bit blocks: in `out`, or in a new tensor of `dtype`."""
-    out = _out(out, q.shape, dtype, tuple(_OUT_FLAG), q.device, "out")
-    ctx, stream = _launch(q.device)
-    with ctx:
-        _check(lib().tide_block_dequant(*q._ptrs, q.rows, q.cols, ctypes.c_void_p(out.data_ptr()),
-                                        _OUT_FLAG[out.dtype], stream))
+    out = _out(out, q.shape, dtype, _OUT_TYPES, q.device, "out")
+    _call(q.device, lib().tide_block_dequant, *q._ptrs, q.rows, q.cols, out.data_ptr(),
+          _OUT_FLAG[out.dtype])
     return out
 
 
@@ -146,7 +154,7 @@ def _workspace(op, m, n, k, flags, device):
     if size <= 0:
         return None, None, 0
     buf = torch.empty(size, dtype=torch.uint8, device=device)
-    return buf, ctypes.c_void_p(buf.data_ptr()), size
+    return buf, buf.data_ptr(), size
 
 
 _PRODUCT_TYPES = (torch.bfloat16, torch.float32)
@@ -159,11 +167,9 @@ def block_mm(x, w, out=None, dtype=torch.bfloat16):
     _same_device(x.device, w)
     out = _out(out, (x.rows, w.rows), dtype, _PRODUCT_TYPES, x.device, "out")
     flags = _OUT_FLAG[out.dtype]
-    ctx, stream = _launch(x.device)
-    with ctx:
-        keep, ptr, size = _workspace(_MM, x.rows, w.rows, x.cols, flags, x.device)
-        _check(lib().tide_block_mm(*x._ptrs, x.rows, *w._ptrs, w.rows, w.cols,
-                                   ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    keep, ptr, size = _workspace(_MM, x.rows, w.rows, x.cols, flags, x.device)
+    _call(x.device, lib().tide_block_mm, *x._ptrs, x.rows, *w._ptrs, w.rows, w.cols,
+          out.data_ptr(), flags, ptr, size)
     return out
 
 
@@ -176,11 +182,9 @@ def block_mm_dx(dy, w, out=None, dtype=torch.bfloat16):
     m, n = dy.shape
     out = _out(out, (m, w.cols), dtype, _PRODUCT_TYPES, dy.device, "out")
     flags = _OUT_FLAG[out.dtype]
-    ctx, stream = _launch(dy.device)
-    with ctx:
-        keep, ptr, size = _workspace(_DX, m, n, w.cols, flags, dy.device)
-        _check(lib().tide_block_mm_dx(ctypes.c_void_p(dy.data_ptr()), m, n, *w._ptrs, w.cols,
-                                      ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    keep, ptr, size = _workspace(_DX, m, n, w.cols, flags, dy.device)
+    _call(dy.device, lib().tide_block_mm_dx, dy.data_ptr(), m, n, *w._ptrs, w.cols,
+          out.data_ptr(), flags, ptr, size)
     return out
 
 
@@ -196,11 +200,22 @@ def block_mm_dw(dy, x, out=None, dtype=torch.bfloat16, accumulate=False):
     m, n = dy.shape
     out = _out(out, (n, x.cols), dtype, _PRODUCT_TYPES, dy.device, "out")
     flags = _OUT_FLAG[out.dtype] | (ACCUMULATE if accumulate else 0)
-    ctx, stream = _launch(dy.device)
-    with ctx:
-        keep, ptr, size = _workspace(_DW, m, n, x.cols, flags, dy.device)
-        _check(lib().tide_block_mm_dw(ctypes.c_void_p(dy.data_ptr()), m, n, *x._ptrs, x.cols,
-                                      ctypes.c_void_p(out.data_ptr()), flags, ptr, size, stream))
+    keep, ptr, size = _workspace(_DW, m, n, x.cols, flags, dy.device)
+    _call(dy.device, lib().tide_block_mm_dw, dy.data_ptr(), m, n, *x._ptrs, x.cols,
+          out.data_ptr(), flags, ptr, size)
+    return out
+
+
+def _linear(x, w, dtype):
+    """block_mm(block_quant(x), w) that keeps no blocks of x (tide_block_linear)."""
+    _matrix(x, "x", _IN_TYPES)
+    m, k = x.shape
+    _same_device(x.device, w)
+    out = _out(None, (m, w.rows), dtype, _PRODUCT_TYPES, x.device, "out")
+    flags = _IN_FLAG[x.dtype] | _OUT_FLAG[dtype]
+    keep, ptr, size = _workspace(_LINEAR, m, w.rows, k, flags, x.device)
+    _call(x.device, lib().tide_block_linear, x.data_ptr(), m, k, *w._ptrs, w.rows,
+          out.data_ptr(), flags, ptr, size)
     return out
 
 
@@ -257,7 +272,7 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False):
         anchor = torch.empty(0, requires_grad=True) if grad is not None else None
         y = _Linear.apply(x, anchor, w, dtype, grad, accumulate)
     else:
-        y = block_mm(block_quant(x), w, dtype=dtype)
+        y = _linear(x, w, dtype)
     return y if len(lead) == 1 else y.view(*lead, w.rows)
 
 
@@ -324,10 +339,8 @@ def block_shard(plan, rank, master, block):
             or block.numel() != plan.S:
         raise ValueError(f"block must be a contiguous int32 device tensor of {plan.S} elements")
     _same_device(master.device, block)
-    ctx, stream = _launch(master.device)
-    with ctx:
-        _check(lib().tide_block_shard(plan.handle, int(rank), ctypes.c_void_p(master.data_ptr()),
-                                      ctypes.c_void_p(block.data_ptr()), 0, stream))
+    _call(master.device, lib().tide_block_shard, plan.handle, int(rank), master.data_ptr(),
+          block.data_ptr(), 0)
 
 
 def _check_unshard(plan, params, device):
@@ -356,10 +369,8 @@ def block_unshard(plan, gathered, params):
     device = gathered.device
     params._ensure(plan, "block_unshard", lambda: _check_unshard(plan, params.tensors, device))
     _same_device(device, params.tensors[0])
-    ctx, stream = _launch(device)
-    with ctx:
-        _check(lib().tide_block_unshard(plan.handle, ctypes.c_void_p(gathered.data_ptr()),
-                                        params.array, _OUT_FLAG[params.tensors[0].dtype], stream))
+    _call(device, lib().tide_block_unshard, plan.handle, gathered.data_ptr(), params.array,
+          _OUT_FLAG[params.tensors[0].dtype])
 
 
 __all__ = ["Blocks", "BlockPlan", "block_quant", "block_dequant", "block_mm", "block_mm_dx",

@@ -37,6 +37,10 @@ enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
 // most rows the skinny kernel takes, and the bounds of a split sum.
 constexpr int64_t kCus = 256;
 constexpr int64_t kSkinnyRows = 64;
+// x's blocks are made inside the product for at most this many rows and bytes
+// of codes (LDS, and work that every workgroup repeats).
+constexpr int64_t kInOneRows = 16;
+constexpr int64_t kInOneBytes = 32768;
 constexpr int64_t kMinSplitSteps = 4;
 constexpr int64_t kMaxSplits = 16;
 
@@ -73,5 +77,24 @@ struct MmArgs {
     uint32_t flags;
 };
 tide_status check_mm(MmOp op, const char *name, const MmArgs &g);
+
+// A product whose x is not in blocks yet.
+struct LinearArgs {
+    const void *x;
+    const void *b, *b_scales;
+    int64_t M, N, K;
+    void *out;
+    void *workspace;
+    int64_t workspace_bytes;
+    uint32_t flags;
+};
+// in_one: the kernel makes x's blocks in LDS.  Else they lie at the start of the
+// workspace, the scales from `scales` on, `blocks` bytes in all.
+struct LinearChoice {
+    bool in_one;
+    int64_t scales, blocks;
+};
+LinearChoice linear_choose(int64_t M, int64_t K);
+tide_status check_linear(const LinearArgs &a);
 
 }  // namespace tide

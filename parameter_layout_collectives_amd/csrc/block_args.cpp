@@ -203,6 +203,47 @@ tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
     return TIDE_OK;
 }
 
+LinearChoice linear_choose(int64_t M, int64_t K) {
+    LinearChoice c = {M <= kInOneRows && M * block_cols(K) <= kInOneBytes, 0, 0};
+    if (c.in_one) return c;
+    const int64_t round = 255;
+    c.scales = (M * block_cols(K) + round) & ~round;
+    c.blocks = (c.scales + M * block_scale_cols(K) + round) & ~round;
+    return c;
+}
+
+tide_status check_linear(const LinearArgs &a) {
+    const char *name = "tide_block_linear";
+    tide_status st = check_flags(name, a.flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 | TIDE_F_OUT_BF16);
+    if (st != TIDE_OK) return st;
+    for (int64_t rows : {a.M, a.N})
+        for (int64_t cols : {a.N, a.K})
+            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
+    if (a.N > kMaxLine || a.K > kMaxLine)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
+    if (a.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
+    if (a.workspace_bytes > 0 && !a.workspace) return bad(name, "workspace is NULL");
+    if (misaligned(a.workspace, 16)) return bad(name, "workspace is not 16-byte aligned");
+    if (a.M == 0 || a.N == 0) return TIDE_OK;
+    const int es = elem_size(in_type(a.flags)), os = elem_size(out_type(a.flags));
+    if (!a.out) return bad(name, "out is NULL");
+    if (misaligned(a.out, os)) return bad(name, "out is not aligned to its element size");
+    const Bytes out = bytes_of(a.out, a.M * a.N * os);
+    const Bytes wsp = bytes_of(a.workspace, a.workspace ? a.workspace_bytes : 0);
+    if (overlap(out, wsp)) return bad(name, "out overlaps the workspace");
+    if (a.K == 0) return TIDE_OK;
+    if (!a.x) return bad(name, "x is NULL");
+    if (misaligned(a.x, es)) return bad(name, "x is not aligned to its element size");
+    st = check_blocks(name, "w's", a.b, a.b_scales);
+    if (st != TIDE_OK) return st;
+    for (const Bytes &in : {bytes_of(a.x, a.M * a.K * es), bytes_of(a.b, a.N * block_cols(a.K)),
+                            bytes_of(a.b_scales, a.N * block_scale_cols(a.K))}) {
+        if (overlap(out, in)) return bad(name, "out overlaps an operand");
+        if (overlap(wsp, in)) return bad(name, "the workspace overlaps an operand");
+    }
+    return TIDE_OK;
+}
+
 MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
                    bool may_split) {
     MmChoice c;
@@ -272,6 +313,10 @@ tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int3
         const tide_status st =
             tide_plan_create(plan->N, 2 * n, d0.data(), words.data(), 4, &p);
         if (st != TIDE_OK) return st;
+        if (p->S / 4 > 0xffffffffll) {
+            tide_plan_destroy(p);
+            return bad(name, "a rank block of more than 2^36 bytes");
+        }
         p->nblk = n;
         p->blk_S = plan->S;
         p->blk_off.swap(off);
@@ -284,7 +329,12 @@ tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int3
 }
 
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {
-    if (op < 0 || op > 2 || m < 0 || n < 0 || k < 0) return -1;
+    if (op < 0 || op > 3 || m < 0 || n < 0 || k < 0) return -1;
+    if (op == 3) {               // tide_block_linear: x's blocks, then the product's
+        const tide::LinearChoice c = tide::linear_choose(m, k);
+        if (c.in_one || n == 0) return 0;
+        return c.blocks + tide_block_workspace(0, m, n, k, flags & TIDE_F_OUT_BF16);
+    }
     // whichever way dY is aligned
     int64_t most = 0;
     for (bool aligned : {false, true})

@@ -21,14 +21,11 @@
 #include <algorithm>
 
 #include "block.h"
+#include "block_device.h"
 
 namespace tide {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kLanes = 256;                        // lanes of a workgroup
@@ -37,106 +34,15 @@ constexpr int kGroups = kLanes / kGroup;           // blocks a workgroup handles
 constexpr int kUnroll = 4;                         // blocks in flight per group
 constexpr int kChunk = kGroups * kUnroll;          // blocks a workgroup handles in all
 
-// 8 consecutive elements as fp32.  `vec`: the first one is 16-byte aligned
-// and all `n` asked for are whole vectors (n is 0 or 8 then).
-template <int ET>
-__device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = 0.0f;
-    if (n <= 0) return;
-    if (ET == kElemF32) {
-        const float *f = reinterpret_cast<const float *>(p);
-        if (vec) {
-            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f));
-            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f + 4));
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
-        } else {
-            for (int i = 0; i < 8; i++)
-                if (i < n) v[i] = f[i];
-        }
-        return;
-    }
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (vec) {
-        const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-#pragma unroll
-        for (int i = 0; i < 4; i++) w[i] = a[i];
-    } else {
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < n) w[i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t h = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-        v[i] = ET == kElemBf16
-                   ? __uint_as_float(h << 16)
-                   : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(h)));
-    }
-}
-
-// The largest value over the 16 lanes of a row (DPP rotations by 8, 4, 2, 1).
-__device__ __forceinline__ uint32_t max16(uint32_t u) {
-    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x128, 0xf, 0xf, false)));
-    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x124, 0xf, 0xf, false)));
-    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x122, 0xf, 0xf, false)));
-    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x121, 0xf, 0xf, false)));
-    return u;
-}
-
-// One lane's 8 values -> 8 codes; the block's scale byte is the same in all
-// 16 lanes.  Patterns of |x| order like the values, so the maximum is taken on
-// them as integers.
-__device__ __forceinline__ u32x2 encode8(const float *v, uint32_t *scale) {
-    uint32_t top = 0;
-    bool odd = false;                     // an inf or a NaN among the 8
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-        const bool finite = u < 0x7f800000u;
-        odd |= !finite;
-        top = max(top, finite ? u : 0u);
-    }
-    top = max16(top);
-    // a = m * 2^k with 1 <= m < 2: a <= 448 * 2^e = 1.75 * 2^(8+e) from
-    // e = k - 8 on if m <= 1.75, else from k - 7 on
-    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = top == 0 ? 0 : min(119, max(-117, e));
-    *scale = static_cast<uint32_t>(e + 127);
-    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(v[i] * s, -448.0f, 448.0f);
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
-    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
-    u32x2 c = {static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
-    if (odd) {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if ((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u) {
-                const uint32_t m = 0xffu << (8 * (i & 3)), nan = 0x7fu << (8 * (i & 3));
-                if (i < 4)
-                    c.x = (c.x & ~m) | nan;
-                else
-                    c.y = (c.y & ~m) | nan;
-            }
-    }
-    return c;
-}
-
-// What a run of rows of one matrix is, for the kernels below.
+// A matrix of a unit, for the kernels below.
 struct Rows {
-    int64_t src;          // first element of the rows in the source (or destination)
-    int64_t codes;        // byte of the first code row, from the block's start
-    int64_t scales;       // byte of the first scale row
-    int64_t rows, real;   // rows to write, and of them rows that exist in the source
-    int64_t cols;
-    uint32_t nb;          // blocks in a row
-    uint32_t wg0;         // first workgroup that works on it
+    int64_t src;           // first element of its rows in the source (or the destination's address)
+    uint32_t codes;        // where its codes and its scales start in a rank block, in 16 bytes
+    uint32_t scales;
+    uint32_t rows, real;   // rows to write, and of them rows that exist in the source
+    uint32_t cols;
+    uint32_t wg0;          // first workgroup that works on it
+    __host__ __device__ uint32_t nb() const { return (cols + kBlockCols - 1) / kBlockCols; }
 };
 
 // Reads blocks [first, first + kChunk) of `d` (row-major), encodes and stores
@@ -146,21 +52,22 @@ __device__ __forceinline__ void encode_chunk(const Rows &d, int64_t first, const
                                              char *codes, char *scales, bool vec) {
     constexpr int ES = ET == kElemF32 ? 4 : 2;
     const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
-    const int64_t units = d.rows * d.nb;
-    const int64_t row0 = first / d.nb;                      // uniform
-    const uint32_t b0 = static_cast<uint32_t>(first - row0 * d.nb);
-    const int64_t cp = static_cast<int64_t>(d.nb) * kBlockCols, sp = (d.nb + 3) / 4 * 4;
+    const uint32_t nb = d.nb();
+    const int64_t units = static_cast<int64_t>(d.rows) * nb;
+    const int64_t row0 = first / nb;                        // uniform
+    const uint32_t b0 = static_cast<uint32_t>(first - row0 * nb);
+    const int64_t cp = static_cast<int64_t>(nb) * kBlockCols, sp = (nb + 3) / 4 * 4;
     float v[kUnroll][8];
     int64_t row[kUnroll];
     uint32_t blk[kUnroll];
 #pragma unroll
     for (int q = 0; q < kUnroll; q++) {
         const uint32_t i = b0 + q * kGroups + group;        // < nb + kChunk
-        row[q] = row0 + i / d.nb;
-        blk[q] = i % d.nb;
+        row[q] = row0 + i / nb;
+        blk[q] = i % nb;
         const int64_t c = static_cast<int64_t>(blk[q]) * kBlockCols + lane * 8;
         const bool there = first + q * kGroups + group < units && row[q] < d.real;
-        const int64_t left = d.cols - c;
+        const int64_t left = static_cast<int64_t>(d.cols) - c;
         load8<ET>(src + (row[q] * d.cols + c) * ES,
                   there ? static_cast<int>(left < 8 ? left : 8) : 0, vec, v[q]);
     }
@@ -173,7 +80,7 @@ __device__ __forceinline__ void encode_chunk(const Rows &d, int64_t first, const
                                    lane * 8) = c;
         char *s = scales + row[q] * sp + blk[q];
         if (lane == 0) *s = static_cast<char>(scale);
-        if (blk[q] == d.nb - 1 && lane > 0 && blk[q] + lane < sp) s[lane] = 127;
+        if (blk[q] == nb - 1 && lane > 0 && blk[q] + lane < sp) s[lane] = 127;
     }
 }
 
@@ -181,8 +88,8 @@ template <int ET>
 __global__ __launch_bounds__(kLanes) void quant_kernel(const char *__restrict__ x, int64_t rows,
                                                        int64_t cols, char *__restrict__ codes,
                                                        char *__restrict__ scales, int vec) {
-    const Rows d{0, 0, 0, rows, rows, cols,
-                 static_cast<uint32_t>((cols + kBlockCols - 1) / kBlockCols), 0};
+    const Rows d{0, 0, 0, static_cast<uint32_t>(rows), static_cast<uint32_t>(rows),
+                 static_cast<uint32_t>(cols), 0};
     encode_chunk<ET>(d, static_cast<int64_t>(blockIdx.x) * kChunk, x, codes, scales, vec != 0);
 }
 
@@ -285,7 +192,7 @@ __global__ __launch_bounds__(kLanes) void dequant_kernel(const char *__restrict_
 // A unit's matrices travel as kernel arguments (no table in device memory, so
 // nothing to allocate, upload or keep for a captured launch): as many per
 // launch as fit 4 KB.
-constexpr int kPerLaunch = 56;
+constexpr int kPerLaunch = 112;
 struct ShardArgs {
     Rows m[kPerLaunch];
     int n;
@@ -294,7 +201,7 @@ struct UnshardArgs {
     Rows m[kPerLaunch];             // rows = the matrix's rows, real = rows per rank
     int n;
 };
-static_assert(sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
+static_assert(sizeof(Rows) == 32 && sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
 
 // The matrix that workgroup `wg` works on: the last one with wg0 <= wg.
 template <class A>
@@ -315,7 +222,8 @@ __global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *
     const Rows d = a.m[matrix_of(a, blockIdx.x)];
     const bool vec = aligned && d.src % 4 == 0 && d.cols % 8 == 0;
     encode_chunk<kElemF32>(d, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
-                           master + d.src * 4, block + d.codes, block + d.scales, vec);
+                           master + d.src * 4, block + static_cast<int64_t>(d.codes) * 16,
+                           block + static_cast<int64_t>(d.scales) * 16, vec);
 }
 
 // `src` of a matrix holds its destination's address here; row r lies in rank
@@ -327,14 +235,18 @@ __global__ __launch_bounds__(kLanes) void unshard_kernel(UnshardArgs a,
     const Rows d = a.m[matrix_of(a, blockIdx.x)];
     char *out = reinterpret_cast<char *>(d.src);
     const bool vec = d.src % 16 == 0 && d.cols % 8 == 0;
-    const int64_t cp = static_cast<int64_t>(d.nb) * kBlockCols, sp = (d.nb + 3) / 4 * 4;
-    const int64_t c = d.real;
-    decode_chunk<ET>(d.rows, d.cols, d.nb, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
+    const uint32_t nb = d.nb();
+    const int64_t cp = static_cast<int64_t>(nb) * kBlockCols, sp = (nb + 3) / 4 * 4;
+    const int64_t at_codes = static_cast<int64_t>(d.codes) * 16;
+    const int64_t at_scales = static_cast<int64_t>(d.scales) * 16;
+    const uint32_t c = d.real;
+    decode_chunk<ET>(d.rows, d.cols, nb, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
                      [=](int64_t r, const char **codes, const char **scales) {
-                         const int64_t rank = r / c, in = r - rank * c;
+                         const uint32_t row = static_cast<uint32_t>(r), rank = row / c;
+                         const int64_t in = row - rank * c;
                          const char *b = gathered + rank * rank_bytes;
-                         *codes = b + d.codes + in * cp;
-                         *scales = b + d.scales + in * sp;
+                         *codes = b + at_codes + in * cp;
+                         *scales = b + at_scales + in * sp;
                      },
                      out, vec);
 }
@@ -360,7 +272,7 @@ tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Laun
         for (; j < bp->nblk && a.n < kPerLaunch; j++) {
             Rows r;
             fill(j, &r);
-            const int64_t units = r.rows * r.nb;
+            const int64_t units = static_cast<int64_t>(r.rows) * r.nb();
             if (units == 0) continue;
             if (grid + chunks(units) > kMaxGrid) break;
             r.wg0 = static_cast<uint32_t>(grid);
@@ -378,7 +290,8 @@ tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Laun
     return TIDE_OK;
 }
 
-uint32_t blocks_of(int64_t cols) { return static_cast<uint32_t>(block_count(cols)); }
+// An offset in 4-byte words (a multiple of 4) in 16 bytes.
+uint32_t in16(int64_t words) { return static_cast<uint32_t>(words / 4); }
 
 }  // namespace
 }  // namespace tide
@@ -443,14 +356,10 @@ extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, con
         "tide_block_shard", plan,
         [&](int32_t j, Rows *r) {
             const int64_t c = plan->c[j], d0 = plan->d0[j];
-            *r = Rows{plan->blk_off[j],
-                      plan->off[j] * 4,
-                      plan->off[plan->nblk + j] * 4,
-                      c,
-                      std::min(c, std::max<int64_t>(0, d0 - rank * c)),
-                      plan->blk_inner[j],
-                      blocks_of(plan->blk_inner[j]),
-                      0};
+            *r = Rows{plan->blk_off[j], in16(plan->off[j]), in16(plan->off[plan->nblk + j]),
+                      static_cast<uint32_t>(c),
+                      static_cast<uint32_t>(std::min(c, std::max<int64_t>(0, d0 - rank * c))),
+                      static_cast<uint32_t>(plan->blk_inner[j]), 0};
         },
         [&](const ShardArgs &a, unsigned grid) {
             shard_kernel<<<dim3(grid), dim3(kLanes), 0, s>>>(
@@ -472,13 +381,9 @@ extern "C" tide_status tide_block_unshard(const tide_plan *plan, const void *gat
         "tide_block_unshard", plan,
         [&](int32_t j, Rows *r) {
             *r = Rows{static_cast<int64_t>(reinterpret_cast<uintptr_t>(params[j])),
-                      plan->off[j] * 4,
-                      plan->off[plan->nblk + j] * 4,
-                      plan->d0[j],
-                      plan->c[j],
-                      plan->blk_inner[j],
-                      blocks_of(plan->blk_inner[j]),
-                      0};
+                      in16(plan->off[j]), in16(plan->off[plan->nblk + j]),
+                      static_cast<uint32_t>(plan->d0[j]), static_cast<uint32_t>(plan->c[j]),
+                      static_cast<uint32_t>(plan->blk_inner[j]), 0};
         },
         [&](const UnshardArgs &a, unsigned grid) {
             const dim3 gr(grid), b(kLanes);

@@ -11,20 +11,16 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block.h"
+#include "block_device.h"
 
 namespace tide {
 namespace {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -708,25 +704,79 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
 // one 4-byte load of scales) and join through LDS in wave order.  Codes go from
 // memory to registers as 16-byte loads, become bf16 there (exactly) and enter
 // the bf16 instruction; the k-order inside a load is the same on both sides.
+//
+// SRC: where X comes from.  kFromCodes: 8-bit blocks in memory.  Else an element
+// type: every workgroup makes the blocks itself, in LDS, while its first codes
+// of W are on their way; for the few rows this is for that costs less than a
+// launch of its own.
 constexpr int kSkinnyWaves = 8;
+constexpr int kFromCodes = -1;
 
-template <int MT>
+template <int MT, int SRC>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
+    constexpr bool CODES = SRC == kFromCodes;
+    constexpr int XQ = MT <= 2 ? 4 : 1;              // blocks of X in flight
+    extern __shared__ __attribute__((aligned(16))) char made[];
     __shared__ __attribute__((aligned(16))) f32x4 part[kSkinnyWaves][MT][64];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int r16 = lane & 15, g = lane >> 4;
     const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t nb = (p.sum + 127) / 128;
+    const int nb = static_cast<int>((p.sum + 127) / 128);
     const int64_t wrow = min(j0 + r16, p.cols - 1);
     const char *w = p.b + wrow * p.b_pitch + g * 16;
     const char *ws = p.bs + wrow * p.bs_pitch;
-    const char *x[MT], *xs[MT];
+    u32x4 wv[4][2];
+    uint32_t wsc = 0;
+    auto load_w = [&](int b, int n) {
+        wsc = *reinterpret_cast<const uint32_t *>(ws + b);
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-        const int64_t row = min(static_cast<int64_t>(m * 16 + r16), p.rows - 1);
-        x[m] = p.a + row * p.a_pitch + g * 16;
-        xs[m] = p.as + row * p.as_pitch;
+        for (int q = 0; q < 4; q++)
+            if (q < n) {
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    wv[q][h] = *reinterpret_cast<const u32x4 *>(w + (b + q) * 128 + h * 64);
+            }
+    };
+    int b = wave * 4;
+    if (b < nb) load_w(b, min(nb - b, 4));
+
+    // X's blocks: codes with a pitch of 16 bytes more than a row, so that 16
+    // rows' pieces lie in different banks, and then the scale bytes
+    const char *x[MT], *xs[MT];
+    if (CODES) {
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            const int64_t row = min(static_cast<int64_t>(m * 16 + r16), p.rows - 1);
+            x[m] = p.a + row * p.a_pitch + g * 16;
+            xs[m] = p.as + row * p.as_pitch;
+        }
+    } else {
+        constexpr int ES = SRC == kElemF32 ? 4 : 2;
+        const int rows = static_cast<int>(p.rows), units = rows * nb;
+        const int pitch = nb * 128 + 16, spitch = (nb + 3) / 4 * 4;
+        char *const scales = made + rows * pitch;
+        for (int u0 = 0; u0 < units; u0 += kSkinnyWaves * 4) {
+            const int u = u0 + (t >> 4), row = u / nb, blk = u % nb, c = blk * 128 + (t & 15) * 8;
+            const int left = u < units ? static_cast<int>(min(p.sum - c, static_cast<int64_t>(8))) : 0;
+            float v[8];
+            load8<CODES ? kElemBf16 : SRC>(p.a + (static_cast<int64_t>(row) * p.sum + c) * ES, left,
+                                           p.aligned != 0, v);
+            uint32_t scale;
+            const u32x2 codes = encode8(v, &scale);
+            if (u < units) {
+                *reinterpret_cast<u32x2 *>(made + row * pitch + c) = codes;
+                if ((t & 15) == 0) scales[row * spitch + blk] = static_cast<char>(scale);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            const int row = min(m * 16 + r16, rows - 1);
+            x[m] = made + row * pitch + g * 16;
+            xs[m] = scales + row * spitch;
+        }
     }
+
     f32x4 acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; m++) acc[m] = f32x4{0, 0, 0, 0};
@@ -741,31 +791,33 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
         u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h + 1], s, true);
         return u.v;
     };
-    for (int64_t b = wave * 4; b < nb; b += kSkinnyWaves * 4) {
-        const int n = static_cast<int>(min(nb - b, static_cast<int64_t>(4)));
-        const uint32_t wsc = *reinterpret_cast<const uint32_t *>(ws + b);
+    // Blocks b .. b + n - 1, n = 4 with FULL.
+    auto group = [&](auto full, int n) {
+        constexpr bool FULL = decltype(full)::value;
         uint32_t xsc[MT];
+        u32x4 xv[XQ][2][MT];
+        auto load_x = [&](int q) {
 #pragma unroll
-        for (int m = 0; m < MT; m++) xsc[m] = *reinterpret_cast<const uint32_t *>(xs[m] + b);
-        u32x4 wv[4][2];
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (q < n) {
-#pragma unroll
-                for (int h = 0; h < 2; h++)
-                    wv[q][h] = __builtin_nontemporal_load(
-                        reinterpret_cast<const u32x4 *>(w + (b + q) * 128 + h * 64));
-            }
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            if (q >= n) continue;
-            const float sw = __uint_as_float((wsc >> (8 * q) & 0xffu) << 23);
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                u32x4 xv[MT];
+            for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int m = 0; m < MT; m++)
-                    xv[m] = *reinterpret_cast<const u32x4 *>(x[m] + (b + q) * 128 + h * 64);
+                    xv[q % XQ][h][m] =
+                        *reinterpret_cast<const u32x4 *>(x[m] + (b + q) * 128 + h * 64);
+        };
+#pragma unroll
+        for (int m = 0; m < MT; m++) xsc[m] = *reinterpret_cast<const uint32_t *>(xs[m] + b);
+        if (XQ == 4) {
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                if (FULL || q < n) load_x(q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            if (!FULL && q >= n) break;
+            if (XQ < 4) load_x(q);
+            const float sw = __uint_as_float((wsc >> (8 * q) & 0xffu) << 23);
+#pragma unroll
+            for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const bf16x8 wf = widen(wv[q][h], e, sw);
@@ -773,11 +825,19 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
                     for (int m = 0; m < MT; m++) {
                         const float sx = __uint_as_float((xsc[m] >> (8 * q) & 0xffu) << 23);
                         acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wf, widen(xv[m], e, sx), acc[m], 0, 0, 0);
+                            wf, widen(xv[q % XQ][h][m], e, sx), acc[m], 0, 0, 0);
                     }
                 }
-            }
         }
+    };
+    for (; b < nb; b += kSkinnyWaves * 4) {
+        const int n = min(nb - b, 4);
+        if (n == 4)
+            group(std::true_type{}, 4);
+        else
+            group(std::false_type{}, n);
+        const int next = b + kSkinnyWaves * 4;
+        if (next < nb) load_w(next, min(nb - next, 4));
     }
 #pragma unroll
     for (int m = 0; m < MT; m++) part[wave][m][lane] = acc[m];
@@ -850,11 +910,11 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
     if (c.kernel == kMmSkinny) {
         const dim3 g(static_cast<unsigned>((p.cols + 15) / 16)), b(kSkinnyWaves * 64);
         if (p.rows <= 16)
-            skinny_kernel<1><<<g, b, 0, s>>>(p);
+            skinny_kernel<1, kFromCodes><<<g, b, 0, s>>>(p);
         else if (p.rows <= 32)
-            skinny_kernel<2><<<g, b, 0, s>>>(p);
+            skinny_kernel<2, kFromCodes><<<g, b, 0, s>>>(p);
         else
-            skinny_kernel<4><<<g, b, 0, s>>>(p);
+            skinny_kernel<4, kFromCodes><<<g, b, 0, s>>>(p);
     } else if (c.kernel == kMmEight) {
         if (c.tile == 256)
             eight_kernel<256, 2, 4><<<grid, dim3(512), 0, s>>>(p);
@@ -874,6 +934,58 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
         e = hipGetLastError();
     }
     if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
+    clear_error();
+    return TIDE_OK;
+}
+
+// x w^T for an x that is not in blocks yet: in one launch for few rows, else
+// through blocks in the workspace.
+tide_status run_linear(const LinearArgs &a, void *stream) {
+    const char *name = "tide_block_linear";
+    tide_status st = check_linear(a);
+    if (st != TIDE_OK) return st;
+    const ElemType in = in_type(a.flags);
+    const uint32_t oflags = a.flags & TIDE_F_OUT_BF16;
+    const LinearChoice c = linear_choose(a.M, a.K);
+    char *const ws = static_cast<char *>(a.workspace);
+    if (!c.in_one || a.N == 0 || a.M == 0 || a.K == 0) {
+        if (a.M && a.N && a.K) {
+            if (a.workspace_bytes < c.blocks)
+                return fail(TIDE_E_INVALID, std::string(name) + ": the workspace holds " +
+                                                std::to_string(a.workspace_bytes) + " bytes, x's " +
+                                                "blocks need " + std::to_string(c.blocks));
+            st = tide_block_quant(a.x, a.M, a.K, ws, ws + c.scales, a.flags & ~oflags, stream);
+            if (st != TIDE_OK) return st;
+        }
+        const int64_t left = std::max<int64_t>(a.workspace_bytes - c.blocks, 0);
+        return run_mm(kMm, name,
+                      MmArgs{ws, ws ? ws + c.scales : nullptr, a.b, a.b_scales, a.M, a.N, a.K, a.out,
+                             left ? ws + c.blocks : nullptr, left, oflags},
+                      stream);
+    }
+    MmLaunch p = {};
+    p.rows = a.M;
+    p.cols = a.N;
+    p.sum = a.K;
+    p.a = static_cast<const char *>(a.x);
+    p.b = static_cast<const char *>(a.b);
+    p.bs = static_cast<const char *>(a.b_scales);
+    p.b_pitch = block_cols(a.K);
+    p.bs_pitch = block_scale_cols(a.K);
+    p.out = static_cast<char *>(a.out);
+    p.out_bf16 = oflags != 0;
+    p.aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.K % 8 == 0;
+    const dim3 g(static_cast<unsigned>((a.N + 15) / 16)), b(kSkinnyWaves * 64);
+    const unsigned lds =
+        static_cast<unsigned>(a.M * (block_cols(a.K) + 16 + block_scale_cols(a.K)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    switch (in) {
+        case kElemBf16: skinny_kernel<1, kElemBf16><<<g, b, lds, s>>>(p); break;
+        case kElemF16: skinny_kernel<1, kElemF16><<<g, b, lds, s>>>(p); break;
+        case kElemF32: skinny_kernel<1, kElemF32><<<g, b, lds, s>>>(p); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("tide_block_linear: kernel launch", e);
     clear_error();
     return TIDE_OK;
 }
@@ -909,4 +1021,12 @@ extern "C" tide_status tide_block_mm_dw(const void *dy, int64_t m, int64_t n, co
                   MmArgs{dy, nullptr, x_codes, x_scales, m, n, k, dw, workspace, workspace_bytes,
                          flags},
                   stream);
+}
+
+extern "C" tide_status tide_block_linear(const void *x, int64_t m, int64_t k, const void *w_codes,
+                                         const void *w_scales, int64_t n, void *out,
+                                         uint32_t flags, void *workspace, int64_t workspace_bytes,
+                                         void *stream) {
+    return run_linear(
+        LinearArgs{x, w_codes, w_scales, m, n, k, out, workspace, workspace_bytes, flags}, stream);
 }

@@ -151,6 +151,43 @@ def test_product_operand_refusals(call, kw, status, needle):
     assert needle in err()
 
 
+def linear(x=A, m=4, k=200, w=C, ws=D, n=8, out=E, flags=0, wsp=0, size=0):
+    return lib().tide_block_linear(P(x), m, k, P(w), P(ws), n, P(out), flags, P(wsp), size, None)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    c for c in COMMON if c[0] not in (dict(out=A), dict(flags=0x80))] + [
+    (dict(flags=0x40), E_UNSUPPORTED, "flag"),
+    (dict(flags=0x18), E_INVALID, "both"),
+    (dict(x=0), E_INVALID, "x is NULL"),
+    (dict(x=A + 1), E_INVALID, "x is not aligned"),
+    (dict(x=A + 2, flags=0x10), E_INVALID, "x is not aligned"),
+    (dict(w=0), E_INVALID, "w's codes are NULL"),
+    (dict(w=C + 8), E_INVALID, "16-byte"),
+    (dict(ws=D + 2), E_INVALID, "4-byte"),
+    (dict(out=A + 1584), E_INVALID, "overlaps"),
+    (dict(m=100), E_INVALID, "x's blocks need"),           # no room for x's blocks
+    (dict(m=100, wsp=W, size=256), E_INVALID, "x's blocks need")])
+def test_linear_refusals(kw, status, needle):
+    assert linear(**kw) == status
+    assert needle in err()
+
+
+def test_linear_of_nothing():
+    assert linear(m=0, x=0, out=0) == 0
+    assert linear(n=0, w=0, ws=0, out=0) == 0
+
+
+def test_linear_workspace():
+    L = lib()
+    assert L.tide_block_workspace(3, 1, 4096, 4096, 0x20) == 0         # in one launch
+    assert L.tide_block_workspace(3, 100, 4096, 0, 0x20) == 0
+    m, n, k = 100, 4096, 1000
+    blocks = (100 * 1024 + 255) // 256 * 256 + (100 * 8 + 255) // 256 * 256
+    assert L.tide_block_workspace(3, m, n, k, 0x20) == \
+        blocks + L.tide_block_workspace(0, m, n, k, 0x20)
+
+
 def test_workspace():
     L = lib()
     for op in range(3):
@@ -159,7 +196,7 @@ def test_workspace():
     assert L.tide_block_workspace(0, 1, 4096, 4096, 0x20) == 0         # few rows: one kernel
     size = L.tide_block_workspace(2, 8192, 256, 256, 0)                # a long sum, 4 tiles
     assert size > 0 and size % (256 * 256 * 4) == 0
-    assert L.tide_block_workspace(3, 1, 1, 1, 0) == -1
+    assert L.tide_block_workspace(4, 1, 1, 1, 0) == -1
     assert L.tide_block_workspace(0, -1, 1, 1, 0) == -1
 
 
@@ -211,7 +248,7 @@ def test_block_plan_refusals_of_plans():
     assert create(tide.BlockPlan(plan), [0])[0] == E_INVALID and "itself" in err()
     assert create(plan, [0], out=False)[0] == E_INVALID
     assert lib().tide_plan_create_blocks(plan.handle, 1, None, ctypes.byref(P())) == E_INVALID
-    big = tide.Plan([(1, 1 << 40)], 2)
+    big = tide.Plan([(1 << 31, 0)], 2)
     assert create(big, [0])[0] == E_INVALID and "2^31" in err()
     with pytest.raises(tide.TideError):
         tide.BlockPlan(tide.Plan([(4,)], 2))             # no matrix to select

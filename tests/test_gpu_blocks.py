@@ -412,6 +412,35 @@ def test_on_two_streams_at_once():
         assert torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 72, 4096), (1, 33, 28672), (3, 200, 1111),
+                                   (16, 130, 2048), (16, 16, 2049), (17, 64, 700), (8, 100, 4097),
+                                   (130, 200, 392), (600, 512, 1000)])
+def test_linear_in_one_call(shape, dtype):
+    """tide_block_linear equals tide_block_quant and tide_block_mm, bit for bit,
+    from any alignment of x."""
+    m, n, k = shape
+    note(f"block_linear in one call {shape} {dtype}")
+    w = tide.block_quant(rand((n, k), 22, FP, 0.02))
+    base = rand((1, m * k + 1), 23, dtype).view(-1)
+    for lead in (0, 1):
+        x = base[lead:lead + m * k].view(m, k)
+        for out in (BF, FP):
+            got = tide.block_linear(x, w, dtype=out)
+            assert torch.equal(got, tide.block_mm(tide.block_quant(x), w, dtype=out)), (lead, out)
+
+
+def test_linear_in_one_call_of_special_values():
+    note("block_linear special values")
+    x = special_rows().to(BF).cuda()
+    w = tide.block_quant(rand((24, 256), 24, FP, 0.02))
+    for rows in (x[:16], x[-16:], x):
+        rows = rows.contiguous()
+        got, want = tide.block_linear(rows, w), tide.block_mm(tide.block_quant(rows), w)
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(0), want.nan_to_num(0))
+
+
 # ------------------------------------------------------------------- together
 
 def linear_reference(xq, w, dy, k):
