@@ -33,14 +33,21 @@ inline int elem_size(ElemType t) { return t == kElemF32 ? 4 : 2; }
 //   kMmDw  i = row of W, j = column, c = token: I = dY transposed, J = X
 enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
 
-// The card's compute units (a product's tiles are counted against them), the
-// most rows the skinny kernel takes, and the bounds of a split sum.
+// The card's compute units: a product's tiles are counted against them.
 constexpr int64_t kCus = 256;
-constexpr int64_t kSkinnyRows = 64;
-// x's blocks are made inside the product for at most this many rows and bytes
-// of codes (LDS, and work that every workgroup repeats).
-constexpr int64_t kInOneRows = 16;
-constexpr int64_t kInOneBytes = 32768;
+// The skinny kernel takes up to 16 rows, and up to 64 if W is small: there the
+// second launch of a cut sum costs more than the tiles gain.  32 rows, n = k =
+// 4096: 9.4 us (tiles and join: 14.9); n = 8192, k = 28672: 96 us (68).
+constexpr int64_t kSkinnyRows = 16;
+constexpr int64_t kSkinnyMost = 64;
+constexpr int64_t kSkinnyWeights = int64_t(1) << 24;
+// x's blocks are made inside the product for one row of at most 28 KB of codes,
+// or more rows of at most 8 KB together: every workgroup repeats that work.  One
+// row, n = 14336, k = 4096: 16.2 us, as the product alone; 8 rows: 30.1 us
+// (product alone 17.1, and a launch for the blocks about 4).
+constexpr int64_t kInOneRow = 28672;     // 56 KB of LDS
+constexpr int64_t kInOneBytes = 8192;
+// The least steps in a piece of a cut sum, and the most pieces.
 constexpr int64_t kMinSplitSteps = 4;
 constexpr int64_t kMaxSplits = 16;
 

@@ -204,7 +204,8 @@ tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
 }
 
 LinearChoice linear_choose(int64_t M, int64_t K) {
-    LinearChoice c = {M <= kInOneRows && M * block_cols(K) <= kInOneBytes, 0, 0};
+    const int64_t bytes = M * block_cols(K);
+    LinearChoice c = {M <= kSkinnyRows && bytes <= (M == 1 ? kInOneRow : kInOneBytes), 0, 0};
     if (c.in_one) return c;
     const int64_t round = 255;
     c.scales = (M * block_cols(K) + round) & ~round;
@@ -250,7 +251,8 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
     const int64_t sum = op == kMm ? K : op == kMmDx ? N : M;
     const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16);
-    c.kernel = op == kMm && M <= kSkinnyRows ? kMmSkinny : eight ? kMmEight : kMmWide;
+    const bool skinny = M <= kSkinnyRows || (M <= kSkinnyMost && N * K <= kSkinnyWeights);
+    c.kernel = op == kMm && skinny ? kMmSkinny : eight ? kMmEight : kMmWide;
     const int64_t step = eight ? 128 : 64;
     const int64_t steps = (sum + step - 1) / step;
     auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };

@@ -700,22 +700,38 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
 // ---------------------------------------------------------------------------
 //
 // W's bytes bound it: each workgroup takes 16 rows of W and all rows of X (MT
-// groups of 16), its waves cut the sum at multiples of 512 columns (4 blocks:
-// one 4-byte load of scales) and join through LDS in wave order.  Codes go from
-// memory to registers as 16-byte loads, become bf16 there (exactly) and enter
-// the bf16 instruction; the k-order inside a load is the same on both sides.
+// groups of 16), its waves cut the sum into groups of 4 blocks (one load of
+// scales each) and join through LDS in wave order.  Codes go from memory to
+// registers as 16-byte loads, become bf16 there (exactly) and enter the bf16
+// instruction; the k-order inside a load is the same on both sides.  Reading W
+// this way alone takes 12.5 us for 14336 x 4096 and 41.5 us (5.7 TB/s) for
+// 8192 x 28672.
 //
 // SRC: where X comes from.  kFromCodes: 8-bit blocks in memory.  Else an element
-// type: every workgroup makes the blocks itself, in LDS, while its first codes
-// of W are on their way; for the few rows this is for that costs less than a
-// launch of its own.
+// type: every workgroup makes the blocks itself, and their bf16 values, in LDS,
+// while its first codes of W are on their way; for the few values this is for
+// that costs less than a launch of its own.
 constexpr int kSkinnyWaves = 8;
 constexpr int kFromCodes = -1;
+
+// 8 codes times 2^e (as a float) in bf16.
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float s) {
+    union {
+        bf16x2 p[4];
+        bf16x8 v;
+    } u;
+    u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+    u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+    u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+    u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+    return u.v;
+}
 
 template <int MT, int SRC>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
     constexpr bool CODES = SRC == kFromCodes;
-    constexpr int XQ = MT <= 2 ? 4 : 1;              // blocks of X in flight
+    constexpr int GB = 4;                            // blocks in a group
+    constexpr int XQ = CODES && MT <= 2 ? GB : 1;    // blocks of X in flight
     extern __shared__ __attribute__((aligned(16))) char made[];
     __shared__ __attribute__((aligned(16))) f32x4 part[kSkinnyWaves][MT][64];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -725,23 +741,23 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
     const int64_t wrow = min(j0 + r16, p.cols - 1);
     const char *w = p.b + wrow * p.b_pitch + g * 16;
     const char *ws = p.bs + wrow * p.bs_pitch;
-    u32x4 wv[4][2];
+    u32x4 wv[GB][2];
     uint32_t wsc = 0;
     auto load_w = [&](int b, int n) {
         wsc = *reinterpret_cast<const uint32_t *>(ws + b);
 #pragma unroll
-        for (int q = 0; q < 4; q++)
+        for (int q = 0; q < GB; q++)
             if (q < n) {
 #pragma unroll
                 for (int h = 0; h < 2; h++)
                     wv[q][h] = *reinterpret_cast<const u32x4 *>(w + (b + q) * 128 + h * 64);
             }
     };
-    int b = wave * 4;
-    if (b < nb) load_w(b, min(nb - b, 4));
+    int b = wave * GB;
+    if (b < nb) load_w(b, min(nb - b, GB));
 
-    // X's blocks: codes with a pitch of 16 bytes more than a row, so that 16
-    // rows' pieces lie in different banks, and then the scale bytes
+    // Codes: X's pieces in memory.  Else its values in LDS, with a pitch of 16
+    // bytes more than a row, so that 16 rows' pieces lie in different banks.
     const char *x[MT], *xs[MT];
     if (CODES) {
 #pragma unroll
@@ -752,9 +768,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
         }
     } else {
         constexpr int ES = SRC == kElemF32 ? 4 : 2;
-        const int rows = static_cast<int>(p.rows), units = rows * nb;
-        const int pitch = nb * 128 + 16, spitch = (nb + 3) / 4 * 4;
-        char *const scales = made + rows * pitch;
+        const int rows = static_cast<int>(p.rows), units = rows * nb, pitch = nb * 256 + 16;
         for (int u0 = 0; u0 < units; u0 += kSkinnyWaves * 4) {
             const int u = u0 + (t >> 4), row = u / nb, blk = u % nb, c = blk * 128 + (t & 15) * 8;
             const int left = u < units ? static_cast<int>(min(p.sum - c, static_cast<int64_t>(8))) : 0;
@@ -763,39 +777,24 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
                                            p.aligned != 0, v);
             uint32_t scale;
             const u32x2 codes = encode8(v, &scale);
-            if (u < units) {
-                *reinterpret_cast<u32x2 *>(made + row * pitch + c) = codes;
-                if ((t & 15) == 0) scales[row * spitch + blk] = static_cast<char>(scale);
-            }
+            if (u < units)
+                *reinterpret_cast<bf16x8 *>(made + row * pitch + c * 2) =
+                    widen8(codes.x, codes.y, __uint_as_float(scale << 23));
         }
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MT; m++) {
-            const int row = min(m * 16 + r16, rows - 1);
-            x[m] = made + row * pitch + g * 16;
-            xs[m] = scales + row * spitch;
-        }
+        for (int m = 0; m < MT; m++)
+            x[m] = made + min(m * 16 + r16, rows - 1) * pitch + g * 32;
     }
 
     f32x4 acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; m++) acc[m] = f32x4{0, 0, 0, 0};
-    auto widen = [](u32x4 c, int h, float s) {
-        union {
-            bf16x2 p[4];
-            bf16x8 v;
-        } u;
-        u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h], s, false);
-        u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h], s, true);
-        u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h + 1], s, false);
-        u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * h + 1], s, true);
-        return u.v;
-    };
-    // Blocks b .. b + n - 1, n = 4 with FULL.
+    // Blocks b .. b + n - 1, n = GB with FULL.
     auto group = [&](auto full, int n) {
         constexpr bool FULL = decltype(full)::value;
         uint32_t xsc[MT];
-        u32x4 xv[XQ][2][MT];
+        u32x4 xv[XQ][2][MT];             // codes
         auto load_x = [&](int q) {
 #pragma unroll
             for (int h = 0; h < 2; h++)
@@ -804,40 +803,47 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
                     xv[q % XQ][h][m] =
                         *reinterpret_cast<const u32x4 *>(x[m] + (b + q) * 128 + h * 64);
         };
+        if (CODES) {
 #pragma unroll
-        for (int m = 0; m < MT; m++) xsc[m] = *reinterpret_cast<const uint32_t *>(xs[m] + b);
-        if (XQ == 4) {
+            for (int m = 0; m < MT; m++) xsc[m] = *reinterpret_cast<const uint32_t *>(xs[m] + b);
+        }
+        if (XQ == GB) {
 #pragma unroll
-            for (int q = 0; q < 4; q++)
+            for (int q = 0; q < GB; q++)
                 if (FULL || q < n) load_x(q);
         }
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
+        for (int q = 0; q < GB; q++) {
             if (!FULL && q >= n) break;
-            if (XQ < 4) load_x(q);
+            if (CODES && XQ < GB) load_x(q);
             const float sw = __uint_as_float((wsc >> (8 * q) & 0xffu) << 23);
 #pragma unroll
             for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const bf16x8 wf = widen(wv[q][h], e, sw);
+                    const bf16x8 wf = widen8(wv[q][h][2 * e], wv[q][h][2 * e + 1], sw);
 #pragma unroll
                     for (int m = 0; m < MT; m++) {
-                        const float sx = __uint_as_float((xsc[m] >> (8 * q) & 0xffu) << 23);
-                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wf, widen(xv[q % XQ][h][m], e, sx), acc[m], 0, 0, 0);
+                        bf16x8 xf;
+                        if (CODES)
+                            xf = widen8(xv[q % XQ][h][m][2 * e], xv[q % XQ][h][m][2 * e + 1],
+                                        __uint_as_float((xsc[m] >> (8 * q) & 0xffu) << 23));
+                        else
+                            xf = *reinterpret_cast<const bf16x8 *>(x[m] + (b + q) * 256 + h * 128 +
+                                                                   e * 16);
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[m], 0, 0, 0);
                     }
                 }
         }
     };
-    for (; b < nb; b += kSkinnyWaves * 4) {
-        const int n = min(nb - b, 4);
-        if (n == 4)
-            group(std::true_type{}, 4);
+    for (; b < nb; b += kSkinnyWaves * GB) {
+        const int n = min(nb - b, GB);
+        if (n == GB)
+            group(std::true_type{}, GB);
         else
             group(std::false_type{}, n);
-        const int next = b + kSkinnyWaves * 4;
-        if (next < nb) load_w(next, min(nb - next, 4));
+        const int next = b + kSkinnyWaves * GB;
+        if (next < nb) load_w(next, min(nb - next, GB));
     }
 #pragma unroll
     for (int m = 0; m < MT; m++) part[wave][m][lane] = acc[m];
@@ -976,8 +982,7 @@ tide_status run_linear(const LinearArgs &a, void *stream) {
     p.out_bf16 = oflags != 0;
     p.aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.K % 8 == 0;
     const dim3 g(static_cast<unsigned>((a.N + 15) / 16)), b(kSkinnyWaves * 64);
-    const unsigned lds =
-        static_cast<unsigned>(a.M * (block_cols(a.K) + 16 + block_scale_cols(a.K)));
+    const unsigned lds = static_cast<unsigned>(a.M * (2 * block_cols(a.K) + 16));
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (in) {
         case kElemBf16: skinny_kernel<1, kElemBf16><<<g, b, lds, s>>>(p); break;

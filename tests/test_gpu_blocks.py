@@ -414,7 +414,7 @@ def test_on_two_streams_at_once():
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 72, 4096), (1, 33, 28672), (3, 200, 1111),
-                                   (16, 130, 2048), (16, 16, 2049), (17, 64, 700), (8, 100, 4097),
+                                   (16, 130, 2048), (16, 16, 2049), (17, 64, 700), (8, 100, 4097), (17, 40, 128), (64, 40, 100),
                                    (130, 200, 392), (600, 512, 1000)])
 def test_linear_in_one_call(shape, dtype):
     """tide_block_linear equals tide_block_quant and tide_block_mm, bit for bit,
