@@ -22,16 +22,24 @@ buffer and places it with tide_ag.  The optimizer updates `master` from
 this is one GPU's emulation of the data-parallel group; across GPUs each
 rank would hold only its rows and its peers' blocks would arrive over the
 network.
+
+With `blocks`, the matrices named there are gathered in 8-bit blocks instead:
+all_gather() casts their master shards into 8-bit rank blocks and places those,
+half the bytes of a bf16 gather, and params holds them as Blocks, which
+linear() multiplies by without ever making them bf16.  Its backward pass reads
+an 8-bit checkpoint of the layer's input and writes the weight gradient that
+reduce_scatter() takes.
 """
 import contextlib
 
 import torch
 
-from . import Plan, ag, grad_table, pack, rs
+from . import BlockPlan, Plan, ag, block_linear, block_shard, grad_table, pack, rs
 
 
 class TideUnit:
-    def __init__(self, shapes, world, device="cuda", align=1, param_dtype=torch.bfloat16):
+    def __init__(self, shapes, world, device="cuda", align=1, param_dtype=torch.bfloat16,
+                 blocks=()):
         self.plan = Plan(shapes, world, align)
         N, S = world, self.plan.S
         self.shapes = [tuple(s) for s in shapes]
@@ -39,8 +47,24 @@ class TideUnit:
         self.param_dtype = param_dtype
         self.master = torch.zeros(N, S, dtype=torch.float32, device=device)
         self.grad = torch.zeros(N, S, dtype=torch.float32, device=device)
+        self.blocks = [int(i) for i in blocks]
+        # the parameters gathered in param_dtype, and their plan
+        self.rest = [i for i in range(len(self.shapes)) if i not in self.blocks]
+        self.rest_plan = self.plan
+        if self.blocks:
+            self.block_plan = BlockPlan(self.plan, self.blocks)
+            self.block_gathered = self.block_plan.empty(device)
+            weights = self.block_plan.blocks(device)
+            self.block_views = self.block_plan.views(weights)
+            self.rest_plan = Plan([self.shapes[i] for i in self.rest], N, align) \
+                if self.rest else None
+        S = self.rest_plan.S if self.rest_plan is not None else 0
         self.gathered = torch.zeros(N * S, dtype=param_dtype, device=device)
-        self.params = [torch.empty(s, dtype=param_dtype, device=device) for s in self.shapes]
+        self.params = [None] * len(self.shapes)
+        for i in self.rest:
+            self.params[i] = torch.empty(self.shapes[i], dtype=param_dtype, device=device)
+        for j, i in enumerate(self.blocks):
+            self.params[i] = weights[j]
 
     def load(self, full):
         """Shard full fp32 tensors into the master rows (tide_pack of 4-byte
@@ -58,9 +82,37 @@ class TideUnit:
             rs(self.plan, R, table, self.grad[R], small=small, avg=avg, stream=stream)
 
     def all_gather(self, small=False, copy_engine=False, stream=None):
-        """Master shards -> param dtype into the gathered buffer -> params."""
+        """Master shards -> param dtype into the gathered buffer -> params, and
+        for the matrices of `blocks` 8-bit rank blocks -> Blocks."""
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            self.gathered.view(self.world, self.plan.S).copy_(self.master)
-        ag(self.plan, self.gathered, self.params, small=small, copy_engine=copy_engine,
-           stream=stream)
+            if not self.blocks:
+                self.gathered.view(self.world, self.plan.S).copy_(self.master)
+            else:
+                for r in range(self.world):
+                    block_shard(self.block_plan, r, self.master[r], self.block_gathered[r])
+                self._copy_rest()
+        if self.blocks:
+            ag(self.block_plan, self.block_gathered, self.block_views, small=small,
+               copy_engine=copy_engine, stream=stream)
+        if self.rest:
+            ag(self.rest_plan, self.gathered, [self.params[i] for i in self.rest], small=small,
+               copy_engine=copy_engine, stream=stream)
 
+    def _copy_rest(self):
+        """The master shards of the parameters outside `blocks`, cast, each at its
+        place in the rank blocks of the rest's plan."""
+        if not self.rest:
+            return
+        out = self.gathered.view(self.world, self.rest_plan.S)
+        for j, i in enumerate(self.rest):
+            src, _, seg = self.plan.param(i)
+            dst, _, _ = self.rest_plan.param(j)
+            out[:, dst:dst + seg].copy_(self.master[:, src:src + seg])
+
+    def linear(self, i, x, grad=None, accumulate=False, dtype=None):
+        """x [..., k] times parameter i (one of `blocks`, [n, k]) -> [..., n]: see
+        block_linear.  grad: where the backward pass writes the weight gradient
+        ([n, k], bf16 or fp32), e.g. the tensor that reduce_scatter() will read."""
+        if i not in self.blocks:
+            raise ValueError(f"parameter {i} is not gathered in blocks")
+        return block_linear(x, self.params[i], dtype=dtype, grad=grad, accumulate=accumulate)

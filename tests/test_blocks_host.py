@@ -407,3 +407,18 @@ def test_binding_refuses_wrong_gather_buffers():
         bp.views([stub_blocks(4, 200)])
     with pytest.raises(ValueError):
         bp.views([stub_blocks(4, 200), stub_blocks(8, 9)])
+
+
+def test_custom_ops_declare_what_they_write():
+    import parameter_layout_collectives_amd.torch_ops  # noqa: F401 - registers the ops
+    for name, written in [("block_shard", ["Tensor(a3!) block"]),
+                          ("block_unshard", ["Tensor(a2!)[] params"]),
+                          ("block_quant", ["Tensor(a1!) codes", "Tensor(a2!) scales"]),
+                          ("block_dequant", ["Tensor(a2!) out"]),
+                          ("block_mm", ["Tensor(a5!) out"]),
+                          ("block_mm_dx", ["Tensor(a3!) out"]),
+                          ("block_mm_dw", ["Tensor(a3!) out"])]:
+        schema = str(getattr(torch.ops.tide, name).default._schema)
+        for w in written:
+            assert w in schema, (name, schema)
+        assert schema.count("!") == len(written), (name, schema)

@@ -562,3 +562,115 @@ def test_captured_linear(m):
         for i, x in enumerate(xs):
             for got, want in zip(outs[i], step(x)):
                 assert torch.equal(got, want)
+
+
+def test_custom_ops():
+    import parameter_layout_collectives_amd.torch_ops as tops
+    note("block custom ops")
+    ops = torch.ops.tide
+    m, n, k = 70, 48, 200
+    x, wr, dy = rand((m, k), 60), rand((n, k), 61, FP, 0.02), rand((m, n), 62, BF, 1e-3)
+    q, w = tide.Blocks.empty(m, k), tide.Blocks.empty(n, k)
+    ops.block_quant(x, q.codes, q.scales)
+    ops.block_quant(wr, w.codes, w.scales)
+    y, dx = torch.empty(m, n, dtype=BF, device="cuda"), torch.empty(m, k, dtype=BF, device="cuda")
+    dw, back = torch.zeros(n, k, device="cuda"), torch.empty(m, k, dtype=BF, device="cuda")
+    ops.block_mm(q.codes, q.scales, w.codes, w.scales, k, y)
+    ops.block_mm_dx(dy, w.codes, w.scales, dx)
+    ops.block_mm_dw(dy, q.codes, q.scales, dw)
+    ops.block_mm_dw(dy, q.codes, q.scales, dw, True)
+    ops.block_dequant(q.codes, q.scales, back)
+    once = tide.block_mm_dw(dy, q, dtype=FP)
+    assert torch.equal(y, tide.block_mm(q, w)) and torch.equal(dx, tide.block_mm_dx(dy, w))
+    assert torch.equal(dw, once + once) and torch.equal(back, tide.block_dequant(q))
+    plan, full, master = shards([(9, 130), (4, 4)], 2, 63)
+    pid = tops.register_plan(tide.BlockPlan(plan))
+    try:
+        bp = tops._PLANS[pid]
+        gathered = bp.empty()
+        for r in range(2):
+            ops.block_shard(pid, r, master[r], gathered[r])
+        params = [torch.empty(s, dtype=BF, device="cuda") for s in bp.matrices]
+        ops.block_unshard(pid, gathered, params)
+        for p, f in zip(params, full):
+            assert torch.equal(p, tide.block_dequant(tide.block_quant(f)))
+    finally:
+        tops.unregister_plan(pid)
+
+
+UNIT = [(96, 200), (200,), (200, 96), (40, 200)]
+
+
+def unit_with_weights(world, blocks, seed=70):
+    from parameter_layout_collectives_amd.fsdp import TideUnit
+    full = [rand((1, s[0]) if len(s) == 1 else s, seed + i, FP, 0.05).view(s)
+            for i, s in enumerate(UNIT)]
+    unit = TideUnit(UNIT, world, blocks=blocks)
+    unit.load(full)
+    return unit, full
+
+
+@pytest.mark.parametrize("world", [1, 3, 8])
+@pytest.mark.parametrize("kw", [{}, {"small": True}, {"copy_engine": True}])
+def test_unit_gathers_matrices_in_blocks(world, kw):
+    note(f"TideUnit blocks world={world} {kw}")
+    unit, full = unit_with_weights(world, [0, 2])
+    unit.all_gather(**kw)
+    torch.cuda.synchronize()
+    for i, f in enumerate(full):
+        if i in (0, 2):
+            want = ref.quant(f)
+            got = bytes_of(unit.params[i])
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        else:
+            assert torch.equal(unit.params[i], f.to(BF))
+    every, _ = unit_with_weights(world, range(4))          # the vector as a column too
+    assert torch.equal(tide.block_dequant(every.params[1], dtype=FP).view(-1),
+                       tide.block_dequant(tide.block_quant(full[1].view(-1, 1)), dtype=FP).view(-1))
+    with pytest.raises(ValueError):
+        unit.linear(3, torch.empty(1, 200, device="cuda"))
+
+
+def test_unit_trains_through_blocks():
+    """A step of a two-layer unit as it would be used: gather in blocks on a side
+    stream, forward and backward of every rank's micro-batch through linear(),
+    reduce-scatter of the gradients, an update of the master shards, gather.
+    Gradients are the formula's at the gathered weights, and the update is what
+    the next gather holds."""
+    note("TideUnit blocks training step")
+    N, m = 4, 33
+    unit, full = unit_with_weights(N, [0, 2])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    unit.all_gather(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    w0, w2 = unit.params[0], unit.params[2]
+    grads, want = [], []
+    for r in range(N):
+        g = [torch.zeros(s, device="cuda") for s in UNIT]
+        x = rand((m, 200), 80 + r, BF, 0.5).requires_grad_()
+        h = unit.linear(0, x, grad=g[0])
+        a = torch.relu(h)
+        y = unit.linear(2, a, grad=g[2], dtype=FP)
+        dy = rand((m, 200), 90 + r, BF, 1e-2).float()
+        y.backward(dy)
+        grads.append(g)
+        aq = tide.block_quant(a.detach())
+        da = tide.block_mm_dx(dy.to(BF), w2)
+        dh = da * (h.detach() > 0)
+        assert torch.equal(x.grad, tide.block_mm_dx(dh, w0))
+        want.append((tide.block_mm_dw(dh, tide.block_quant(x.detach()), dtype=FP),
+                     tide.block_mm_dw(dy.to(BF), aq, dtype=FP)))
+    for g, (d0, d2) in zip(grads, want):
+        assert torch.equal(g[0], d0) and torch.equal(g[2], d2)
+    unit.reduce_scatter(grads)
+    unit.master -= 0.1 * unit.grad
+    unit.all_gather()
+    for i, k in ((0, 0), (2, 1)):
+        total = want[0][k]
+        for r in range(1, N):
+            total = total + want[r][k]
+        new = full[i] - 0.1 * (total / N)
+        q = tide.block_quant(new)
+        assert torch.equal(bytes_of(unit.params[i])[0], bytes_of(q)[0])
+        assert torch.equal(bytes_of(unit.params[i])[1], bytes_of(q)[1])
