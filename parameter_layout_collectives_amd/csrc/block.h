@@ -55,7 +55,7 @@ constexpr int64_t kMaxSplits = 16;
 enum MmKernel { kMmEight, kMmWide, kMmSkinny };
 struct MmChoice {
     MmKernel kernel;
-    int tile;            // 256 or 128 rows and columns of the output per workgroup
+    int tile;            // 256, 128 or 64 rows and columns of the output per workgroup
     int splits;          // pieces of the sum (1: no workspace)
     int64_t chunk;       // steps of the sum in one piece
     int64_t workspace;   // bytes

@@ -256,7 +256,11 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     const int64_t step = eight ? 128 : 64;
     const int64_t steps = (sum + step - 1) / step;
     auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };
-    c.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256 : 128;
+    // Large tiles once they fill three quarters of the card, small ones (not in
+    // the 8-bit kernel) while middle ones would leave half of it idle.
+    c.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256
+             : !eight && tiles(128) < kCus / 2     ? 64
+                                                   : 128;
     c.splits = 1;
     c.chunk = steps;
     c.workspace = 0;

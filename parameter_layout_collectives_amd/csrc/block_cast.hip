@@ -203,18 +203,17 @@ struct UnshardArgs {
 };
 static_assert(sizeof(Rows) == 32 && sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
 
-// The matrix that workgroup `wg` works on: the last one with wg0 <= wg.
+// The matrix that workgroup `wg` works on: the last one with wg0 <= wg.  Every
+// lane compares two of them: one load's latency, where a search would have
+// seven in a row.
 template <class A>
 __device__ __forceinline__ int matrix_of(const A &a, uint32_t wg) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.m[mid].wg0 <= wg)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
+    static_assert(kPerLaunch <= 128, "two matrices per lane");
+    const int lane = threadIdx.x & 63;
+    const int i = min(lane, a.n - 1), j = min(lane + 64, a.n - 1);
+    const bool first = lane < a.n && a.m[i].wg0 <= wg;
+    const bool second = lane + 64 < a.n && a.m[j].wg0 <= wg;
+    return __builtin_amdgcn_readfirstlane(__popcll(__ballot(first)) + __popcll(__ballot(second)) - 1);
 }
 
 __global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *__restrict__ master,

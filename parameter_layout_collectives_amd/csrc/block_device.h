@@ -61,29 +61,47 @@ __device__ __forceinline__ uint32_t max16(uint32_t u) {
     return u;
 }
 
+// The block exponent of a largest finite magnitude, given as its pattern:
+// a = m * 2^k with 1 <= m < 2 is at most 448 * 2^e = 1.75 * 2^(8+e) from e = k - 8
+// on if m <= 1.75, else from k - 7 on.
+__device__ __forceinline__ int exponent_of(uint32_t top) {
+    const int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return top == 0 ? 0 : min(119, max(-117, e));
+}
+
 // One lane's 8 values -> 8 codes; the block's scale byte is the same in all
 // 16 lanes.  Patterns of |x| order like the values, so the maximum is taken on
-// them as integers.
+// them as integers.  A block with an infinity or a NaN, or with a value that has
+// to be cut at 448 * 2^119, shows as a maximum above that number's pattern and
+// takes the long way.
 __device__ __forceinline__ u32x2 encode8(const float *v, uint32_t *scale) {
     uint32_t top = 0;
-    bool odd = false;                     // an inf or a NaN among the 8
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-        const bool finite = u < 0x7f800000u;
-        odd |= !finite;
-        top = max(top, finite ? u : 0u);
-    }
+    for (int i = 0; i < 8; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
     top = max16(top);
-    // a = m * 2^k with 1 <= m < 2: a <= 448 * 2^e = 1.75 * 2^(8+e) from
-    // e = k - 8 on if m <= 1.75, else from k - 7 on
-    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = top == 0 ? 0 : min(119, max(-117, e));
-    *scale = static_cast<uint32_t>(e + 127);
-    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     float y[8];
+    bool odd = false;                     // an inf or a NaN among this lane's 8
+    int e;
+    if (top <= 0x7f600000u) {
+        e = exponent_of(top);
+        const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(v[i] * s, -448.0f, 448.0f);
+        for (int i = 0; i < 8; i++) y[i] = v[i] * s;
+    } else {                              // the same for all 16 lanes
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+            const bool finite = u < 0x7f800000u;
+            odd |= !finite;
+            top = max(top, finite ? u : 0u);
+        }
+        e = exponent_of(max16(top));
+        const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(v[i] * s, -448.0f, 448.0f);
+    }
+    *scale = static_cast<uint32_t>(e + 127);
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);

@@ -102,21 +102,39 @@ __device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t c
     }
 }
 
-// Adds the splits' sums in split order.
+// Adds the splits' sums in split order.  vec: n and the output's alignment allow
+// 4 values at a time.
 __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ partial, int splits,
                                                    int64_t n, char *__restrict__ out, int out_bf16,
-                                                   int accumulate) {
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
-         i += static_cast<int64_t>(gridDim.x) * 1024) {
-        const int m = static_cast<int>(min(n - i, static_cast<int64_t>(4)));
-        for (int e = 0; e < m; e++) {
-            float s = partial[i + e];
-            for (int q = 1; q < splits; q++) s += partial[q * n + i + e];
+                                                   int accumulate, int vec) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 1024;
+    for (int64_t k = i; k < n; k += step) {
+        if (vec) {
+            f32x4 s = *reinterpret_cast<const f32x4 *>(partial + k);
+#pragma unroll 4
+            for (int q = 1; q < splits; q++)
+                s += *reinterpret_cast<const f32x4 *>(partial + q * n + k);
             if (out_bf16) {
-                __bf16 *o = reinterpret_cast<__bf16 *>(out) + i + e;
+                bf16x4 *o = reinterpret_cast<bf16x4 *>(reinterpret_cast<__bf16 *>(out) + k);
+                if (accumulate) s += __builtin_convertvector(*o, f32x4);
+                *reinterpret_cast<u32x2 *>(o) = u32x2{pack2(s[0], s[1]), pack2(s[2], s[3])};
+            } else {
+                f32x4 *o = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(out) + k);
+                if (accumulate) s += *o;
+                *o = s;
+            }
+            continue;
+        }
+        const int m = static_cast<int>(min(n - k, static_cast<int64_t>(4)));
+        for (int e = 0; e < m; e++) {
+            float s = partial[k + e];
+            for (int q = 1; q < splits; q++) s += partial[q * n + k + e];
+            if (out_bf16) {
+                __bf16 *o = reinterpret_cast<__bf16 *>(out) + k + e;
                 *o = static_cast<__bf16>(accumulate ? static_cast<float>(*o) + s : s);
             } else {
-                float *o = reinterpret_cast<float *>(out) + i + e;
+                float *o = reinterpret_cast<float *>(out) + k + e;
                 *o = accumulate ? *o + s : s;
             }
         }
@@ -355,8 +373,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
 //   across  (sum index is the memory row): 64 rows of T bf16; a wave's 16 lanes
 //           read 4 rows x 32 bytes with the transposing read, which hands each
 //           lane 4 values along the sum.  The 32-byte piece h of row c lies at
-//           h ^ ((c & 3) | (c >> 1 & 4)), so the rows of a read fall into
-//           different banks.
+//           h ^ ((c & 3) | (c >> 1 & 4)), or h ^ (c & 3) for T = 64, so the rows of
+//           a read fall into different banks.
 enum Mode { kBf16Along, kBf16Across, kCodesAlong, kCodesAcross };
 
 __host__ __device__ constexpr bool is_across(Mode m) {
@@ -366,7 +384,10 @@ __host__ __device__ constexpr bool is_codes(Mode m) {
     return m == kCodesAlong || m == kCodesAcross;
 }
 
-__device__ __forceinline__ int swz_across(int c) { return (c & 3) | ((c >> 1) & 4); }
+template <int T>
+__device__ __forceinline__ int swz_across(int c) {
+    return T == 64 ? c & 3 : (c & 3) | ((c >> 1) & 4);
+}
 
 // 16 bytes per lane from r + at + off straight into LDS, from `to` on.  The
 // builtin for it would make the compiler wait for the load before the next
@@ -500,7 +521,7 @@ struct Stage {
 
     static __device__ __forceinline__ int lds_at(int r, int chunk) {   // 16-byte chunk of row r
         if (is_across(M))
-            return r * T * 2 + ((((chunk >> 1) ^ swz_across(r)) << 1 | (chunk & 1)) << 4);
+            return r * T * 2 + ((((chunk >> 1) ^ swz_across<T>(r)) << 1 | (chunk & 1)) << 4);
         return r * 128 + ((chunk ^ (r & 7)) << 4);
     }
 
@@ -543,7 +564,7 @@ struct Stage {
             i16x4 h[2];
             bf16x8 v;
         } u;
-        const int c = g * 8 + (r16 >> 2);        // swz_across is the same for all kk and h
+        const int c = g * 8 + (r16 >> 2);        // the swizzle is the same for all kk and h
         const LDS_AS char *p = lds + lds_at(c, at / 8 + ((r16 & 3) >> 1)) + (r16 & 1) * 8;
 #pragma unroll
         for (int h = 0; h < 2; h++)
@@ -563,7 +584,7 @@ template <Mode MI, Mode MJ, int T, int WI, int WJ, bool ALIGNED>
 struct Wide {
     static constexpr int NT = WI * WJ * 64;
     static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
-    static constexpr int RING = 4, D = RING - 1, LINES = 2 * FI;
+    static constexpr int LINES = 2 * FI, RING = FI >= 4 ? 4 : 2, D = RING - 1;
     static constexpr int TILE = T * 128;                   // bytes of one operand's tile
     typedef Stage<MI, T, NT, ALIGNED> SI;
     typedef Stage<MJ, T, NT, true> SJ;
@@ -859,12 +880,17 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(MmLaunch p) {
 
 template <Mode MI, Mode MJ>
 void launch_wide(const MmLaunch &p, int tile, dim3 grid, hipStream_t s) {
+    constexpr bool any = is_codes(MI);       // no bf16 operand to be aligned
     if (tile == 256)
         wide_kernel<MI, MJ, 256, 2, 4, true><<<grid, dim3(512), 0, s>>>(p);
-    else if (is_codes(MI) || p.aligned)
+    else if (tile == 128 && (any || p.aligned))
         wide_kernel<MI, MJ, 128, 2, 2, true><<<grid, dim3(256), 0, s>>>(p);
+    else if (tile == 128)
+        wide_kernel<MI, MJ, 128, 2, 2, any><<<grid, dim3(256), 0, s>>>(p);
+    else if (any || p.aligned)
+        wide_kernel<MI, MJ, 64, 2, 2, true><<<grid, dim3(256), 0, s>>>(p);
     else
-        wide_kernel<MI, MJ, 128, 2, 2, is_codes(MI)><<<grid, dim3(256), 0, s>>>(p);
+        wide_kernel<MI, MJ, 64, 2, 2, any><<<grid, dim3(256), 0, s>>>(p);
 }
 
 tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
@@ -935,8 +961,10 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
     }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && c.splits > 1) {
+        const int vec =
+            n % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (p.out_bf16 ? 8 : 16) == 0;
         join_kernel<<<dim3(flat), dim3(256), 0, s>>>(p.partial, c.splits, n, p.out, p.out_bf16,
-                                                     p.accumulate);
+                                                     p.accumulate, vec);
         e = hipGetLastError();
     }
     if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
