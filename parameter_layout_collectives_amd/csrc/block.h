@@ -51,14 +51,15 @@ constexpr int64_t kInOneBytes = 8192;
 constexpr int64_t kMinSplitSteps = 4;
 constexpr int64_t kMaxSplits = 16;
 
-// How a product runs: the kernel, and into how many pieces its sum is cut.
+// How a product runs: the kernel, its tile, and which tiles' sums are cut.
 enum MmKernel { kMmEight, kMmWide, kMmSkinny };
 struct MmChoice {
     MmKernel kernel;
     int tile;            // 256, 128 or 64 rows and columns of the output per workgroup
-    int splits;          // pieces of the sum (1: no workspace)
-    int64_t chunk;       // steps of the sum in one piece
-    int64_t workspace;   // bytes
+    int64_t direct;      // tiles that one workgroup computes; the others are cut
+    int splits;          // into so many pieces each,
+    int64_t chunk;       // of so many steps
+    int64_t workspace;   // bytes for the pieces' sums
 };
 // aligned: dY's rows can be loaded in 16-byte pieces.
 MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,

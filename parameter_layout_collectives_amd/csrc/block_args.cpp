@@ -261,18 +261,29 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     c.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256
              : !eight && tiles(128) < kCus / 2     ? 64
                                                    : 128;
+    const int64_t t = tiles(c.tile);
+    c.direct = t;
     c.splits = 1;
     c.chunk = steps;
     c.workspace = 0;
     if (c.kernel == kMmSkinny || !may_split) return c;
-    const int64_t t = tiles(c.tile), full = kCus * (c.tile == 256 ? 1 : 2);
-    if (t * 2 <= full && steps >= 2 * kMinSplitSteps) {
-        int64_t s = std::min(full / t, steps / kMinSplitSteps);
-        s = std::min<int64_t>(s, kMaxSplits);
-        c.chunk = ((steps + s - 1) / s + 3) / 4 * 4;   // scale bytes are read in fours
-        c.splits = static_cast<int>((steps + c.chunk - 1) / c.chunk);
-        if (c.splits > 1) c.workspace = rows * cols * 4 * c.splits;
+    // The tiles that run at one time; what is left after whole rounds of them is
+    // cut if that leaves at least half of the card idle.  The pieces' sums go
+    // through memory, so a piece has at least kMinSplitSteps steps, and behind
+    // whole rounds (where a round is long) at least four times that.
+    const int64_t full = kCus * (c.tile == 256 ? 1 : 2);
+    const int64_t left = t % full, least = t < full ? kMinSplitSteps : 4 * kMinSplitSteps;
+    if (left == 0 || left * 2 > full || steps < 2 * least) return c;
+    const int64_t s = std::min({full / left, steps / least, kMaxSplits});
+    c.chunk = ((steps + s - 1) / s + 3) / 4 * 4;       // scale bytes are read in fours
+    const int64_t pieces = (steps + c.chunk - 1) / c.chunk;
+    if (pieces < 2) {
+        c.chunk = steps;
+        return c;
     }
+    c.splits = static_cast<int>(pieces);
+    c.direct = t - left;
+    c.workspace = left * pieces * c.tile * c.tile * 4;
     return c;
 }
 

@@ -30,12 +30,14 @@ struct MmLaunch {
     const char *a, *as;          // I: X's codes and scales, or dY
     const char *b, *bs;          // J: codes and scales
     char *out;
-    float *partial;              // splits x [rows, cols] sums, or null
+    float *partial;              // pieces' sums, T x T each
     int64_t rows, cols, sum;     // of the output, and the length of the sum
     int64_t a_pitch, as_pitch;   // bytes between rows
     int64_t b_pitch, bs_pitch;
-    int64_t chunk;               // steps of the sum per split
-    int tr, tc;                  // tiles along rows and columns
+    int64_t chunk;               // steps of the sum in one piece of a cut tile
+    int splits;                  // pieces of a cut tile
+    uint32_t direct;             // tiles that are not cut: the first ones
+    uint32_t tr, tc;             // tiles along rows and columns
     int out_bf16, accumulate, aligned;
 };
 
@@ -45,38 +47,50 @@ __device__ __forceinline__ uint32_t uniform(int64_t v) {
     return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
 }
 
-// Workgroup `id` of tr x tc tiles -> its tile.  IDs go to the 8 XCDs in turn
-// and each XCD has its own L2: every XCD takes one contiguous run of tiles, and
-// within it 8 tile rows advance together, so that the tiles an XCD works on at
-// one time share their operands' rows.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tr, uint32_t tc, uint32_t *r,
-                                        uint32_t *c) {
-    const uint32_t n = tr * tc, q = n / 8, rm = n % 8, x = id % 8;
-    const uint32_t v = x * q + min(x, rm) + id / 8;
-    const uint32_t per = 8 * tc, g = v / per, in = v - g * per;
-    const uint32_t h = min(8u, tr - 8 * g);
-    *r = uniform(8 * g + in % h);
-    *c = uniform(in / h);
+// What a workgroup computes: a tile of the output and a piece of its sum.
+struct Work {
+    uint32_t r, c;               // tile
+    int64_t s0, s1;              // steps of the sum
+    float *part;                 // where a piece's T x T sums go, or null for a whole tile
+};
+
+// Tiles are numbered so that 8 tile rows advance together.  The first `direct`
+// are whole; workgroup IDs go to the 8 XCDs in turn and each XCD has its own L2,
+// so every XCD takes one contiguous run of them, and the tiles it works on at
+// one time share their operands' rows.  The others' pieces follow.
+template <int T>
+__device__ __forceinline__ Work work_of(const MmLaunch &p, int64_t steps) {
+    const uint32_t id = blockIdx.x;
+    Work w;
+    uint32_t v;
+    if (id < p.direct) {
+        const uint32_t q = p.direct / 8, rm = p.direct % 8, x = id % 8;
+        v = x * q + min(x, rm) + id / 8;
+        w.s0 = 0;
+        w.s1 = steps;
+        w.part = nullptr;
+    } else {
+        const uint32_t k = id - p.direct, piece = uniform(k % p.splits);
+        v = p.direct + k / p.splits;
+        w.s0 = piece * p.chunk;
+        w.s1 = min(w.s0 + p.chunk, steps);
+        w.part = p.partial + static_cast<int64_t>(k) * T * T;
+    }
+    const uint32_t per = 8 * p.tc, g = v / per, in = v - g * per, h = min(8u, p.tr - 8 * g);
+    w.r = uniform(8 * g + in % h);
+    w.c = uniform(in / h);
+    return w;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
-// Stores 4 neighbouring results of one output row (n of them exist).
+// Stores 4 neighbouring results of one output row, as many as exist.
 __device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t col, f32x4 v) {
     const int64_t left = p.cols - col;
     if (row >= p.rows || left <= 0) return;
     const int64_t at = row * p.cols + col;
-    if (p.partial) {
-        float *o = p.partial + at + static_cast<int64_t>(blockIdx.y) * p.rows * p.cols;
-        if (left >= 4 && (p.cols & 3) == 0)
-            *reinterpret_cast<f32x4 *>(o) = v;
-        else
-            for (int i = 0; i < 4; i++)
-                if (i < left) o[i] = v[i];
-        return;
-    }
     if (p.out_bf16) {
         __bf16 *o = reinterpret_cast<__bf16 *>(p.out) + at;
         if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
@@ -102,43 +116,42 @@ __device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t c
     }
 }
 
-// Adds the splits' sums in split order.  vec: n and the output's alignment allow
-// 4 values at a time.
-__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ partial, int splits,
-                                                   int64_t n, char *__restrict__ out, int out_bf16,
-                                                   int accumulate, int vec) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 1024;
-    for (int64_t k = i; k < n; k += step) {
-        if (vec) {
-            f32x4 s = *reinterpret_cast<const f32x4 *>(partial + k);
+// A wave's 16 x 16 fragments of a tile: this lane's line of the first at (i, j).
+template <int T, int FI, int FJ>
+__device__ __forceinline__ void store_tile(const MmLaunch &p, const Work &w, int i, int j,
+                                           const f32x4 (&acc)[FI][FJ]) {
+#pragma unroll
+    for (int x = 0; x < FI; x++)
+#pragma unroll
+        for (int y = 0; y < FJ; y++) {
+            const int li = i + x * 16, lj = j + y * 16;
+            const int64_t row = static_cast<int64_t>(w.r) * T + li;
+            const int64_t col = static_cast<int64_t>(w.c) * T + lj;
+            if (!w.part)
+                store4(p, row, col, acc[x][y]);
+            else if (row < p.rows && col < p.cols)
+                *reinterpret_cast<f32x4 *>(w.part + li * T + lj) = acc[x][y];
+        }
+}
+
+// The cut tiles: adds the pieces' sums in their order.  A workgroup takes 1024
+// values of a tile.
+template <int T>
+__global__ __launch_bounds__(256) void join_kernel(MmLaunch p) {
+    const uint32_t per_tile = T * T / 1024;
+    const uint32_t k = blockIdx.x / per_tile;
+    const uint32_t at = blockIdx.x % per_tile * 1024 + threadIdx.x * 4;
+    const uint32_t v = p.direct + k;
+    const uint32_t per = 8 * p.tc, g = v / per, in = v - g * per, h = min(8u, p.tr - 8 * g);
+    const int64_t row = static_cast<int64_t>(8 * g + in % h) * T + at / T;
+    const int64_t col = static_cast<int64_t>(in / h) * T + at % T;
+    if (row >= p.rows || col >= p.cols) return;
+    const float *s = p.partial + static_cast<int64_t>(k) * p.splits * T * T + at;
+    f32x4 sum = *reinterpret_cast<const f32x4 *>(s);
 #pragma unroll 4
-            for (int q = 1; q < splits; q++)
-                s += *reinterpret_cast<const f32x4 *>(partial + q * n + k);
-            if (out_bf16) {
-                bf16x4 *o = reinterpret_cast<bf16x4 *>(reinterpret_cast<__bf16 *>(out) + k);
-                if (accumulate) s += __builtin_convertvector(*o, f32x4);
-                *reinterpret_cast<u32x2 *>(o) = u32x2{pack2(s[0], s[1]), pack2(s[2], s[3])};
-            } else {
-                f32x4 *o = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(out) + k);
-                if (accumulate) s += *o;
-                *o = s;
-            }
-            continue;
-        }
-        const int m = static_cast<int>(min(n - k, static_cast<int64_t>(4)));
-        for (int e = 0; e < m; e++) {
-            float s = partial[k + e];
-            for (int q = 1; q < splits; q++) s += partial[q * n + k + e];
-            if (out_bf16) {
-                __bf16 *o = reinterpret_cast<__bf16 *>(out) + k + e;
-                *o = static_cast<__bf16>(accumulate ? static_cast<float>(*o) + s : s);
-            } else {
-                float *o = reinterpret_cast<float *>(out) + k + e;
-                *o = accumulate ? *o + s : s;
-            }
-        }
-    }
+    for (int q = 1; q < p.splits; q++)
+        sum += *reinterpret_cast<const f32x4 *>(s + static_cast<int64_t>(q) * T * T);
+    store4(p, row, col, sum);
 }
 
 // An empty sum: zeros.
@@ -315,12 +328,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
     __shared__ __attribute__((aligned(1024))) char lds[E::LDS];
     const int t = threadIdx.x, lane = t & 63;
     const int r16 = lane & 15, g = lane >> 4;
-    uint32_t tr, tc;
-    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
-    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
-    const uint32_t nb = static_cast<uint32_t>((p.sum + 127) / 128);
-    const uint32_t s0 = static_cast<uint32_t>(blockIdx.y * p.chunk);
-    const uint32_t s1 = min(s0 + static_cast<uint32_t>(p.chunk), nb);
+    const Work work = work_of<T>(p, (p.sum + 127) / 128);
+    const int64_t i0 = static_cast<int64_t>(work.r) * T, j0 = static_cast<int64_t>(work.c) * T;
+    const uint32_t s0 = uniform(work.s0), s1 = uniform(work.s1);
     const uint32_t ni = uniform(min(p.rows - i0, static_cast<int64_t>(T)));
     const uint32_t nj = uniform(min(p.cols - j0, static_cast<int64_t>(T)));
 
@@ -349,12 +359,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
     // (below 64 KB) reach both.
     LDS_AS char *const b = (LDS_AS char *)lds, *const w = b + 4 * E::TILE;
     e.run(b, b + E::TILE, b + 2 * E::TILE, b + 3 * E::TILE, w, w + E::WORDS, s0, s1);
-#pragma unroll
-    for (int x = 0; x < E::FI; x++)
-#pragma unroll
-        for (int y = 0; y < E::FJ; y++)
-            store4(p, i0 + wi * (T / WI) + x * 16 + r16, j0 + wj * (T / WJ) + y * 16 + g * 4,
-                   e.acc[x][y]);
+    store_tile<T>(p, work, wi * (T / WI) + r16, wj * (T / WJ) + g * 4, e.acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -681,11 +686,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
     typedef Wide<MI, MJ, T, WI, WJ, ALIGNED> K;
     __shared__ __attribute__((aligned(1024))) char lds[4 * K::TILE];
     const int t = threadIdx.x, lane = t & 63;
-    uint32_t tr, tc;
-    tile_of(blockIdx.x, p.tr, p.tc, &tr, &tc);
-    const int64_t i0 = static_cast<int64_t>(tr) * T, j0 = static_cast<int64_t>(tc) * T;
-    const int64_t steps = (p.sum + 63) / 64;
-    const int64_t s0 = blockIdx.y * p.chunk, s1 = min(s0 + p.chunk, steps);
+    const Work work = work_of<T>(p, (p.sum + 63) / 64);
+    const int64_t i0 = static_cast<int64_t>(work.r) * T, j0 = static_cast<int64_t>(work.c) * T;
+    const uint32_t s0 = uniform(work.s0), s1 = uniform(work.s1);
     // Codes exist up to the end of their last block.
     const int64_t whole = static_cast<int64_t>(127);
     const int64_t cols = MJ == kCodesAcross ? (p.cols + whole) & ~whole : p.cols;
@@ -697,8 +700,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
     k.lane = lane;
     k.wi = k.wave / WJ;
     k.wj = k.wave % WJ;
-    k.si.init(p.a, p.as, p.a_pitch, p.as_pitch, i0, p.rows, isum, uniform(s0), t);
-    k.sj.init(p.b, p.bs, p.b_pitch, p.bs_pitch, j0, cols, jsum, uniform(s0), t);
+    k.si.init(p.a, p.as, p.a_pitch, p.as_pitch, i0, p.rows, isum, s0, t);
+    k.sj.init(p.b, p.bs, p.b_pitch, p.bs_pitch, j0, cols, jsum, s0, t);
 #pragma unroll
     for (int x = 0; x < K::FI; x++)
 #pragma unroll
@@ -706,14 +709,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void wide_kernel(MmLaunch p) {
     // I's two buffers, then J's: one address and constant offsets (below 64 KB)
     // reach both buffers of an operand.
     LDS_AS char *const b = (LDS_AS char *)lds;
-    k.run(b, b + K::TILE, b + 2 * K::TILE, b + 3 * K::TILE, uniform(s1 - s0));
+    k.run(b, b + K::TILE, b + 2 * K::TILE, b + 3 * K::TILE, s1 - s0);
     const int r16 = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int x = 0; x < K::FI; x++)
-#pragma unroll
-        for (int y = 0; y < K::FJ; y++)
-            store4(p, i0 + k.wi * (T / WI) + x * 16 + r16, j0 + k.wj * (T / WJ) + y * 16 + g * 4,
-                   k.acc[x][y]);
+    store_tile<T>(p, work, k.wi * (T / WI) + r16, k.wj * (T / WJ) + g * 4, k.acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -932,13 +930,17 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
     p.b_pitch = block_cols(a.K);
     p.bs_pitch = block_scale_cols(a.K);
     p.chunk = c.chunk;
-    if (c.splits > 1) p.partial = static_cast<float *>(a.workspace);
+    p.splits = c.splits;
+    p.direct = static_cast<uint32_t>(c.direct);
+    p.partial = static_cast<float *>(a.workspace);
     const int64_t tr = (p.rows + c.tile - 1) / c.tile, tc = (p.cols + c.tile - 1) / c.tile;
-    if (tr * tc > 0xffffffffll / 512 || (p.cols + 15) / 16 > 0xffffffffll / 512)
+    const int64_t cut = (tr * tc - c.direct) * c.splits;
+    if (tr * tc > 0xffffffffll / 512 || cut * (c.tile * c.tile / 1024) > 0xffffffffll / 256 ||
+        (p.cols + 15) / 16 > 0xffffffffll / 512)
         return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
-    p.tr = static_cast<int>(tr);
-    p.tc = static_cast<int>(tc);
-    const dim3 grid(static_cast<unsigned>(tr * tc), static_cast<unsigned>(c.splits));
+    p.tr = static_cast<uint32_t>(tr);
+    p.tc = static_cast<uint32_t>(tc);
+    const dim3 grid(static_cast<unsigned>(c.direct + cut));
     if (c.kernel == kMmSkinny) {
         const dim3 g(static_cast<unsigned>((p.cols + 15) / 16)), b(kSkinnyWaves * 64);
         if (p.rows <= 16)
@@ -960,11 +962,14 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
         launch_wide<kBf16Across, kCodesAcross>(p, c.tile, grid, s);
     }
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && c.splits > 1) {
-        const int vec =
-            n % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (p.out_bf16 ? 8 : 16) == 0;
-        join_kernel<<<dim3(flat), dim3(256), 0, s>>>(p.partial, c.splits, n, p.out, p.out_bf16,
-                                                     p.accumulate, vec);
+    if (e == hipSuccess && cut && c.kernel != kMmSkinny) {
+        const dim3 g(static_cast<unsigned>((tr * tc - c.direct) * (c.tile * c.tile / 1024))), b(256);
+        if (c.tile == 256)
+            join_kernel<256><<<g, b, 0, s>>>(p);
+        else if (c.tile == 128)
+            join_kernel<128><<<g, b, 0, s>>>(p);
+        else
+            join_kernel<64><<<g, b, 0, s>>>(p);
         e = hipGetLastError();
     }
     if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);

@@ -194,8 +194,10 @@ def test_workspace():
         assert L.tide_block_workspace(op, 8192, 8192, 8192, 0) == 0    # enough tiles
         assert L.tide_block_workspace(op, 0, 0, 0, 0) == 0
     assert L.tide_block_workspace(0, 1, 4096, 4096, 0x20) == 0         # few rows: one kernel
-    size = L.tide_block_workspace(2, 8192, 256, 256, 0)                # a long sum, 4 tiles
-    assert size > 0 and size % (256 * 256 * 4) == 0
+    # a long sum for few tiles, and tiles left over after whole rounds
+    for op, m, n, k in ((2, 8192, 256, 256), (2, 8192, 14336, 4096)):
+        size = L.tide_block_workspace(op, m, n, k, 0)
+        assert size > 0 and size % (64 * 64 * 4) == 0
     assert L.tide_block_workspace(4, 1, 1, 1, 0) == -1
     assert L.tide_block_workspace(0, -1, 1, 1, 0) == -1
 

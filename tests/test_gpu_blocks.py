@@ -279,6 +279,24 @@ def test_products_over_large_tiles():
     check_products(4000, 4104, 3600)
 
 
+@pytest.mark.parametrize("shape", [(4400, 4200, 4250), (4200, 4400, 2200)])
+def test_products_of_tiles_left_over(shape):
+    """Whole rounds of tiles and some left over, whose sums are cut."""
+    check_products(*shape)
+
+
+def test_accumulate_over_tiles_left_over():
+    note("block_mm_dw accumulate, tiles left over")
+    m, n, k = 2100, 4400, 4200
+    x, _, dy = operands(m, n, k, 7)
+    old = rand((n, k), 8, FP, 1e-2)
+    out = old.clone()
+    tide.block_mm_dw(dy, x, out=out, accumulate=True)
+    want, mass = ref.product(dy.double().t().contiguous(),
+                             ref.values(x.codes, x.scales, k).t().contiguous())
+    assert ref.off(out, want + old.double(), mass + old.double().abs(), m + 1) <= 1.0
+
+
 def test_products_without_elements():
     note("block products of empty operands")
     x, w, dy = operands(5, 7, 0, 1)
