@@ -14,7 +14,10 @@
  *                rank's fp32 block of the flat rank-major shard buffer,
  *                summed in fp32 in rank order (no pack copy);
  *   tide_ag      TIDE-AG placement: a rank-major gathered buffer -> full
- *                per-parameter tensors (no copy-out pass).
+ *                per-parameter tensors (no copy-out pass);
+ *   tide_block_* matrices in 8-bit blocks: the gather of sharded weights at half
+ *                the bytes, 8-bit activation checkpoints, and the products of a
+ *                linear layer and of its backward pass over both.
  *
  * Notation.  N = world (ranks), P = nparams.  Parameter i is a row-major
  * tensor viewed as [dim0_i, inner_i] (inner = product of the trailing dims;
@@ -392,7 +395,7 @@ tide_status tide_block_unshard(const tide_plan *plan, const void *gathered, void
  * (TIDE_E_UNSUPPORTED above).  The output is fp32, or bf16 with
  * TIDE_F_OUT_BF16; it must not overlap an operand.  Sums are held in fp32.
  * Products are exact, except in tide_block_mm with a bf16 output and more than
- * 64 rows: the 8-bit matrix instruction there adds 128 products at a time with
+ * 16 rows: the 8-bit matrix instruction there adds 128 products at a time with
  * fewer bits (an error of about 2e-5 of the result's norm on normal data,
  * against 2e-3 of the rounding to bf16).  Results do not depend on timing: the
  * same call gives the same bits.  An empty sum gives zeros.

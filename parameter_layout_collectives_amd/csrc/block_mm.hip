@@ -182,6 +182,14 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // inside a step is free as long as both sides agree: a lane reads chunks g and
 // g + 4 (g = lane / 16).  Two buffers: the next step's codes travel to registers
 // while this one is multiplied.
+//
+// 256 x 256 tiles, 8192 x 8192 x 8192: 0.43 ms, 2.5 PFLOP/s (torch's product of
+// the same 8-bit numbers without block scales: 3.2); 8192 x 28672 x 8192: 1.7 ms.
+// Counters there: matrix units busy 55% of the cycles, LDS 26%, no bank conflicts,
+// clock about 2.1 GHz.  Leaving out three quarters of the loads makes it 15%
+// faster, leaving out most LDS reads nothing.  Slower here: 32 x 32 x 64
+// fragments (6%), a burst of all loads behind the barrier (2%), a raised wave
+// priority around the multiplications (3%).
 // Buffer descriptor of `bytes` bytes at p (the same in all lanes): loads past
 // its end give zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint32_t bytes) {
@@ -371,6 +379,11 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
 // fp32 sums round.  This is the kernel where a scale cannot go into the matrix
 // instruction, because it changes along the sum (dX and dW: one scale per row
 // of W or X and 128 columns, summed over rows), and for fp32 outputs.
+//
+// 8192 x 8192 x 8192: dX 0.72 to 0.84 ms, dW 0.75 to 0.87 ms (torch's bf16 product
+// on the same cards 0.67 to 0.73 ms, 0.90 to 0.98 ms with its left operand
+// transposed), fp32 product 0.83 to 0.90 ms; matrix units busy 62% of the cycles,
+// clock 1.7 to 2.0 GHz.
 //
 // A step of the sum is 64 values.  LDS layouts of an operand's tile:
 //   along   (sum index contiguous in memory): T rows of 64 bf16, 8 chunks of 16
