@@ -263,6 +263,8 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False):
         dtype = torch.float32 if x.dtype == torch.float32 else torch.bfloat16
     if grad is not None:
         _out(grad, w.shape, None, _PRODUCT_TYPES, w.device, "grad")
+    elif accumulate:
+        raise ValueError("accumulate needs a grad to add to")
     lead = x.shape[:-1]
     if x.dim() != 2:
         x = x.reshape(_numel(lead), w.cols)

@@ -267,10 +267,10 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     c.chunk = steps;
     c.workspace = 0;
     if (c.kernel == kMmSkinny || !may_split) return c;
-    // The tiles that run at one time; what is left after whole rounds of them is
+    // The tiles that run at one time; what is left after whole sets of them is
     // cut if that leaves at least half of the card idle.  The pieces' sums go
     // through memory, so a piece has at least kMinSplitSteps steps, and behind
-    // whole rounds (where a round is long) at least four times that.
+    // whole sets (where one is long) at least four times that.
     const int64_t full = kCus * (c.tile == 256 ? 1 : 2);
     const int64_t left = t % full, least = t < full ? kMinSplitSteps : 4 * kMinSplitSteps;
     if (left == 0 || left * 2 > full || steps < 2 * least) return c;

@@ -375,6 +375,10 @@ extern "C" tide_status tide_block_unshard(const tide_plan *plan, const void *gat
                                           void *const *params, uint32_t flags, void *stream) {
     tide_status st = check_block_unshard(plan, gathered, params, flags);
     if (st != TIDE_OK) return st;
+    if (plan->psi == 0) {
+        clear_error();
+        return TIDE_OK;
+    }
     const ElemType t = out_type(flags);
     const int64_t rank_bytes = plan->S * 4;
     hipStream_t s = static_cast<hipStream_t>(stream);

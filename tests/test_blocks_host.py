@@ -194,7 +194,7 @@ def test_workspace():
         assert L.tide_block_workspace(op, 8192, 8192, 8192, 0) == 0    # enough tiles
         assert L.tide_block_workspace(op, 0, 0, 0, 0) == 0
     assert L.tide_block_workspace(0, 1, 4096, 4096, 0x20) == 0         # few rows: one kernel
-    # a long sum for few tiles, and tiles left over after whole rounds
+    # a long sum for few tiles, and tiles left over after whole sets
     for op, m, n, k in ((2, 8192, 256, 256), (2, 8192, 14336, 4096)):
         size = L.tide_block_workspace(op, m, n, k, 0)
         assert size > 0 and size % (64 * 64 * 4) == 0
@@ -303,6 +303,11 @@ def test_unshard_refusals():
         assert needle in err(), kw
 
 
+def test_unshard_of_nothing():
+    empty = tide.BlockPlan(tide.Plan([(0, 5), (7, 0)], 2))
+    assert lib().tide_block_unshard(empty.handle, None, None, 0x20, None) == 0
+
+
 class _Stub:
     """A tensor's attributes without memory: what it passes the binding's checks
     with, the library would refuse (address 0)."""
@@ -378,6 +383,7 @@ def test_binding_refuses_wrong_operands():
             lambda: tide.block_mm_dw(dy, x, accumulate=True),
             lambda: tide.block_mm_dw(dy, x, out=_Stub((8, 201), bf)),
             lambda: tide.block_linear(_Stub((4, 199), bf), w),
+            lambda: tide.block_linear(_Stub((4, 200), bf), w, accumulate=True),
             lambda: tide.block_linear(_Stub((4, 200), bf, contiguous=False), w),
             lambda: tide.block_linear(_Stub((4, 200), bf), w, grad=_Stub((8, 199), bf)),
             lambda: tide.block_linear(_Stub((4, 200), bf), w, grad=_Stub((8, 200), torch.float16))]:

@@ -281,7 +281,7 @@ def test_products_over_large_tiles():
 
 @pytest.mark.parametrize("shape", [(4400, 4200, 4250), (4200, 4400, 2200)])
 def test_products_of_tiles_left_over(shape):
-    """Whole rounds of tiles and some left over, whose sums are cut."""
+    """Whole sets of tiles and some left over, whose sums are cut."""
     check_products(*shape)
 
 
@@ -580,6 +580,42 @@ def test_captured_linear(m):
         for i, x in enumerate(xs):
             for got, want in zip(outs[i], step(x)):
                 assert torch.equal(got, want)
+
+
+def test_captured_backward_through_autograd():
+    """Forward and backward through autograd in a graph, over a leaf that no live
+    eager graph holds; eager passes over other leaves run between the replays."""
+    note("block_linear autograd captured")
+    m, n, k = 70, 96, 640
+    w = tide.block_quant(rand((n, k), 43, FP, 0.02))
+    dy = rand((m, n), 44, BF, 1e-3)
+    x, dw = rand((m, k), 45), torch.zeros(n, k, device="cuda")
+
+    def step(leaf, grad):
+        y = tide.block_linear(leaf, w, grad=grad, accumulate=True)
+        dx, = torch.autograd.grad(y, leaf, dy)
+        return y.detach(), dx
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x.clone().requires_grad_(), torch.zeros_like(dw))    # one pass outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    leaf = x.clone().requires_grad_()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=side):
+        y, dx = step(leaf, dw)
+    total = torch.zeros_like(dw)
+    dw.zero_()
+    for it in range(3):
+        new = rand((m, k), 46 + it)
+        with torch.no_grad():
+            leaf.copy_(new)
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        want = step(new.clone().requires_grad_(), total)
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1]) and torch.equal(dw, total)
 
 
 def test_custom_ops():
