@@ -38,7 +38,7 @@ constexpr int kUnroll = 4;                         // blocks in flight per group
 constexpr int kChunk = kGroups * kUnroll;          // blocks a workgroup handles in all
 
 // A matrix of a unit, for the kernels below.
-struct Rows {
+struct alignas(16) Rows {
     int64_t src;           // first element of its rows in the source (or the destination's address)
     uint32_t codes;        // where its codes and its scales start in a rank block, in 16 bytes
     uint32_t scales;
@@ -206,22 +206,39 @@ struct UnshardArgs {
 };
 static_assert(sizeof(Rows) == 32 && sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
 
-// The matrix that workgroup `wg` works on: the last one with wg0 <= wg.  Every
-// lane compares two of them: one load's latency, where a search would have
-// seven in a row.
+// The matrix that workgroup `wg` works on: the last one with wg0 <= wg.  Kernel
+// arguments may lie in host memory, so they are read once, all of them by every
+// wave (two matrices per lane), and the one that is wanted comes from its lane:
+// one latency, where a search would have eight in a row.
 template <class A>
-__device__ __forceinline__ int matrix_of(const A &a, uint32_t wg) {
-    static_assert(kPerLaunch <= 128, "two matrices per lane");
+__device__ __forceinline__ Rows matrix_of(const A &a, uint32_t wg) {
+    static_assert(kPerLaunch <= 128 && sizeof(Rows) == 32, "two matrices of 8 words per lane");
     const int lane = threadIdx.x & 63;
-    const int i = min(lane, a.n - 1), j = min(lane + 64, a.n - 1);
-    const bool first = lane < a.n && a.m[i].wg0 <= wg;
-    const bool second = lane + 64 < a.n && a.m[j].wg0 <= wg;
-    return __builtin_amdgcn_readfirstlane(__popcll(__ballot(first)) + __popcll(__ballot(second)) - 1);
+    union Words {
+        u32x4 v[2];
+        Rows m;
+    } one, two;
+    const int i = min(lane, kPerLaunch - 1), j = min(lane + 64, kPerLaunch - 1);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        one.v[h] = reinterpret_cast<const u32x4 *>(&a.m[i])[h];
+        two.v[h] = reinterpret_cast<const u32x4 *>(&a.m[j])[h];
+    }
+    const uint64_t first = __ballot(lane < a.n && one.m.wg0 <= wg);
+    const uint64_t second = __ballot(lane + 64 < a.n && two.m.wg0 <= wg);
+    const int k = __builtin_amdgcn_readfirstlane(__popcll(first) + __popcll(second) - 1);
+    Words w;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        const uint32_t x = k < 64 ? one.v[e / 4][e & 3] : two.v[e / 4][e & 3];
+        w.v[e / 4][e & 3] = __builtin_amdgcn_readlane(x, k & 63);
+    }
+    return w.m;
 }
 
 __global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *__restrict__ master,
                                                        char *__restrict__ block, int aligned) {
-    const Rows d = a.m[matrix_of(a, blockIdx.x)];
+    const Rows d = matrix_of(a, blockIdx.x);
     const bool vec = aligned && d.src % 4 == 0 && d.cols % 8 == 0;
     encode_chunk<kElemF32>(d, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
                            master + d.src * 4, block + static_cast<int64_t>(d.codes) * 16,
@@ -234,7 +251,7 @@ template <int ET>
 __global__ __launch_bounds__(kLanes) void unshard_kernel(UnshardArgs a,
                                                          const char *__restrict__ gathered,
                                                          int64_t rank_bytes) {
-    const Rows d = a.m[matrix_of(a, blockIdx.x)];
+    const Rows d = matrix_of(a, blockIdx.x);
     char *out = reinterpret_cast<char *>(d.src);
     const bool vec = d.src % 16 == 0 && d.cols % 8 == 0;
     const uint32_t nb = d.nb();

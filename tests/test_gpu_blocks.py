@@ -133,7 +133,8 @@ UNITS = [([(5, 7), (16,), (33, 4)], 4, [0, 2]),
          ([(333, 1000), (37, 129), (64, 64)], 6, None),
          ([(9, 260), (3, 640)], 16, None),          # more ranks than rows
          ([(128, 512), (1, 1), (0, 5), (7, 0)], 3, None),
-         ([(2, 130)] * 70, 2, None)]                # more matrices than one launch takes
+         ([(2, 130)] * 70, 2, None),                # more matrices than a wave has lanes
+         ([(1 + i % 4, 120 + i) for i in range(250)], 3, None)]   # more than one launch takes
 
 
 def shards(shapes, world, seed):
