@@ -193,47 +193,75 @@ __global__ __launch_bounds__(kLanes) void dequant_kernel(const char *__restrict_
 }
 
 // A unit's matrices travel as kernel arguments (no table in device memory, so
-// nothing to allocate, upload or keep for a captured launch): as many per
-// launch as fit 4 KB.
+// nothing to allocate, upload or keep for a captured launch): as many slots per
+// launch as fit 4 KB.  A matrix takes one slot; matrices that repeat at a fixed
+// distance (an MoE layer's experts) take two for all of them, the first one's
+// Rows and a Step.
 constexpr int kPerLaunch = 112;
+constexpr uint32_t kIsStep = 0xffffffffu;   // past every workgroup's number
+struct alignas(16) Step {
+    int64_t src;           // from one matrix to the next, as in Rows
+    uint32_t codes, scales;
+    uint32_t wgs;          // workgroups per matrix
+    uint32_t unused[2];
+    uint32_t mark;         // kIsStep, where Rows holds wg0
+};
+union Slot {
+    Rows m;
+    Step step;
+    u32x4 v[2];
+};
 struct ShardArgs {
-    Rows m[kPerLaunch];
+    Slot m[kPerLaunch];
     int n;
 };
 struct UnshardArgs {
-    Rows m[kPerLaunch];             // rows = the matrix's rows, real = rows per rank
+    Slot m[kPerLaunch];             // rows = the matrix's rows, real = rows per rank
     int n;
 };
-static_assert(sizeof(Rows) == 32 && sizeof(Rows) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
+static_assert(sizeof(Slot) == 32 && sizeof(Slot) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
+static_assert(offsetof(Rows, wg0) == 28 && offsetof(Step, mark) == 28, "wg0 and mark share a word");
 
 // The matrix that workgroup `wg` works on: the last one with wg0 <= wg.  Kernel
 // arguments may lie in host memory, so they are read once, all of them by every
-// wave (two matrices per lane), and the one that is wanted comes from its lane:
-// one latency, where a search would have eight in a row.
+// wave (two slots per lane), and the one that is wanted comes from its lane: one
+// latency, where a search would have eight in a row.
 template <class A>
 __device__ __forceinline__ Rows matrix_of(const A &a, uint32_t wg) {
-    static_assert(kPerLaunch <= 128 && sizeof(Rows) == 32, "two matrices of 8 words per lane");
+    static_assert(kPerLaunch <= 128, "two slots per lane");
     const int lane = threadIdx.x & 63;
-    union Words {
-        u32x4 v[2];
-        Rows m;
-    } one, two;
+    Slot one, two;
     const int i = min(lane, kPerLaunch - 1), j = min(lane + 64, kPerLaunch - 1);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        one.v[h] = reinterpret_cast<const u32x4 *>(&a.m[i])[h];
-        two.v[h] = reinterpret_cast<const u32x4 *>(&a.m[j])[h];
+        one.v[h] = a.m[i].v[h];
+        two.v[h] = a.m[j].v[h];
     }
+    const auto slot = [&](int k) {
+        Slot w;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint32_t x = k < 64 ? one.v[e / 4][e & 3] : two.v[e / 4][e & 3];
+            w.v[e / 4][e & 3] = __builtin_amdgcn_readlane(x, k & 63);
+        }
+        return w;
+    };
+    // slot 0 is always a matrix with wg0 = 0, so a bit of `first` is set
     const uint64_t first = __ballot(lane < a.n && one.m.wg0 <= wg);
     const uint64_t second = __ballot(lane + 64 < a.n && two.m.wg0 <= wg);
-    const int k = __builtin_amdgcn_readfirstlane(__popcll(first) + __popcll(second) - 1);
-    Words w;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-        const uint32_t x = k < 64 ? one.v[e / 4][e & 3] : two.v[e / 4][e & 3];
-        w.v[e / 4][e & 3] = __builtin_amdgcn_readlane(x, k & 63);
+    const int k = __builtin_amdgcn_readfirstlane(second ? 127 - __clzll(second) : 63 - __clzll(first));
+    Rows d = slot(k).m;
+    if (k + 1 < a.n) {
+        const Step s = slot(k + 1).step;
+        if (s.mark == kIsStep) {
+            const uint32_t q = (wg - d.wg0) / s.wgs;
+            d.src += static_cast<int64_t>(q) * s.src;
+            d.codes += q * s.codes;
+            d.scales += q * s.scales;
+            d.wg0 += q * s.wgs;
+        }
     }
-    return w.m;
+    return d;
 }
 
 __global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *__restrict__ master,
@@ -279,8 +307,49 @@ tide_status too_many(const char *name) {
     return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
 }
 
-// Launches `launch(args, grid)` over the plan's matrices, kPerLaunch at a time;
-// `fill(j, &rows)` describes matrix j, with rows.rows = 0 for nothing to do.
+int64_t chunks_of(const Rows &r) { return chunks(static_cast<int64_t>(r.rows) * r.nb()); }
+
+// The smallest group of matrices from `j` on whose shapes come three times in a
+// row, or 0.
+int32_t period(const tide_plan *bp, int32_t j) {
+    constexpr int32_t kMost = 8;
+    for (int32_t p = 1; p <= kMost && p <= (bp->nblk - j) / 3; p++) {
+        int32_t i = j;
+        while (i < j + 2 * p && bp->d0[i] == bp->d0[i + p] && bp->blk_inner[i] == bp->blk_inner[i + p])
+            i++;
+        if (i == j + 2 * p) return p;
+    }
+    return 0;
+}
+
+// How many groups of `p` matrices from `j` on have one group's shapes and lie at
+// one distance, `step`.
+template <class Fill>
+int32_t repeats(const tide_plan *bp, Fill fill, int32_t j, int32_t p, Step *step) {
+    Rows a, b;
+    fill(j, &a);
+    fill(j + p, &b);
+    const uint64_t src = static_cast<uint64_t>(b.src) - static_cast<uint64_t>(a.src);
+    *step = Step{static_cast<int64_t>(src), b.codes - a.codes, b.scales - a.scales, 0, {}, kIsStep};
+    for (uint32_t q = 1; ; q++)
+        for (int32_t t = 0; t < p; t++) {
+            const int64_t i = j + t + static_cast<int64_t>(q) * p;
+            if (i >= bp->nblk) return static_cast<int32_t>(q);
+            fill(j + t, &a);
+            fill(static_cast<int32_t>(i), &b);
+            if (chunks_of(a) == 0 || b.rows != a.rows || b.real != a.real || b.cols != a.cols ||
+                static_cast<uint64_t>(b.src) != static_cast<uint64_t>(a.src) + q * src ||
+                b.codes != a.codes + q * step->codes || b.scales != a.scales + q * step->scales)
+                return static_cast<int32_t>(q);
+        }
+}
+
+// Launches `launch(args, grid)` over the plan's matrices, as many at a time as
+// the slots hold; `fill(j, &rows)` describes matrix j, with rows.rows = 0 for
+// nothing to do.  In a unit of more matrices than one launch has slots, groups
+// that come three times or more (experts, each of them with its gate, up and
+// down projection, say) share theirs; twice would take as many, and a smaller
+// unit has its one launch without the search.
 template <class Args, class Fill, class Launch>
 tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Launch launch) {
     int32_t j = 0;
@@ -288,15 +357,39 @@ tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Laun
         Args a;
         a.n = 0;
         int64_t grid = 0;
-        for (; j < bp->nblk && a.n < kPerLaunch; j++) {
+        while (j < bp->nblk) {
             Rows r;
             fill(j, &r);
-            const int64_t units = static_cast<int64_t>(r.rows) * r.nb();
-            if (units == 0) continue;
-            if (grid + chunks(units) > kMaxGrid) break;
-            r.wg0 = static_cast<uint32_t>(grid);
-            grid += chunks(units);
-            a.m[a.n++] = r;
+            if (chunks_of(r) == 0) {
+                j++;
+                continue;
+            }
+            Step step;
+            int32_t p = bp->nblk > kPerLaunch ? period(bp, j) : 0;
+            int64_t n = p ? repeats(bp, fill, j, p, &step) : 1;
+            if (n < 3) p = n = 1;
+            int64_t wgs = 0;
+            for (int32_t t = 0; t < p; t++) {
+                fill(j + t, &r);
+                wgs += chunks_of(r);
+            }
+            if (n > 1 && wgs * n > kMaxGrid) {       // one by one, over several launches
+                p = n = 1;
+                fill(j, &r);
+                wgs = chunks_of(r);
+            }
+            if (grid + wgs * n > kMaxGrid || a.n + (n > 1 ? 2 * p : 1) > kPerLaunch) break;
+            for (int32_t t = 0; t < p; t++) {
+                fill(j + t, &r);
+                r.wg0 = static_cast<uint32_t>(grid);
+                a.m[a.n++].m = r;
+                grid += chunks_of(r) * n;
+                if (n > 1) {
+                    step.wgs = static_cast<uint32_t>(chunks_of(r));
+                    a.m[a.n++].step = step;
+                }
+            }
+            j += p * static_cast<int32_t>(n);
         }
         if (a.n == 0) {
             if (j < bp->nblk) return too_many(name);

@@ -134,7 +134,10 @@ UNITS = [([(5, 7), (16,), (33, 4)], 4, [0, 2]),
          ([(9, 260), (3, 640)], 16, None),          # more ranks than rows
          ([(128, 512), (1, 1), (0, 5), (7, 0)], 3, None),
          ([(2, 130)] * 70, 2, None),                # more matrices than a wave has lanes
-         ([(1 + i % 4, 120 + i) for i in range(250)], 3, None)]   # more than one launch takes
+         ([(1 + i % 4, 120 + i) for i in range(250)], 3, None),   # more than one launch takes
+         ([(5, 7)] + [(3, 130), (3, 130), (4, 65)] * 60, 3, None),   # ... that repeat in threes
+         ([(2, 130)] * 150 + [(0, 5)] + [(9, 260)] * 4 + [(1, 1)], 5, None),
+         ([(7, 20)] + [(6, 136), (6, 136)] * 100, 2, [0, 1, 2, 5] + list(range(8, 190)))]
 
 
 def shards(shapes, world, seed):
@@ -171,6 +174,29 @@ def test_gather_in_blocks(unit):
             assert torch.equal(got[0], want[0]), (i, "codes")
             assert torch.equal(got[1], want[1]), (i, "scales")
             assert torch.equal(params[j].double().cpu(), ref.values(*want, m.shape[1])), i
+
+
+@pytest.mark.parametrize("lead", [0, 1, 8])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_many_matrices_of_one_tensor(lead, gap):
+    """Parameters at fixed distances: experts that are views of one tensor; the
+    elements between them stay."""
+    note(f"block gather of views, lead {lead}, gap {gap}")
+    shapes, world = [(3, 40)] + [(4, 136), (3, 130)] * 70 + [(2, 136)], 3
+    plan, full, master = shards(shapes, world, 90)
+    bp = tide.BlockPlan(plan)
+    gathered = bp.empty()
+    for r in range(world):
+        tide.block_shard(bp, r, master[r], gathered[r])
+    flat = torch.full((lead + sum(a * b + gap for a, b in shapes) + 8,), 7.0, dtype=BF, device="cuda")
+    want = flat.cpu()
+    params, at = [], lead
+    for (a, b), f in zip(shapes, full):
+        params.append(flat[at:at + a * b].view(a, b))
+        want[at:at + a * b] = ref.values(*ref.quant(f), b).to(BF).view(-1)
+        at += a * b + gap
+    tide.block_unshard(bp, gathered, params)
+    assert torch.equal(flat.cpu(), want)
 
 
 def test_shard_pads_missing_rows_with_zeros():
