@@ -211,14 +211,15 @@ union Slot {
     Step step;
     u32x4 v[2];
 };
-struct ShardArgs {
-    Slot m[kPerLaunch];
+template <int N>
+struct Slots {
+    Slot m[N];
     int n;
 };
-struct UnshardArgs {
-    Slot m[kPerLaunch];             // rows = the matrix's rows, real = rows per rank
-    int n;
-};
+// What a wave reads of the slots and a launch copies should follow what the unit
+// fills: with 16 slots an 8B layer's 9 casts and placement (7 matrices) take 318
+// us, with 112 325; an MoE layer's 17 launches (14 slots) 964 and 1001.
+constexpr int kFew = 16;
 static_assert(sizeof(Slot) == 32 && sizeof(Slot) * kPerLaunch <= 3600, "matrix descriptors exceed the kernel arguments");
 static_assert(offsetof(Rows, wg0) == 28 && offsetof(Step, mark) == 28, "wg0 and mark share a word");
 
@@ -226,29 +227,29 @@ static_assert(offsetof(Rows, wg0) == 28 && offsetof(Step, mark) == 28, "wg0 and 
 // arguments may lie in host memory, so they are read once, all of them by every
 // wave (two slots per lane), and the one that is wanted comes from its lane: one
 // latency, where a search would have eight in a row.
-template <class A>
-__device__ __forceinline__ Rows matrix_of(const A &a, uint32_t wg) {
-    static_assert(kPerLaunch <= 128, "two slots per lane");
+template <int N>
+__device__ __forceinline__ Rows matrix_of(const Slots<N> &a, uint32_t wg) {
+    static_assert(N <= 128, "two slots per lane");
     const int lane = threadIdx.x & 63;
     Slot one, two;
-    const int i = min(lane, kPerLaunch - 1), j = min(lane + 64, kPerLaunch - 1);
+    const int i = min(lane, N - 1), j = min(lane + 64, N - 1);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         one.v[h] = a.m[i].v[h];
-        two.v[h] = a.m[j].v[h];
+        two.v[h] = N > 64 ? a.m[j].v[h] : one.v[h];
     }
     const auto slot = [&](int k) {
         Slot w;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const uint32_t x = k < 64 ? one.v[e / 4][e & 3] : two.v[e / 4][e & 3];
+            const uint32_t x = N <= 64 || k < 64 ? one.v[e / 4][e & 3] : two.v[e / 4][e & 3];
             w.v[e / 4][e & 3] = __builtin_amdgcn_readlane(x, k & 63);
         }
         return w;
     };
     // slot 0 is always a matrix with wg0 = 0, so a bit of `first` is set
     const uint64_t first = __ballot(lane < a.n && one.m.wg0 <= wg);
-    const uint64_t second = __ballot(lane + 64 < a.n && two.m.wg0 <= wg);
+    const uint64_t second = N > 64 ? __ballot(lane + 64 < a.n && two.m.wg0 <= wg) : 0;
     const int k = __builtin_amdgcn_readfirstlane(second ? 127 - __clzll(second) : 63 - __clzll(first));
     Rows d = slot(k).m;
     if (k + 1 < a.n) {
@@ -264,7 +265,8 @@ __device__ __forceinline__ Rows matrix_of(const A &a, uint32_t wg) {
     return d;
 }
 
-__global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *__restrict__ master,
+template <int N>
+__global__ __launch_bounds__(kLanes) void shard_kernel(Slots<N> a, const char *__restrict__ master,
                                                        char *__restrict__ block, int aligned) {
     const Rows d = matrix_of(a, blockIdx.x);
     const bool vec = aligned && d.src % 4 == 0 && d.cols % 8 == 0;
@@ -273,10 +275,10 @@ __global__ __launch_bounds__(kLanes) void shard_kernel(ShardArgs a, const char *
                            block + static_cast<int64_t>(d.scales) * 16, vec);
 }
 
-// `src` of a matrix holds its destination's address here; row r lies in rank
-// block r / c at row r % c.
-template <int ET>
-__global__ __launch_bounds__(kLanes) void unshard_kernel(UnshardArgs a,
+// `src` of a matrix holds its destination's address here, `rows` its rows and
+// `real` the c rows of a rank; row r lies in rank block r / c at row r % c.
+template <int ET, int N>
+__global__ __launch_bounds__(kLanes) void unshard_kernel(Slots<N> a,
                                                          const char *__restrict__ gathered,
                                                          int64_t rank_bytes) {
     const Rows d = matrix_of(a, blockIdx.x);
@@ -349,12 +351,13 @@ int32_t repeats(const tide_plan *bp, Fill fill, int32_t j, int32_t p, Step *step
 // nothing to do.  In a unit of more matrices than one launch has slots, groups
 // that come three times or more (experts, each of them with its gate, up and
 // down projection, say) share theirs; twice would take as many, and a smaller
-// unit has its one launch without the search.
-template <class Args, class Fill, class Launch>
+// unit has its one launch without the search.  The MoE layer's 389 matrices take
+// one launch instead of four, its 16 casts 632 us instead of 784.
+template <class Fill, class Launch>
 tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Launch launch) {
     int32_t j = 0;
     while (j < bp->nblk) {
-        Args a;
+        Slots<kPerLaunch> a;
         a.n = 0;
         int64_t grid = 0;
         while (j < bp->nblk) {
@@ -395,7 +398,14 @@ tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Laun
             if (j < bp->nblk) return too_many(name);
             break;
         }
-        launch(a, static_cast<unsigned>(grid));
+        if (a.n <= kFew) {
+            Slots<kFew> few;
+            few.n = a.n;
+            std::copy(a.m, a.m + a.n, few.m);
+            launch(few, static_cast<unsigned>(grid));
+        } else {
+            launch(a, static_cast<unsigned>(grid));
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
     }
@@ -464,7 +474,7 @@ extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, con
     if (st != TIDE_OK) return st;
     const int aligned = reinterpret_cast<uintptr_t>(master) % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    st = over_matrices<ShardArgs>(
+    st = over_matrices(
         "tide_block_shard", plan,
         [&](int32_t j, Rows *r) {
             const int64_t c = plan->c[j], d0 = plan->d0[j];
@@ -473,7 +483,7 @@ extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, con
                       static_cast<uint32_t>(std::min(c, std::max<int64_t>(0, d0 - rank * c))),
                       static_cast<uint32_t>(plan->blk_inner[j]), 0};
         },
-        [&](const ShardArgs &a, unsigned grid) {
+        [&](const auto &a, unsigned grid) {
             shard_kernel<<<dim3(grid), dim3(kLanes), 0, s>>>(
                 a, reinterpret_cast<const char *>(master), static_cast<char *>(block), aligned);
         });
@@ -493,7 +503,7 @@ extern "C" tide_status tide_block_unshard(const tide_plan *plan, const void *gat
     const int64_t rank_bytes = plan->S * 4;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const char *g = static_cast<const char *>(gathered);
-    st = over_matrices<UnshardArgs>(
+    st = over_matrices(
         "tide_block_unshard", plan,
         [&](int32_t j, Rows *r) {
             *r = Rows{static_cast<int64_t>(reinterpret_cast<uintptr_t>(params[j])),
@@ -501,7 +511,7 @@ extern "C" tide_status tide_block_unshard(const tide_plan *plan, const void *gat
                       static_cast<uint32_t>(plan->d0[j]), static_cast<uint32_t>(plan->c[j]),
                       static_cast<uint32_t>(plan->blk_inner[j]), 0};
         },
-        [&](const UnshardArgs &a, unsigned grid) {
+        [&](const auto &a, unsigned grid) {
             const dim3 gr(grid), b(kLanes);
             switch (t) {
                 case kElemBf16: unshard_kernel<kElemBf16><<<gr, b, 0, s>>>(a, g, rank_bytes); break;
