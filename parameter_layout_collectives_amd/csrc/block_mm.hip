@@ -23,6 +23,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Four values of an output row of any width: aligned as one value is.
+typedef uint32_t row_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef __bf16 row_bf16x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float row_f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 #define LDS_AS __attribute__((address_space(3)))
 
@@ -93,12 +97,12 @@ __device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t c
     const int64_t at = row * p.cols + col;
     if (p.out_bf16) {
         __bf16 *o = reinterpret_cast<__bf16 *>(p.out) + at;
-        if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+        if (left >= 4) {
             if (p.accumulate) {
-                const bf16x4 old = *reinterpret_cast<const bf16x4 *>(o);
+                const bf16x4 old = *reinterpret_cast<const row_bf16x4 *>(o);
                 for (int i = 0; i < 4; i++) v[i] += static_cast<float>(old[i]);
             }
-            *reinterpret_cast<u32x2 *>(o) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+            *reinterpret_cast<row_u32x2 *>(o) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
         } else {
             for (int i = 0; i < 4; i++)
                 if (i < left)
@@ -107,9 +111,9 @@ __device__ __forceinline__ void store4(const MmLaunch &p, int64_t row, int64_t c
         return;
     }
     float *o = reinterpret_cast<float *>(p.out) + at;
-    if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-        if (p.accumulate) v += *reinterpret_cast<const f32x4 *>(o);
-        *reinterpret_cast<f32x4 *>(o) = v;
+    if (left >= 4) {
+        if (p.accumulate) v += *reinterpret_cast<const row_f32x4 *>(o);
+        *reinterpret_cast<row_f32x4 *>(o) = v;
     } else {
         for (int i = 0; i < 4; i++)
             if (i < left) o[i] = p.accumulate ? o[i] + v[i] : v[i];
