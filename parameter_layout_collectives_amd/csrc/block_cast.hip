@@ -16,9 +16,12 @@
 // All four move bytes with little arithmetic, so HBM bounds them: 16 lanes
 // share a block, 8 elements each (two 16-byte loads of fp32, one of bf16), and
 // each 16-lane group has kUnroll blocks in flight.  Measured: quantising 8192 x
-// 8192 bf16 38.9 us (5.2 TB/s), reading it back 31 to 33 us (6.1 to 6.5 TB/s); one
-// of 8 ranks of an 8B layer's matrices 27.0 us (5.0 TB/s), placing the whole layer
-// in bf16 93.8 us (7.0 TB/s, part of it from the last-level cache).
+// 8192 bf16 39.4 us (5.2 TB/s), reading it back 32 to 36 us (5.6 to 6.3 TB/s); one
+// of 8 ranks of an 8B layer's matrices 26.7 us (5.1 TB/s), placing the whole layer
+// in bf16 94.7 us (7.0 TB/s, part of it from the last-level cache).  Rows of any
+// width and start are read and written in vectors aligned as one element is, all
+// but the last elements of a row: 8191 x 8189 bf16 44.8 and 38.9 us, where 8
+// accesses per lane took 77.5 and 94.5.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -109,10 +112,10 @@ __device__ __forceinline__ void decode8(u32x2 c, uint32_t scale, char *p, int n,
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = static_cast<float>(h[i / 2][i & 1]);
-        if (vec) {
-            f32x4 *o = reinterpret_cast<f32x4 *>(p);
-            __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, o);
-            __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, o + 1);
+        if (vec || n >= 8) {
+            row_f32x4 *o = reinterpret_cast<row_f32x4 *>(p);
+            __builtin_nontemporal_store(row_f32x4{v[0], v[1], v[2], v[3]}, o);
+            __builtin_nontemporal_store(row_f32x4{v[4], v[5], v[6], v[7]}, o + 1);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -131,8 +134,9 @@ __device__ __forceinline__ void decode8(u32x2 c, uint32_t scale, char *p, int n,
             w[i] = __builtin_bit_cast(uint32_t, f);
         }
     }
-    if (vec) {
-        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4 *>(p));
+    if (vec || n >= 8) {
+        __builtin_nontemporal_store(half_u32x4{w[0], w[1], w[2], w[3]},
+                                    reinterpret_cast<half_u32x4 *>(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -267,9 +271,9 @@ __device__ __forceinline__ Rows matrix_of(const Slots<N> &a, uint32_t wg) {
 
 template <int N>
 __global__ __launch_bounds__(kLanes) void shard_kernel(Slots<N> a, const char *__restrict__ master,
-                                                       char *__restrict__ block, int aligned) {
+                                                       char *__restrict__ block) {
     const Rows d = matrix_of(a, blockIdx.x);
-    const bool vec = aligned && d.src % 4 == 0 && d.cols % 8 == 0;
+    const bool vec = d.cols % 8 == 0;
     encode_chunk<kElemF32>(d, static_cast<int64_t>(blockIdx.x - d.wg0) * kChunk,
                            master + d.src * 4, block + static_cast<int64_t>(d.codes) * 16,
                            block + static_cast<int64_t>(d.scales) * 16, vec);
@@ -283,7 +287,7 @@ __global__ __launch_bounds__(kLanes) void unshard_kernel(Slots<N> a,
                                                          int64_t rank_bytes) {
     const Rows d = matrix_of(a, blockIdx.x);
     char *out = reinterpret_cast<char *>(d.src);
-    const bool vec = d.src % 16 == 0 && d.cols % 8 == 0;
+    const bool vec = d.cols % 8 == 0;
     const uint32_t nb = d.nb();
     const int64_t cp = static_cast<int64_t>(nb) * kBlockCols, sp = (nb + 3) / 4 * 4;
     const int64_t at_codes = static_cast<int64_t>(d.codes) * 16;
@@ -427,7 +431,7 @@ extern "C" tide_status tide_block_quant(const void *x, int64_t rows, int64_t col
     if (rows && cols) {
         const int64_t grid = chunks(rows * block_count(cols));
         if (grid > kMaxGrid) return too_many("tide_block_quant");
-        const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && cols % 8 == 0;
+        const int vec = cols % 8 == 0;
         const dim3 g(static_cast<unsigned>(grid)), b(kLanes);
         hipStream_t s = static_cast<hipStream_t>(stream);
         const char *in = static_cast<const char *>(x);
@@ -451,7 +455,7 @@ extern "C" tide_status tide_block_dequant(const void *codes, const void *scales,
     if (rows && cols) {
         const int64_t grid = chunks(rows * block_count(cols));
         if (grid > kMaxGrid) return too_many("tide_block_dequant");
-        const int vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && cols % 8 == 0;
+        const int vec = cols % 8 == 0;
         const dim3 g(static_cast<unsigned>(grid)), b(kLanes);
         hipStream_t s = static_cast<hipStream_t>(stream);
         const char *c = static_cast<const char *>(codes), *sc = static_cast<const char *>(scales);
@@ -472,7 +476,6 @@ extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, con
                                         void *block, uint32_t flags, void *stream) {
     tide_status st = check_block_shard(plan, rank, master, block, flags);
     if (st != TIDE_OK) return st;
-    const int aligned = reinterpret_cast<uintptr_t>(master) % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = over_matrices(
         "tide_block_shard", plan,
@@ -485,7 +488,7 @@ extern "C" tide_status tide_block_shard(const tide_plan *plan, int32_t rank, con
         },
         [&](const auto &a, unsigned grid) {
             shard_kernel<<<dim3(grid), dim3(kLanes), 0, s>>>(
-                a, reinterpret_cast<const char *>(master), static_cast<char *>(block), aligned);
+                a, reinterpret_cast<const char *>(master), static_cast<char *>(block));
         });
     if (st == TIDE_OK) clear_error();
     return st;

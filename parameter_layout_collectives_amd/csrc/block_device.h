@@ -12,8 +12,12 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// 8 consecutive elements as fp32.  `vec`: the first one is 16-byte aligned
-// and all `n` asked for are whole vectors (n is 0 or 8 then).
+// Vectors of a row of any width and start: aligned as one element is.
+typedef uint32_t half_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float row_f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// 8 consecutive elements as fp32.  `vec`: all `n` asked for are whole vectors
+// (n is 0 or 8 then).
 template <int ET>
 __device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) {
 #pragma unroll
@@ -21,9 +25,9 @@ __device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) 
     if (n <= 0) return;
     if (ET == kElemF32) {
         const float *f = reinterpret_cast<const float *>(p);
-        if (vec) {
-            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f));
-            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(f + 4));
+        if (vec || n >= 8) {
+            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const row_f32x4 *>(f));
+            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const row_f32x4 *>(f + 4));
 #pragma unroll
             for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
         } else {
@@ -33,8 +37,8 @@ __device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) 
         return;
     }
     uint32_t w[4] = {0, 0, 0, 0};
-    if (vec) {
-        const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    if (vec || n >= 8) {
+        const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const half_u32x4 *>(p));
 #pragma unroll
         for (int i = 0; i < 4; i++) w[i] = a[i];
     } else {
