@@ -18,9 +18,9 @@
 // each 16-lane group has kUnroll blocks in flight.  Measured: quantising 8192 x
 // 8192 bf16 39.4 us (5.2 TB/s), reading it back 32 to 36 us (5.6 to 6.3 TB/s); one
 // of 8 ranks of an 8B layer's matrices 26.7 us (5.1 TB/s), placing the whole layer
-// in bf16 94.7 us (7.0 TB/s, part of it from the last-level cache).  Rows of any
+// in bf16 94.7 us (6.9 TB/s, part of it from the last-level cache).  Rows of any
 // width and start are read and written in vectors aligned as one element is, all
-// but the last elements of a row: 8191 x 8189 bf16 44.8 and 38.9 us, where 8
+// but the last elements of a row: 8191 x 8189 bf16 44.0 and 39.0 us, where 8
 // accesses per lane took 77.5 and 94.5.
 #include <hip/hip_runtime.h>
 

@@ -44,8 +44,12 @@ __device__ __forceinline__ void load8(const char *p, int n, bool vec, float *v) 
     } else {
         const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < n) w[i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+        for (int i = 0; i < 8; i++) {
+            // no branch, as each would wait for its load (60000 x 999: 73 -> 59 us);
+            // in fp32 it is the other way round (10^6 x 41: 66 us, so 76)
+            const uint32_t x = h[min(i, n - 1)];
+            w[i / 2] |= i < n ? x << (16 * (i & 1)) : 0;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
