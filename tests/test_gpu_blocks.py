@@ -221,6 +221,24 @@ def test_shard_pads_missing_rows_with_zeros():
             assert torch.equal(scales[:live[r]].cpu(), want[1])
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float16, FP])
+@pytest.mark.parametrize("lead", [1, 3])
+def test_x_that_starts_anywhere(dtype, lead):
+    """The same blocks and products whatever x's alignment, for rows of whole
+    vectors and others, made in one kernel (few rows) and in two."""
+    note(f"x at element {lead}, {dtype}")
+    w = tide.block_quant(rand((40, 264), 95))
+    for rows, cols in ((1, 264), (3, 264), (70, 264), (5, 261), (70, 135)):
+        x = rand((rows, cols), 96).to(dtype)
+        buf = torch.full((lead + rows * cols + 8,), float("nan"), dtype=dtype, device="cuda")
+        moved = buf[lead:lead + rows * cols].view(rows, cols)
+        moved.copy_(x)
+        assert all(torch.equal(a, b) for a, b in zip(bytes_of(tide.block_quant(moved)),
+                                                     bytes_of(tide.block_quant(x))))
+        if cols == w.cols:
+            assert torch.equal(tide.block_linear(moved, w), tide.block_linear(x, w))
+
+
 def test_unaligned_master_and_params():
     note("block gather unaligned")
     shapes, world = [(6, 136), (5, 136)], 2
