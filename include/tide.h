@@ -150,6 +150,16 @@ typedef struct tide_plan tide_plan;
  * value rounded once, to infinity past 65504).  Excludes TIDE_F_OUT_BF16. */
 #define TIDE_F_OUT_F16 0x80u
 
+/* Flag, tide_block_mm and tide_block_linear with TIDE_F_OUT_BF16 only: with more
+ * than 16 rows let the 8-bit matrix instruction add the products, which is about
+ * twice as fast for many rows.  It adds 128 of them at a time, lined up with the
+ * largest, and cuts what falls below its adder: the error of a result is up to
+ * 2^-12 of the sum of its products' magnitudes (2^-13.3 measured at worst over
+ * random codes; 2e-5 of the result's norm on normal data, against 2e-3 of the
+ * rounding to bf16).  Where large products cancel, as outlier columns' may, that
+ * can be more than the result itself. */
+#define TIDE_F_SHORT_SUMS 0x100u
+
 /* ---------------------------------------------------------------------- */
 /* Plan (host only; makes no HIP call).                                    */
 /* ---------------------------------------------------------------------- */
@@ -393,12 +403,10 @@ tide_status tide_block_unshard(const tide_plan *plan, const void *gathered, void
  *   tide_block_mm_dw  dw[n, k]  = dY^T X       (the weights' gradient)
  * All matrices are row-major without gaps; n and k may be at most 2^22
  * (TIDE_E_UNSUPPORTED above).  The output is fp32, or bf16 with
- * TIDE_F_OUT_BF16; it must not overlap an operand.  Sums are held in fp32.
- * Products are exact, except in tide_block_mm with a bf16 output and more than
- * 16 rows: the 8-bit matrix instruction there adds 128 products at a time with
- * fewer bits (an error of about 2e-5 of the result's norm on normal data,
- * against 2e-3 of the rounding to bf16).  Results do not depend on timing: the
- * same call gives the same bits.  An empty sum gives zeros.
+ * TIDE_F_OUT_BF16; it must not overlap an operand.  Products are exact and
+ * sums are held in fp32 (but see TIDE_F_SHORT_SUMS, for tide_block_mm).  Results
+ * do not depend on timing: the same call gives the same bits.  An empty sum
+ * gives zeros.
  *   workspace  device memory of tide_block_workspace() bytes, 16-byte aligned,
  *              used during the call only; with fewer bytes (NULL and 0) the
  *              call runs without cutting its sum into pieces, which is slower

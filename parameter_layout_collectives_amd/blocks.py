@@ -33,6 +33,7 @@ from ._lib import lib
 BLOCK = 128            # columns of a block
 ACCUMULATE = 0x40
 OUT_F16 = 0x80
+SHORT_SUMS = 0x100
 
 _IN_FLAG = {torch.bfloat16: 0, torch.float16: GRAD_F16, torch.float32: GRAD_F32}
 _OUT_FLAG = {torch.float32: 0, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}
@@ -160,13 +161,24 @@ def _workspace(op, m, n, k, flags, device):
 _PRODUCT_TYPES = (torch.bfloat16, torch.float32)
 
 
-def block_mm(x, w, out=None, dtype=torch.bfloat16):
-    """x w^T for x [m, k] and w [n, k] in 8-bit blocks: [m, n] in bf16 or fp32."""
+def _mm_flags(dtype, short_sums):
+    if short_sums and dtype != torch.bfloat16:
+        raise ValueError("short_sums needs a bfloat16 output")
+    return _OUT_FLAG[dtype] | (SHORT_SUMS if short_sums else 0)
+
+
+def block_mm(x, w, out=None, dtype=torch.bfloat16, short_sums=False):
+    """x w^T for x [m, k] and w [n, k] in 8-bit blocks: [m, n] in bf16 or fp32.
+
+    Sums are held in fp32.  With short_sums (bf16 only) the 8-bit matrix
+    instruction adds the products of more than 16 rows: up to twice as fast, off by
+    up to 2^-12 of the sum of the products' magnitudes, which matters where large
+    products cancel (TIDE_F_SHORT_SUMS in include/tide.h)."""
     if x.cols != w.cols:
         raise ValueError(f"x has {x.cols} columns, w has {w.cols}")
     _same_device(x.device, w)
     out = _out(out, (x.rows, w.rows), dtype, _PRODUCT_TYPES, x.device, "out")
-    flags = _OUT_FLAG[out.dtype]
+    flags = _mm_flags(out.dtype, short_sums)
     keep, ptr, size = _workspace(_MM, x.rows, w.rows, x.cols, flags, x.device)
     _call(x.device, lib().tide_block_mm, *x._ptrs, x.rows, *w._ptrs, w.rows, w.cols,
           out.data_ptr(), flags, ptr, size)
@@ -206,13 +218,13 @@ def block_mm_dw(dy, x, out=None, dtype=torch.bfloat16, accumulate=False):
     return out
 
 
-def _linear(x, w, dtype):
+def _linear(x, w, dtype, short_sums):
     """block_mm(block_quant(x), w) that keeps no blocks of x (tide_block_linear)."""
     _matrix(x, "x", _IN_TYPES)
     m, k = x.shape
     _same_device(x.device, w)
     out = _out(None, (m, w.rows), dtype, _PRODUCT_TYPES, x.device, "out")
-    flags = _IN_FLAG[x.dtype] | _OUT_FLAG[dtype]
+    flags = _IN_FLAG[x.dtype] | _mm_flags(dtype, short_sums)
     keep, ptr, size = _workspace(_LINEAR, m, w.rows, k, flags, x.device)
     _call(x.device, lib().tide_block_linear, x.data_ptr(), m, k, *w._ptrs, w.rows,
           out.data_ptr(), flags, ptr, size)
@@ -221,11 +233,11 @@ def _linear(x, w, dtype):
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, anchor, w, dtype, grad, accumulate):
+    def forward(ctx, x, anchor, w, dtype, grad, accumulate, short_sums):
         q = block_quant(x)
         ctx.save_for_backward(q.codes, q.scales, w.codes, w.scales)
         ctx.cols, ctx.x_dtype, ctx.grad, ctx.accumulate = w.cols, x.dtype, grad, accumulate
-        return block_mm(q, w, dtype=dtype)
+        return block_mm(q, w, dtype=dtype, short_sums=short_sums)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -240,15 +252,15 @@ class _Linear(torch.autograd.Function):
             dx = dx.to(ctx.x_dtype) if half else dx
         if ctx.grad is not None:
             block_mm_dw(dy, Blocks(qc, qs, ctx.cols), out=ctx.grad, accumulate=ctx.accumulate)
-        return dx, None, None, None, None, None
+        return dx, None, None, None, None, None, None
 
 
-def block_linear(x, w, dtype=None, grad=None, accumulate=False):
+def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False):
     """A linear layer: x [..., k] times w [n, k] (8-bit blocks) -> [..., n].
 
     x (bf16, fp16 or fp32, contiguous) becomes 8-bit blocks, which are all that
     is kept of it for the backward pass.  dtype: the output's, bf16 or fp32
-    (default: fp32 for an fp32 x, else bf16).
+    (default: fp32 for an fp32 x, else bf16).  short_sums: see block_mm.
     The backward pass takes the output's gradient in bf16, returns x's gradient
     in x's dtype, treating the rounding of x to 8 bits as the identity, and
     writes the weights' gradient to `grad` ([n, k], bf16 or fp32; as the
@@ -272,9 +284,9 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False):
         # With an x that needs no gradient, this empty leaf is what makes
         # autograd run the backward pass, and with it the weights' gradient.
         anchor = torch.empty(0, requires_grad=True) if grad is not None else None
-        y = _Linear.apply(x, anchor, w, dtype, grad, accumulate)
+        y = _Linear.apply(x, anchor, w, dtype, grad, accumulate, short_sums)
     else:
-        y = _linear(x, w, dtype)
+        y = _linear(x, w, dtype, short_sums)
     return y if len(lead) == 1 else y.view(*lead, w.rows)
 
 

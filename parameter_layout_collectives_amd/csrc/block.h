@@ -35,16 +35,23 @@ enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
 
 // The card's compute units: a product's tiles are counted against them.
 constexpr int64_t kCus = 256;
-// The skinny kernel takes up to 16 rows, and up to 64 if W is small: there the
-// second launch of a cut sum costs more than the tiles gain.  32 rows, n = k =
-// 4096: 9.4 us (tiles and join: 14.9); n = 8192, k = 28672: 96 us (68).
-constexpr int64_t kSkinnyRows = 16;
+// The skinny kernel takes up to 32 rows (16 against the 8-bit instruction's
+// tiles), and up to 64 if W is small: there the second launch of a cut sum costs
+// more than the tiles gain.  Skinny against tiles with fp32 sums and join, us:
+//   n = 8192, k = 28672:  17 rows 73 / 88, 28: 89 / 93, 32: 95 / 94, 48: 131 / 100
+//   n = 14336, k = 4096:  17 rows 23 / 27, 28: 27 / 28, 32: 29 / 28, 64: 49 / 29
+//   n = k = 4096:         32 rows 9.4 / 12.0, 48: 11.7 / 12.9, 64: 13.2 / 14.0
+//   n = k = 2048:         40 rows 6.2 / 8.7, 64: 7.3 / 9.5
+// and against the 8-bit instruction's, n = 8192, k = 28672, 32 rows: 95 / 61.
+constexpr int64_t kSkinnyRows = 32;
+constexpr int64_t kSkinnyShort = 16;
 constexpr int64_t kSkinnyMost = 64;
 constexpr int64_t kSkinnyWeights = int64_t(1) << 24;
 // x's blocks are made inside the product for one row of at most 28 KB of codes,
 // or more rows of at most 8 KB together: every workgroup repeats that work.  One
 // row, n = 14336, k = 4096: 16.2 us, as the product alone; 8 rows: 30.1 us
 // (product alone 17.1, and a launch for the blocks about 4).
+constexpr int64_t kInOneRows = 16;
 constexpr int64_t kInOneRow = 28672;     // 56 KB of LDS
 constexpr int64_t kInOneBytes = 8192;
 // The least steps in a piece of a cut sum, and the most pieces.

@@ -32,6 +32,8 @@ tide_status check_flags(const char *name, uint32_t flags, uint32_t known) {
         return bad(name, "TIDE_F_GRAD_F16 and TIDE_F_GRAD_F32 both set");
     if ((flags & TIDE_F_OUT_BF16) && (flags & TIDE_F_OUT_F16))
         return bad(name, "TIDE_F_OUT_BF16 and TIDE_F_OUT_F16 both set");
+    if ((flags & TIDE_F_SHORT_SUMS) && !(flags & TIDE_F_OUT_BF16))
+        return bad(name, "TIDE_F_SHORT_SUMS without TIDE_F_OUT_BF16");
     return TIDE_OK;
 }
 
@@ -155,8 +157,8 @@ tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void 
 }
 
 tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
-    const uint32_t known =
-        TIDE_F_OUT_BF16 | (op == kMmDw ? static_cast<uint32_t>(TIDE_F_ACCUMULATE) : 0u);
+    const uint32_t known = TIDE_F_OUT_BF16 | (op == kMmDw ? TIDE_F_ACCUMULATE : 0u) |
+                           (op == kMm ? TIDE_F_SHORT_SUMS : 0u);
     tide_status st = check_flags(name, g.flags, known);
     if (st != TIDE_OK) return st;
     if (g.M < 0 || g.N < 0 || g.K < 0) return bad(name, "negative size");
@@ -205,7 +207,7 @@ tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
 
 LinearChoice linear_choose(int64_t M, int64_t K) {
     const int64_t bytes = M * block_cols(K);
-    LinearChoice c = {M <= kSkinnyRows && bytes <= (M == 1 ? kInOneRow : kInOneBytes), 0, 0};
+    LinearChoice c = {M <= kInOneRows && bytes <= (M == 1 ? kInOneRow : kInOneBytes), 0, 0};
     if (c.in_one) return c;
     const int64_t round = 255;
     c.scales = (M * block_cols(K) + round) & ~round;
@@ -215,7 +217,8 @@ LinearChoice linear_choose(int64_t M, int64_t K) {
 
 tide_status check_linear(const LinearArgs &a) {
     const char *name = "tide_block_linear";
-    tide_status st = check_flags(name, a.flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 | TIDE_F_OUT_BF16);
+    tide_status st = check_flags(name, a.flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 |
+                                                    TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS);
     if (st != TIDE_OK) return st;
     for (int64_t rows : {a.M, a.N})
         for (int64_t cols : {a.N, a.K})
@@ -250,8 +253,9 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     MmChoice c;
     const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
     const int64_t sum = op == kMm ? K : op == kMmDx ? N : M;
-    const bool eight = op == kMm && (flags & TIDE_F_OUT_BF16);
-    const bool skinny = M <= kSkinnyRows || (M <= kSkinnyMost && N * K <= kSkinnyWeights);
+    const bool eight = op == kMm && (flags & TIDE_F_SHORT_SUMS);
+    const bool skinny = M <= (eight ? kSkinnyShort : kSkinnyRows) ||
+                        (M <= kSkinnyMost && N * K <= kSkinnyWeights);
     c.kernel = op == kMm && skinny ? kMmSkinny : eight ? kMmEight : kMmWide;
     const int64_t step = eight ? 128 : 64;
     const int64_t steps = (sum + step - 1) / step;
@@ -350,7 +354,7 @@ int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32
     if (op == 3) {               // tide_block_linear: x's blocks, then the product's
         const tide::LinearChoice c = tide::linear_choose(m, k);
         if (c.in_one || n == 0) return 0;
-        return c.blocks + tide_block_workspace(0, m, n, k, flags & TIDE_F_OUT_BF16);
+        return c.blocks + tide_block_workspace(0, m, n, k, flags & (TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS));
     }
     // whichever way dY is aligned
     int64_t most = 0;

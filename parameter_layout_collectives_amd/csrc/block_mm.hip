@@ -169,15 +169,18 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 }
 
 // ---------------------------------------------------------------------------
-// Y = X W^T with the 8-bit matrix instruction (bf16 output)
+// Y = X W^T with the 8-bit matrix instruction (TIDE_F_SHORT_SUMS)
 // ---------------------------------------------------------------------------
 //
 // One step of the sum is one block of 128 columns: the scaled instruction
 // (16 x 16 x 128) takes both operands' e8m0 scales, so a block's scale costs no
-// arithmetic.  Its sums of 128 products keep fewer bits than fp32 (1.6e-5 of
-// the result's norm on normal data); the bf16 output's own rounding is 100
-// times that, and an fp32 output takes the kernel below, whose products are
-// exact.
+// arithmetic.  But its sums of 128 products keep fewer bits than fp32: they are
+// lined up with the largest and cut at about 2^-13 of their magnitudes' sum.  On
+// normal data that is 1.6e-5 of the result's norm, 100 times less than the bf16
+// output's own rounding; where large products cancel it can exceed the result
+// (pairs of 448 * 448 that cancel among 392 products: off by 92 in about 200).  So
+// this kernel runs only where the caller asks for it; without the flag sums are
+// held in fp32 by the kernel below.
 //
 // A T x T tile of the output per workgroup, WI x WJ waves.  A row's 128 codes
 // are 8 chunks of 16 bytes; chunk h of row r lies at h ^ (r & 7) in LDS, so the
@@ -381,7 +384,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
 // bf16 number), so every product of the bf16 instruction is exact and only the
 // fp32 sums round.  This is the kernel where a scale cannot go into the matrix
 // instruction, because it changes along the sum (dX and dW: one scale per row
-// of W or X and 128 columns, summed over rows), and for fp32 outputs.
+// of W or X and 128 columns, summed over rows), and for Y = X W^T, whose sums the
+// 8-bit instruction would cut.
 //
 // 8192 x 8192 x 8192: dX 0.72 to 0.84 ms, dW 0.75 to 0.87 ms (torch's bf16 product
 // on the same cards 0.67 to 0.73 ms, 0.90 to 0.98 ms with its left operand
@@ -1000,7 +1004,7 @@ tide_status run_linear(const LinearArgs &a, void *stream) {
     tide_status st = check_linear(a);
     if (st != TIDE_OK) return st;
     const ElemType in = in_type(a.flags);
-    const uint32_t oflags = a.flags & TIDE_F_OUT_BF16;
+    const uint32_t oflags = a.flags & (TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS);
     const LinearChoice c = linear_choose(a.M, a.K);
     char *const ws = static_cast<char *>(a.workspace);
     if (!c.in_one || a.N == 0 || a.M == 0 || a.K == 0) {
@@ -1028,7 +1032,7 @@ tide_status run_linear(const LinearArgs &a, void *stream) {
     p.b_pitch = block_cols(a.K);
     p.bs_pitch = block_scale_cols(a.K);
     p.out = static_cast<char *>(a.out);
-    p.out_bf16 = oflags != 0;
+    p.out_bf16 = (oflags & TIDE_F_OUT_BF16) != 0;
     p.aligned = a.K % 8 == 0;          // x is read in whole vectors
     const dim3 g(static_cast<unsigned>((a.N + 15) / 16)), b(kSkinnyWaves * 64);
     const unsigned lds = static_cast<unsigned>(a.M * (2 * block_cols(a.K) + 16));

@@ -109,10 +109,11 @@ class TideUnit:
             dst, _, _ = self.rest_plan.param(j)
             out[:, dst:dst + seg].copy_(self.master[:, src:src + seg])
 
-    def linear(self, i, x, grad=None, accumulate=False, dtype=None):
+    def linear(self, i, x, grad=None, accumulate=False, dtype=None, short_sums=False):
         """x [..., k] times parameter i (one of `blocks`, [n, k]) -> [..., n]: see
         block_linear.  grad: where the backward pass writes the weight gradient
         ([n, k], bf16 or fp32), e.g. the tensor that reduce_scatter() will read."""
         if i not in self.blocks:
             raise ValueError(f"parameter {i} is not gathered in blocks")
-        return block_linear(x, self.params[i], dtype=dtype, grad=grad, accumulate=accumulate)
+        return block_linear(x, self.params[i], dtype=dtype, grad=grad, accumulate=accumulate,
+                            short_sums=short_sums)

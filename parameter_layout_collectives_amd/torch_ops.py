@@ -10,7 +10,7 @@
     torch.ops.tide.block_unshard(block_pid, gathered, params)
     torch.ops.tide.block_quant(x, codes, scales)
     torch.ops.tide.block_dequant(codes, scales, out)
-    torch.ops.tide.block_mm(x_codes, x_scales, w_codes, w_scales, cols, out)
+    torch.ops.tide.block_mm(x_codes, x_scales, w_codes, w_scales, cols, out, short_sums)
     torch.ops.tide.block_mm_dx(dy, w_codes, w_scales, out)
     torch.ops.tide.block_mm_dw(dy, x_codes, x_scales, out, accumulate)
 
@@ -156,12 +156,14 @@ def _(codes, scales, out):
 
 @torch.library.custom_op("tide::block_mm", mutates_args=("out",))
 def block_mm_op(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
-                w_scales: torch.Tensor, cols: int, out: torch.Tensor) -> None:
-    block_mm(Blocks(x_codes, x_scales, cols), Blocks(w_codes, w_scales, cols), out=out)
+                w_scales: torch.Tensor, cols: int, out: torch.Tensor,
+                short_sums: bool = False) -> None:
+    block_mm(Blocks(x_codes, x_scales, cols), Blocks(w_codes, w_scales, cols), out=out,
+             short_sums=short_sums)
 
 
 @block_mm_op.register_fake
-def _(x_codes, x_scales, w_codes, w_scales, cols, out):
+def _(x_codes, x_scales, w_codes, w_scales, cols, out, short_sums=False):
     return None
 
 

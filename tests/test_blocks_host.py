@@ -430,3 +430,12 @@ def test_custom_ops_declare_what_they_write():
         for w in written:
             assert w in schema, (name, schema)
         assert schema.count("!") == len(written), (name, schema)
+
+
+def test_short_sums_refusals():
+    assert mm(flags=0x100) == E_INVALID and "SHORT_SUMS" in err()        # fp32 output
+    assert linear(flags=0x100) == E_INVALID and "SHORT_SUMS" in err()
+    assert dx(flags=0x120) == E_UNSUPPORTED and "flag" in err()
+    assert dw(flags=0x120) == E_UNSUPPORTED and "flag" in err()
+    assert dequant(flags=0x120) == E_UNSUPPORTED and "flag" in err()
+    assert mm(m=0, x=0, xs=0, out=0, flags=0x120) == 0
