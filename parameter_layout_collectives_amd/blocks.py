@@ -83,36 +83,77 @@ class Blocks:
     """A matrix [rows, cols] in 8-bit blocks.
 
     codes: [rows, cols rounded up to 128], float8_e4m3fn or uint8.
-    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu."""
+    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu.
+    Either may be replaced by another tensor of its shape, and its storage may be
+    released and restored in between, as an FSDP unit does with gathered weights:
+    every call asks the tensors where they are, and refuses one without memory."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "device", "_ptrs")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_device")
 
     def __init__(self, codes, scales, cols):
+        self._set(codes, scales, int(cols))
+
+    def _set(self, codes, scales, cols):
         _matrix(codes, "codes", (torch.float8_e4m3fn, torch.uint8))
         _matrix(scales, "scales", (torch.uint8, torch.float8_e8m0fnu))
-        self.cols = int(cols)
-        self.rows = codes.shape[0]
-        self.device = codes.device
         _same_device(codes.device, scales)
-        if self.cols < 0 or codes.shape[1] != _code_cols(self.cols) \
-                or tuple(scales.shape) != (self.rows, _scale_cols(self.cols)):
+        rows = codes.shape[0]
+        if cols < 0 or codes.shape[1] != _code_cols(cols) \
+                or tuple(scales.shape) != (rows, _scale_cols(cols)):
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
-                             f"hold {self.rows} rows of {self.cols} columns")
-        self.codes, self.scales = codes, scales
-        self._ptrs = codes.data_ptr(), scales.data_ptr()
+                             f"hold {rows} rows of {cols} columns")
+        self._codes, self._scales = codes, scales
+        self._rows, self._cols, self._device = rows, cols, codes.device
 
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
         self = object.__new__(cls)          # right by construction: no checks
-        self.codes = torch.empty((rows, _code_cols(cols)), dtype=torch.float8_e4m3fn, device=device)
-        self.scales = torch.empty((rows, _scale_cols(cols)), dtype=torch.uint8, device=device)
-        self.rows, self.cols, self.device = rows, cols, self.codes.device
-        self._ptrs = self.codes.data_ptr(), self.scales.data_ptr()
+        self._codes = torch.empty((rows, _code_cols(cols)), dtype=torch.float8_e4m3fn,
+                                  device=device)
+        self._scales = torch.empty((rows, _scale_cols(cols)), dtype=torch.uint8, device=device)
+        self._rows, self._cols, self._device = rows, cols, self._codes.device
         return self
 
     @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._replace(t, self._scales)
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @scales.setter
+    def scales(self, t):
+        self._replace(self._codes, t)
+
+    def _replace(self, codes, scales):
+        if codes.shape[0] != self._rows:
+            raise ValueError(f"codes of {codes.shape[0]} rows in place of {self._rows}")
+        self._set(codes, scales, self._cols)
+
+    @property
+    def rows(self):
+        return self._rows
+
+    @property
+    def cols(self):
+        return self._cols
+
+    @property
+    def device(self):
+        return self._device
+
+    @property
     def shape(self):
-        return self.rows, self.cols
+        return self._rows, self._cols
+
+    @property
+    def _ptrs(self):
+        return self._codes.data_ptr(), self._scales.data_ptr()
 
 
 def _out(out, shape, dtype, dtypes, device, what):

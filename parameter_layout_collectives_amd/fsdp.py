@@ -55,7 +55,6 @@ class TideUnit:
             self.block_plan = BlockPlan(self.plan, self.blocks)
             self.block_gathered = self.block_plan.empty(device)
             weights = self.block_plan.blocks(device)
-            self.block_views = self.block_plan.views(weights)
             self.rest_plan = Plan([self.shapes[i] for i in self.rest], N, align) \
                 if self.rest else None
         S = self.rest_plan.S if self.rest_plan is not None else 0
@@ -92,8 +91,9 @@ class TideUnit:
                     block_shard(self.block_plan, r, self.master[r], self.block_gathered[r])
                 self._copy_rest()
         if self.blocks:
-            ag(self.block_plan, self.block_gathered, self.block_views, small=small,
-               copy_engine=copy_engine, stream=stream)
+            views = self.block_plan.views([self.params[i] for i in self.blocks])
+            ag(self.block_plan, self.block_gathered, views, small=small, copy_engine=copy_engine,
+               stream=stream)
         if self.rest:
             ag(self.rest_plan, self.gathered, [self.params[i] for i in self.rest], small=small,
                copy_engine=copy_engine, stream=stream)
