@@ -293,7 +293,9 @@ class _Linear(torch.autograd.Function):
             dx = dx.to(ctx.x_dtype) if half else dx
         if ctx.grad is not None:
             block_mm_dw(dy, Blocks(qc, qs, ctx.cols), out=ctx.grad, accumulate=ctx.accumulate)
-        return dx, None, None, None, None, None, None
+        # the anchor's gradient: an empty tensor of this stream
+        da = dy.new_empty(0, dtype=torch.float32) if ctx.needs_input_grad[1] else None
+        return dx, da, None, None, None, None, None
 
 
 def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False):
@@ -306,8 +308,9 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
     in x's dtype, treating the rounding of x to 8 bits as the identity, and
     writes the weights' gradient to `grad` ([n, k], bf16 or fp32; as the
     reduce-scatter takes it), or adds it there with accumulate.  Without `grad`
-    the weights are frozen.  w's blocks must hold the same values in the
-    backward pass as in the forward pass."""
+    the weights are frozen.  Like other gradients, `grad` is written on the forward
+    pass's stream, and the stream that calls backward() waits for it.  w's blocks
+    must hold the same values in the backward pass as in the forward pass."""
     if x.shape[-1] != w.cols:
         raise ValueError(f"x has {x.shape[-1]} columns, w has {w.cols}")
     if not x.is_contiguous():
@@ -323,8 +326,11 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
         x = x.reshape(_numel(lead), w.cols)
     if torch.is_grad_enabled() and (x.requires_grad or grad is not None):
         # With an x that needs no gradient, this empty leaf is what makes
-        # autograd run the backward pass, and with it the weights' gradient.
-        anchor = torch.empty(0, requires_grad=True) if grad is not None else None
+        # autograd run the backward pass, and with it the weights' gradient.  It
+        # lies on x's device, made under the forward pass's stream: autograd joins
+        # the stream that calls backward() with those of device leaves, so that
+        # `grad` may be read there.
+        anchor = torch.empty(0, device=x.device, requires_grad=True) if grad is not None else None
         y = _Linear.apply(x, anchor, w, dtype, grad, accumulate, short_sums)
     else:
         y = _linear(x, w, dtype, short_sums)

@@ -1,0 +1,46 @@
+"""The weights' gradient of block_linear and the streams of its passes."""
+import pytest
+import torch
+
+import parameter_layout_collectives_amd as tide
+from gpu_helpers import note
+from test_gpu_blocks import BF, FP, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("x_grad", [False, True])
+@pytest.mark.parametrize("two", [False, True])
+def test_weight_gradient_is_ordered_before_the_caller(x_grad, two):
+    """Forward on a side stream, backward() called from another one, which reads
+    `grad` right away: much work is queued on the side stream before the backward
+    pass's, so an unordered read would find the old values."""
+    note(f"block_linear backward from another stream, x_grad={x_grad}, two layers={two}")
+    m, n, k = 200, 264, 392
+    w, w2 = (tide.block_quant(rand(s, 2 + i, FP, 0.02)) for i, s in enumerate([(n, k), (k, n)]))
+    dy = rand((m, k if two else n), 3, BF, 1e-3)
+    big = rand((4096, 4096), 4)
+    x = rand((m, k), 1)
+
+    def passes(stream, grads):
+        xl = x.clone().requires_grad_(x_grad)
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            y = tide.block_linear(xl, w, grad=grads[0])
+            if two:
+                y = tide.block_linear(y, w2, grad=grads[1])
+            for _ in range(20):
+                big @ big
+        y.backward(dy)
+        return [g.clone() for g in grads] + ([xl.grad.clone()] if x_grad else [])
+
+    here = torch.cuda.current_stream()
+    shapes = [(n, k), (k, n)]
+    want = passes(here, [torch.full(s, 7.0, device="cuda") for s in shapes])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    grads = [torch.full(s, 7.0, device="cuda") for s in shapes]
+    got = passes(side, grads)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not bool((want[0] == 7.0).any())
