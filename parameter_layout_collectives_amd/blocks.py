@@ -19,6 +19,10 @@ gathers its weights this way moves half the bytes of a bf16 all-gather
 ("FSDP通信终局：TIDE零拷贝集合通信优化", §"FSDP2通信开销的根源": the all-gather's
 bytes are part of every step).
 
+block_linear is the differentiable call, in reverse mode.  The others are what it
+is made of: their results carry no gradient, whatever their inputs require.  A
+forward-mode dual tensor is refused by all of them.
+
 The calls run on PyTorch's current stream of the tensors' device; outputs and
 workspaces that they make come from PyTorch's allocator, so they may be
 captured into a graph.
@@ -26,6 +30,7 @@ captured into a graph.
 import ctypes
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import GRAD_F16, GRAD_F32, OUT_BF16, Plan, PointerTable, _check, _numel
 from ._lib import lib
@@ -65,7 +70,13 @@ def _call(device, fn, *args):
             _check(fn(*args, _raw_stream(index)))
 
 
+def _no_dual(t, what):
+    if unpack_dual(t).tangent is not None:
+        raise NotImplementedError(f"{what} is a dual tensor: no forward-mode derivative")
+
+
 def _matrix(t, what, dtypes):
+    _no_dual(t, what)
     if t.dtype not in dtypes:
         raise TypeError(f"{what} is {t.dtype}, expected one of "
                         f"{', '.join(str(d).replace('torch.', '') for d in dtypes)}")
@@ -170,7 +181,8 @@ def _out(out, shape, dtype, dtypes, device, what):
 
 
 def block_quant(x, out=None):
-    """x [rows, cols] (bf16, fp16 or fp32) in 8-bit blocks: `out` or new Blocks."""
+    """x [rows, cols] (bf16, fp16 or fp32) in 8-bit blocks: `out` or new Blocks.
+    They carry no gradient to x."""
     _matrix(x, "x", _IN_TYPES)
     rows, cols = x.shape
     if out is None:
@@ -313,6 +325,7 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
     must hold the same values in the backward pass as in the forward pass."""
     if x.shape[-1] != w.cols:
         raise ValueError(f"x has {x.shape[-1]} columns, w has {w.cols}")
+    _no_dual(x, "x")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     if dtype is None:
@@ -392,6 +405,7 @@ class BlockPlan(Plan):
 def block_shard(plan, rank, master, block):
     """Rank `rank`'s fp32 master shard (source_S elements) -> its 8-bit rank
     block (plan.S int32 words, e.g. a row of plan.empty())."""
+    _no_dual(master, "master")
     if master.dtype != torch.float32 or not master.is_cuda or not master.is_contiguous() \
             or master.numel() != plan.source_S:
         raise ValueError(f"master must be a contiguous float32 device tensor of "
@@ -409,6 +423,7 @@ def _check_unshard(plan, params, device):
     if dtype not in _OUT_FLAG:
         raise TypeError(f"params must be bfloat16, float16 or float32, got {dtype}")
     for j, (t, s) in enumerate(zip(params, plan.matrices)):
+        _no_dual(t, f"params[{j}]")
         if t.dtype != dtype or t.device != device or not t.is_contiguous() \
                 or t.numel() != s[0] * s[1]:
             raise ValueError(f"params[{j}] must be a contiguous {dtype} tensor on {device} with "
