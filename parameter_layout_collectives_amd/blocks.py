@@ -287,15 +287,18 @@ def _linear(x, w, dtype, short_sums):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, anchor, w, dtype, grad, accumulate, short_sums):
-        q = block_quant(x)
-        ctx.save_for_backward(q.codes, q.scales, w.codes, w.scales)
         ctx.cols, ctx.x_dtype, ctx.grad, ctx.accumulate = w.cols, x.dtype, grad, accumulate
+        if grad is None:         # frozen weights: nothing of x is needed again
+            ctx.save_for_backward(w.codes, w.scales)
+            return _linear(x, w, dtype, short_sums)
+        q = block_quant(x)
+        ctx.save_for_backward(w.codes, w.scales, q.codes, q.scales)
         return block_mm(q, w, dtype=dtype, short_sums=short_sums)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        qc, qs, wc, ws = ctx.saved_tensors
+        wc, ws, *q = ctx.saved_tensors
         dy = dy.to(torch.bfloat16).contiguous()
         dx = None
         if ctx.needs_input_grad[0]:
@@ -304,7 +307,7 @@ class _Linear(torch.autograd.Function):
                              dtype=torch.float32 if half else ctx.x_dtype)
             dx = dx.to(ctx.x_dtype) if half else dx
         if ctx.grad is not None:
-            block_mm_dw(dy, Blocks(qc, qs, ctx.cols), out=ctx.grad, accumulate=ctx.accumulate)
+            block_mm_dw(dy, Blocks(*q, ctx.cols), out=ctx.grad, accumulate=ctx.accumulate)
         # the anchor's gradient: an empty tensor of this stream
         da = dy.new_empty(0, dtype=torch.float32) if ctx.needs_input_grad[1] else None
         return dx, da, None, None, None, None, None
@@ -314,7 +317,7 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
     """A linear layer: x [..., k] times w [n, k] (8-bit blocks) -> [..., n].
 
     x (bf16, fp16 or fp32, contiguous) becomes 8-bit blocks, which are all that
-    is kept of it for the backward pass.  dtype: the output's, bf16 or fp32
+    is kept of it for the backward pass, and only for the weights' gradient.  dtype: the output's, bf16 or fp32
     (default: fp32 for an fp32 x, else bf16).  short_sums: see block_mm.
     The backward pass takes the output's gradient in bf16, returns x's gradient
     in x's dtype, treating the rounding of x to 8 bits as the identity, and

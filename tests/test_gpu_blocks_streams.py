@@ -1,4 +1,4 @@
-"""The weights' gradient of block_linear and the streams of its passes."""
+"""The weights' gradient of block_linear, the streams of its passes, and what it keeps."""
 import pytest
 import torch
 
@@ -44,3 +44,26 @@ def test_weight_gradient_is_ordered_before_the_caller(x_grad, two):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert not bool((want[0] == 7.0).any())
+
+
+@pytest.mark.parametrize("m", [3, 40, 200])
+def test_frozen_weights_keep_nothing_of_x(m):
+    note(f"block_linear with frozen weights keeps no checkpoint {m}")
+    n, k = 72, 264
+    w = tide.block_quant(rand((n, k), 2, FP, 0.02))
+    x, dy = rand((m, k), 1).requires_grad_(), rand((m, n), 3, BF, 1e-3)
+    kept = []
+
+    def pack(t):
+        kept.append(t.data_ptr())
+        return t
+    weights = [w.codes.data_ptr(), w.scales.data_ptr()]
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        y = tide.block_linear(x, w)
+        assert kept == weights
+        dw = torch.empty(n, k, device="cuda")
+        same = tide.block_linear(x, w, grad=dw)
+    assert kept[2:4] == weights and len(kept) == 6
+    assert torch.equal(y, same)
+    y.backward(dy)
+    assert torch.equal(x.grad, tide.block_mm_dx(dy, w))
