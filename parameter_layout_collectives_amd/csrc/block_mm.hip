@@ -203,14 +203,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint3
                                              0x00020000);
 }
 
-// Every wave's loads into LDS have landed, but for the LATER loads it has asked
-// for since (loads return in order), and every wave's reads of LDS are done.
+// This wave's loads have arrived, those into LDS among them.
+__device__ __forceinline__ void arrived() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0); the other counters as they are
+}
+
+// Every wave's loads into LDS have landed, and every wave's reads of LDS are done.
 // __syncthreads() alone need not wait for loads into LDS: the compiler counts
 // them for reads that may alias, which the buffers' __restrict__ denies.
-template <int LATER = 0>
 __device__ __forceinline__ void landed() {
-    static_assert(LATER < 16, "the counter's low bits");
-    __builtin_amdgcn_s_waitcnt(0x0f70 | LATER);   // vmcnt(LATER); the other counters as they are
+    arrived();
     __syncthreads();
 }
 
@@ -418,7 +420,7 @@ __device__ __forceinline__ int swz_across(int c) {
 // builtin for it would make the compiler wait for the load before the next
 // transposing read of LDS, of whatever buffer: it cannot tell that they do not
 // meet.  An asm statement is not counted, which is safe: its only output is
-// LDS, for which landed() waits, and loads return in order, so a wait for a
+// LDS, for which arrived() waits, and loads return in order, so a wait for a
 // counted load is at worst longer than needed.
 __device__ __forceinline__ void direct_load(__amdgpu_buffer_rsrc_t r, LDS_AS char *to, uint32_t at,
                                             uint32_t off) {
@@ -613,7 +615,6 @@ struct Wide {
     static constexpr int TILE = T * 128;                   // bytes of one operand's tile
     typedef Stage<MI, T, NT, ALIGNED> SI;
     typedef Stage<MJ, T, NT, true> SJ;
-    static constexpr int JLOADS = 2 * SJ::SLOTS;           // codes and scales
     static constexpr int IPUTS = SI::DIRECT ? 0 : SI::SLOTS, PUTS = IPUTS + SJ::SLOTS;
     static_assert(LINES % RING == 0 && D <= FI,
                   "a step starts at ring entry 0, and its first half is over when the next "
@@ -659,15 +660,15 @@ struct Wide {
 #pragma unroll
             for (int q = 0; q < PUTS; q++)
                 if (!LAST && n == FROM + q * (TO - FROM) / PUTS) put(there_i, there_j, q);
+            // The loads straight into LDS were asked for a step ago.  They are waited
+            // for before others set out: a wait for all but a number of later loads
+            // would hold only as long as the compiler keeps that number.
+            if (SI::DIRECT && !LAST && n == TO) arrived();
             if (!LAST && n == TO) sj.fetch(here_j, wave);
             if (!LAST && n == TO && !SI::DIRECT) si.fetch(here_i, wave);
             if (!LAST && n + D == LINES) {
-                if (SI::DIRECT) {
-                    landed<JLOADS>();
-                    si.fetch(here_i, wave);
-                } else {
-                    __syncthreads();
-                }
+                __syncthreads();
+                if (SI::DIRECT) si.fetch(here_i, wave);
                 rows(r[0], there_j, 0);
             }
             if (!LAST && n + D >= LINES) l[(n + D) % RING] = line(there_i, n + D - LINES);
