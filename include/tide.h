@@ -349,7 +349,7 @@ tide_status tide_rs_noalloc(const tide_plan *plan, int32_t rank, const void *con
  * nothing and may be captured into a graph at any time.  Errors and streams
  * as for tide_rs; the current device has to be the one that holds the data. */
 
-/* Cp and Sp for C columns (-1 if C < 0). */
+/* Cp and Sp for C columns (-1 if C < 0 or C >= 2^31). */
 int64_t tide_block_cols(int64_t cols);
 int64_t tide_block_scale_cols(int64_t cols);
 
@@ -434,7 +434,7 @@ tide_status tide_block_linear(const void *x, int64_t m, int64_t k, const void *w
                               void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace that the call `op` (0 mm, 1 mm_dx, 2 mm_dw, 3 linear) uses
- * for these sizes and flags; 0 if none, -1 for a bad argument. */
+ * for these sizes and flags; 0 if none, -1 for sizes or flags that it refuses. */
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags);
 
 /* ---------------------------------------------------------------------- */

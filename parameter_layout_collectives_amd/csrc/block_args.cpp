@@ -58,6 +58,26 @@ tide_status check_blocks(const char *name, const char *which, const void *codes,
     return TIDE_OK;
 }
 
+// Flags and sizes of a product; `known`: the flags it takes.
+tide_status check_product(const char *name, int64_t M, int64_t N, int64_t K, uint32_t flags,
+                          uint32_t known) {
+    tide_status st = check_flags(name, flags, known);
+    if (st != TIDE_OK) return st;
+    for (int64_t rows : {M, N})
+        for (int64_t cols : {N, K})
+            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
+    if (N > kMaxLine || K > kMaxLine)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
+    return TIDE_OK;
+}
+
+uint32_t known_flags(MmOp op) {
+    return TIDE_F_OUT_BF16 | (op == kMmDw ? TIDE_F_ACCUMULATE : 0u) |
+           (op == kMm ? TIDE_F_SHORT_SUMS : 0u);
+}
+constexpr uint32_t kLinearFlags =
+    TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 | TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS;
+
 tide_status check_block_plan(const char *name, const tide_plan *bp) {
     if (!bp) return bad(name, "plan is NULL");
     if (!bp->nblk) return bad(name, "not a plan of tide_plan_create_blocks");
@@ -157,16 +177,8 @@ tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void 
 }
 
 tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
-    const uint32_t known = TIDE_F_OUT_BF16 | (op == kMmDw ? TIDE_F_ACCUMULATE : 0u) |
-                           (op == kMm ? TIDE_F_SHORT_SUMS : 0u);
-    tide_status st = check_flags(name, g.flags, known);
+    tide_status st = check_product(name, g.M, g.N, g.K, g.flags, known_flags(op));
     if (st != TIDE_OK) return st;
-    if (g.M < 0 || g.N < 0 || g.K < 0) return bad(name, "negative size");
-    for (int64_t rows : {g.M, g.N})
-        for (int64_t cols : {g.N, g.K})
-            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
-    if (g.N > kMaxLine || g.K > kMaxLine)
-        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
     if (g.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
     if (g.workspace_bytes > 0 && !g.workspace) return bad(name, "workspace is NULL");
     if (g.workspace && misaligned(g.workspace, 16))
@@ -217,14 +229,8 @@ LinearChoice linear_choose(int64_t M, int64_t K) {
 
 tide_status check_linear(const LinearArgs &a) {
     const char *name = "tide_block_linear";
-    tide_status st = check_flags(name, a.flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 |
-                                                    TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS);
+    tide_status st = check_product(name, a.M, a.N, a.K, a.flags, kLinearFlags);
     if (st != TIDE_OK) return st;
-    for (int64_t rows : {a.M, a.N})
-        for (int64_t cols : {a.N, a.K})
-            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
-    if (a.N > kMaxLine || a.K > kMaxLine)
-        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
     if (a.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
     if (a.workspace_bytes > 0 && !a.workspace) return bad(name, "workspace is NULL");
     if (misaligned(a.workspace, 16)) return bad(name, "workspace is not 16-byte aligned");
@@ -298,10 +304,12 @@ using tide::fail;
 
 extern "C" {
 
-int64_t tide_block_cols(int64_t cols) { return cols < 0 ? -1 : tide::block_cols(cols); }
+int64_t tide_block_cols(int64_t cols) {
+    return cols < 0 || cols >= tide::kMaxDim ? -1 : tide::block_cols(cols);
+}
 
 int64_t tide_block_scale_cols(int64_t cols) {
-    return cols < 0 ? -1 : tide::block_scale_cols(cols);
+    return cols < 0 || cols >= tide::kMaxDim ? -1 : tide::block_scale_cols(cols);
 }
 
 tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int32_t *select,
@@ -350,7 +358,14 @@ tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int3
 }
 
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {
-    if (op < 0 || op > 3 || m < 0 || n < 0 || k < 0) return -1;
+    const char *name = "tide_block_workspace";
+    if (op < 0 || op > 3) {
+        bad(name, "op outside [0, 3]");
+        return -1;
+    }
+    const uint32_t known =
+        op == 3 ? tide::kLinearFlags : tide::known_flags(static_cast<tide::MmOp>(op));
+    if (tide::check_product(name, m, n, k, flags, known) != TIDE_OK) return -1;
     if (op == 3) {               // tide_block_linear: x's blocks, then the product's
         const tide::LinearChoice c = tide::linear_choose(m, k);
         if (c.in_one || n == 0) return 0;
