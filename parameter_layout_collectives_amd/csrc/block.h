@@ -68,7 +68,10 @@ struct MmChoice {
     int64_t chunk;       // of so many steps
     int64_t workspace;   // bytes for the pieces' sums
 };
-// aligned: dY's rows can be loaded in 16-byte pieces.
+// dY's rows can be loaded in 16-byte pieces (X's and W's codes always can).
+inline bool mm_aligned(MmOp op, const void *dy, int64_t N) {
+    return op == kMm || (reinterpret_cast<uintptr_t>(dy) % 16 == 0 && N % 8 == 0);
+}
 MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
                    bool may_split);
 

@@ -58,9 +58,10 @@ tide_status check_blocks(const char *name, const char *which, const void *codes,
     return TIDE_OK;
 }
 
-// Flags and sizes of a product; `known`: the flags it takes.
-tide_status check_product(const char *name, int64_t M, int64_t N, int64_t K, uint32_t flags,
-                          uint32_t known) {
+// Flags and sizes of a product; `known`: the flags it takes.  A launch counts its
+// lanes in 32 bits: that too is checked here, before anything is enqueued.
+tide_status check_product(const char *name, MmOp op, int64_t M, int64_t N, int64_t K,
+                          uint32_t flags, uint32_t known, bool aligned) {
     tide_status st = check_flags(name, flags, known);
     if (st != TIDE_OK) return st;
     for (int64_t rows : {M, N})
@@ -68,6 +69,12 @@ tide_status check_product(const char *name, int64_t M, int64_t N, int64_t K, uin
             if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
     if (N > kMaxLine || K > kMaxLine)
         return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
+    const int64_t rows = op == kMmDw ? N : M, cols = op == kMm ? N : K;
+    const MmChoice c = mm_choose(op, M, N, K, flags, aligned, true);
+    const int64_t tiles = ((rows + c.tile - 1) / c.tile) * ((cols + c.tile - 1) / c.tile);
+    const int64_t cut = (tiles - c.direct) * c.splits;
+    if (tiles + cut > 0xffffffffll / 512 || cut * (c.tile * c.tile / 1024) > 0xffffffffll / 256)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
     return TIDE_OK;
 }
 
@@ -177,7 +184,8 @@ tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void 
 }
 
 tide_status check_mm(MmOp op, const char *name, const MmArgs &g) {
-    tide_status st = check_product(name, g.M, g.N, g.K, g.flags, known_flags(op));
+    tide_status st = check_product(name, op, g.M, g.N, g.K, g.flags, known_flags(op),
+                                   mm_aligned(op, g.a, g.N));
     if (st != TIDE_OK) return st;
     if (g.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
     if (g.workspace_bytes > 0 && !g.workspace) return bad(name, "workspace is NULL");
@@ -229,7 +237,7 @@ LinearChoice linear_choose(int64_t M, int64_t K) {
 
 tide_status check_linear(const LinearArgs &a) {
     const char *name = "tide_block_linear";
-    tide_status st = check_product(name, a.M, a.N, a.K, a.flags, kLinearFlags);
+    tide_status st = check_product(name, kMm, a.M, a.N, a.K, a.flags, kLinearFlags, true);
     if (st != TIDE_OK) return st;
     if (a.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
     if (a.workspace_bytes > 0 && !a.workspace) return bad(name, "workspace is NULL");
@@ -363,9 +371,11 @@ int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32
         bad(name, "op outside [0, 3]");
         return -1;
     }
-    const uint32_t known =
-        op == 3 ? tide::kLinearFlags : tide::known_flags(static_cast<tide::MmOp>(op));
-    if (tide::check_product(name, m, n, k, flags, known) != TIDE_OK) return -1;
+    const tide::MmOp mm = op == 3 ? tide::kMm : static_cast<tide::MmOp>(op);
+    const uint32_t known = op == 3 ? tide::kLinearFlags : tide::known_flags(mm);
+    if (tide::check_product(name, mm, m, n, k, flags, known, tide::mm_aligned(mm, nullptr, n)) !=
+        TIDE_OK)
+        return -1;
     if (op == 3) {               // tide_block_linear: x's blocks, then the product's
         const tide::LinearChoice c = tide::linear_choose(m, k);
         if (c.in_one || n == 0) return 0;

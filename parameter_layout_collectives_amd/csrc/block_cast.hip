@@ -359,6 +359,11 @@ int32_t repeats(const tide_plan *bp, Fill fill, int32_t j, int32_t p, Step *step
 // one launch instead of four, its 16 casts 632 us instead of 784.
 template <class Fill, class Launch>
 tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Launch launch) {
+    for (int32_t i = 0; i < bp->nblk; i++) {     // before anything is enqueued
+        Rows r;
+        fill(i, &r);
+        if (chunks_of(r) > kMaxGrid) return too_many(name);
+    }
     int32_t j = 0;
     while (j < bp->nblk) {
         Slots<kPerLaunch> a;
@@ -398,10 +403,7 @@ tide_status over_matrices(const char *name, const tide_plan *bp, Fill fill, Laun
             }
             j += p * static_cast<int32_t>(n);
         }
-        if (a.n == 0) {
-            if (j < bp->nblk) return too_many(name);
-            break;
-        }
+        if (a.n == 0) break;
         if (a.n <= kFew) {
             Slots<kFew> few;
             few.n = a.n;

@@ -938,7 +938,7 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
         clear_error();
         return TIDE_OK;
     }
-    p.aligned = op == kMm || (reinterpret_cast<uintptr_t>(a.a) % 16 == 0 && a.N % 8 == 0);
+    p.aligned = mm_aligned(op, a.a, a.N);
     MmChoice c = mm_choose(op, a.M, a.N, a.K, a.flags, p.aligned, true);
     if (c.workspace > a.workspace_bytes)
         c = mm_choose(op, a.M, a.N, a.K, a.flags, p.aligned, false);
@@ -956,9 +956,6 @@ tide_status run_mm(MmOp op, const char *name, const MmArgs &a, void *stream) {
     p.partial = static_cast<float *>(a.workspace);
     const int64_t tr = (p.rows + c.tile - 1) / c.tile, tc = (p.cols + c.tile - 1) / c.tile;
     const int64_t cut = (tr * tc - c.direct) * c.splits;
-    if (tr * tc > 0xffffffffll / 512 || cut * (c.tile * c.tile / 1024) > 0xffffffffll / 256 ||
-        (p.cols + 15) / 16 > 0xffffffffll / 512)
-        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
     p.tr = static_cast<uint32_t>(tr);
     p.tc = static_cast<uint32_t>(tc);
     const dim3 grid(static_cast<unsigned>(c.direct + cut));

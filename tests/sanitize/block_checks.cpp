@@ -2,6 +2,8 @@
 // choice of a product's kernel) under AddressSanitizer and
 // UndefinedBehaviorSanitizer.  Built with g++ from csrc/plan.cpp,
 // csrc/block_args.cpp and this file only: no HIP call, no GPU.
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <limits>
@@ -40,7 +42,10 @@ void workspace_refusals() {
         }
         EXPECT(tide_block_workspace(op, 64, (1 << 22) + 1, 64, kBf16) == -1);
         EXPECT(tide_block_workspace(op, 64, 64, 1 << 23, kBf16) == -1);
-        EXPECT(tide_block_workspace(op, (int64_t(1) << 31) - 1, 1 << 22, 1 << 22, kBf16) >= 0);
+        EXPECT(tide_block_workspace(op, int64_t(3) << 29, 8, 1, kBf16) >= 0);
+        EXPECT((tide_block_workspace(op, 1, 1 << 22, 1 << 22, kBf16) == -1) == (op == 2));
+        // more lanes than a launch counts
+        EXPECT(tide_block_workspace(op, (int64_t(1) << 31) - 1, 1 << 22, 1 << 22, kBf16) == -1);
         EXPECT(tide_block_workspace(op, 64, -1, 64, kBf16) == -1);
         EXPECT(tide_block_workspace(op, 64, 64, 64, 0x80000000u) == -1);
         EXPECT((tide_block_workspace(op, 64, 64, 64, kBf16 | TIDE_F_ACCUMULATE) == -1) == (op != 2));
@@ -89,6 +94,15 @@ void choices(std::mt19937_64 &g) {
     };
     for (int t = 0; t < 20000; t++) {
         const int64_t M = size(t % 3 ? 15 : 30), N = size(t % 3 ? 15 : 22), K = size(t % 3 ? 15 : 22);
+        // twice as many lanes as a launch counts and more, or an eighth as many and less
+        const double most = std::max({1.0 * M * N, 1.0 * M * K, 1.0 * N * K});
+        if (most > std::ldexp(1.0, 36)) {
+            if (1.0 * M * N > std::ldexp(1.0, 40)) {
+                EXPECT(tide_block_workspace(0, M, N, K, kBf16) == -1);
+                EXPECT(tide_block_workspace(3, M, N, K, kBf16) == -1);
+            }
+            continue;
+        }
         for (int op = 0; op < 3; op++) choice(op, M, N, K, g() % 2 ? kBf16 : 0);
         choice(0, M, N, K, kShort);
         for (uint32_t f : {uint32_t(0), kBf16, kShort, kBf16 | TIDE_F_GRAD_F16}) {
