@@ -48,13 +48,20 @@ constexpr int64_t kSkinnyShort = 16;
 constexpr int64_t kSkinnyMost = 64;
 constexpr int64_t kSkinnyWeights = int64_t(1) << 24;
 // x's blocks are made inside the product for one row of at most 28 KB of codes,
-// or more rows of at most 8 KB together: every workgroup repeats that work.  One
-// row, n = 14336, k = 4096: 16.2 us, as the product alone; 8 rows: 30.1 us
-// (product alone 17.1, and a launch for the blocks about 4).
+// or more rows of at most 8 KB together: every workgroup repeats that work.
+// In one launch against two, us:
+//   one row, n = 8192:    k = 24576 41 / 47, 28672 49 / 55, 32768 66 / 62
+//   n = 14336, k = 4096:  1 row 15.6 / 18.8, 2: 17.6 / 20.2, 3: 19.3 / 20.4,
+//                         4: 21.2 / 20.8, 8: 28.2 / 22.1
+//   16 rows, n = 4096:    k = 512 3.5 / 6.2, 1024 7.2 / 8.2
 constexpr int64_t kInOneRows = 16;
 constexpr int64_t kInOneRow = 28672;     // 56 KB of LDS
 constexpr int64_t kInOneBytes = 8192;
-// The least steps in a piece of a cut sum, and the most pieces.
+// The least steps (64 or 128 values) in a piece of a cut sum, and the most pieces.
+// 4 steps against 8, us: 512 x 512 over 512 6.6 / 5.2, over 2048 11.7 / 9.2;
+// 512 x 1024 over 1024 11 / 10; 64 x 64 over 512 5.7 / 4.7, over 1024 5.9 / 6.7;
+// 128 x 512 over 1024 6.4 / 7.0.  16 pieces against 8 and 32, over 16384: 64 x 64
+// (dW) 11.0 / 14.8 / 10.3, 128 x 512 12.8 / 15.6 / 15.3.
 constexpr int64_t kMinSplitSteps = 4;
 constexpr int64_t kMaxSplits = 16;
 

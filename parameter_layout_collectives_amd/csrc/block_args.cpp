@@ -275,7 +275,18 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     const int64_t steps = (sum + step - 1) / step;
     auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); };
     // Large tiles once they fill three quarters of the card, small ones (not in
-    // the 8-bit kernel) while middle ones would leave half of it idle.
+    // the 8-bit kernel) while middle ones would leave half of it idle.  x w^T, us:
+    //   256 / 128 wide over 1024 and 8192:
+    //     2560 x 3328 (130 large tiles)  34 / 36, 186 / 156
+    //     2816 x 4096 (176)              33 / 35, 187 / 227
+    //     3584 x 3584 (196)              35 / 43, 187 / 279
+    //   128 / 64 wide over 512, 2048 and 8192:
+    //     1024 x 1152 (72 middle tiles)  14 / 7, 27 / 18, 39 / 61
+    //     1280 x 1280 (100)              17 / 7, 26 / 18, 46 / 63
+    //     1408 x 1536 (132)              22 / 8, 27 / 21, 62 / 67
+    //     1920 x 1920 (225)              24 / 11, 32 / 29, 83 / 105
+    // So the borders lie where sums of about 8192 (large tiles) and 4096 (small
+    // ones) change sides; shorter and longer ones would have theirs elsewhere.
     c.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256
              : !eight && tiles(128) < kCus / 2     ? 64
                                                    : 128;
@@ -286,9 +297,12 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     c.workspace = 0;
     if (c.kernel == kMmSkinny || !may_split) return c;
     // The tiles that run at one time; what is left after whole sets of them is
-    // cut if that leaves at least half of the card idle.  The pieces' sums go
-    // through memory, so a piece has at least kMinSplitSteps steps, and behind
-    // whole sets (where one is long) at least four times that.
+    // cut if that leaves at least half of the card idle (more tiles could not be
+    // cut in two: 256 + 128 large tiles, 4096 x 6144, over 8192: cut 330 us, else
+    // 384).  The pieces' sums go through memory, so a piece has at least
+    // kMinSplitSteps steps, and behind whole sets (where one is long) at least four
+    // times that (256 + 16 large tiles, 4352 x 4096, over 2048: pieces of 16 steps
+    // 90 us, of 8 82, not cut 105; over 8192 243, 242, cut in fewer 257).
     const int64_t full = kCus * (c.tile == 256 ? 1 : 2);
     const int64_t left = t % full, least = t < full ? kMinSplitSteps : 4 * kMinSplitSteps;
     if (left == 0 || left * 2 > full || steps < 2 * least) return c;
