@@ -354,8 +354,9 @@ int64_t tide_block_cols(int64_t cols);
 int64_t tide_block_scale_cols(int64_t cols);
 
 /* Write x [rows, cols] (bf16; fp16 or fp32 by TIDE_F_GRAD_F16 / _F32) in 8-bit
- * blocks.  Any element alignment of x; 16-byte aligned x with cols a multiple
- * of 8 takes the vector path.  The outputs may not overlap x or each other. */
+ * blocks.  Any element alignment of x and any width of its rows are read in
+ * vectors, all but a row's last elements.  The outputs may not overlap x or each
+ * other. */
 tide_status tide_block_quant(const void *x, int64_t rows, int64_t cols, void *codes,
                              void *scales, uint32_t flags, void *stream);
 

@@ -94,7 +94,9 @@ class Blocks:
     """A matrix [rows, cols] in 8-bit blocks.
 
     codes: [rows, cols rounded up to 128], float8_e4m3fn or uint8.
-    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu.
+    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu,
+    10 to 246.  Codes past the last column are 0 and scales past the last block 127,
+    as block_quant, block_shard and ag() write them: the products count on it.
     Either may be replaced by another tensor of its shape, and its storage may be
     released and restored in between, as an FSDP unit does with gathered weights:
     every call asks the tensors where they are, and refuses one without memory."""
@@ -299,6 +301,8 @@ class _Linear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         wc, ws, *q = ctx.saved_tensors
+        # dy enters the bf16 matrix instruction, as w and q do exactly: an fp32 dy is
+        # rounded to 8 significant bits here, where w and q hold 4.
         dy = dy.to(torch.bfloat16).contiguous()
         dx = None
         if ctx.needs_input_grad[0]:

@@ -35,15 +35,19 @@ enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
 
 // The card's compute units: a product's tiles are counted against them.
 constexpr int64_t kCus = 256;
-// The skinny kernel takes up to 32 rows (16 against the 8-bit instruction's
+// The skinny kernel takes up to 24 rows (16 against the 8-bit instruction's
 // tiles), and up to 64 if W is small: there the second launch of a cut sum costs
-// more than the tiles gain.  Skinny against tiles with fp32 sums and join, us:
-//   n = 8192, k = 28672:  17 rows 73 / 88, 28: 89 / 93, 32: 95 / 94, 48: 131 / 100
-//   n = 14336, k = 4096:  17 rows 23 / 27, 28: 27 / 28, 32: 29 / 28, 64: 49 / 29
+// more than the tiles gain.  Skinny against tiles with fp32 sums and join, us, W
+// from memory (and from the last-level cache, where tiles gain more):
+//   n = 8192, k = 28672:  17 rows 73 / 88 (64 / 61), 24: 83 / 90 (74 / 63),
+//                         28: 88 / 92 (80 / 64), 32: 95 / 94 (85 / 70)
+//   n = 14336, k = 4096:  17 rows 23 / 27 (22 / 21), 24: 25 / 27 (23 / 22),
+//                         28: 27 / 28 (26 / 22), 32: 29 / 28 (27 / 22)
+//   n = k = 5120:         17 rows 13 / 14, 20: 14 / 14, 24: 15 / 14, 32: 17 / 15
 //   n = k = 4096:         32 rows 9.4 / 12.0, 48: 11.7 / 12.9, 64: 13.2 / 14.0
 //   n = k = 2048:         40 rows 6.2 / 8.7, 64: 7.3 / 9.5
 // and against the 8-bit instruction's, n = 8192, k = 28672, 32 rows: 95 / 61.
-constexpr int64_t kSkinnyRows = 32;
+constexpr int64_t kSkinnyRows = 24;
 constexpr int64_t kSkinnyShort = 16;
 constexpr int64_t kSkinnyMost = 64;
 constexpr int64_t kSkinnyWeights = int64_t(1) << 24;

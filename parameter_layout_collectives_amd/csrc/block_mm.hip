@@ -186,8 +186,8 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // are 8 chunks of 16 bytes; chunk h of row r lies at h ^ (r & 7) in LDS, so the
 // 16 lanes that read one chunk of 16 rows touch all banks.  Operand k-order
 // inside a step is free as long as both sides agree: a lane reads chunks g and
-// g + 4 (g = lane / 16).  Two buffers: the next step's codes travel to registers
-// while this one is multiplied.
+// g + 4 (g = lane / 16).  Two buffers: the next step's codes travel straight into
+// the other one while this one is multiplied.
 //
 // 256 x 256 tiles, 8192 x 8192 x 8192: 0.43 ms, 2.5 PFLOP/s (torch's product of
 // the same 8-bit numbers without block scales: 3.2); 8192 x 28672 x 8192: 1.7 ms.
@@ -196,8 +196,11 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // faster, leaving out most LDS reads nothing.  Slower here: 32 x 32 x 64
 // fragments (6%), a burst of all loads behind the barrier (2%), a raised wave
 // priority around the multiplications (3%).
+
 // Buffer descriptor of `bytes` bytes at p (the same in all lanes): loads past
-// its end give zeros.
+// its end give zeros.  The end is compared with the lane's offset plus the scalar
+// one and does not wrap: checked on the card for every form of load used here,
+// with sums past 2^32 too, as is that only the words past the end become zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char *p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, static_cast<int>(bytes),
                                              0x00020000);
@@ -391,7 +394,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void eight_kernel(MmLaunch p) {
 //
 // 8192 x 8192 x 8192: dX 0.72 to 0.84 ms, dW 0.75 to 0.87 ms (torch's bf16 product
 // on the same cards 0.67 to 0.73 ms, 0.90 to 0.98 ms with its left operand
-// transposed), fp32 product 0.83 to 0.90 ms; matrix units busy 62% of the cycles,
+// transposed), Y 0.81 to 0.90 ms; matrix units busy 62% of the cycles,
 // clock 1.7 to 2.0 GHz.
 //
 // A step of the sum is 64 values.  LDS layouts of an operand's tile:

@@ -132,8 +132,8 @@ void variants() {
     };
     const Row rows[] = {
         {0, 16, 200, 700, kBf16, true, tide::kMmSkinny, 64, false},
-        {0, 32, 8192, 4099, kBf16, true, tide::kMmSkinny, 128, false},
-        {0, 33, 8192, 4099, kBf16, true, tide::kMmWide, 64, true},
+        {0, 24, 8192, 4099, kBf16, true, tide::kMmSkinny, 128, false},
+        {0, 25, 8192, 4099, kBf16, true, tide::kMmWide, 64, true},
         {0, 64, 300, 520, kBf16, true, tide::kMmSkinny, 64, false},
         {0, 65, 72, 2048, kBf16, true, tide::kMmWide, 64, true},
         {0, 1500, 1510, 2060, kBf16, true, tide::kMmWide, 128, true},

@@ -78,7 +78,7 @@ def test_products_of_few_rows(shape):
     check_products(*shape)
 
 
-@pytest.mark.parametrize("shape", [(32, 8192, 4099), (33, 8192, 4099)])
+@pytest.mark.parametrize("shape", [(24, 8192, 4099), (25, 8192, 4099), (33, 8192, 4099)])
 def test_products_of_a_large_w(shape):
     check_products(*shape)
 
