@@ -76,7 +76,6 @@ def _no_dual(t, what):
 
 
 def _matrix(t, what, dtypes):
-    _no_dual(t, what)
     if t.dtype not in dtypes:
         raise TypeError(f"{what} is {t.dtype}, expected one of "
                         f"{', '.join(str(d).replace('torch.', '') for d in dtypes)}")
@@ -88,6 +87,12 @@ def _same_device(device, *tensors):
     for t in tensors:
         if t.device != device:
             raise ValueError(f"tensors on {device} and {t.device}")
+
+
+def _values(t, what, dtypes):
+    """_matrix for numbers that a derivative could go through."""
+    _no_dual(t, what)
+    _matrix(t, what, dtypes)
 
 
 class Blocks:
@@ -175,7 +180,7 @@ def _out(out, shape, dtype, dtypes, device, what):
         if dtype not in dtypes:
             raise TypeError(f"{what} cannot be {dtype}")
         return torch.empty(shape, dtype=dtype, device=device)
-    _matrix(out, what, dtypes)
+    _values(out, what, dtypes)
     _same_device(device, out)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {tuple(shape)}")
@@ -185,7 +190,7 @@ def _out(out, shape, dtype, dtypes, device, what):
 def block_quant(x, out=None):
     """x [rows, cols] (bf16, fp16 or fp32) in 8-bit blocks: `out` or new Blocks.
     They carry no gradient to x."""
-    _matrix(x, "x", _IN_TYPES)
+    _values(x, "x", _IN_TYPES)
     rows, cols = x.shape
     if out is None:
         out = Blocks.empty(rows, cols, x.device)
@@ -242,7 +247,7 @@ def block_mm(x, w, out=None, dtype=torch.bfloat16, short_sums=False):
 
 def block_mm_dx(dy, w, out=None, dtype=torch.bfloat16):
     """dy w for dy [m, n] in bf16 and w [n, k] in 8-bit blocks: [m, k] in bf16 or fp32."""
-    _matrix(dy, "dy", (torch.bfloat16,))
+    _values(dy, "dy", (torch.bfloat16,))
     if dy.shape[1] != w.rows:
         raise ValueError(f"dy has {dy.shape[1]} columns, w has {w.rows} rows")
     _same_device(dy.device, w)
@@ -258,7 +263,7 @@ def block_mm_dx(dy, w, out=None, dtype=torch.bfloat16):
 def block_mm_dw(dy, x, out=None, dtype=torch.bfloat16, accumulate=False):
     """dy^T x for dy [m, n] in bf16 and the checkpoint x [m, k] in 8-bit blocks:
     [n, k] in bf16 or fp32; with accumulate, added to what `out` holds."""
-    _matrix(dy, "dy", (torch.bfloat16,))
+    _values(dy, "dy", (torch.bfloat16,))
     if dy.shape[0] != x.rows:
         raise ValueError(f"dy has {dy.shape[0]} rows, x has {x.rows}")
     if accumulate and out is None:
