@@ -189,10 +189,11 @@ __global__ __launch_bounds__(256) void zero_kernel(char *out, int64_t n, int es)
 // g + 4 (g = lane / 16).  Two buffers: the next step's codes travel straight into
 // the other one while this one is multiplied.
 //
-// 256 x 256 tiles, 8192 x 8192 x 8192: 0.43 ms, 2.5 PFLOP/s (torch's product of
-// the same 8-bit numbers without block scales: 3.2); 8192 x 28672 x 8192: 1.7 ms.
-// Counters there: matrix units busy 55% of the cycles, LDS 26%, no bank conflicts,
-// clock about 2.1 GHz.  Leaving out three quarters of the loads makes it 15%
+// 256 x 256 tiles, 8192 x 8192 x 8192: 0.43 to 0.48 ms, 2.3 to 2.5 PFLOP/s (torch's
+// product of the same 8-bit numbers without block scales: 3.2); 8192 x 28672 x
+// 8192: 1.7 ms.  Counters there: matrix units busy 53 to 62% of the cycles, LDS 25
+// to 30%, no bank conflicts, waits in 35 to 43% of the wave cycles, clock 1.8 to 2.1
+// GHz.  Leaving out three quarters of the loads makes it 15%
 // faster, leaving out most LDS reads nothing.  Slower here: 32 x 32 x 64
 // fragments (6%), a burst of all loads behind the barrier (2%), a raised wave
 // priority around the multiplications (3%).
