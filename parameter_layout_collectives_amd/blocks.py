@@ -106,7 +106,7 @@ class Blocks:
     released and restored in between, as an FSDP unit does with gathered weights:
     every call asks the tensors where they are, and refuses one without memory."""
 
-    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_device")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_device", "_word_views")
 
     def __init__(self, codes, scales, cols):
         self._set(codes, scales, int(cols))
@@ -120,7 +120,7 @@ class Blocks:
                 or tuple(scales.shape) != (rows, _scale_cols(cols)):
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
                              f"hold {rows} rows of {cols} columns")
-        self._codes, self._scales = codes, scales
+        self._codes, self._scales, self._word_views = codes, scales, None
         self._rows, self._cols, self._device = rows, cols, codes.device
 
     @classmethod
@@ -130,6 +130,7 @@ class Blocks:
                                   device=device)
         self._scales = torch.empty((rows, _scale_cols(cols)), dtype=torch.uint8, device=device)
         self._rows, self._cols, self._device = rows, cols, self._codes.device
+        self._word_views = None
         return self
 
     @property
@@ -149,6 +150,7 @@ class Blocks:
         self._replace(self._codes, t)
 
     def _replace(self, codes, scales):
+        _matrix(codes, "codes", (torch.float8_e4m3fn, torch.uint8))
         if codes.shape[0] != self._rows:
             raise ValueError(f"codes of {codes.shape[0]} rows in place of {self._rows}")
         self._set(codes, scales, self._cols)
@@ -168,6 +170,12 @@ class Blocks:
     @property
     def shape(self):
         return self._rows, self._cols
+
+    def words(self):
+        """(codes, scales) as int32 views."""
+        if self._word_views is None:
+            self._word_views = _words(self._codes), _words(self._scales)
+        return self._word_views
 
     @property
     def _ptrs(self):
@@ -326,8 +334,9 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
     """A linear layer: x [..., k] times w [n, k] (8-bit blocks) -> [..., n].
 
     x (bf16, fp16 or fp32, contiguous) becomes 8-bit blocks, which are all that
-    is kept of it for the backward pass, and only for the weights' gradient.  dtype: the output's, bf16 or fp32
-    (default: fp32 for an fp32 x, else bf16).  short_sums: see block_mm.
+    is kept of it for the backward pass, and only for the weights' gradient.
+    dtype: the output's, bf16 or fp32 (default: fp32 for an fp32 x, else bf16).
+    short_sums: see block_mm.
     The backward pass takes the output's gradient in bf16, returns x's gradient
     in x's dtype, treating the rounding of x to 8 bits as the identity, and
     writes the weights' gradient to `grad` ([n, k], bf16 or fp32; as the
@@ -355,7 +364,8 @@ def block_linear(x, w, dtype=None, grad=None, accumulate=False, short_sums=False
         # lies on x's device, made under the forward pass's stream: autograd joins
         # the stream that calls backward() with those of device leaves, so that
         # `grad` may be read there.
-        anchor = torch.empty(0, device=x.device, requires_grad=True) if grad is not None else None
+        anchor = None if grad is None else \
+            torch.empty(0, dtype=torch.float32, device=x.device, requires_grad=True)
         y = _Linear.apply(x, anchor, w, dtype, grad, accumulate, short_sums)
     else:
         y = _linear(x, w, dtype, short_sums)
@@ -411,7 +421,8 @@ class BlockPlan(Plan):
         """The int32 views of a list of Blocks that ag() takes as parameters."""
         if [b.shape for b in blocks] != self.matrices:
             raise ValueError("need one Blocks per matrix, of its shape")
-        return [_words(b.codes) for b in blocks] + [_words(b.scales) for b in blocks]
+        words = [b.words() for b in blocks]
+        return [c for c, _ in words] + [s for _, s in words]
 
 
 def block_shard(plan, rank, master, block):

@@ -33,7 +33,8 @@ inline int elem_size(ElemType t) { return t == kElemF32 ? 4 : 2; }
 //   kMmDw  i = row of W, j = column, c = token: I = dY transposed, J = X
 enum MmOp { kMm = 0, kMmDx = 1, kMmDw = 2 };
 
-// The card's compute units: a product's tiles are counted against them.
+// MI355X's compute units: a product's tiles are counted against them.  Fewer of
+// them (a partition of the card) would change the choice's speed, not its results.
 constexpr int64_t kCus = 256;
 // The skinny kernel takes up to 24 rows (16 against the 8-bit instruction's
 // tiles), and up to 64 if W is small: there the second launch of a cut sum costs

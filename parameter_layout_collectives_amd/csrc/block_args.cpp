@@ -393,7 +393,8 @@ int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32
     if (op == 3) {               // tide_block_linear: x's blocks, then the product's
         const tide::LinearChoice c = tide::linear_choose(m, k);
         if (c.in_one || n == 0) return 0;
-        return c.blocks + tide_block_workspace(0, m, n, k, flags & (TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS));
+        return c.blocks +
+               tide_block_workspace(0, m, n, k, flags & (TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS));
     }
     // whichever way dY is aligned
     int64_t most = 0;

@@ -67,3 +67,28 @@ def test_a_replacement_has_to_fit():
         with pytest.raises(AttributeError):
             setattr(q, name, value)
     assert q.shape == (4, 200)
+
+
+def test_views_follow_the_tensors():
+    plan = tide.BlockPlan(tide.Plan([(64, 1000)], 2))
+    q = tide.Blocks.empty(64, 1000, device="cpu")
+    first = plan.views([q])
+    assert [v.data_ptr() for v in first] == list(q._ptrs)
+    for t in (q.codes, q.scales):
+        size = t.untyped_storage().nbytes()
+        t.untyped_storage().resize_(0)
+        hold = torch.empty(size, dtype=torch.uint8)
+        t.untyped_storage().resize_(size)
+        del hold
+    assert [v.data_ptr() for v in plan.views([q])] == list(q._ptrs)
+
+
+def test_views_of_replaced_tensors(monkeypatch):
+    monkeypatch.setattr(impl, "_words", lambda t: t.at)
+    plan = tide.BlockPlan(tide.Plan([(8, 200)], 2))
+    w = blocks_at(8, 200, 3 << 20, 4 << 20)
+    assert plan.views([w]) == [3 << 20, 4 << 20]
+    w.codes = _At(6 << 20, (8, 256), torch.uint8)
+    assert plan.views([w]) == [6 << 20, 4 << 20]
+    w.scales = _At(7 << 20, (8, 4), torch.uint8)
+    assert plan.views([w]) == [6 << 20, 7 << 20]

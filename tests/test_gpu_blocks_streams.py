@@ -67,3 +67,54 @@ def test_frozen_weights_keep_nothing_of_x(m):
     assert torch.equal(y, same)
     y.backward(dy)
     assert torch.equal(x.grad, tide.block_mm_dx(dy, w))
+
+
+def test_weight_gradient_of_autograd_grad():
+    """The same through torch.autograd.grad(), which runs no leaf's accumulation."""
+    note("block_linear autograd.grad from another stream")
+    m, n, k = 200, 264, 392
+    w, dy, x = tide.block_quant(rand((n, k), 2, FP, 0.02)), rand((m, n), 3, BF, 1e-3), rand((m, k), 1)
+    big = rand((4096, 4096), 4)
+    want = tide.block_mm_dw(dy, tide.block_quant(x), dtype=FP)
+    dw = torch.full((n, k), 7.0, device="cuda")
+    xl = x.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = tide.block_linear(xl * 1.0, w, grad=dw)
+        for _ in range(20):
+            big @ big
+    dx, = torch.autograd.grad(y, xl, dy)
+    got, dx = dw.clone(), dx.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(dx, tide.block_mm_dx(dy, w))
+
+
+def test_captured_weight_gradient_alone():
+    """A captured forward and backward pass over an x that needs no gradient."""
+    note("block_linear captured, x without gradient")
+    m, n, k = 70, 96, 640
+    w, dy = tide.block_quant(rand((n, k), 43, FP, 0.02)), rand((m, n), 44, BF, 1e-3)
+    x, dw = rand((m, k), 45), torch.zeros(n, k, device="cuda")
+
+    def step(grad):
+        y = tide.block_linear(x, w, grad=grad, accumulate=True)
+        y.backward(dy)
+        return y.detach()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(torch.zeros_like(dw))                     # one pass outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=side):
+        y = step(dw)
+    total = torch.zeros_like(dw)
+    dw.zero_()
+    for it in range(3):
+        x.copy_(rand((m, k), 46 + it))
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, step(total)) and torch.equal(dw, total)
