@@ -240,8 +240,8 @@ def block_mm(x, w, out=None, dtype=torch.bfloat16, short_sums=False):
 
     Sums are held in fp32.  With short_sums (bf16 only) the 8-bit matrix
     instruction adds the products of more than 16 rows: up to twice as fast, off by
-    up to 2^-12 of the sum of the products' magnitudes, which matters where large
-    products cancel (TIDE_F_SHORT_SUMS in include/tide.h)."""
+    up to about 2^-10 of the sum of the products' magnitudes, which matters where
+    large products cancel (TIDE_F_SHORT_SUMS in include/tide.h)."""
     if x.cols != w.cols:
         raise ValueError(f"x has {x.cols} columns, w has {w.cols}")
     _same_device(x.device, w)

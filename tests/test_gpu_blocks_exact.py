@@ -130,8 +130,8 @@ def test_operands_between_nans(shape):
 @pytest.mark.parametrize("shape", [(17, 64, 700), (40, 5000, 4099), (130, 200, 392), (500, 300, 2000),
                                    (2100, 1100, 1300), (4000, 4104, 1100)])
 def test_short_sums(shape):
-    """The 8-bit instruction's sums, where the caller asks for them: within the
-    documented 2^-12 of the products' magnitudes, through every entry point."""
+    """The 8-bit instruction's sums, where the caller asks for them, on normal data
+    and through every entry point."""
     m, n, k = shape
     note(f"block products with short sums {shape}")
     g = torch.Generator(device="cuda").manual_seed(3)
@@ -152,3 +152,51 @@ def test_short_sums(shape):
                  lambda: tide.block_linear(xr, w, dtype=FP, short_sums=True)):
         with pytest.raises(ValueError):
             call()
+
+
+def scaled_exponents(v):
+    """The exponent that each e4m3 value stands under: subnormals under -6."""
+    return torch.where(v == 0, -1000, (torch.frexp(v)[1] - 1).clamp_min(-6)).float()
+
+
+def short_bound(x, w):
+    """What short sums may lose of x w^T, codes under the scale 2^0: of 8 neighbouring
+    products those that lie below 2^-13 of the largest exponent's power, 7 of them."""
+    ex, ew = scaled_exponents(x), scaled_exponents(w)
+    total = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=x.device)
+    for k in range(0, x.shape[1], 8):
+        e = (ex[:, None, k:k + 8] + ew[None, :, k:k + 8]).amax(2).double()
+        total += 7 * 2.0 ** -13 * torch.exp2(e)
+    return total
+
+
+def code_blocks(v):
+    """Blocks whose codes are v itself, under the scale 2^0."""
+    q = tide.Blocks.empty(*v.shape)
+    q.codes.view(torch.uint8).zero_()
+    q.scales.fill_(127)
+    q.codes.view(torch.uint8)[:, :v.shape[1]] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+    return q
+
+
+@pytest.mark.parametrize("large", [(448.0, 448.0), (256.0, 256.0), (1.0, 1.0), (256.0, 2.0 ** -9),
+                                   (2.0 ** -9, 2.0 ** -9)])
+@pytest.mark.parametrize("k,apart", [(128, 1), (128, 64), (1100, 8)])
+def test_short_sums_lose_what_is_documented(large, k, apart):
+    """Large products that cancel, inside a group of 8 and across groups, beside
+    every pair of codes: what is lost stays within the documented bound."""
+    note(f"short sums beside {large}, k={k}, {apart} apart")
+    t = ref.e4m3_table()[:127].float().cuda()
+    x, w = t[:, None].repeat(1, k), t[:, None].repeat(1, k)
+    for at in range(0, k - 127, 128):
+        x[:, at] = x[:, at + apart] = large[0]
+        w[:, at], w[:, at + apart] = large[1], -large[1]
+    q, r = code_blocks(x), code_blocks(w)
+    want, mass = ref.product(x.double(), w.double())
+    got = tide.block_mm(q, r, short_sums=True)
+    tol = short_bound(x, w) + mass * k * 2.0 ** -23
+    tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    assert bool(((got.double() - want).abs() <= tol).all())
+    # sums in fp32 keep what a sum of k products in fp32 keeps
+    assert ref.off(tide.block_mm(q, r), want, mass, k) <= 1.0
+    assert ref.off(tide.block_mm(q, r, dtype=FP), want, mass, k) <= 1.0
