@@ -17,7 +17,11 @@
  *                per-parameter tensors (no copy-out pass);
  *   tide_block_* matrices in 8-bit blocks: the gather of sharded weights at half
  *                the bytes, 8-bit activation checkpoints, and the products of a
- *                linear layer and of its backward pass over both.
+ *                linear layer and of its backward pass over both;
+ *   tide_mx_*    matrices in microscaled 4-bit blocks: their sharded gather, and
+ *                the products of a layer whose weights are frozen or serve;
+ *   tide_ortho   gradient matrices orthogonalised by Newton-Schulz products, the
+ *                update of a Muon optimizer between the two collectives.
  *
  * Notation.  N = world (ranks), P = nparams.  Parameter i is a row-major
  * tensor viewed as [dim0_i, inner_i] (inner = product of the trailing dims;
@@ -161,6 +165,9 @@ typedef struct tide_plan tide_plan;
  * bf16.  Where large products cancel, as outlier columns' may, it can be more than
  * the result itself. */
 #define TIDE_F_SHORT_SUMS 0x100u
+
+/* Flag, tide_mx_linear only: x enters the product as its 4-bit blocks hold it. */
+#define TIDE_F_QUANT_X 0x200u
 
 /* ---------------------------------------------------------------------- */
 /* Plan (host only; makes no HIP call).                                    */
@@ -439,6 +446,122 @@ tide_status tide_block_linear(const void *x, int64_t m, int64_t k, const void *w
 /* Bytes of workspace that the call `op` (0 mm, 1 mm_dx, 2 mm_dw, 3 linear) uses
  * for these sizes and flags; 0 if none, -1 for sizes or flags that it refuses. */
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags);
+
+/* ---------------------------------------------------------------------- */
+/* Matrices in microscaled 4-bit blocks: the gather of sharded weights at  */
+/* 0.53 bytes an element, and the products of a layer over them.           */
+/* ---------------------------------------------------------------------- */
+
+/* Format.  A row-major matrix [R, C] is held as
+ *   codes   [R, Cp / 2] bytes, Cp = tide_mx_cols(C) = C rounded up to 128; byte
+ *           c / 2 of a row holds the codes of columns c (even, its low half) and
+ *           c + 1
+ *   scales  [R, Cp / 32] bytes
+ * and element (r, c) is e2m1(code) * 2^(scales[r*Cp/32 + c/32] - 127).  e2m1 has a
+ * sign (the code's high bit) and the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 of codes
+ * 0 to 7.  A block is 32 columns of one row (the last one may be shorter), so a
+ * dim-0 shard boundary never cuts a block.  With a = max|x| over a block, its
+ * exponent e is the smallest integer with a <= 6 * 2^e, kept within [-125, 125] (0
+ * if a = 0), its scale byte e + 127, and each code the e2m1 number nearest to
+ * x * 2^-e, ties to the even code; |x| above 6 * 2^125 becomes that.  A block that
+ * holds an infinity or a NaN has scale byte 255 and codes 0 and stands for NaNs.
+ * Codes past column C are 0, scale bytes of blocks past it 127.  Every value of
+ * the format is a bf16 number.  Operands given to the calls below hold scale bytes
+ * of 2..252 or 255 and those zeros, as tide_mx_quant and tide_mx_shard write them.
+ *
+ * codes have to be 16-byte aligned and scales 4-byte aligned.  Sizes, graph
+ * capture, errors and streams as for the 8-bit blocks. */
+
+/* Cp for C columns (-1 if C < 0 or C >= 2^31). */
+int64_t tide_mx_cols(int64_t cols);
+
+/* As tide_block_quant and tide_block_dequant. */
+tide_status tide_mx_quant(const void *x, int64_t rows, int64_t cols, void *codes, void *scales,
+                           uint32_t flags, void *stream);
+tide_status tide_mx_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                             void *out, uint32_t flags, void *stream);
+
+/* As tide_plan_create_blocks, tide_block_shard and tide_block_unshard: parameter j
+ * of the new plan is [dim0, Cp/8] words, the codes, and parameter n + j is
+ * [dim0, Cp/128] words, the scales, of matrix select[j]. */
+tide_status tide_plan_create_mx(const tide_plan *plan, int32_t n, const int32_t *select,
+                                 tide_plan **out_plan);
+tide_status tide_mx_shard(const tide_plan *plan, int32_t rank, const float *master, void *block,
+                           uint32_t flags, void *stream);
+tide_status tide_mx_unshard(const tide_plan *plan, const void *gathered, void *const *params,
+                             uint32_t flags, void *stream);
+
+/* The products of a linear layer with weights W [n, k] in 4-bit blocks:
+ *   tide_mx_mm      out[m, n] = X W^T, X [m, k] in 4-bit blocks
+ *   tide_mx_linear  out[m, n] = x W^T, x [m, k] in bf16; with TIDE_F_QUANT_X
+ *                    tide_mx_quant of x (bf16; fp16 or fp32 by TIDE_F_GRAD_F16 /
+ *                    _F32) and the product of the blocks in one call, in one launch
+ *                    for few rows
+ *   tide_mx_mm_dx   dx[m, k]  = dY W, the output's gradient dY [m, n] in bf16
+ * (The weights' gradient does not read the weights: tide_block_mm_dw makes it from
+ * an 8-bit checkpoint of x.)  Rows without gaps, any element alignment of x and dY;
+ * n and k at most 2^22 (TIDE_E_UNSUPPORTED above).  The output is fp32, or bf16 with
+ * TIDE_F_OUT_BF16; it must not overlap an operand.  Products are exact and sums are
+ * held in fp32, those of two 4-bit factors too.  The same call gives the same bits.
+ * An empty sum gives zeros.
+ *   workspace  device memory of tide_mx_workspace() bytes, 16-byte aligned, used
+ *              during the call only.  With fewer bytes (NULL and 0) a call may be
+ *              slower and round differently; TIDE_F_QUANT_X with more than 16 rows
+ *              needs what x's blocks take (TIDE_E_INVALID with less). */
+tide_status tide_mx_mm(const void *x_codes, const void *x_scales, int64_t m, const void *w_codes,
+                        const void *w_scales, int64_t n, int64_t k, void *out, uint32_t flags,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+tide_status tide_mx_linear(const void *x, int64_t m, int64_t k, const void *w_codes,
+                            const void *w_scales, int64_t n, void *out, uint32_t flags,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+tide_status tide_mx_mm_dx(const void *dy, int64_t m, int64_t n, const void *w_codes,
+                           const void *w_scales, int64_t k, void *dx, uint32_t flags,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that the call `op` (0 mm, 1 mm_dx, 2 linear) uses for these
+ * sizes and flags; 0 if none, -1 for sizes or flags that it refuses. */
+int64_t tide_mx_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags);
+
+/* ---------------------------------------------------------------------- */
+/* Orthogonalised updates.                                                 */
+/* ---------------------------------------------------------------------- */
+
+/* For each of n matrices G = src[i] [rows[i], cols[i]] (row-major without gaps,
+ * bf16; fp16 or fp32 by TIDE_F_GRAD_F16 / _F32, one type for all), out[i] = X in
+ * bf16 after `steps` steps from X = G / ||G||_F:
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * with step s's a, b, c = coefficients[3*s .. 3*s+2].  An odd polynomial of X acts on
+ * its singular values alone; with 5 steps of (3.4445, -4.7750, 2.0315) those above
+ * 2e-3 of ||G||_F come to lie between 0.68 and 1.21, so X is G's nearest
+ * matrix with orthonormal rows (or columns, if it has more rows), roughly.  A zero
+ * matrix gives zeros, one that holds an infinity or a NaN gives NaNs.
+ *
+ * Exactness.  ||G||_F is summed in fp64, products in fp32.  Between products X is
+ * held in pairs of fp16 numbers (22 bits), X X^T and the polynomial's matrix as an
+ * fp32 diagonal and a rest in fp16, and the products' factors are fp16 numbers.
+ * Against 64 bits X is off by 3e-4 to 1e-3 of its norm, 1.6e-3 for matrices of a low
+ * rank, where its rounding to bf16 is 1.7e-3.  fp16's range asks for singular values
+ * of every step's X up to 3.9 and |b x^2 + c x^4| there up to 63; beyond that the
+ * result holds infinities or NaNs.
+ *
+ *   src, out      host arrays of n device pointers, element-aligned (NULL allowed
+ *                 for a matrix without elements).  An out may be its or another
+ *                 matrix's src (all are read first); two outs may not overlap.
+ *   rows, cols    host arrays; 0 to 2^22, the smaller of the two at most 2^15
+ *                 (TIDE_E_UNSUPPORTED above)
+ *   steps         1 to 64
+ *   coefficients  host array of 3 * steps finite floats
+ *   flags         TIDE_F_GRAD_F16, TIDE_F_GRAD_F32 or neither
+ *   workspace     device memory of tide_ortho_workspace() bytes, 256-byte aligned
+ *                 (TIDE_E_INVALID with fewer), used during the call only
+ * Keeps nothing between calls, allocates nothing, may be captured into a graph at
+ * any time; the same call gives the same bits, whatever else is in the list. */
+tide_status tide_ortho(int32_t n, const void *const *src, void *const *out, const int64_t *rows,
+                       const int64_t *cols, int32_t steps, const float *coefficients,
+                       uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for n matrices of these sizes, -1 for sizes that it refuses. */
+int64_t tide_ortho_workspace(int32_t n, const int64_t *rows, const int64_t *cols);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics.                                                            */

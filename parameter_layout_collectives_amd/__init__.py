@@ -7,6 +7,8 @@ kernels of libtide.so.  PyTorch supplies device memory and streams.
     rs(plan, rank, grads, out)                  # tide_rs  (TIDE-RS)
     ag(plan, rank_src, params)                  # tide_ag  (TIDE-AG placement)
     y = block_linear(x, w, grad=dw)             # a linear layer in 8-bit blocks (blocks.py)
+    y = fp4_linear(x, w)                        # ... in 4-bit blocks (fp4.py)
+    u = ortho(g)                                # a Muon update (ortho.py)
 
 TIDE-RS and TIDE-AG are described in "FSDP通信终局：TIDE零拷贝集合通信优化"
 (kongchang.com), §"TIDE的设计思路：布局感知的零拷贝通信".
@@ -74,6 +76,7 @@ class Plan:
         self._destroy = lib().tide_plan_destroy
         _check(lib().tide_plan_create(self.world, P, d0, inner, int(align), ctypes.byref(h)))
         self._h = h
+        self.align = int(align)
         self.S = int(lib().tide_plan_shard_numel(h))
         self.P = P
         # what a pointer table is checked against (compared by identity)
@@ -379,3 +382,13 @@ from .blocks import (Blocks, BlockPlan, block_dequant, block_linear, block_mm,  
 
 __all__ += ["Blocks", "BlockPlan", "block_quant", "block_dequant", "block_mm", "block_mm_dx",
             "block_mm_dw", "block_linear", "block_shard", "block_unshard"]
+
+from .fp4 import (Fp4Blocks, Fp4Plan, fp4_dequant, fp4_linear, fp4_mm, fp4_mm_dx,  # noqa: E402
+                  fp4_quant, fp4_shard, fp4_unshard)
+
+__all__ += ["Fp4Blocks", "Fp4Plan", "fp4_quant", "fp4_dequant", "fp4_mm", "fp4_mm_dx", "fp4_linear",
+            "fp4_shard", "fp4_unshard"]
+
+from .ortho import ortho  # noqa: E402
+
+__all__ += ["ortho"]

@@ -38,6 +38,18 @@ SIGNATURES = {
     "tide_block_mm_dw": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
     "tide_block_linear": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
     "tide_block_workspace": (_i64, [_i32, _i64, _i64, _i64, _u32]),
+    "tide_mx_cols": (_i64, [_i64]),
+    "tide_mx_quant": (_i32, [_p, _i64, _i64, _p, _p, _u32, _p]),
+    "tide_mx_dequant": (_i32, [_p, _p, _i64, _i64, _p, _u32, _p]),
+    "tide_plan_create_mx": (_i32, [_p, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_p)]),
+    "tide_mx_shard": (_i32, [_p, _i32, _p, _p, _u32, _p]),
+    "tide_mx_unshard": (_i32, [_p, _p, _p, _u32, _p]),
+    "tide_mx_mm": (_i32, [_p, _p, _i64, _p, _p, _i64, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_mx_linear": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_mx_mm_dx": (_i32, [_p, _i64, _i64, _p, _p, _i64, _p, _u32, _p, _i64, _p]),
+    "tide_mx_workspace": (_i64, [_i32, _i64, _i64, _i64, _u32]),
+    "tide_ortho": (_i32, [_i32, _p, _p, _pi64, _pi64, _i32, _p, _u32, _p, _i64, _p]),
+    "tide_ortho_workspace": (_i64, [_i32, _pi64, _pi64]),
     "tide_last_error": (ctypes.c_char_p, []),
     "tide_status_string": (ctypes.c_char_p, [_i32]),
 }

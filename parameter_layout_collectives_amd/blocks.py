@@ -95,16 +95,9 @@ def _values(t, what, dtypes):
     _matrix(t, what, dtypes)
 
 
-class Blocks:
-    """A matrix [rows, cols] in 8-bit blocks.
-
-    codes: [rows, cols rounded up to 128], float8_e4m3fn or uint8.
-    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu,
-    10 to 246.  Codes past the last column are 0 and scales past the last block 127,
-    as block_quant, block_shard and ag() write them: the products count on it.
-    Either may be replaced by another tensor of its shape, and its storage may be
-    released and restored in between, as an FSDP unit does with gathered weights:
-    every call asks the tensors where they are, and refuses one without memory."""
+class _Codes:
+    """What matrices in 8-bit and 4-bit blocks have in common: two tensors and a
+    number of columns."""
 
     __slots__ = ("_codes", "_scales", "_rows", "_cols", "_device", "_word_views")
 
@@ -112,12 +105,12 @@ class Blocks:
         self._set(codes, scales, int(cols))
 
     def _set(self, codes, scales, cols):
-        _matrix(codes, "codes", (torch.float8_e4m3fn, torch.uint8))
+        _matrix(codes, "codes", self._code_types)
         _matrix(scales, "scales", (torch.uint8, torch.float8_e8m0fnu))
         _same_device(codes.device, scales)
         rows = codes.shape[0]
-        if cols < 0 or codes.shape[1] != _code_cols(cols) \
-                or tuple(scales.shape) != (rows, _scale_cols(cols)):
+        if cols < 0 or codes.shape[1] != self._code_cols(cols) \
+                or tuple(scales.shape) != (rows, self._scale_cols(cols)):
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
                              f"hold {rows} rows of {cols} columns")
         self._codes, self._scales, self._word_views = codes, scales, None
@@ -126,9 +119,10 @@ class Blocks:
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
         self = object.__new__(cls)          # right by construction: no checks
-        self._codes = torch.empty((rows, _code_cols(cols)), dtype=torch.float8_e4m3fn,
+        self._codes = torch.empty((rows, cls._code_cols(cols)), dtype=cls._code_types[0],
                                   device=device)
-        self._scales = torch.empty((rows, _scale_cols(cols)), dtype=torch.uint8, device=device)
+        self._scales = torch.empty((rows, cls._scale_cols(cols)), dtype=torch.uint8,
+                                   device=device)
         self._rows, self._cols, self._device = rows, cols, self._codes.device
         self._word_views = None
         return self
@@ -150,7 +144,7 @@ class Blocks:
         self._replace(self._codes, t)
 
     def _replace(self, codes, scales):
-        _matrix(codes, "codes", (torch.float8_e4m3fn, torch.uint8))
+        _matrix(codes, "codes", self._code_types)
         if codes.shape[0] != self._rows:
             raise ValueError(f"codes of {codes.shape[0]} rows in place of {self._rows}")
         self._set(codes, scales, self._cols)
@@ -177,9 +171,29 @@ class Blocks:
             self._word_views = _words(self._codes), _words(self._scales)
         return self._word_views
 
+
+class Blocks(_Codes):
+    """A matrix [rows, cols] in 8-bit blocks.
+
+    codes: [rows, cols rounded up to 128], float8_e4m3fn or uint8.
+    scales: [rows, blocks of a row rounded up to 4], uint8 or float8_e8m0fnu,
+    10 to 246.  Codes past the last column are 0 and scales past the last block 127,
+    as block_quant, block_shard and ag() write them: the products count on it.
+    Either may be replaced by another tensor of its shape, and its storage may be
+    released and restored in between, as an FSDP unit does with gathered weights:
+    every call asks the tensors where they are, and refuses one without memory."""
+
+    __slots__ = ()
+    _code_types = (torch.float8_e4m3fn, torch.uint8)
+    _code_cols, _scale_cols = staticmethod(_code_cols), staticmethod(_scale_cols)
+
     @property
     def _ptrs(self):
         return self._codes.data_ptr(), self._scales.data_ptr()
+
+    @property
+    def _ptrs4(self):
+        raise TypeError("8-bit blocks where 4-bit ones are expected")
 
 
 def _out(out, shape, dtype, dtypes, device, what):
@@ -379,13 +393,7 @@ def _words(t):
     return t.view(torch.int32)
 
 
-class BlockPlan(Plan):
-    """The plan of an 8-bit gather of `plan`'s matrices (tide_plan_create_blocks).
-
-    select: indices of plan's parameters, by default all 2-D ones.  Its own
-    parameters are the codes and then the scales of the selected matrices in
-    int32 words, so ag(plan, gathered, plan.views(blocks)) places them."""
-
+class _CodesPlan(Plan):
     def __init__(self, plan, select=None):
         self._h = None
         if select is None:
@@ -395,15 +403,16 @@ class BlockPlan(Plan):
         arr = (ctypes.c_int32 * max(n, 1))(*self.select)
         h = ctypes.c_void_p()
         self._destroy = lib().tide_plan_destroy
-        _check(lib().tide_plan_create_blocks(plan.handle, n, arr, ctypes.byref(h)))
+        _check(getattr(lib(), self._create)(plan.handle, n, arr, ctypes.byref(h)))
         self._h = h
         self.world = plan.world
         self.matrices = []
         for i in self.select:
             s = plan.shapes[i]
             self.matrices.append((s[0] if s else 1, _numel(s[1:])))
-        self.shapes = [(d, _code_cols(c) // 4) for d, c in self.matrices] + \
-                      [(d, _scale_cols(c) // 4) for d, c in self.matrices]
+        kind = self._kind
+        self.shapes = [(d, kind._code_cols(c) // 4) for d, c in self.matrices] + \
+                      [(d, kind._scale_cols(c) // 4) for d, c in self.matrices]
         self.P = 2 * n
         self.S = int(lib().tide_plan_shard_numel(h))
         self.source_S = plan.S
@@ -414,20 +423,35 @@ class BlockPlan(Plan):
         return torch.empty(self.world, self.S, dtype=torch.int32, device=device)
 
     def blocks(self, device="cuda"):
-        """One (uninitialised) Blocks per matrix, for ag() to place into."""
-        return [Blocks.empty(d, c, device) for d, c in self.matrices]
+        """One (uninitialised) matrix in blocks per matrix, for ag() to place into."""
+        return [self._kind.empty(d, c, device) for d, c in self.matrices]
 
     def views(self, blocks):
-        """The int32 views of a list of Blocks that ag() takes as parameters."""
-        if [b.shape for b in blocks] != self.matrices:
-            raise ValueError("need one Blocks per matrix, of its shape")
+        """The int32 views of a list of such matrices that ag() takes as parameters."""
+        if [b.shape for b in blocks] != self.matrices or \
+                not all(isinstance(b, self._kind) for b in blocks):
+            raise ValueError(f"need one {self._kind.__name__} per matrix, of its shape")
         words = [b.words() for b in blocks]
         return [c for c, _ in words] + [s for _, s in words]
+
+
+class BlockPlan(_CodesPlan):
+    """The plan of an 8-bit gather of `plan`'s matrices (tide_plan_create_blocks).
+
+    select: indices of plan's parameters, by default all 2-D ones.  Its own
+    parameters are the codes and then the scales of the selected matrices in
+    int32 words, so ag(plan, gathered, plan.views(blocks)) places them."""
+
+    _create, _kind = "tide_plan_create_blocks", Blocks
 
 
 def block_shard(plan, rank, master, block):
     """Rank `rank`'s fp32 master shard (source_S elements) -> its 8-bit rank
     block (plan.S int32 words, e.g. a row of plan.empty())."""
+    _shard(lib().tide_block_shard, plan, rank, master, block)
+
+
+def _shard(fn, plan, rank, master, block):
     _no_dual(master, "master")
     if master.dtype != torch.float32 or not master.is_cuda or not master.is_contiguous() \
             or master.numel() != plan.source_S:
@@ -437,7 +461,7 @@ def block_shard(plan, rank, master, block):
             or block.numel() != plan.S:
         raise ValueError(f"block must be a contiguous int32 device tensor of {plan.S} elements")
     _same_device(master.device, block)
-    _call(master.device, lib().tide_block_shard, plan.handle, int(rank), master.data_ptr(),
+    _call(master.device, fn, plan.handle, int(rank), master.data_ptr(),
           block.data_ptr(), 0)
 
 
@@ -458,17 +482,21 @@ def block_unshard(plan, gathered, params):
 
     params: one tensor per matrix of the plan, all bf16, all fp16 or all fp32,
     or a PointerTable of them."""
+    _unshard(lib().tide_block_unshard, "block_unshard", plan, gathered, params)
+
+
+def _unshard(fn, name, plan, gathered, params):
     if gathered.dtype != torch.int32 or not gathered.is_cuda or not gathered.is_contiguous() \
             or gathered.numel() != plan.world * plan.S:
         raise ValueError(f"gathered must be a contiguous int32 device tensor of "
                          f"{plan.world * plan.S} elements")
     if not isinstance(params, PointerTable):
         params = PointerTable(params)
-    params.check_len(len(plan.matrices), "block_unshard")
+    params.check_len(len(plan.matrices), name)
     device = gathered.device
-    params._ensure(plan, "block_unshard", lambda: _check_unshard(plan, params.tensors, device))
+    params._ensure(plan, name, lambda: _check_unshard(plan, params.tensors, device))
     _same_device(device, params.tensors[0])
-    _call(device, lib().tide_block_unshard, plan.handle, gathered.data_ptr(), params.array,
+    _call(device, fn, plan.handle, gathered.data_ptr(), params.array,
           _OUT_FLAG[params.tensors[0].dtype])
 
 

@@ -25,7 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtide.so")
 
 SOURCES = ["plan.cpp", "block_args.cpp", "runtime.hip", "kernels.hip", "noalloc.hip",
-           "block_cast.hip", "block_mm.hip"]
+           "block_cast.hip", "block_mm.hip", "fp4_args.cpp", "fp4_cast.hip", "fp4_mm.hip",
+           "ortho_args.cpp", "ortho.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

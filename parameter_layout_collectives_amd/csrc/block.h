@@ -84,17 +84,49 @@ struct MmChoice {
 inline bool mm_aligned(MmOp op, const void *dy, int64_t N) {
     return op == kMm || (reinterpret_cast<uintptr_t>(dy) % 16 == 0 && N % 8 == 0);
 }
+// Cuts the sums of the tiles left over after whole sets of `tiles`, where that
+// pays (may be called with c.direct = tiles, c.splits = 1 and c.chunk = steps).
+void cut_sums(MmChoice &c, int64_t tiles, int64_t steps);
 MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
                    bool may_split);
 
-tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
-                              const void *scales, uint32_t flags);
-tide_status check_block_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
-                                const void *out, uint32_t flags);
-tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *master,
-                              const void *block, uint32_t flags);
-tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void *const *params,
-                                uint32_t flags);
+// A format of blocked matrices: bytes of the codes and of the scales of a row of c
+// columns.
+struct Format {
+    int bits;
+    int64_t code_bytes(int64_t c) const { return bits == 4 ? block_cols(c) / 2 : block_cols(c); }
+    int64_t scale_bytes(int64_t c) const {
+        return bits == 4 ? block_cols(c) / 32 : block_scale_cols(c);
+    }
+};
+constexpr Format kEights = {8}, kFours = {4};
+
+tide_status check_quant(const char *name, Format f, const void *x, int64_t rows, int64_t cols,
+                        const void *codes, const void *scales, uint32_t flags);
+tide_status check_dequant(const char *name, Format f, const void *codes, const void *scales,
+                          int64_t rows, int64_t cols, const void *out, uint32_t flags);
+tide_status check_shard(const char *name, Format f, const tide_plan *bp, int32_t rank,
+                        const void *master, const void *block, uint32_t flags);
+tide_status check_unshard(const char *name, Format f, const tide_plan *bp, const void *gathered,
+                          void *const *params, uint32_t flags);
+tide_status create_plan(const char *name, Format f, const tide_plan *plan, int32_t n,
+                        const int32_t *select, tide_plan **out_plan);
+inline tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
+                                     const void *scales, uint32_t flags) {
+    return check_quant("tide_block_quant", kEights, x, rows, cols, codes, scales, flags);
+}
+inline tide_status check_block_dequant(const void *codes, const void *scales, int64_t rows,
+                                       int64_t cols, const void *out, uint32_t flags) {
+    return check_dequant("tide_block_dequant", kEights, codes, scales, rows, cols, out, flags);
+}
+inline tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *master,
+                                     const void *block, uint32_t flags) {
+    return check_shard("tide_block_shard", kEights, bp, rank, master, block, flags);
+}
+inline tide_status check_block_unshard(const tide_plan *bp, const void *gathered,
+                                       void *const *params, uint32_t flags) {
+    return check_unshard("tide_block_unshard", kEights, bp, gathered, params, flags);
+}
 
 // Operands of a product as its entry point got them: `a` is X's codes or dY.
 struct MmArgs {

@@ -4,59 +4,10 @@
 #include <new>
 
 #include "block.h"
+#include "checks.h"
 
 namespace tide {
 namespace {
-
-constexpr int64_t kMaxDim = int64_t(1) << 31;   // rows and columns of a block matrix
-constexpr int64_t kMaxLine = int64_t(1) << 22;  // n and k of a product: its kernels address the
-                                                // rows of a tile, 2 * 2^22 bytes each, in 32 bits
-
-struct Bytes {
-    uintptr_t lo, hi;
-};
-Bytes bytes_of(const void *p, int64_t n) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + static_cast<uintptr_t>(n)};
-}
-bool overlap(const Bytes &a, const Bytes &b) { return a.lo < b.hi && b.lo < a.hi; }
-bool misaligned(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
-
-tide_status bad(const char *name, const char *what) {
-    return fail(TIDE_E_INVALID, std::string(name) + ": " + what);
-}
-
-tide_status check_flags(const char *name, uint32_t flags, uint32_t known) {
-    if (flags & ~known) return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": unknown flag bits");
-    if ((flags & TIDE_F_GRAD_F16) && (flags & TIDE_F_GRAD_F32))
-        return bad(name, "TIDE_F_GRAD_F16 and TIDE_F_GRAD_F32 both set");
-    if ((flags & TIDE_F_OUT_BF16) && (flags & TIDE_F_OUT_F16))
-        return bad(name, "TIDE_F_OUT_BF16 and TIDE_F_OUT_F16 both set");
-    if ((flags & TIDE_F_SHORT_SUMS) && !(flags & TIDE_F_OUT_BF16))
-        return bad(name, "TIDE_F_SHORT_SUMS without TIDE_F_OUT_BF16");
-    return TIDE_OK;
-}
-
-tide_status check_dims(const char *name, int64_t rows, int64_t cols) {
-    if (rows < 0 || cols < 0) return bad(name, "negative size");
-    if (rows >= kMaxDim || cols >= kMaxDim) return bad(name, "a size of 2^31 or more");
-    // the products' byte offsets then fit int64 with room to spare
-    if (rows && block_cols(cols) > (int64_t(1) << 60) / rows) return bad(name, "sizes overflow");
-    return TIDE_OK;
-}
-
-// A matrix in 8-bit blocks: both pointers present and aligned for the widest
-// loads the kernels make of them.
-tide_status check_blocks(const char *name, const char *which, const void *codes,
-                         const void *scales) {
-    if (!codes) return bad(name, (std::string(which) + " codes are NULL").c_str());
-    if (!scales) return bad(name, (std::string(which) + " scales are NULL").c_str());
-    if (misaligned(codes, 16))
-        return bad(name, (std::string(which) + " codes are not 16-byte aligned").c_str());
-    if (misaligned(scales, 4))
-        return bad(name, (std::string(which) + " scales are not 4-byte aligned").c_str());
-    return TIDE_OK;
-}
 
 // Flags and sizes of a product; `known`: the flags it takes.  A launch counts its
 // lanes in 32 bits: that too is checked here, before anything is enqueued.
@@ -85,17 +36,18 @@ uint32_t known_flags(MmOp op) {
 constexpr uint32_t kLinearFlags =
     TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 | TIDE_F_OUT_BF16 | TIDE_F_SHORT_SUMS;
 
-tide_status check_block_plan(const char *name, const tide_plan *bp) {
+tide_status check_plan(const char *name, Format f, const tide_plan *bp) {
     if (!bp) return bad(name, "plan is NULL");
-    if (!bp->nblk) return bad(name, "not a plan of tide_plan_create_blocks");
+    if (!bp->nblk || bp->blk_bits != f.bits)
+        return bad(name, f.bits == 4 ? "not a plan of tide_plan_create_mx"
+                                     : "not a plan of tide_plan_create_blocks");
     return TIDE_OK;
 }
 
 }  // namespace
 
-tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const void *codes,
-                              const void *scales, uint32_t flags) {
-    const char *name = "tide_block_quant";
+tide_status check_quant(const char *name, Format f, const void *x, int64_t rows, int64_t cols,
+                        const void *codes, const void *scales, uint32_t flags) {
     tide_status st = check_flags(name, flags, TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32);
     if (st == TIDE_OK) st = check_dims(name, rows, cols);
     if (st != TIDE_OK || rows == 0 || cols == 0) return st;
@@ -104,16 +56,15 @@ tide_status check_block_quant(const void *x, int64_t rows, int64_t cols, const v
     if (misaligned(x, es)) return bad(name, "x is not aligned to its element size");
     st = check_blocks(name, "the output's", codes, scales);
     if (st != TIDE_OK) return st;
-    const Bytes in = bytes_of(x, rows * cols * es), c = bytes_of(codes, rows * block_cols(cols)),
-                s = bytes_of(scales, rows * block_scale_cols(cols));
+    const Bytes in = bytes_of(x, rows * cols * es), c = bytes_of(codes, rows * f.code_bytes(cols)),
+                s = bytes_of(scales, rows * f.scale_bytes(cols));
     if (overlap(in, c) || overlap(in, s) || overlap(c, s))
         return bad(name, "an output overlaps the input or the other output");
     return TIDE_OK;
 }
 
-tide_status check_block_dequant(const void *codes, const void *scales, int64_t rows, int64_t cols,
-                                const void *out, uint32_t flags) {
-    const char *name = "tide_block_dequant";
+tide_status check_dequant(const char *name, Format f, const void *codes, const void *scales,
+                          int64_t rows, int64_t cols, const void *out, uint32_t flags) {
     tide_status st = check_flags(name, flags, TIDE_F_OUT_BF16 | TIDE_F_OUT_F16);
     if (st == TIDE_OK) st = check_dims(name, rows, cols);
     if (st != TIDE_OK || rows == 0 || cols == 0) return st;
@@ -123,16 +74,15 @@ tide_status check_block_dequant(const void *codes, const void *scales, int64_t r
     if (!out) return bad(name, "out is NULL");
     if (misaligned(out, es)) return bad(name, "out is not aligned to its element size");
     const Bytes o = bytes_of(out, rows * cols * es);
-    if (overlap(o, bytes_of(codes, rows * block_cols(cols))) ||
-        overlap(o, bytes_of(scales, rows * block_scale_cols(cols))))
+    if (overlap(o, bytes_of(codes, rows * f.code_bytes(cols))) ||
+        overlap(o, bytes_of(scales, rows * f.scale_bytes(cols))))
         return bad(name, "out overlaps the input");
     return TIDE_OK;
 }
 
-tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *master,
-                              const void *block, uint32_t flags) {
-    const char *name = "tide_block_shard";
-    tide_status st = check_block_plan(name, bp);
+tide_status check_shard(const char *name, Format f, const tide_plan *bp, int32_t rank,
+                        const void *master, const void *block, uint32_t flags) {
+    tide_status st = check_plan(name, f, bp);
     if (st != TIDE_OK) return st;
     if (rank < 0 || rank >= bp->N)
         return fail(TIDE_E_INVALID, std::string(name) + ": rank " + std::to_string(rank) +
@@ -148,10 +98,9 @@ tide_status check_block_shard(const tide_plan *bp, int32_t rank, const void *mas
     return TIDE_OK;
 }
 
-tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void *const *params,
-                                uint32_t flags) {
-    const char *name = "tide_block_unshard";
-    tide_status st = check_block_plan(name, bp);
+tide_status check_unshard(const char *name, Format f, const tide_plan *bp, const void *gathered,
+                          void *const *params, uint32_t flags) {
+    tide_status st = check_plan(name, f, bp);
     if (st != TIDE_OK) return st;
     st = check_flags(name, flags, TIDE_F_OUT_BF16 | TIDE_F_OUT_F16);
     if (st != TIDE_OK || bp->psi == 0) return st;
@@ -180,6 +129,51 @@ tide_status check_block_unshard(const tide_plan *bp, const void *gathered, void 
     std::sort(dst.begin(), dst.end(), [](const Bytes &a, const Bytes &b) { return a.lo < b.lo; });
     for (size_t k = 1; k < dst.size(); k++)
         if (overlap(dst[k - 1], dst[k])) return bad(name, "a destination overlaps another");
+    return TIDE_OK;
+}
+
+tide_status create_plan(const char *name, Format f, const tide_plan *plan, int32_t n,
+                        const int32_t *select, tide_plan **out_plan) {
+    if (!out_plan) return bad(name, "out_plan is NULL");
+    *out_plan = nullptr;
+    if (!plan) return bad(name, "plan is NULL");
+    if (plan->nblk) return bad(name, "plan is a block plan itself");
+    if (n < 1 || n > plan->P) return bad(name, "n outside [1, nparams]");
+    if (!select) return bad(name, "select is NULL");
+    try {
+        std::vector<int64_t> d0(2 * static_cast<size_t>(n)), words(d0.size()), off(n), inner(n);
+        std::vector<char> seen(plan->P, 0);
+        for (int32_t j = 0; j < n; j++) {
+            const int32_t i = select[j];
+            if (i < 0 || i >= plan->P) return bad(name, "select holds an index out of range");
+            if (seen[i]) return bad(name, "select holds an index twice");
+            seen[i] = 1;
+            const tide_status st = check_dims(name, plan->d0[i], plan->inner[i]);
+            if (st != TIDE_OK) return st;
+            d0[j] = d0[n + j] = plan->d0[i];
+            words[j] = f.code_bytes(plan->inner[i]) / 4;
+            words[n + j] = f.scale_bytes(plan->inner[i]) / 4;
+            off[j] = plan->off[i];
+            inner[j] = plan->inner[i];
+        }
+        // offsets at multiples of 4 words: every segment starts 16-byte aligned
+        tide_plan *p = nullptr;
+        const tide_status st =
+            tide_plan_create(plan->N, 2 * n, d0.data(), words.data(), 4, &p);
+        if (st != TIDE_OK) return st;
+        if (p->S / 4 > 0xffffffffll) {
+            tide_plan_destroy(p);
+            return bad(name, "a rank block of more than 2^36 bytes");
+        }
+        p->nblk = n;
+        p->blk_bits = f.bits;
+        p->blk_S = plan->S;
+        p->blk_off.swap(off);
+        p->blk_inner.swap(inner);
+        *out_plan = p;
+    } catch (const std::bad_alloc &) {
+        return fail(TIDE_E_NOMEM, std::string(name) + ": out of host memory");
+    }
     return TIDE_OK;
 }
 
@@ -262,6 +256,27 @@ tide_status check_linear(const LinearArgs &a) {
     return TIDE_OK;
 }
 
+void cut_sums(MmChoice &c, int64_t tiles, int64_t steps) {
+    // The tiles that run at one time; what is left after whole sets of them is
+    // cut if that leaves at least half of the card idle (more tiles could not be
+    // cut in two: 256 + 128 large tiles, 4096 x 6144, over 8192: cut 330 us, else
+    // 384).  The pieces' sums go through memory, so a piece has at least
+    // kMinSplitSteps steps, and behind whole sets (where one is long) at least four
+    // times that (256 + 16 large tiles, 4352 x 4096, over 2048: pieces of 16 steps
+    // 90 us, of 8 82, not cut 105; over 8192 243, 242, cut in fewer 257).
+    const int64_t full = kCus * (c.tile == 256 ? 1 : 2);
+    const int64_t left = tiles % full, least = tiles < full ? kMinSplitSteps : 4 * kMinSplitSteps;
+    if (left == 0 || left * 2 > full || steps < 2 * least) return;
+    const int64_t s = std::min({full / left, steps / least, kMaxSplits});
+    const int64_t chunk = ((steps + s - 1) / s + 3) / 4 * 4;   // scale bytes are read in fours
+    const int64_t pieces = (steps + chunk - 1) / chunk;
+    if (pieces < 2) return;
+    c.chunk = chunk;
+    c.splits = static_cast<int>(pieces);
+    c.direct = tiles - left;
+    c.workspace = left * pieces * c.tile * c.tile * 4;
+}
+
 MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
                    bool may_split) {
     MmChoice c;
@@ -296,26 +311,7 @@ MmChoice mm_choose(MmOp op, int64_t M, int64_t N, int64_t K, uint32_t flags, boo
     c.chunk = steps;
     c.workspace = 0;
     if (c.kernel == kMmSkinny || !may_split) return c;
-    // The tiles that run at one time; what is left after whole sets of them is
-    // cut if that leaves at least half of the card idle (more tiles could not be
-    // cut in two: 256 + 128 large tiles, 4096 x 6144, over 8192: cut 330 us, else
-    // 384).  The pieces' sums go through memory, so a piece has at least
-    // kMinSplitSteps steps, and behind whole sets (where one is long) at least four
-    // times that (256 + 16 large tiles, 4352 x 4096, over 2048: pieces of 16 steps
-    // 90 us, of 8 82, not cut 105; over 8192 243, 242, cut in fewer 257).
-    const int64_t full = kCus * (c.tile == 256 ? 1 : 2);
-    const int64_t left = t % full, least = t < full ? kMinSplitSteps : 4 * kMinSplitSteps;
-    if (left == 0 || left * 2 > full || steps < 2 * least) return c;
-    const int64_t s = std::min({full / left, steps / least, kMaxSplits});
-    c.chunk = ((steps + s - 1) / s + 3) / 4 * 4;       // scale bytes are read in fours
-    const int64_t pieces = (steps + c.chunk - 1) / c.chunk;
-    if (pieces < 2) {
-        c.chunk = steps;
-        return c;
-    }
-    c.splits = static_cast<int>(pieces);
-    c.direct = t - left;
-    c.workspace = left * pieces * c.tile * c.tile * 4;
+    cut_sums(c, t, steps);
     return c;
 }
 
@@ -336,47 +332,7 @@ int64_t tide_block_scale_cols(int64_t cols) {
 
 tide_status tide_plan_create_blocks(const tide_plan *plan, int32_t n, const int32_t *select,
                                     tide_plan **out_plan) {
-    const char *name = "tide_plan_create_blocks";
-    if (!out_plan) return bad(name, "out_plan is NULL");
-    *out_plan = nullptr;
-    if (!plan) return bad(name, "plan is NULL");
-    if (plan->nblk) return bad(name, "plan is a block plan itself");
-    if (n < 1 || n > plan->P) return bad(name, "n outside [1, nparams]");
-    if (!select) return bad(name, "select is NULL");
-    try {
-        std::vector<int64_t> d0(2 * static_cast<size_t>(n)), words(d0.size()), off(n), inner(n);
-        std::vector<char> seen(plan->P, 0);
-        for (int32_t j = 0; j < n; j++) {
-            const int32_t i = select[j];
-            if (i < 0 || i >= plan->P) return bad(name, "select holds an index out of range");
-            if (seen[i]) return bad(name, "select holds an index twice");
-            seen[i] = 1;
-            const tide_status st = tide::check_dims(name, plan->d0[i], plan->inner[i]);
-            if (st != TIDE_OK) return st;
-            d0[j] = d0[n + j] = plan->d0[i];
-            words[j] = tide::block_cols(plan->inner[i]) / 4;
-            words[n + j] = tide::block_scale_cols(plan->inner[i]) / 4;
-            off[j] = plan->off[i];
-            inner[j] = plan->inner[i];
-        }
-        // offsets at multiples of 4 words: every segment starts 16-byte aligned
-        tide_plan *p = nullptr;
-        const tide_status st =
-            tide_plan_create(plan->N, 2 * n, d0.data(), words.data(), 4, &p);
-        if (st != TIDE_OK) return st;
-        if (p->S / 4 > 0xffffffffll) {
-            tide_plan_destroy(p);
-            return bad(name, "a rank block of more than 2^36 bytes");
-        }
-        p->nblk = n;
-        p->blk_S = plan->S;
-        p->blk_off.swap(off);
-        p->blk_inner.swap(inner);
-        *out_plan = p;
-    } catch (const std::bad_alloc &) {
-        return fail(TIDE_E_NOMEM, std::string(name) + ": out of host memory");
-    }
-    return TIDE_OK;
+    return tide::create_plan("tide_plan_create_blocks", tide::kEights, plan, n, select, out_plan);
 }
 
 int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {

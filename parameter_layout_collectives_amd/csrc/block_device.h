@@ -1,5 +1,5 @@
-// Device code that the kernels of the 8-bit blocks share: 8 elements of any
-// input type as fp32, and 8 fp32 values as e4m3 codes with their block's scale.
+// Device code that the kernels of the 8-bit and 4-bit blocks share: 8 elements of
+// any input type as fp32, and 8 fp32 values as codes with their block's scale.
 #pragma once
 
 #include "block.h"
@@ -127,6 +127,41 @@ __device__ __forceinline__ u32x2 encode8(const float *v, uint32_t *scale) {
             }
     }
     return c;
+}
+
+// The largest value over the 4 lanes of a quad.
+__device__ __forceinline__ uint32_t max4(uint32_t u) {
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0xb1, 0xf, 0xf, false)));
+    u = max(u, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x4e, 0xf, 0xf, false)));
+    return u;
+}
+
+// One lane's 8 values -> 8 e2m1 codes, the even value of a pair in the low half of
+// its byte; 4 lanes share a block of 32 and its scale byte.  With the largest
+// magnitude a = m * 2^k, 1 <= m < 2, a <= 6 * 2^e = 1.5 * 2^(2+e) from e = k - 2 on if
+// m <= 1.5, else from k - 1 on; e is kept in [-125, 125], so that the values are
+// normal bf16 numbers.  Above 6 * 2^125 values are cut there (by the
+// median).  A block that holds an infinity or a NaN has scale byte 255 and
+// codes 0: e2m1 has neither, and all of the block reads back as NaN.
+__device__ __forceinline__ uint32_t encode4(const float *v, uint32_t *scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = max4(top);
+    int e = static_cast<int>(top >> 23) - 127 - 2 + ((top & 0x7fffffu) > 0x400000u ? 1 : 0);
+    e = top == 0 ? 0 : min(125, max(-125, e));
+    const bool finite = top < 0x7f800000u;
+    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(v[i] * s, -6.0f, 6.0f);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[0], y[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], 1.0f, 3);
+    *scale = finite ? static_cast<uint32_t>(e + 127) : 255u;
+    return finite ? c : 0;
 }
 
 }  // namespace

@@ -1,0 +1,167 @@
+// Host side of the 4-bit block operators: argument checks and the choice of a
+// product's kernel.  Makes no HIP call.
+#include <algorithm>
+
+#include "checks.h"
+#include "fp4.h"
+
+namespace tide {
+namespace {
+
+uint32_t known_flags(Fp4Op op) {
+    return TIDE_F_OUT_BF16 |
+           (op == kFp4Linear ? TIDE_F_QUANT_X | TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32 : 0u);
+}
+
+constexpr int64_t kRound = 255;
+int64_t rounded(int64_t n) { return (n + kRound) & ~kRound; }
+
+// Flags and sizes; as in the 8-bit products, a launch counts its lanes in 32 bits.
+tide_status check_product(const char *name, Fp4Op op, int64_t M, int64_t N, int64_t K,
+                          uint32_t flags) {
+    tide_status st = check_flags(name, flags, known_flags(op));
+    if (st != TIDE_OK) return st;
+    if ((flags & (TIDE_F_GRAD_F16 | TIDE_F_GRAD_F32)) && !(flags & TIDE_F_QUANT_X))
+        return bad(name, "an x in fp16 or fp32 without TIDE_F_QUANT_X");
+    for (int64_t rows : {M, N})
+        for (int64_t cols : {N, K})
+            if ((st = check_dims(name, rows, cols)) != TIDE_OK) return st;
+    if (N > kMaxLine || K > kMaxLine)
+        return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": n or k above 2^22");
+    const int64_t cols = op == kFp4Dx ? K : N;
+    for (bool aligned : {false, true}) {
+        const Fp4Choice c = fp4_choose(op, M, N, K, flags, aligned, INT64_MAX);
+        if (c.kernel != kFp4Tiles && c.kernel != kFp4Wide) continue;
+        const int64_t T = c.mm.tile, tiles = ((M + T - 1) / T) * ((cols + T - 1) / T);
+        const int64_t cut = (tiles - c.mm.direct) * c.mm.splits;
+        if (c.mm.direct + cut > 0xffffffffll / (T == 256 ? 512 : 256) ||
+            (tiles - c.mm.direct) * (T * T / 1024) > 0xffffffffll / 256 ||
+            ((flags & TIDE_F_QUANT_X) && M * block_count(K) > 0xffffffffll / 4 - 64))
+            return fail(TIDE_E_UNSUPPORTED, std::string(name) + ": more than 2^32 lanes");
+    }
+    return TIDE_OK;
+}
+
+// Rows that the skinny kernel takes.
+constexpr int64_t kFewRows = 16;
+// x is prepared inside the product for so many bytes of bf16 rows.
+constexpr int64_t kInOneBytesFp4 = 57344 + 16;
+
+}  // namespace
+
+bool fp4_whole(const void *x, int64_t K) {
+    return K % kBlockCols == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+}
+
+Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
+                     int64_t workspace_bytes) {
+    Fp4Choice c = {};
+    const int64_t cols = op == kFp4Dx ? K : N, sum = op == kFp4Dx ? N : K;
+    const bool quant = op == kFp4Linear && (flags & TIDE_F_QUANT_X);
+    const int64_t padded = M * block_cols(K) * 2;       // x as bf16 rows of whole units
+    if (op != kFp4Dx && M <= kFewRows) {
+        if (op == kFp4Linear && M * (block_cols(K) * 2 + 16) <= kInOneBytesFp4) {
+            c.kernel = kFp4SkinnyInOne;
+            return c;
+        }
+        if (workspace_bytes >= rounded(padded)) {
+            c.kernel = kFp4Skinny;
+            c.x = rounded(padded);
+            return c;
+        }
+    }
+    c.kernel = op == kFp4Mm || quant ? kFp4Tiles : kFp4Wide;
+    if (quant) {
+        c.x_scales = rounded(M * kFours.code_bytes(K));
+        c.x = rounded(c.x_scales + M * kFours.scale_bytes(K));
+    }
+    auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((cols + t - 1) / t); };
+    const bool four = c.kernel == kFp4Tiles;
+    c.mm.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256
+                : !four && tiles(128) < kCus / 2      ? 64
+                                                      : 128;
+    const int64_t step = four ? 256 : 64;
+    c.mm.direct = tiles(c.mm.tile);
+    c.mm.splits = 1;
+    c.mm.chunk = (sum + step - 1) / step;
+    c.mm.workspace = 0;
+    MmChoice cut = c.mm;
+    cut_sums(cut, c.mm.direct, c.mm.chunk);
+    if (c.x + cut.workspace <= workspace_bytes) c.mm = cut;
+    return c;
+}
+
+tide_status check_fp4(Fp4Op op, const char *name, const Fp4Args &a) {
+    tide_status st = check_product(name, op, a.M, a.N, a.K, a.flags);
+    if (st != TIDE_OK) return st;
+    if (a.workspace_bytes < 0) return bad(name, "workspace_bytes < 0");
+    if (a.workspace_bytes > 0 && !a.workspace) return bad(name, "workspace is NULL");
+    if (misaligned(a.workspace, 16)) return bad(name, "workspace is not 16-byte aligned");
+    const int64_t ocols = op == kFp4Dx ? a.K : a.N, sum = op == kFp4Dx ? a.N : a.K;
+    if (a.M == 0 || ocols == 0) return TIDE_OK;
+    const int os = elem_size(out_type(a.flags));
+    if (!a.out) return bad(name, "out is NULL");
+    if (misaligned(a.out, os)) return bad(name, "out is not aligned to its element size");
+    const Bytes out = bytes_of(a.out, a.M * ocols * os);
+    const Bytes wsp = bytes_of(a.workspace, a.workspace ? a.workspace_bytes : 0);
+    if (overlap(out, wsp)) return bad(name, "out overlaps the workspace");
+    if (sum == 0) return TIDE_OK;
+    Bytes in[4];
+    int n = 0;
+    if (op == kFp4Mm) {
+        st = check_blocks(name, "x's", a.a, a.a_scales);
+        if (st != TIDE_OK) return st;
+        in[n++] = bytes_of(a.a, a.M * kFours.code_bytes(a.K));
+        in[n++] = bytes_of(a.a_scales, a.M * kFours.scale_bytes(a.K));
+    } else {
+        const char *what = op == kFp4Dx ? "dy" : "x";
+        const int es = elem_size(in_type(a.flags));
+        if (!a.a) return bad(name, (std::string(what) + " is NULL").c_str());
+        if (misaligned(a.a, es))
+            return bad(name, (std::string(what) + " is not aligned to its element size").c_str());
+        in[n++] = bytes_of(a.a, a.M * (op == kFp4Dx ? a.N : a.K) * es);
+    }
+    st = check_blocks(name, "w's", a.b, a.b_scales);
+    if (st != TIDE_OK) return st;
+    in[n++] = bytes_of(a.b, a.N * kFours.code_bytes(a.K));
+    in[n++] = bytes_of(a.b_scales, a.N * kFours.scale_bytes(a.K));
+    for (int k = 0; k < n; k++) {
+        if (overlap(out, in[k])) return bad(name, "out overlaps an operand");
+        if (overlap(wsp, in[k])) return bad(name, "the workspace overlaps an operand");
+    }
+    return TIDE_OK;
+}
+
+}  // namespace tide
+
+using tide::bad;
+
+extern "C" {
+
+int64_t tide_mx_cols(int64_t cols) {
+    return cols < 0 || cols >= tide::kMaxDim ? -1 : tide::block_cols(cols);
+}
+
+tide_status tide_plan_create_mx(const tide_plan *plan, int32_t n, const int32_t *select,
+                                 tide_plan **out_plan) {
+    return tide::create_plan("tide_plan_create_mx", tide::kFours, plan, n, select, out_plan);
+}
+
+int64_t tide_mx_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t flags) {
+    const char *name = "tide_mx_workspace";
+    if (op < 0 || op > 2) {
+        bad(name, "op outside [0, 2]");
+        return -1;
+    }
+    const tide::Fp4Op o = static_cast<tide::Fp4Op>(op);
+    if (tide::check_product(name, o, m, n, k, flags) != TIDE_OK) return -1;
+    if (m == 0 || (o == tide::kFp4Dx ? k : n) == 0 || (o == tide::kFp4Dx ? n : k) == 0) return 0;
+    int64_t most = 0;                    // whichever way dY or x is aligned
+    for (bool aligned : {false, true}) {
+        const tide::Fp4Choice c = tide::fp4_choose(o, m, n, k, flags, aligned, INT64_MAX);
+        most = std::max(most, c.x + c.mm.workspace);
+    }
+    return most;
+}
+
+}  // extern "C"

@@ -83,6 +83,7 @@ struct tide_plan {
     // whose fp32 shard lies at blk_off[j] of a source rank block of blk_S
     // elements.  nblk = 0: an ordinary plan.
     int32_t nblk = 0;
+    int32_t blk_bits = 8;        // 4: a plan of tide_plan_create_mx
     int64_t blk_S = 0;
     std::vector<int64_t> blk_off, blk_inner;
     mutable std::mutex mu;

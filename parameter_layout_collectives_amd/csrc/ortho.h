@@ -1,0 +1,80 @@
+// Orthogonalised updates: the workspace's layout and the argument checks
+// (ortho_args.cpp, host only), and the launches (ortho.hip).
+#pragma once
+
+#include <vector>
+
+#include "block.h"
+
+namespace tide {
+
+// P X takes X's lo as well up to this many rows (the smaller side): see ortho.hip.
+constexpr uint32_t kOrthoBoth = 256;
+
+// Equal matrices [nr, nc] of one call, as the kernels see them.  r is the smaller
+// side; the padded sizes are multiples of 64, zeros in between.
+struct OrthoGroup {
+    uint32_t nr, nc;             // rows and columns
+    uint32_t nrp, ncp;           // padded
+    uint32_t first, count;       // its matrices' numbers
+    uint32_t parts;              // pieces of a matrix's sum of squares
+    uint32_t wg0;                // first workgroup of a launch that works on them
+    int64_t base, stride;        // bytes of the first matrix in the workspace, and from one to the next
+
+    __host__ __device__ bool tall() const { return nr > nc; }
+    __host__ __device__ uint32_t r() const { return tall() ? nc : nr; }
+    __host__ __device__ uint32_t rp() const { return tall() ? ncp : nrp; }
+    // X is held twice (a step reads one and writes the other), each time as two
+    // fp16 matrices hi and lo of the padded size: wide ones below one another,
+    // tall ones' rows side by side, so that both form one factor of twice the
+    // length of the sum.  Pitch and distance in elements.
+    __host__ __device__ int64_t pitch() const { return tall() ? 2 * static_cast<int64_t>(ncp) : ncp; }
+    __host__ __device__ int64_t lo() const {
+        return tall() ? static_cast<int64_t>(ncp) : static_cast<int64_t>(nrp) * ncp;
+    }
+    __host__ __device__ int64_t x_bytes() const { return 4 * static_cast<int64_t>(nrp) * ncp; }
+    // Whether lo enters P X, too.
+    __host__ __device__ bool both() const { return r() <= kOrthoBoth; }
+    // Then the fp16 matrices A = X X^T [rp, rp] and P [rp, rp], or twice in each row
+    // [rp, 2 rp] against hi and lo, without their diagonals, and these in fp32 [rp].
+    __host__ __device__ int64_t p_pitch() const {
+        return (both() ? 2 : 1) * static_cast<int64_t>(rp());
+    }
+    __host__ __device__ int64_t a_at() const { return 2 * x_bytes(); }
+    __host__ __device__ int64_t p_at() const {
+        return a_at() + 2 * static_cast<int64_t>(rp()) * rp();
+    }
+    __host__ __device__ int64_t a_diag() const { return p_at() + 2 * rp() * p_pitch(); }
+    __host__ __device__ int64_t p_diag() const { return a_diag() + 4 * rp(); }
+    __host__ __device__ int64_t bytes() const { return p_diag() + 4 * rp(); }
+};
+
+constexpr uint32_t kOrthoParts = 256;          // most pieces of a sum of squares
+constexpr int64_t kOrthoPiece = 16384;         // elements of a piece, if that is not too many
+constexpr int kOrthoGroups = 48;               // groups per launch, as kernel arguments
+
+struct OrthoArgs {
+    int32_t n;
+    const void *const *src;
+    void *const *out;
+    const int64_t *rows, *cols;
+    int32_t steps;
+    const float *coefficients;
+    uint32_t flags;
+    void *workspace;
+    int64_t workspace_bytes;
+};
+// The call's groups, its matrices in their order, and the workspace:
+// {src, out} pointers, one pair a matrix, from 0 on; sums of squares, kOrthoParts
+// doubles a matrix, from `sums` on; {scale, its square} of a matrix's first
+// step from `scales` on; the groups' matrices.
+struct OrthoPlan {
+    std::vector<OrthoGroup> groups;
+    std::vector<int32_t> order;
+    int64_t sums = 0, scales = 0, bytes = 0;
+};
+tide_status ortho_plan(const char *name, int32_t n, const int64_t *rows, const int64_t *cols,
+                       OrthoPlan *plan);
+tide_status check_ortho(const OrthoArgs &a, OrthoPlan *plan);
+
+}  // namespace tide

@@ -28,18 +28,25 @@ all_gather() casts their master shards into 8-bit rank blocks and places those,
 half the bytes of a bf16 gather, and params holds them as Blocks, which
 linear() multiplies by without ever making them bf16.  Its backward pass reads
 an 8-bit checkpoint of the layer's input and writes the weight gradient that
-reduce_scatter() takes.
+reduce_scatter() takes.  `fp4` does the same with 4-bit blocks, about a quarter of
+the bytes, for weights that are frozen, serve, or train behind 4-bit products.
+
+muon_step() is the optimizer's step in between for the unit's matrices: momentum
+on the shards, the update gathered as parameters are, orthogonalised (ortho.py) and
+scattered back onto the master shards.
 """
 import contextlib
 
 import torch
 
-from . import BlockPlan, Plan, ag, block_linear, block_shard, grad_table, pack, rs
+from . import (BlockPlan, Fp4Plan, Plan, ag, block_linear, block_shard, fp4_linear, fp4_shard,
+               grad_table, ortho, pack, rs)
+from .ortho import COEFFICIENTS
 
 
 class TideUnit:
     def __init__(self, shapes, world, device="cuda", align=1, param_dtype=torch.bfloat16,
-                 blocks=()):
+                 blocks=(), fp4=()):
         self.plan = Plan(shapes, world, align)
         N, S = world, self.plan.S
         self.shapes = [tuple(s) for s in shapes]
@@ -48,22 +55,36 @@ class TideUnit:
         self.master = torch.zeros(N, S, dtype=torch.float32, device=device)
         self.grad = torch.zeros(N, S, dtype=torch.float32, device=device)
         self.blocks = [int(i) for i in blocks]
+        self.fp4 = [int(i) for i in fp4]
+        if set(self.blocks) & set(self.fp4):
+            raise ValueError("a parameter is named in blocks and in fp4")
         # the parameters gathered in param_dtype, and their plan
-        self.rest = [i for i in range(len(self.shapes)) if i not in self.blocks]
+        coded = self.blocks + self.fp4
+        self.rest = [i for i in range(len(self.shapes)) if i not in coded]
         self.rest_plan = self.plan
+        self.params = [None] * len(self.shapes)
+        # (indices, plan, gathered buffer, shard call) of the matrices in blocks
+        self._coded = []
         if self.blocks:
             self.block_plan = BlockPlan(self.plan, self.blocks)
             self.block_gathered = self.block_plan.empty(device)
-            weights = self.block_plan.blocks(device)
+            self._coded.append((self.blocks, self.block_plan, self.block_gathered, block_shard))
+        if self.fp4:
+            self.fp4_plan = Fp4Plan(self.plan, self.fp4)
+            self.fp4_gathered = self.fp4_plan.empty(device)
+            self._coded.append((self.fp4, self.fp4_plan, self.fp4_gathered, fp4_shard))
+        if coded:
             self.rest_plan = Plan([self.shapes[i] for i in self.rest], N, align) \
                 if self.rest else None
         S = self.rest_plan.S if self.rest_plan is not None else 0
         self.gathered = torch.zeros(N * S, dtype=param_dtype, device=device)
-        self.params = [None] * len(self.shapes)
         for i in self.rest:
             self.params[i] = torch.empty(self.shapes[i], dtype=param_dtype, device=device)
-        for j, i in enumerate(self.blocks):
-            self.params[i] = weights[j]
+        for indices, plan, _, _ in self._coded:
+            for i, w in zip(indices, plan.blocks(device)):
+                self.params[i] = w
+        self.momentum = None     # [N, S] fp32, made by the first muon_step
+        self._muon = None        # its matrices and their plan
 
     def load(self, full):
         """Shard full fp32 tensors into the master rows (tide_pack of 4-byte
@@ -82,38 +103,97 @@ class TideUnit:
 
     def all_gather(self, small=False, copy_engine=False, stream=None):
         """Master shards -> param dtype into the gathered buffer -> params, and
-        for the matrices of `blocks` 8-bit rank blocks -> Blocks."""
+        for the matrices of `blocks` and `fp4` 8-bit or 4-bit rank blocks -> Blocks or
+        Fp4Blocks."""
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            if not self.blocks:
+            if not self._coded:
                 self.gathered.view(self.world, self.plan.S).copy_(self.master)
             else:
-                for r in range(self.world):
-                    block_shard(self.block_plan, r, self.master[r], self.block_gathered[r])
-                self._copy_rest()
-        if self.blocks:
-            views = self.block_plan.views([self.params[i] for i in self.blocks])
-            ag(self.block_plan, self.block_gathered, views, small=small, copy_engine=copy_engine,
-               stream=stream)
+                for _, plan, gathered, shard in self._coded:
+                    for r in range(self.world):
+                        shard(plan, r, self.master[r], gathered[r])
+                if self.rest:
+                    self._copy_segments(self.master, self.rest, self.rest_plan,
+                                        self.gathered.view(self.world, self.rest_plan.S))
+        for indices, plan, gathered, _ in self._coded:
+            ag(plan, gathered, plan.views([self.params[i] for i in indices]), small=small,
+               copy_engine=copy_engine, stream=stream)
         if self.rest:
             ag(self.rest_plan, self.gathered, [self.params[i] for i in self.rest], small=small,
                copy_engine=copy_engine, stream=stream)
 
-    def _copy_rest(self):
-        """The master shards of the parameters outside `blocks`, cast, each at its
-        place in the rank blocks of the rest's plan."""
-        if not self.rest:
-            return
-        out = self.gathered.view(self.world, self.rest_plan.S)
-        for j, i in enumerate(self.rest):
+    def _copy_segments(self, shards, select, plan, out):
+        """The shards of the parameters `select`, cast, each at its place in the rank
+        blocks `out` of their own plan."""
+        for j, i in enumerate(select):
             src, _, seg = self.plan.param(i)
-            dst, _, _ = self.rest_plan.param(j)
-            out[:, dst:dst + seg].copy_(self.master[:, src:src + seg])
+            dst, _, _ = plan.param(j)
+            out[:, dst:dst + seg].copy_(shards[:, src:src + seg])
 
-    def linear(self, i, x, grad=None, accumulate=False, dtype=None, short_sums=False):
-        """x [..., k] times parameter i (one of `blocks`, [n, k]) -> [..., n]: see
-        block_linear.  grad: where the backward pass writes the weight gradient
-        ([n, k], bf16 or fp32), e.g. the tensor that reduce_scatter() will read."""
+    def muon_step(self, lr, momentum=0.95, nesterov=True, weight_decay=0.0, select=None,
+                  scale=None, steps=5, coefficients=COEFFICIENTS):
+        """One Muon step on the master shards, from `grad` as reduce_scatter() left it:
+
+            buf <- momentum * buf + grad            (fp32, on the shards)
+            u    = grad + momentum * buf, or buf without nesterov
+            O    = ortho(u), the whole matrix in bf16
+            W   <- (1 - lr * weight_decay) W - lr * scale(rows, cols) * O
+
+        select: the parameters that are updated, by default all 2-D ones, the same in
+        every call; others are left as they are, for another optimizer.  A parameter of
+        more dimensions is taken as the matrix [dim0, inner].  scale: by default
+        sqrt(max(1, rows / cols)).  all_gather() then makes params of the new W."""
+        if select is None:
+            select = [i for i, s in enumerate(self.shapes) if len(s) == 2]
+        select = [int(i) for i in select]
+        if not select:
+            return
+        if self._muon is None:
+            self.momentum = torch.zeros_like(self.master)
+            self._muon = select, Plan([self.shapes[i] for i in select], self.world, self.plan.align)
+        elif self._muon[0] != select:
+            raise ValueError(f"earlier steps updated parameters {self._muon[0]}, not {select}")
+        plan, device = self._muon[1], self.master.device
+        u = torch.zeros(self.world, plan.S, dtype=torch.bfloat16, device=device)
+        for j, i in enumerate(select):
+            src, _, seg = self.plan.param(i)
+            dst, _, _ = plan.param(j)
+            buf, g = self.momentum[:, src:src + seg], self.grad[:, src:src + seg]
+            buf.mul_(momentum).add_(g)
+            u[:, dst:dst + seg].copy_(torch.add(g, buf, alpha=momentum) if nesterov else buf)
+        full = [torch.empty(self.shapes[i], dtype=torch.bfloat16, device=device) for i in select]
+        ag(plan, u.view(-1), full)
+        mats = [t.view(t.shape[0], -1) if t.dim() else t.view(1, 1) for t in full]
+        mats = [m for m in mats if m.numel()]
+        ortho(mats, out=mats, steps=steps, coefficients=coefficients)
+        pack(plan, full, u.view(-1))
+        for j, i in enumerate(select):
+            src, _, seg = self.plan.param(i)
+            dst, _, _ = plan.param(j)
+            rows = self.shapes[i][0] if self.shapes[i] else 1
+            cols = full[j].numel() // rows if rows else 0
+            if not seg or not cols:
+                continue
+            k = scale(rows, cols) if scale is not None else max(1.0, rows / cols) ** 0.5
+            w = self.master[:, src:src + seg]
+            if weight_decay:
+                w.mul_(1 - lr * weight_decay)
+            w.add_(u[:, dst:dst + seg], alpha=-lr * k)
+
+    def linear(self, i, x, grad=None, accumulate=False, dtype=None, short_sums=False,
+               quant_x=False):
+        """x [..., k] times parameter i (one of `blocks` or `fp4`, [n, k]) -> [..., n]:
+        see block_linear (short_sums) and fp4_linear (quant_x).  grad: where the
+        backward pass writes the weight gradient ([n, k], bf16 or fp32), e.g. the
+        tensor that reduce_scatter() will read."""
+        if i in self.fp4:
+            if short_sums:
+                raise ValueError("short_sums is for parameters in 8-bit blocks")
+            return fp4_linear(x, self.params[i], dtype=dtype, quant_x=quant_x, grad=grad,
+                              accumulate=accumulate)
         if i not in self.blocks:
             raise ValueError(f"parameter {i} is not gathered in blocks")
+        if quant_x:
+            raise ValueError("quant_x is for parameters in 4-bit blocks")
         return block_linear(x, self.params[i], dtype=dtype, grad=grad, accumulate=accumulate,
                             short_sums=short_sums)

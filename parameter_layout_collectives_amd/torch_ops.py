@@ -13,8 +13,16 @@
     torch.ops.tide.block_mm(x_codes, x_scales, w_codes, w_scales, cols, out, short_sums)
     torch.ops.tide.block_mm_dx(dy, w_codes, w_scales, out)
     torch.ops.tide.block_mm_dw(dy, x_codes, x_scales, out, accumulate)
+    torch.ops.tide.fp4_shard(fp4_pid, rank, master, block)
+    torch.ops.tide.fp4_unshard(fp4_pid, gathered, params)
+    torch.ops.tide.fp4_quant(x, codes, scales)
+    torch.ops.tide.fp4_dequant(codes, scales, out)
+    torch.ops.tide.fp4_mm(x_codes, x_scales, w_codes, w_scales, cols, out)
+    torch.ops.tide.fp4_linear(x, w_codes, w_scales, out_dtype, quant_x)
+    torch.ops.tide.fp4_mm_dx(dy, w_codes, w_scales, out)
+    torch.ops.tide.ortho(g, out, steps, coefficients)
 
-(block_pid: the id of a registered BlockPlan.)
+(block_pid, fp4_pid: the id of a registered BlockPlan or Fp4Plan.)
 They are how a training framework calls the collectives in place of
 FSDP2's gradient pack and all-gather copy-out ("FSDP通信终局：TIDE零拷贝集合
 通信优化", §"TIDE的设计思路": TIDE sits under FSDP2 and keeps its
@@ -31,8 +39,9 @@ from typing import List
 
 import torch
 
-from . import (Blocks, Plan, ag, block_dequant, block_mm, block_mm_dw, block_mm_dx, block_quant,
-               block_shard, block_unshard, pack, rs, rs_slots)
+from . import (Blocks, Fp4Blocks, Plan, ag, block_dequant, block_mm, block_mm_dw, block_mm_dx,
+               block_quant, block_shard, block_unshard, fp4_dequant, fp4_linear, fp4_mm, fp4_mm_dx,
+               fp4_quant, fp4_shard, fp4_unshard, ortho, pack, rs, rs_slots)
 
 _PLANS = {}
 _LOCK = threading.Lock()
@@ -186,4 +195,91 @@ def block_mm_dw_op(dy: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tens
 
 @block_mm_dw_op.register_fake
 def _(dy, x_codes, x_scales, out, accumulate=False):
+    return None
+
+
+# Matrices in 4-bit blocks (fp4.py), likewise.
+
+@torch.library.custom_op("tide::fp4_shard", mutates_args=("block",))
+def fp4_shard_op(pid: int, rank: int, master: torch.Tensor, block: torch.Tensor) -> None:
+    fp4_shard(_plan(pid), rank, master, block)
+
+
+@fp4_shard_op.register_fake
+def _(pid, rank, master, block):
+    return None
+
+
+@torch.library.custom_op("tide::fp4_unshard", mutates_args=("params",))
+def fp4_unshard_op(pid: int, gathered: torch.Tensor, params: List[torch.Tensor]) -> None:
+    fp4_unshard(_plan(pid), gathered, list(params))
+
+
+@fp4_unshard_op.register_fake
+def _(pid, gathered, params):
+    return None
+
+
+@torch.library.custom_op("tide::fp4_quant", mutates_args=("codes", "scales"))
+def fp4_quant_op(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor) -> None:
+    fp4_quant(x, out=Fp4Blocks(codes, scales, x.shape[1]))
+
+
+@fp4_quant_op.register_fake
+def _(x, codes, scales):
+    return None
+
+
+@torch.library.custom_op("tide::fp4_dequant", mutates_args=("out",))
+def fp4_dequant_op(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor) -> None:
+    fp4_dequant(Fp4Blocks(codes, scales, out.shape[1]), out=out)
+
+
+@fp4_dequant_op.register_fake
+def _(codes, scales, out):
+    return None
+
+
+@torch.library.custom_op("tide::fp4_mm", mutates_args=("out",))
+def fp4_mm_op(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
+              w_scales: torch.Tensor, cols: int, out: torch.Tensor) -> None:
+    fp4_mm(Fp4Blocks(x_codes, x_scales, cols), Fp4Blocks(w_codes, w_scales, cols), out=out)
+
+
+@fp4_mm_op.register_fake
+def _(x_codes, x_scales, w_codes, w_scales, cols, out):
+    return None
+
+
+@torch.library.custom_op("tide::fp4_linear", mutates_args=())
+def fp4_linear_op(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                  out_dtype: torch.dtype, quant_x: bool = False) -> torch.Tensor:
+    return fp4_linear(x, Fp4Blocks(w_codes, w_scales, x.shape[-1]), dtype=out_dtype,
+                      quant_x=quant_x)
+
+
+@fp4_linear_op.register_fake
+def _(x, w_codes, w_scales, out_dtype, quant_x=False):
+    return x.new_empty(*x.shape[:-1], w_codes.shape[0], dtype=out_dtype)
+
+
+@torch.library.custom_op("tide::fp4_mm_dx", mutates_args=("out",))
+def fp4_mm_dx_op(dy: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                 out: torch.Tensor) -> None:
+    fp4_mm_dx(dy, Fp4Blocks(w_codes, w_scales, out.shape[1]), out=out)
+
+
+@fp4_mm_dx_op.register_fake
+def _(dy, w_codes, w_scales, out):
+    return None
+
+
+@torch.library.custom_op("tide::ortho", mutates_args=("out",))
+def ortho_op(g: List[torch.Tensor], out: List[torch.Tensor], steps: int,
+             coefficients: List[float]) -> None:
+    ortho(list(g), out=list(out), steps=steps, coefficients=coefficients)
+
+
+@ortho_op.register_fake
+def _(g, out, steps, coefficients):
     return None
