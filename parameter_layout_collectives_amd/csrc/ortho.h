@@ -24,27 +24,20 @@ struct OrthoGroup {
     __host__ __device__ bool tall() const { return nr > nc; }
     __host__ __device__ uint32_t r() const { return tall() ? nc : nr; }
     __host__ __device__ uint32_t rp() const { return tall() ? ncp : nrp; }
-    // X is held twice (a step reads one and writes the other), each time as two
-    // fp16 matrices hi and lo of the padded size: wide ones below one another,
-    // tall ones' rows side by side, so that both form one factor of twice the
-    // length of the sum.  Pitch and distance in elements.
-    __host__ __device__ int64_t pitch() const { return tall() ? 2 * static_cast<int64_t>(ncp) : ncp; }
-    __host__ __device__ int64_t lo() const {
-        return tall() ? static_cast<int64_t>(ncp) : static_cast<int64_t>(nrp) * ncp;
-    }
+    // fp16 matrices [R, C] lie in panels of 32 columns, [C / 32, R, 32]: the bytes that a
+    // workgroup loads for one step of a sum, along the rows or across them, are runs of
+    // 1 KB or more.  X is held twice (a step reads one and writes the other), each time
+    // as a matrix hi and behind it lo.
     __host__ __device__ int64_t x_bytes() const { return 4 * static_cast<int64_t>(nrp) * ncp; }
+    __host__ __device__ int64_t lo() const { return static_cast<int64_t>(nrp) * ncp; }
     // Whether lo enters P X, too.
     __host__ __device__ bool both() const { return r() <= kOrthoBoth; }
-    // Then the fp16 matrices A = X X^T [rp, rp] and P [rp, rp], or twice in each row
-    // [rp, 2 rp] against hi and lo, without their diagonals, and these in fp32 [rp].
-    __host__ __device__ int64_t p_pitch() const {
-        return (both() ? 2 : 1) * static_cast<int64_t>(rp());
-    }
+    // Then A = X X^T and P [rp, rp] without their diagonals, and these in fp32 [rp].
     __host__ __device__ int64_t a_at() const { return 2 * x_bytes(); }
     __host__ __device__ int64_t p_at() const {
         return a_at() + 2 * static_cast<int64_t>(rp()) * rp();
     }
-    __host__ __device__ int64_t a_diag() const { return p_at() + 2 * rp() * p_pitch(); }
+    __host__ __device__ int64_t a_diag() const { return p_at() + 2 * static_cast<int64_t>(rp()) * rp(); }
     __host__ __device__ int64_t p_diag() const { return a_diag() + 4 * rp(); }
     __host__ __device__ int64_t bytes() const { return p_diag() + 4 * rp(); }
 };

@@ -38,8 +38,8 @@
 namespace tide {
 namespace {
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kScaleA = 4096.0f, kScaleP = 1024.0f;
 
@@ -109,6 +109,11 @@ __global__ __launch_bounds__(256) void squares_kernel(Groups a, Space s) {
     if (threadIdx.x == 0) s.sums[static_cast<int64_t>(g.first + m) * kOrthoParts + q] = v;
 }
 
+// Where (row, col) of a matrix of `rows` rows in panels lies, in elements.
+__device__ __forceinline__ int64_t panel_at(uint32_t rows, uint32_t row, uint32_t col) {
+    return ((static_cast<int64_t>(col >> 5) * rows + row) << 5) + (col & 31);
+}
+
 // 2^ex: X's scale.  About sqrt(r c), which brings the first X's elements near 1.
 __host__ __device__ inline int x_exponent(uint32_t nr, uint32_t nc) {
     int e = 0;
@@ -151,88 +156,222 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
         h[i] = static_cast<_Float16>(v);
         l[i] = static_cast<_Float16>(v - static_cast<float>(h[i]));
     }
-    _Float16 *X = reinterpret_cast<_Float16 *>(s.base + g.base + m * g.stride) + row * g.pitch() + col;
+    _Float16 *X = reinterpret_cast<_Float16 *>(s.base + g.base + m * g.stride) + panel_at(g.nrp, row, col);
     *reinterpret_cast<f16x8 *>(X) = h;
     *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
 }
 
 // ------------------------------------------------------- the products
 
-// out[i, j] = sum over c of I(i, c) J(c, j) for fp16 factors that lie in memory
-// padded and aligned, so that both go straight into LDS; the layouts and
-// fragments of the bf16 products' stages (which move bits).  Two buffers: the step
-// after next is asked for once the barrier has freed a buffer, so its loads have a
-// whole step to arrive; the next step's first fragments are read under this step's
-// last multiplications.
-template <Mode MI, Mode MJ, int T, int WI, int WJ>
+// out[i, j] = sum over c of I(i, c) J(c, j) for fp16 factors in panels, so that both
+// go straight into LDS, in runs of at least 1 KB: rows of 64 bytes each from a
+// row-major matrix, half lines of the cache, take 1.5 times as long.  A T x T tile of
+// the output per workgroup of 4 waves, 2 x 2; one step of the sum is 32 values, 64 T
+// bytes of a factor:
+//   along   (the sum runs along the rows): T rows of one panel
+//   across  (the sum runs over the rows): 32 rows of T / 32 panels, read with the
+//           transposing read, which hands each lane 4 values along the sum
+// In both, chunk h (16 bytes) of a panel's row r lies at h ^ key(r) in LDS: the rows
+// that a read of either kind takes at a time fall into different banks.
+constexpr int kThreads = 256;
+constexpr int kStep = 32, kBuffers = 5;
+
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const char *scalar(const char *p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    return reinterpret_cast<const char *>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ int key(int r) { return r >> 3 & 3; }
+
+template <bool ACROSS, int T>
+struct Feed {
+    static constexpr int SLOTS = T * 4 / kThreads;         // 16-byte loads per thread and step
+    static constexpr int BYTES = T * 64;
+
+    const char *base;            // of the next step
+    int64_t left;                // bytes from base to the end of what may be read
+    uint32_t advance;            // bytes from one step to the next
+    uint32_t panel;              // bytes of a panel
+    int live;                    // steps that are left: after them nothing may be read
+    int turn;                    // steps until the sum goes on elsewhere,
+    int64_t jump, again;         // so many bytes from there, with so many left
+    uint32_t off;                // this thread's first slot
+
+    // Lines [first, first + T) of a matrix [rows, cols] in panels, for `steps` steps;
+    // after `half` of them the sum goes on `to` bytes from the matrix's start (a
+    // multiple of its size).
+    __device__ __forceinline__ void init(const char *p, uint32_t rows, uint32_t cols, uint32_t first,
+                                         uint32_t steps, uint32_t half, int64_t to, int t) {
+        live = uniform(steps);
+        panel = uniform(static_cast<int64_t>(rows) * 64);
+        const int64_t bytes = static_cast<int64_t>(panel) * (cols / 32);
+        turn = uniform(half);
+        int64_t at;
+        if (ACROSS) {
+            at = static_cast<int64_t>(first / 32) * panel;
+            left = bytes - at;
+            advance = kStep * 64;
+        } else {
+            at = static_cast<int64_t>(first) * 64;
+            left = min(static_cast<int64_t>(rows - first), static_cast<int64_t>(T)) * 64;
+            advance = panel;
+        }
+        base = scalar(p + at);
+        jump = to - static_cast<int64_t>(half) * advance;
+        left = again = uniform64(left);
+        jump = uniform64(jump);
+        const int row = t / 4;                              // of 64, in a panel
+        const int at16 = (row & 31) * 64 + ((t & 3) ^ key(row)) * 16;
+        off = at16 + (row >> 5) * (ACROSS ? panel : 32 * 64);
+    }
+    static __device__ __forceinline__ int64_t uniform64(int64_t v) {
+        return static_cast<int64_t>(reinterpret_cast<uint64_t>(scalar(reinterpret_cast<const char *>(v))));
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer() const {
+        const int64_t most = 0xffffffc0ll;
+        return buffer_of(base, live > 0 ? static_cast<uint32_t>(left < most ? left : most) : 0);
+    }
+    // Asks for slot q of the next step: 64 rows further (along), 2 panels (across).
+    // What lies outside, and past the last step everything, comes as zeros.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, LDS_AS char *lds, int wave, int q) const {
+        direct_load(r, lds + (wave + q * 4) * 1024, off, q * (ACROSS ? 2 * panel : 64 * 64));
+    }
+    __device__ __forceinline__ void next() {
+        live--;
+        base += advance;
+        if (ACROSS) left -= advance;
+        if (--turn == 0) {
+            base += jump;
+            if (ACROSS) left = again;
+        }
+    }
+    // A fragment is 32 lines x 16 values: lane (r32, g) holds values 8 g + 0..7 of line
+    // r32.  This lane's part of its address.
+    static __device__ __forceinline__ int lane_at(int lane) {
+        if (!ACROSS) {
+            const int r = lane & 31, g = lane >> 5;
+            return r * 64 + ((g ^ key(r)) << 4);
+        }
+        // rows 8 g + q, and 4 further on; columns 16 h + 4 p .. + 3 (chunks 2 h + p / 2)
+        const int q = lane >> 2 & 3, p = lane & 3, h = lane >> 4 & 1, row = (lane >> 5) * 8 + q;
+        return row * 64 + (((2 * h + (p >> 1)) ^ key(row)) << 4) + (p & 1) * 8;
+    }
+    // The fragment of lines [32 f, 32 f + 32), values [16 k, 16 k + 16) of the step.
+    static __device__ __forceinline__ f16x8 frag(const LDS_AS char *lds, int lane, int f, int k) {
+        if (!ACROSS)             // chunks 2 k and 2 k + 1
+            return *reinterpret_cast<const LDS_AS f16x8 *>(lds + f * 2048 + (lane ^ k * 32));
+        union {
+            i16x4 h[2];
+            f16x8 v;
+        } u;
+        // rows 16 k on: key() differs in its second bit
+        const LDS_AS char *p = lds + f * 2048 + k * 1024 + (lane ^ k * 32);
+        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)p);
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)(p + 256));
+        return u.v;
+    }
+};
+
+// kBuffers steps are in LDS.  While one is multiplied, the fragments of the next are
+// read, a J and an I fragment per line (all multiplications of one I fragment), and
+// the loads of the fourth after it set out into the buffer that the barrier has just
+// freed; so a step's loads have two to three steps to arrive, and reads and loads
+// come evenly.
+template <bool AI, bool AJ, int T>
 struct Half {
-    static constexpr int NT = WI * WJ * 64;
-    static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;
-    static constexpr int LINES = 2 * FI, RING = FI >= 4 ? 4 : 2, D = RING - 1;
-    static constexpr int TILE = T * 128;
-    typedef Stage<MI, T, NT, true> SI;
-    typedef Stage<MJ, T, NT, true> SJ;
-    static_assert(SI::DIRECT && SJ::DIRECT, "factors go straight into LDS");
-    static_assert(LINES % RING == 0 && D <= FI,
-                  "a step starts at ring entry 0, and its first half is over when the next "
-                  "step's J fragments replace it");
+    static constexpr int F = T / 2 / 32;                   // 32 x 32 fragments of a wave, each way
+    static constexpr int LINES = 2 * F;                    // of a step: 2 x 16 values
+    static constexpr int D = LINES >= 8 ? 3 : 1, RING = D + 1;   // I fragments read ahead
+    typedef Feed<AI, T> FI;
+    typedef Feed<AJ, T> FJ;
+    static constexpr int LOADS = FI::SLOTS + FJ::SLOTS;
+    static constexpr int PER_LINE = LOADS / LINES;         // loads issued with a line
+    static constexpr int TILE = FI::BYTES, BUFFER = 2 * TILE, LDS = kBuffers * BUFFER;
+    static_assert(LINES % RING == 0 && LOADS % LINES == 0, "a step starts at ring entry 0");
 
-    SI si;
-    SJ sj;
-    int lane, wave, wi, wj;
-    f32x4 acc[FI][FJ];
+    FI fi;
+    FJ fj;
+    int lane, wave, wi, wj, ai, aj;
+    f32x16 acc[F][F];
 
-    __device__ __forceinline__ void fetch(LDS_AS char *ti, LDS_AS char *tj) {
-        si.fetch(ti, wave);
-        sj.fetch(tj, wave);
+    // All but this wave's newest N loads have arrived, and every wave is here.  The
+    // fragments read before have all been multiplied but for those of the current
+    // step, whose buffer stays: reads need not be waited for.  Loads return in order,
+    // and any that the compiler might add only make the wait longer.
+    template <int N>
+    static __device__ __forceinline__ void wait() {
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t ri, __amdgpu_buffer_rsrc_t rj,
+                                         LDS_AS char *b, int q) const {
+        if (q < FI::SLOTS)
+            fi.load(ri, b, wave, q);
+        else
+            fj.load(rj, b + TILE, wave, q - FI::SLOTS);
     }
     __device__ __forceinline__ f16x8 line(const LDS_AS char *b, int n) const {
-        return __builtin_bit_cast(f16x8, SI::frag(b, wi * (T / WI) + n % FI * 16, n / FI, lane));
+        return FI::frag(b + wi * (TILE / 2), ai, n % F, n / F);
     }
-    __device__ __forceinline__ void rows(f16x8 *r, const LDS_AS char *b, int kk) const {
-#pragma unroll
-        for (int y = 0; y < FJ; y++)
-            r[y] = __builtin_bit_cast(f16x8, SJ::frag(b, wj * (T / WJ) + y * 16, kk, lane));
+    __device__ __forceinline__ f16x8 row(const LDS_AS char *b, int n) const {
+        return FJ::frag(b + TILE + wj * (TILE / 2), aj, n % F, n / F);
     }
-    template <bool LAST>
-    __device__ __forceinline__ void step(f16x8 *l, f16x8 (*r)[FJ], LDS_AS char *here_i,
-                                         LDS_AS char *here_j, LDS_AS char *there_i,
-                                         LDS_AS char *there_j) {
-        rows(r[1], here_j, 1);
+    // One step from `here`; `there` is the next one, `to` receives the fourth after it.
+    __device__ __forceinline__ void step(f16x8 *l, const f16x8 *r, f16x8 *next, const LDS_AS char *here,
+                                         const LDS_AS char *there, LDS_AS char *to) {
+        const __amdgpu_buffer_rsrc_t ri = fi.buffer(), rj = fj.buffer();
+        // the next step has arrived; newer are the loads of those behind it
+        wait<(kBuffers - 3) * LOADS>();
 #pragma unroll
         for (int n = 0; n < LINES; n++) {
-            if (n + D < LINES) l[(n + D) % RING] = line(here_i, n + D);
-            if (!LAST && n + D == LINES) {
-                landed();
-                fetch(here_i, here_j);
-                rows(r[0], there_j, 0);
-            }
-            if (!LAST && n + D >= LINES) l[(n + D) % RING] = line(there_i, n + D - LINES);
+            l[(n + D) % RING] = n + D < LINES ? line(here, n + D) : line(there, n + D - LINES);
+            next[n] = row(there, n);
 #pragma unroll
-            for (int y = 0; y < FJ; y++)
-                acc[n % FI][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    r[n / FI][y], l[n % RING], acc[n % FI][y], 0, 0, 0);
+            for (int y = 0; y < F; y++) {
+                acc[n % F][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[n / F * F + y], l[n % RING],
+                                                                       acc[n % F][y], 0, 0, 0);
+                if (y == 0) {
+#pragma unroll
+                    for (int q = 0; q < PER_LINE; q++) load(ri, rj, to, n * PER_LINE + q);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+        fi.next();
+        fj.next();
     }
-    __device__ __forceinline__ void run(LDS_AS char *__restrict__ i0, LDS_AS char *__restrict__ i1,
-                                        LDS_AS char *__restrict__ j0, LDS_AS char *__restrict__ j1,
-                                        uint32_t steps) {
-        fetch(i0, j0);
-        fetch(i1, j1);
-        landed();
-        f16x8 l[RING], r[2][FJ];
-        rows(r[0], j0, 0);
+    __device__ __forceinline__ void run(LDS_AS char *lds, uint32_t steps) {
+        ai = FI::lane_at(lane);
+        aj = FJ::lane_at(lane);
 #pragma unroll
-        for (int n = 0; n < D; n++) l[n] = line(i0, n);
-        // Past the last step zeros are fetched, or values that nothing uses,
-        // which keeps branches out of the loop.
-        for (; steps > 1; steps -= 2) {
-            step<false>(l, r, i0, j0, i1, j1);
-            step<false>(l, r, i1, j1, i0, j0);
+        for (int b = 0; b < kBuffers - 1; b++) {
+            const __amdgpu_buffer_rsrc_t ri = fi.buffer(), rj = fj.buffer();
+#pragma unroll
+            for (int q = 0; q < LOADS; q++) load(ri, rj, lds + b * BUFFER, q);
+            fi.next();
+            fj.next();
         }
-        if (steps) step<true>(l, r, i0, j0, i1, j1);
-        landed();                // no load may still be on its way to LDS at the end
+        wait<(kBuffers - 2) * LOADS>();
+        f16x8 l[RING], r0[LINES], r1[LINES];
+#pragma unroll
+        for (int n = 0; n < LINES; n++) r0[n] = row(lds, n);
+#pragma unroll
+        for (int n = 0; n < D; n++) l[n] = line(lds, n);
+        uint32_t here = 0, to = (kBuffers - 1) * BUFFER;
+        auto after = [](uint32_t b) { return b == (kBuffers - 1) * BUFFER ? 0 : b + BUFFER; };
+        // sums are of 64 values or a multiple: steps come in pairs
+        for (; steps; steps -= 2) {
+            const uint32_t there = after(here), to2 = after(to);
+            step(l, r0, r1, lds + here, lds + there, lds + to);
+            here = after(there);
+            step(l, r1, r0, lds + there, lds + here, lds + to2);
+            to = after(to2);
+        }
+        arrived();               // no load may still be on its way to LDS at the end,
+        __syncthreads();         // nor a read of what the sums will overwrite
     }
 };
 
@@ -254,113 +393,161 @@ __host__ __device__ inline uint32_t tiles_of(const OrthoGroup &g, int stage, uin
     return n * (n + 1) / 2;
 }
 
-__device__ __forceinline__ f16x4 to_half(f32x4 v) {
-    return f16x4{static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]), static_cast<_Float16>(v[2]),
-                 static_cast<_Float16>(v[3])};
-}
+// A wave's sums go through its own part of LDS, 32 rows at a time, so that a lane gets
+// 8 neighbours of a row, 16 bytes of a panel, and a wave's accesses are runs of 1 KB
+// (16 rows of a panel).
+template <int T>
+struct Turn {
+    static constexpr int W = T / 2, PITCH = W * 4 + 16;    // a wave's tile is W x W
+    static constexpr int PASSES = 32 * W / 512;
+    static_assert(32 * PITCH <= kBuffers * 2 * T * 64 / 4, "a wave's part of LDS");
 
-template <int STAGE, Mode MI, Mode MJ, int T, int WI, int WJ>
+    LDS_AS char *lds;
+    int lane;
+    int per;                     // lanes of a row: 4 (a panel's row), or W / 8
+
+    template <int F>
+    __device__ __forceinline__ void put(const f32x16 (&acc)[F][F], int c) const {
+        // a lane holds columns 8 q + 4 g + 0..3 of its row, q = 0..3
+#pragma unroll
+        for (int y = 0; y < F; y++)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                *reinterpret_cast<LDS_AS f32x4 *>(lds + (lane & 31) * PITCH + y * 128 + q * 32 +
+                                                  (lane >> 5) * 16) =
+                    f32x4{acc[c][y][4 * q], acc[c][y][4 * q + 1], acc[c][y][4 * q + 2], acc[c][y][4 * q + 3]};
+    }
+    // This lane's row and first column in pass q.
+    __device__ __forceinline__ int row(int q) const {
+        return per == 4 ? q % 2 * 16 + lane / 4 : q * (64 / (W / 8)) + lane / (W / 8);
+    }
+    __device__ __forceinline__ int col(int q) const {
+        return per == 4 ? q / 2 * 32 + lane % 4 * 8 : lane % (W / 8) * 8;
+    }
+    __device__ __forceinline__ LDS_AS char *at(int q) const { return lds + row(q) * PITCH + col(q) * 4; }
+    __device__ __forceinline__ void get(float *v, int q) const {
+        const f32x4 a = *reinterpret_cast<const LDS_AS f32x4 *>(at(q));
+        const f32x4 b = *reinterpret_cast<const LDS_AS f32x4 *>(at(q) + 16);
+#pragma unroll
+        for (int n = 0; n < 4; n++) v[n] = a[n], v[4 + n] = b[n];
+    }
+    __device__ __forceinline__ void set(int q, const f16x8 &h) const {
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+            *reinterpret_cast<LDS_AS _Float16 *>(at(q) + n * 4) = h[n];
+    }
+    // 8 rows' values of column `col`, as set() left them
+    __device__ __forceinline__ f16x8 column(int row, int col) const {
+        f16x8 h;
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+            h[n] = *reinterpret_cast<const LDS_AS _Float16 *>(lds + (row + n) * PITCH + col * 4);
+        return h;
+    }
+};
+
+template <int STAGE, bool AI, bool AJ, int T>
 __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGroup &g, uint32_t m,
                                              uint32_t ti, uint32_t tj, LDS_AS char *lds) {
-    typedef Half<MI, MJ, T, WI, WJ> K;
+    typedef Half<AI, AJ, T> K;
     const int t = threadIdx.x, lane = t & 63;
     char *const base = p.s.base + g.base + static_cast<int64_t>(m) * g.stride;
     char *const x = base + p.from * g.x_bytes();
-    const int64_t rp = g.rp(), xp = g.pitch() * 2;
-    const int64_t i0 = static_cast<int64_t>(ti) * T, j0 = static_cast<int64_t>(tj) * T;
+    const uint32_t rp = g.rp(), i0 = ti * T, j0 = tj * T;
     K k;
     k.wave = __builtin_amdgcn_readfirstlane(t >> 6);
     k.lane = lane;
-    k.wi = k.wave / WJ;
-    k.wj = k.wave % WJ;
-    int64_t sum;
+    k.wi = k.wave / 2;
+    k.wj = k.wave % 2;
+    // with both(), hi's sum goes on with lo, and P's from its start again
+    const uint32_t once = (STAGE == kGram ? max(g.nrp, g.ncp) : rp) / kStep;
+    const bool twice = STAGE == kApply && g.both();
+    const uint32_t steps = twice ? 2 * once : once, half = twice ? once : ~0u;
+    const int64_t lo = twice ? 2 * g.lo() : 0;
     if (STAGE == kGram) {
-        sum = g.tall() ? g.nrp : g.ncp;
-        k.si.init(x, nullptr, xp, 0, i0, rp, sum, 0, t);
-        k.sj.init(x, nullptr, xp, 0, j0, rp, sum, 0, t);
+        k.fi.init(x, g.nrp, g.ncp, i0, steps, half, 0, t);
+        k.fj.init(x, g.nrp, g.ncp, j0, steps, half, 0, t);
     } else if (STAGE == kPoly) {
-        sum = rp;
-        k.si.init(base + g.a_at(), nullptr, rp * 2, 0, i0, rp, sum, 0, t);
-        k.sj.init(base + g.a_at(), nullptr, rp * 2, 0, j0, rp, sum, 0, t);
+        k.fi.init(base + g.a_at(), rp, rp, i0, steps, half, 0, t);
+        k.fj.init(base + g.a_at(), rp, rp, j0, steps, half, 0, t);
+    } else if (g.tall()) {
+        k.fi.init(x, g.nrp, g.ncp, i0, steps, half, lo, t);
+        k.fj.init(base + g.p_at(), rp, rp, j0, steps, half, 0, t);
     } else {
-        sum = g.p_pitch();
-        if (g.tall()) {
-            k.si.init(x, nullptr, xp, 0, i0, g.nrp, sum, 0, t);
-            k.sj.init(base + g.p_at(), nullptr, sum * 2, 0, j0, rp, sum, 0, t);
-        } else {
-            k.si.init(base + g.p_at(), nullptr, sum * 2, 0, i0, rp, sum, 0, t);
-            k.sj.init(x, nullptr, xp, 0, j0, g.ncp, sum, 0, t);
-        }
+        k.fi.init(base + g.p_at(), rp, rp, i0, steps, half, 0, t);
+        k.fj.init(x, g.nrp, g.ncp, j0, steps, half, lo, t);
     }
 #pragma unroll
-    for (int a = 0; a < K::FI; a++)
+    for (int a = 0; a < K::F; a++)
 #pragma unroll
-        for (int b = 0; b < K::FJ; b++) k.acc[a][b] = f32x4{0, 0, 0, 0};
-    k.run(lds, lds + K::TILE, lds + 2 * K::TILE, lds + 3 * K::TILE, uniform((sum + 63) / 64));
+        for (int b = 0; b < K::F; b++)
+#pragma unroll
+            for (int n = 0; n < 16; n++) k.acc[a][b][n] = 0.0f;
+    k.run(lds, uniform(steps));
 
+    typedef Turn<T> U;
+    // the last step's output is row-major
+    const U turn = {lds + k.wave * (K::LDS / 4), lane, STAGE == kApply && p.last ? U::W / 8 : 4};
     const float2 t1 = p.first ? p.s.scales[g.first + m] : make_float2(1.0f, 1.0f);
     const int ex = x_exponent(g.nr, g.nc);
-    const uint32_t li = static_cast<uint32_t>(i0) + k.wi * (T / WI) + (lane & 15);
-    const uint32_t lj = static_cast<uint32_t>(j0) + k.wj * (T / WJ) + (lane >> 4) * 4;
+    const uint32_t li = i0 + k.wi * U::W, lj = j0 + k.wj * U::W;       // the wave's first row and column
     float *const ad = reinterpret_cast<float *>(base + g.a_diag());
     float *const pd = reinterpret_cast<float *>(base + g.p_diag());
-    if (STAGE == kGram) {
-        const float f = ldexpf(t1.y, -2 * ex);
-        _Float16 *const o = reinterpret_cast<_Float16 *>(base + g.a_at());
-#pragma unroll
-        for (int a = 0; a < K::FI; a++)
-#pragma unroll
-            for (int b = 0; b < K::FJ; b++) {
-                const uint32_t i = li + a * 16, j = lj + b * 16;
-                if (i >= rp || j >= rp) continue;      // X's padding makes A's zeros
-                f32x4 v = k.acc[a][b] * f;
-#pragma unroll
-                for (int n = 0; n < 4; n++)
-                    if (i == j + n) {
-                        ad[i] = v[n];
-                        v[n] = 0.0f;
-                    }
-                const f16x4 h = to_half(v * kScaleA);
-                *reinterpret_cast<f16x4 *>(o + i * rp + j) = h;
-                if (ti != tj)
-#pragma unroll
-                    for (int n = 0; n < 4; n++) o[(j + n) * rp + i] = h[n];
-            }
-        return;
-    }
-    if (STAGE == kPoly) {
-        const _Float16 *const o = reinterpret_cast<const _Float16 *>(base + g.a_at());
-        _Float16 *const q = reinterpret_cast<_Float16 *>(base + g.p_at());
-        const int64_t qp = g.p_pitch();
+    if (STAGE != kApply) {
+        const float f = STAGE == kGram ? ldexpf(t1.y, -2 * ex) : 1.0f / (kScaleA * kScaleA);
+        const _Float16 *const old = reinterpret_cast<const _Float16 *>(base + g.a_at());
+        _Float16 *const to = reinterpret_cast<_Float16 *>(base + (STAGE == kGram ? g.a_at() : g.p_at()));
         const uint32_t r = g.r();
 #pragma unroll
-        for (int b = 0; b < K::FJ; b++) {
-            const uint32_t j = lj + b * 16;
-            if (j >= rp) continue;
-            const f32x4 dj = *reinterpret_cast<const f32x4 *>(ad + j);
+        for (int c = 0; c < K::F; c++) {
+            turn.put(k.acc, c);
 #pragma unroll
-            for (int a = 0; a < K::FI; a++) {
-                const uint32_t i = li + a * 16;
-                if (i >= rp) continue;
-                const float di = ad[i];
-                const f16x4 old = *reinterpret_cast<const f16x4 *>(o + i * rp + j);
-                f32x4 v = k.acc[a][b] * (1.0f / (kScaleA * kScaleA));
+            for (int q = 0; q < U::PASSES; q++) {
+                const uint32_t i = li + c * 32 + turn.row(q), j = lj + turn.col(q);
+                float v[8];
+                turn.get(v, q);
+                f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (i < rp && j < rp) {                  // X's padding makes zeros of A's and P's
+                    const int64_t at = panel_at(rp, i, j);
+                    if (STAGE == kGram) {
 #pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    const float oij = static_cast<float>(old[n]) / kScaleA;
-                    if (i == j + n) {
-                        pd[i] = i < r ? p.ca + p.cb * di + p.cc * (di * di + v[n]) : 0.0f;
-                        v[n] = 0.0f;
+                        for (int n = 0; n < 8; n++) {
+                            v[n] *= f;
+                            if (i == j + n) {
+                                ad[i] = v[n];
+                                v[n] = 0.0f;
+                            }
+                            h[n] = static_cast<_Float16>(v[n] * kScaleA);
+                        }
                     } else {
-                        v[n] = p.cb * oij + p.cc * ((di + dj[n]) * oij + v[n]);
-                    }
-                }
-                const f16x4 h = to_half(v * kScaleP);
-                for (int64_t c = 0; c < qp; c += rp) {
-                    *reinterpret_cast<f16x4 *>(q + i * qp + c + j) = h;
-                    if (ti != tj)
+                        const float di = ad[i];
+                        const f32x4 dl = *reinterpret_cast<const f32x4 *>(ad + j);
+                        const f32x4 dh = *reinterpret_cast<const f32x4 *>(ad + j + 4);
+                        const f16x8 o = *reinterpret_cast<const f16x8 *>(old + at);
 #pragma unroll
-                        for (int n = 0; n < 4; n++) q[(j + n) * qp + c + i] = h[n];
+                        for (int n = 0; n < 8; n++) {
+                            const float oij = static_cast<float>(o[n]) * (1.0f / kScaleA);
+                            const float oo = v[n] * f;
+                            if (i == j + n) {
+                                pd[i] = i < r ? p.ca + p.cb * di + p.cc * (di * di + oo) : 0.0f;
+                                v[n] = 0.0f;
+                            } else {
+                                v[n] = p.cb * oij + p.cc * ((di + (n < 4 ? dl[n] : dh[n - 4])) * oij + oo);
+                            }
+                            h[n] = static_cast<_Float16>(v[n] * kScaleP);
+                        }
+                    }
+                    *reinterpret_cast<f16x8 *>(to + at) = h;
+                }
+                if (ti != tj) turn.set(q, h);
+            }
+            if (ti != tj) {                              // the other side of the diagonal
+#pragma unroll
+                for (int q = 0; q < U::W / 16; q++) {
+                    const int col = q * 16 + lane / 4, row = lane % 4 * 8;
+                    const uint32_t i = li + c * 32 + row, j = lj + col;
+                    const f16x8 h = turn.column(row, col);
+                    if (i < rp && j < rp) *reinterpret_cast<f16x8 *>(to + panel_at(rp, j, i)) = h;
                 }
             }
         }
@@ -370,57 +557,67 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     const _Float16 *const from = reinterpret_cast<const _Float16 *>(x);
     _Float16 *const to = reinterpret_cast<_Float16 *>(base + (1 - p.from) * g.x_bytes());
     const float f = p.last ? ldexpf(t1.x, -ex) : t1.x;
-    MmLaunch out = {};
-    out.out = reinterpret_cast<char *>(p.s.pointers[g.first + m].out);
-    out.rows = g.nr;
-    out.cols = g.nc;
-    out.out_bf16 = 1;
+    __bf16 *const out = p.last ? reinterpret_cast<__bf16 *>(p.s.pointers[g.first + m].out) : nullptr;
+    const bool tall = g.tall();
 #pragma unroll
-    for (int b = 0; b < K::FJ; b++) {
-        const uint32_t j = lj + b * 16;
-        if (j >= g.ncp) continue;
-        f32x4 qj = {0, 0, 0, 0};
-        if (g.tall()) qj = *reinterpret_cast<const f32x4 *>(pd + j);
+    for (int c = 0; c < K::F; c++) {
+        turn.put(k.acc, c);
 #pragma unroll
-        for (int a = 0; a < K::FI; a++) {
-            const uint32_t i = li + a * 16;
-            if (i >= g.nrp) continue;
-            const int64_t at = i * g.pitch() + j;
-            const f16x4 h = *reinterpret_cast<const f16x4 *>(from + at);
-            const f16x4 l = *reinterpret_cast<const f16x4 *>(from + at + g.lo());
-            if (!g.tall()) {
+        for (int q = 0; q < U::PASSES; q++) {
+            const uint32_t i = li + c * 32 + turn.row(q), j = lj + turn.col(q);
+            float v[8];
+            turn.get(v, q);
+            if (i >= g.nrp || j >= g.ncp) continue;
+            const int64_t at = panel_at(g.nrp, i, j);
+            const f16x8 h = *reinterpret_cast<const f16x8 *>(from + at);
+            const f16x8 l = *reinterpret_cast<const f16x8 *>(from + at + g.lo());
+            f32x4 ql, qh;
+            if (tall) {
+                ql = *reinterpret_cast<const f32x4 *>(pd + j);
+                qh = *reinterpret_cast<const f32x4 *>(pd + j + 4);
+            } else {
                 const float qi = pd[i];
-                qj = f32x4{qi, qi, qi, qi};
+                ql = qh = f32x4{qi, qi, qi, qi};
             }
-            f32x4 v;
 #pragma unroll
-            for (int n = 0; n < 4; n++)
-                v[n] = (k.acc[a][b][n] * (1.0f / kScaleP) +
-                        qj[n] * (static_cast<float>(h[n]) + static_cast<float>(l[n]))) * f;
-            if (p.last) {
-                store4(out, i, j, v);
+            for (int n = 0; n < 8; n++)
+                v[n] = (v[n] * (1.0f / kScaleP) +
+                        (n < 4 ? ql[n] : qh[n - 4]) * (static_cast<float>(h[n]) + static_cast<float>(l[n]))) * f;
+            if (!p.last) {
+                f16x8 nh, nl;
+#pragma unroll
+                for (int n = 0; n < 8; n++) {
+                    nh[n] = static_cast<_Float16>(v[n]);
+                    nl[n] = static_cast<_Float16>(v[n] - static_cast<float>(nh[n]));
+                }
+                *reinterpret_cast<f16x8 *>(to + at) = nh;
+                *reinterpret_cast<f16x8 *>(to + at + g.lo()) = nl;
                 continue;
             }
-            const f16x4 nh = to_half(v);
-            f32x4 rest;
+            if (i >= g.nr || j >= g.nc) continue;
+            __bf16 *o = out + static_cast<int64_t>(i) * g.nc + j;
+            if (g.nc - j >= 8) {
+                *reinterpret_cast<half_u32x4 *>(o) =
+                    half_u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+            } else {
 #pragma unroll
-            for (int n = 0; n < 4; n++) rest[n] = v[n] - static_cast<float>(nh[n]);
-            *reinterpret_cast<f16x4 *>(to + at) = nh;
-            *reinterpret_cast<f16x4 *>(to + at + g.lo()) = to_half(rest);
+                for (int n = 0; n < 8; n++)
+                    if (j + n < g.nc) o[n] = static_cast<__bf16>(v[n]);
+            }
         }
     }
 }
 
-template <int STAGE, int T, int WI, int WJ>
-__global__ __launch_bounds__(WI * WJ * 64, 1) void product_kernel(ProductArgs p) {
-    __shared__ __attribute__((aligned(1024))) char lds[4 * T * 128];
+template <int STAGE, int T>
+__global__ __launch_bounds__(kThreads, T == 256 ? 1 : 2) void product_kernel(ProductArgs p) {
+    __shared__ __attribute__((aligned(1024))) char lds[Half<false, false, T>::LDS];
     LDS_AS char *const b = (LDS_AS char *)lds;
     // Workgroup IDs go to the 8 XCDs in turn and each XCD has its own L2, so every
-    // XCD takes one contiguous run of tiles.
-    const uint32_t q = p.total / 8, rm = p.total % 8, xcd = blockIdx.x % 8;
-    const uint32_t v = xcd * q + min(xcd, rm) + blockIdx.x / 8;
-    const OrthoGroup g = group_of(p.a, v);
-    const uint32_t per = tiles_of(g, STAGE, T), in = v - g.wg0;
+    // XCD takes one contiguous run of each group's tiles (all of one length).
+    const OrthoGroup g = group_of(p.a, blockIdx.x);
+    const uint32_t per = tiles_of(g, STAGE, T), n = per * g.count;
+    const uint32_t id = blockIdx.x - g.wg0, xcd = id % 8;
+    const uint32_t in = xcd * (n / 8) + min(xcd, n % 8) + id / 8;
     const uint32_t m = uniform(in / per), at = uniform(in % per);
     if (STAGE == kApply) {
         // 8 tile rows advance together, as in the blocked products
@@ -428,9 +625,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void product_kernel(ProductArgs p)
         const uint32_t pg = 8 * tc, gr = at / pg, l = at - gr * pg, h = min(8u, tr - 8 * gr);
         const uint32_t ti = uniform(8 * gr + l % h), tj = uniform(l / h);
         if (g.tall())
-            product_tile<STAGE, kBf16Along, kBf16Along, T, WI, WJ>(p, g, m, ti, tj, b);
+            product_tile<STAGE, false, false, T>(p, g, m, ti, tj, b);
         else
-            product_tile<STAGE, kBf16Along, kBf16Across, T, WI, WJ>(p, g, m, ti, tj, b);
+            product_tile<STAGE, false, true, T>(p, g, m, ti, tj, b);
         return;
     }
     // at = ti (ti + 1) / 2 + tj, tj <= ti
@@ -440,9 +637,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 1) void product_kernel(ProductArgs p)
     ti = uniform(ti);
     const uint32_t tj = uniform(at - ti * (ti + 1) / 2);
     if (STAGE == kGram && g.tall())
-        product_tile<STAGE, kBf16Across, kBf16Across, T, WI, WJ>(p, g, m, ti, tj, b);
+        product_tile<STAGE, true, true, T>(p, g, m, ti, tj, b);
     else
-        product_tile<STAGE, kBf16Along, kBf16Along, T, WI, WJ>(p, g, m, ti, tj, b);
+        product_tile<STAGE, false, false, T>(p, g, m, ti, tj, b);
 }
 
 constexpr int64_t kMaxWgs = 0xffffffffll / 512;
@@ -501,11 +698,11 @@ tide_status run_product(const OrthoPlan &plan, ProductArgs p, hipStream_t s) {
             p.a = a;
             p.total = total;
             if (T == 256)
-                product_kernel<STAGE, 256, 2, 4><<<dim3(total), dim3(512), 0, s>>>(p);
+                product_kernel<STAGE, 256><<<dim3(total), dim3(kThreads), 0, s>>>(p);
             else if (T == 128)
-                product_kernel<STAGE, 128, 2, 2><<<dim3(total), dim3(256), 0, s>>>(p);
+                product_kernel<STAGE, 128><<<dim3(total), dim3(kThreads), 0, s>>>(p);
             else
-                product_kernel<STAGE, 64, 2, 2><<<dim3(total), dim3(256), 0, s>>>(p);
+                product_kernel<STAGE, 64><<<dim3(total), dim3(kThreads), 0, s>>>(p);
         });
 }
 
