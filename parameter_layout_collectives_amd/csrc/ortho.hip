@@ -400,7 +400,6 @@ template <int T>
 struct Turn {
     static constexpr int W = T / 2, PITCH = W * 4 + 16;    // a wave's tile is W x W
     static constexpr int PASSES = 32 * W / 512;
-    static_assert(32 * PITCH <= kBuffers * 2 * T * 64 / 4, "a wave's part of LDS");
 
     LDS_AS char *lds;
     int lane;
@@ -431,18 +430,22 @@ struct Turn {
 #pragma unroll
         for (int n = 0; n < 4; n++) v[n] = a[n], v[4 + n] = b[n];
     }
+    // The 32 rows once more, as fp16 numbers, behind the sums, to be read down the columns: rows 8 g .. 8 g + 7 of column 16 q + r16 for lane
+    // (r16, g), a run of 1 KB in the matrix's other half.
+    static constexpr int HALF = 32 * PITCH, HALF_PITCH = W * 2 + 16;
+    static_assert(HALF + 32 * HALF_PITCH <= kBuffers * 2 * T * 64 / 4, "a wave's part of LDS");
     __device__ __forceinline__ void set(int q, const f16x8 &h) const {
-#pragma unroll
-        for (int n = 0; n < 8; n++)
-            *reinterpret_cast<LDS_AS _Float16 *>(at(q) + n * 4) = h[n];
+        *reinterpret_cast<LDS_AS f16x8 *>(lds + HALF + row(q) * HALF_PITCH + col(q) * 2) = h;
     }
-    // 8 rows' values of column `col`, as set() left them
-    __device__ __forceinline__ f16x8 column(int row, int col) const {
-        f16x8 h;
-#pragma unroll
-        for (int n = 0; n < 8; n++)
-            h[n] = *reinterpret_cast<const LDS_AS _Float16 *>(lds + (row + n) * PITCH + col * 4);
-        return h;
+    __device__ __forceinline__ f16x8 column(int q) const {
+        union {
+            i16x4 h[2];
+            f16x8 v;
+        } u;
+        const LDS_AS char *p = lds + HALF + ((lane >> 4) * 8 + (lane >> 2 & 3)) * HALF_PITCH + q * 32 + (lane & 3) * 8;
+        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)p);
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)(p + 4 * HALF_PITCH));
+        return u.v;
     }
 };
 
@@ -483,21 +486,49 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
         for (int b = 0; b < K::F; b++)
 #pragma unroll
             for (int n = 0; n < 16; n++) k.acc[a][b][n] = 0.0f;
-    k.run(lds, uniform(steps));
-
     typedef Turn<T> U;
     // the last step's output is row-major
     const U turn = {lds + k.wave * (K::LDS / 4), lane, STAGE == kApply && p.last ? U::W / 8 : 4};
+    const uint32_t li = i0 + k.wi * U::W, lj = j0 + k.wj * U::W;       // the wave's first row and column
+    // What the sums are joined with, 32 rows of the wave's tile at a time: asked for
+    // ahead, the first KEEP times before the products, so that its latency and (all
+    // workgroups come here together) its traffic lie under them.
+    const char *const __restrict__ old = STAGE == kPoly ? base + g.a_at() : x;
+    const uint32_t orows = STAGE == kPoly ? rp : g.nrp, ocols = STAGE == kPoly ? rp : g.ncp;
+    constexpr int PARTS = STAGE == kGram ? 0 : STAGE == kPoly ? 1 : 2;
+    constexpr int KEEP = K::F < 2 ? 1 : 2;
+    f16x8 held[KEEP][U::PASSES][PARTS ? PARTS : 1];
+    auto ask = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < U::PASSES; q++) {
+            const uint32_t i = li + c * 32 + turn.row(q), j = lj + turn.col(q);
+            if (i < orows && j < ocols) {
+                const char *from = old + panel_at(orows, i, j) * 2;
+#pragma unroll
+                for (int h = 0; h < PARTS; h++)
+                    held[c % KEEP][q][h] = *reinterpret_cast<const f16x8 *>(from + h * 2 * g.lo());
+            }
+        }
+    };
+    if (PARTS)
+#pragma unroll
+        for (int c = 0; c < KEEP; c++) ask(c);
+
+    k.run(lds, uniform(steps));
+
     const float2 t1 = p.first ? p.s.scales[g.first + m] : make_float2(1.0f, 1.0f);
     const int ex = x_exponent(g.nr, g.nc);
-    const uint32_t li = i0 + k.wi * U::W, lj = j0 + k.wj * U::W;       // the wave's first row and column
     float *const ad = reinterpret_cast<float *>(base + g.a_diag());
     float *const pd = reinterpret_cast<float *>(base + g.p_diag());
+    const float f = STAGE == kGram    ? ldexpf(t1.y, -2 * ex)
+                    : STAGE == kPoly  ? 1.0f / (kScaleA * kScaleA)
+                    : p.last          ? ldexpf(t1.x, -ex)
+                                      : t1.x;
     if (STAGE != kApply) {
-        const float f = STAGE == kGram ? ldexpf(t1.y, -2 * ex) : 1.0f / (kScaleA * kScaleA);
-        const _Float16 *const old = reinterpret_cast<const _Float16 *>(base + g.a_at());
-        _Float16 *const to = reinterpret_cast<_Float16 *>(base + (STAGE == kGram ? g.a_at() : g.p_at()));
+        _Float16 *const __restrict__ to =
+            reinterpret_cast<_Float16 *>(base + (STAGE == kGram ? g.a_at() : g.p_at()));
         const uint32_t r = g.r();
+        const bool diagonal = ti == tj;
 #pragma unroll
         for (int c = 0; c < K::F; c++) {
             turn.put(k.acc, c);
@@ -508,12 +539,11 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                 turn.get(v, q);
                 f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0};
                 if (i < rp && j < rp) {                  // X's padding makes zeros of A's and P's
-                    const int64_t at = panel_at(rp, i, j);
                     if (STAGE == kGram) {
 #pragma unroll
                         for (int n = 0; n < 8; n++) {
                             v[n] *= f;
-                            if (i == j + n) {
+                            if (diagonal && i == j + n) {
                                 ad[i] = v[n];
                                 v[n] = 0.0f;
                             }
@@ -523,30 +553,29 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                         const float di = ad[i];
                         const f32x4 dl = *reinterpret_cast<const f32x4 *>(ad + j);
                         const f32x4 dh = *reinterpret_cast<const f32x4 *>(ad + j + 4);
-                        const f16x8 o = *reinterpret_cast<const f16x8 *>(old + at);
+                        const f16x8 o = held[c % KEEP][q][0];
 #pragma unroll
                         for (int n = 0; n < 8; n++) {
                             const float oij = static_cast<float>(o[n]) * (1.0f / kScaleA);
                             const float oo = v[n] * f;
-                            if (i == j + n) {
+                            v[n] = p.cb * oij + p.cc * ((di + (n < 4 ? dl[n] : dh[n - 4])) * oij + oo);
+                            if (diagonal && i == j + n) {
                                 pd[i] = i < r ? p.ca + p.cb * di + p.cc * (di * di + oo) : 0.0f;
                                 v[n] = 0.0f;
-                            } else {
-                                v[n] = p.cb * oij + p.cc * ((di + (n < 4 ? dl[n] : dh[n - 4])) * oij + oo);
                             }
                             h[n] = static_cast<_Float16>(v[n] * kScaleP);
                         }
                     }
-                    *reinterpret_cast<f16x8 *>(to + at) = h;
+                    *reinterpret_cast<f16x8 *>(to + panel_at(rp, i, j)) = h;
                 }
-                if (ti != tj) turn.set(q, h);
+                if (!diagonal) turn.set(q, h);
             }
-            if (ti != tj) {                              // the other side of the diagonal
+            if (PARTS && c + KEEP < K::F) ask(c + KEEP);
+            if (!diagonal) {                             // the other side
 #pragma unroll
                 for (int q = 0; q < U::W / 16; q++) {
-                    const int col = q * 16 + lane / 4, row = lane % 4 * 8;
-                    const uint32_t i = li + c * 32 + row, j = lj + col;
-                    const f16x8 h = turn.column(row, col);
+                    const uint32_t i = li + c * 32 + (lane >> 4) * 8, j = lj + q * 16 + (lane & 15);
+                    const f16x8 h = turn.column(q);
                     if (i < rp && j < rp) *reinterpret_cast<f16x8 *>(to + panel_at(rp, j, i)) = h;
                 }
             }
@@ -554,10 +583,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
         return;
     }
     // R X / 2^10 + Q X, as X is held; times the first step's factor
-    const _Float16 *const from = reinterpret_cast<const _Float16 *>(x);
-    _Float16 *const to = reinterpret_cast<_Float16 *>(base + (1 - p.from) * g.x_bytes());
-    const float f = p.last ? ldexpf(t1.x, -ex) : t1.x;
-    __bf16 *const out = p.last ? reinterpret_cast<__bf16 *>(p.s.pointers[g.first + m].out) : nullptr;
+    _Float16 *const __restrict__ to = reinterpret_cast<_Float16 *>(base + (1 - p.from) * g.x_bytes());
+    __bf16 *const __restrict__ out =
+        p.last ? reinterpret_cast<__bf16 *>(p.s.pointers[g.first + m].out) : nullptr;
     const bool tall = g.tall();
 #pragma unroll
     for (int c = 0; c < K::F; c++) {
@@ -568,9 +596,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
             float v[8];
             turn.get(v, q);
             if (i >= g.nrp || j >= g.ncp) continue;
-            const int64_t at = panel_at(g.nrp, i, j);
-            const f16x8 h = *reinterpret_cast<const f16x8 *>(from + at);
-            const f16x8 l = *reinterpret_cast<const f16x8 *>(from + at + g.lo());
+            const f16x8 h = held[c % KEEP][q][0], l = held[c % KEEP][q][PARTS - 1];
             f32x4 ql, qh;
             if (tall) {
                 ql = *reinterpret_cast<const f32x4 *>(pd + j);
@@ -584,6 +610,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                 v[n] = (v[n] * (1.0f / kScaleP) +
                         (n < 4 ? ql[n] : qh[n - 4]) * (static_cast<float>(h[n]) + static_cast<float>(l[n]))) * f;
             if (!p.last) {
+                const int64_t at = panel_at(g.nrp, i, j);
                 f16x8 nh, nl;
 #pragma unroll
                 for (int n = 0; n < 8; n++) {
@@ -605,6 +632,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                     if (j + n < g.nc) o[n] = static_cast<__bf16>(v[n]);
             }
         }
+        if (c + KEEP < K::F) ask(c + KEEP);
     }
 }
 
