@@ -174,7 +174,9 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
 // In both, chunk h (16 bytes) of a panel's row r lies at h ^ key(r) in LDS: the rows
 // that a read of either kind takes at a time fall into different banks.
 constexpr int kThreads = 256;
-constexpr int kStep = 32, kBuffers = 5;
+constexpr int kStep = 32;
+// Steps in LDS: 160 KB of it for one workgroup a unit, 80 KB for two.
+__host__ __device__ constexpr int buffers(int T) { return T == 64 ? 10 : 5; }
 
 // A pointer that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ const char *scalar(const char *p) {
@@ -275,10 +277,10 @@ struct Feed {
     }
 };
 
-// kBuffers steps are in LDS.  While one is multiplied, the fragments of the next are
+// BUFFERS steps are in LDS.  While one is multiplied, the fragments of the next are
 // read, a J and an I fragment per line (all multiplications of one I fragment), and
-// the loads of the fourth after it set out into the buffer that the barrier has just
-// freed; so a step's loads have two to three steps to arrive, and reads and loads
+// the loads of the last one that fits set out into the buffer that the barrier has just
+// freed; so (of 5) a step's loads have two to three steps to arrive, and reads and loads
 // come evenly.
 template <bool AI, bool AJ, int T>
 struct Half {
@@ -289,7 +291,8 @@ struct Half {
     typedef Feed<AJ, T> FJ;
     static constexpr int LOADS = FI::SLOTS + FJ::SLOTS;
     static constexpr int PER_LINE = LOADS / LINES;         // loads issued with a line
-    static constexpr int TILE = FI::BYTES, BUFFER = 2 * TILE, LDS = kBuffers * BUFFER;
+    static constexpr int BUFFERS = buffers(T);
+    static constexpr int TILE = FI::BYTES, BUFFER = 2 * TILE, LDS = BUFFERS * BUFFER;
     static_assert(LINES % RING == 0 && LOADS % LINES == 0, "a step starts at ring entry 0");
 
     FI fi;
@@ -318,12 +321,13 @@ struct Half {
     __device__ __forceinline__ f16x8 row(const LDS_AS char *b, int n) const {
         return FJ::frag(b + TILE + wj * (TILE / 2), aj, n % F, n / F);
     }
-    // One step from `here`; `there` is the next one, `to` receives the fourth after it.
+    // One step from `here`; `there` is the next one, `to` receives the one that comes
+    // BUFFERS - 1 after it.
     __device__ __forceinline__ void step(f16x8 *l, const f16x8 *r, f16x8 *next, const LDS_AS char *here,
                                          const LDS_AS char *there, LDS_AS char *to) {
         const __amdgpu_buffer_rsrc_t ri = fi.buffer(), rj = fj.buffer();
         // the next step has arrived; newer are the loads of those behind it
-        wait<(kBuffers - 3) * LOADS>();
+        wait<(BUFFERS - 3) * LOADS>();
 #pragma unroll
         for (int n = 0; n < LINES; n++) {
             l[(n + D) % RING] = n + D < LINES ? line(here, n + D) : line(there, n + D - LINES);
@@ -347,21 +351,21 @@ struct Half {
         ai = FI::lane_at(lane);
         aj = FJ::lane_at(lane);
 #pragma unroll
-        for (int b = 0; b < kBuffers - 1; b++) {
+        for (int b = 0; b < BUFFERS - 1; b++) {
             const __amdgpu_buffer_rsrc_t ri = fi.buffer(), rj = fj.buffer();
 #pragma unroll
             for (int q = 0; q < LOADS; q++) load(ri, rj, lds + b * BUFFER, q);
             fi.next();
             fj.next();
         }
-        wait<(kBuffers - 2) * LOADS>();
+        wait<(BUFFERS - 2) * LOADS>();
         f16x8 l[RING], r0[LINES], r1[LINES];
 #pragma unroll
         for (int n = 0; n < LINES; n++) r0[n] = row(lds, n);
 #pragma unroll
         for (int n = 0; n < D; n++) l[n] = line(lds, n);
-        uint32_t here = 0, to = (kBuffers - 1) * BUFFER;
-        auto after = [](uint32_t b) { return b == (kBuffers - 1) * BUFFER ? 0 : b + BUFFER; };
+        uint32_t here = 0, to = (BUFFERS - 1) * BUFFER;
+        auto after = [](uint32_t b) { return b == (BUFFERS - 1) * BUFFER ? 0 : b + BUFFER; };
         // sums are of 64 values or a multiple: steps come in pairs
         for (; steps; steps -= 2) {
             const uint32_t there = after(here), to2 = after(to);
@@ -433,7 +437,7 @@ struct Turn {
     // The 32 rows once more, as fp16 numbers, behind the sums, to be read down the columns: rows 8 g .. 8 g + 7 of column 16 q + r16 for lane
     // (r16, g), a run of 1 KB in the matrix's other half.
     static constexpr int HALF = 32 * PITCH, HALF_PITCH = W * 2 + 16;
-    static_assert(HALF + 32 * HALF_PITCH <= kBuffers * 2 * T * 64 / 4, "a wave's part of LDS");
+    static_assert(HALF + 32 * HALF_PITCH <= buffers(T) * 2 * T * 64 / 4, "a wave's part of LDS");
     __device__ __forceinline__ void set(int q, const f16x8 &h) const {
         *reinterpret_cast<LDS_AS f16x8 *>(lds + HALF + row(q) * HALF_PITCH + col(q) * 2) = h;
     }
