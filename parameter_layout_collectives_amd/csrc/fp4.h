@@ -33,12 +33,14 @@ enum Fp4Kernel {
     kFp4SkinnyInOne,  // the same, x (rounded) in LDS in the same launch
 };
 // How a product runs.  `x` bytes at the start of the workspace hold x as the
-// kernel reads it (blocks, their scales from `x_scales` on, or padded bf16 rows);
-// the pieces' sums of a cut product follow.
+// kernel reads it (blocks, their scales from `x_scales` on, or padded bf16 rows) and
+// turned operands (codes, then scales) from `x_turned` and `w_turned` on, or -1; the
+// pieces' sums of a cut product follow.
 struct Fp4Choice {
     Fp4Kernel kernel;
     MmChoice mm;
     int64_t x_scales, x;
+    int64_t x_turned, w_turned;
 };
 Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, bool aligned,
                      int64_t workspace_bytes);

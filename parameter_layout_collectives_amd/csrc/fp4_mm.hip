@@ -31,177 +31,309 @@ namespace {
 // sums, over random codes and scales 2^-20..2^20 apart: off by at most 2^-23.8 of the
 // sum of the magnitudes, and 36 * 2^35 - 36 * 2^35 + 1 in three blocks is 1.
 //
-// A T x T tile of the output per workgroup, WI x WJ waves.  One step of the sum is
-// 256 columns: 128 bytes of a row, 8 chunks of 16, one block each; chunk h of row r
-// lies at h ^ (r & 7) in LDS, so the 16 lanes that read one chunk of 16 rows touch
-// all banks.  Lane (r16, g) multiplies blocks g and g + 4 of its rows.  Two buffers:
-// the next step's codes travel straight into the other one while this one is
-// multiplied.
-template <int T, int WI, int WJ>
+// A T x T tile of the output per workgroup of 4 waves, 2 x 2, in fragments of 32 x 32
+// x 64: of the instruction's shapes the one that leaves most time between two issues
+// of a wave, which stands alone on its SIMD at T = 256.  One step of the sum is 128
+// columns: 64 bytes of a row, 4 chunks of 16, one block each.  Chunk h of row r lies at
+// h ^ (r >> 3 & 3) in LDS, so that the rows that a read takes at a time fall into
+// different banks.  Codes and scales go straight into LDS, BUFFERS steps deep: a load
+// that misses the L2 takes longer than two steps.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTileThreads = 256;
+
+// Where a step finds an operand's codes (64 bytes of a row) or scales (4 bytes): the
+// next row's `row` bytes further, the next step's `step` bytes.  As they lie in the
+// operand row is its pitch; turned into [steps, rows, 64] and [steps, rows, 4], row is
+// 64 and 4 and a load's lines of the cache are whole.
+struct Way {
+    const char *at;
+    uint32_t row, step;
+    int turned;
+};
+struct TilesLaunch : MmLaunch {
+    Way ci, cj, si, sj;
+};
+
+template <int T>
 struct Tiles {
-    static constexpr int NT = WI * WJ * 64, NW = WI * WJ;
-    static constexpr int FI = T / WI / 16, FJ = T / WJ / 16;   // 16 x 16 fragments per wave
-    static constexpr int SLOTS = T * 8 / NT;                   // 16-byte loads per thread and operand
-    static constexpr int TILE = T * 128;                       // bytes of an operand's codes
-    static constexpr int SCALES = 2 * T * 8;                   // and of both operands' scales
-    static constexpr int LDS = 4 * TILE + 2 * SCALES;
-    static constexpr int SLOADS = 2 * T / 32 / NW;             // loads of 32 rows' scales per wave
-    // I's fragments (lines) go through a ring of registers, D ahead of the
-    // multiplications.
-    static constexpr int RING = 2, D = RING - 1;
-    static constexpr uint32_t OUTSIDE = 0x80000000u;           // past every buffer's end
-    static_assert(FI % RING == 0 && SLOTS <= FI, "a step starts at ring entry 0");
+    static constexpr int F = T / 2 / 32;                   // 32 x 32 fragments of a wave, each way
+    static constexpr int LINES = 2 * F;                    // of a step: 2 x 64 columns
+    static constexpr int D = LINES >= 8 ? 3 : 1, RING = D + 1;   // I fragments read ahead
+    static constexpr int SLOTS = T * 4 / kTileThreads;     // 16-byte loads per thread and operand
+    static constexpr int TILE = T * 64;                    // bytes of an operand's codes
+    static constexpr int SLOADS = (2 * T / 64 + 3) / 4;    // loads of 64 rows' scales per wave
+    static constexpr int BUFFER = 2 * TILE + SLOADS * 4 * 256;
+    static constexpr int BUFFERS = T == 64 ? 8 : 4, LDS = BUFFERS * BUFFER;
+    static constexpr int LOADS = 2 * SLOTS + SLOADS;       // spread over a step's lines
+    static_assert(LINES % RING == 0, "a step starts at ring entry 0");
 
-    __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-    uint32_t vc, vc_half;        // this thread's first code slot; in a step of 128 columns
-    uint32_t vs, vs_half;        // its scale words' row, likewise
-    uint32_t half_step;          // the step that has only 128 columns, if any
-    uint32_t pitch, spitch;
-    int wave, fa, fb, sa, sb;    // fragments and their scales, in a buffer
+    struct From {                // a Way, for this thread
+        __amdgpu_buffer_rsrc_t r;
+        uint32_t v, rows, step;  // first slot; 64 rows, and a step, further
+    };
+    From ci, cj, si, sj;
+    int lane, wave, wi, wj, fa;  // fa: a fragment's lane's part of its address
     int shift;                   // of this lane's byte in a word of scales
-    f32x4 acc[FI][FJ];
+    f32x16 acc[F][F];
 
-    // Part q of step s's codes (and with the last one the scales) -> a buffer (I's
-    // codes, J's, scales).
-    __device__ __forceinline__ void fetch(LDS_AS char *ta, LDS_AS char *tb, LDS_AS char *tw,
-                                          uint32_t s, int q) const {
-        const int at = (wave + q * NW) * 1024;
-        const uint32_t off = q * (NT / 8) * pitch + s * 128;
-        const uint32_t v = s == half_step ? vc_half : vc;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDS_AS void *)(ta + at), 16, v, off, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDS_AS void *)(tb + at), 16, v, off, 0, 0);
-        if (q < SLOTS - 1) return;
-        const uint32_t vw = s == half_step ? vs_half : vs;
-        // 32-row groups 0 .. T/32-1 are the tile's rows of I, the others those of J
-#pragma unroll
-        for (int k = 0; k < SLOADS; k++) {
-            const int w = wave + k * NW, half = T / 32;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                w < half ? rsa : rsb, (LDS_AS void *)(tw + w * 256), 4, vw,
-                (w < half ? w : w - half) * 32 * spitch + s * 8, 0, 0);
+    // Load q of step s: scales first (64-row groups 0 .. T/64-1 are the tile's rows of
+    // I, the others those of J), then codes of I and J.
+    __device__ __forceinline__ void load(LDS_AS char *b, uint32_t s, int q) const {
+        if (q < SLOADS) {
+            const int w = wave + q * 4;                    // past the operands: unused
+            const bool i = w < T / 64;
+            const uint32_t k = i ? w : w - T / 64;
+            direct_word(i ? si.r : sj.r, b + 2 * TILE + w * 256, i ? si.v : sj.v,
+                        i ? k * si.rows + s * si.step : k * sj.rows + s * sj.step);
+        } else if (q < LOADS) {
+            const int c = q - SLOADS, k = c % SLOTS;
+            const From &f = c < SLOTS ? ci : cj;
+            direct_load(f.r, b + (c < SLOTS ? 0 : TILE) + (wave + k * 4) * 1024, f.v,
+                        k * f.rows + s * f.step);
         }
     }
-    struct Frag {                // 16 rows of one step
-        u32x4 v[2];              // blocks g and g + 4
-        uint32_t scale[2];       // this lane's in the low byte
-    };
-    __device__ __forceinline__ Frag frag(const LDS_AS char *codes, int at, const LDS_AS char *sc) const {
-        Frag f;
-        f.v[0] = *reinterpret_cast<const LDS_AS u32x4 *>(codes + at);
-        f.v[1] = *reinterpret_cast<const LDS_AS u32x4 *>(codes + (at ^ 64));
-        const u32x2 w = *reinterpret_cast<const LDS_AS u32x2 *>(sc);
-        f.scale[0] = w.x >> shift;
-        f.scale[1] = w.y >> shift;
-        return f;
+    // As direct_load, 4 bytes per lane.
+    static __device__ __forceinline__ void direct_word(__amdgpu_buffer_rsrc_t r, LDS_AS char *to,
+                                                       uint32_t at, uint32_t off) {
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(
+            static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)));
+        asm volatile(
+            "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+            :
+            : "s"(lds), "v"(at), "s"(r), "s"(__builtin_amdgcn_readfirstlane(off))
+            : "memory", "m0");
     }
-    __device__ __forceinline__ void rows(Frag *r, const LDS_AS char *b, const LDS_AS char *w) const {
-#pragma unroll
-        for (int y = 0; y < FJ; y++) r[y] = frag(b + y * 2048, fb, w + sb + y * 128);
+    // All but this wave's newest N loads have landed, and every wave is here.
+    template <int N>
+    static __device__ __forceinline__ void wait() {
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
     }
-    __device__ __forceinline__ Frag line(const LDS_AS char *a, const LDS_AS char *w, int x) const {
-        return frag(a + x * 2048, fa, w + sa + x * 128);
+    // The fragment of rows [32 f, 32 f + 32) of the wave's, columns [64 k, 64 k + 64) of
+    // the step, n = k F + f: lane (r32, g) holds block 2 k + g of row r32.
+    __device__ __forceinline__ u32x4 frag(const LDS_AS char *codes, int half, int n) const {
+        return *reinterpret_cast<const LDS_AS u32x4 *>(codes + half * (TILE / 2) + n % F * 2048 +
+                                                       (fa ^ n / F * 32));
+    }
+    // The scales of rows [row, row + 32): shifted, this lane's blocks g and 2 + g are in
+    // bytes 0 and 2.
+    __device__ __forceinline__ uint32_t scale(const LDS_AS char *words, int row) const {
+        return *reinterpret_cast<const LDS_AS uint32_t *>(words + (row + (lane & 31)) * 4);
     }
     static __device__ __forceinline__ i32x8 wide(u32x4 v) {
         return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]),
                      static_cast<int>(v[3]), 0, 0, 0, 0};
     }
-    __device__ __forceinline__ void multiply(int x, const Frag &l, const Frag *r) {
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-            for (int y = 0; y < FJ; y++)
-                acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    wide(r[y].v[h]), wide(l.v[h]), acc[x][y], 4, 4, 0,
-                    static_cast<int>(r[y].scale[h]), 0, static_cast<int>(l.scale[h]));
+    struct Step {                // what is read ahead for a step
+        u32x4 j[LINES];
+        uint32_t sj[F], si[F];
+    };
+    __device__ __forceinline__ void scales(Step &r, const LDS_AS char *b, int n) const {
+        r.si[n] = scale(b + 2 * TILE, wi * (T / 2) + n * 32);
+        r.sj[n] = scale(b + 2 * TILE, T + wj * (T / 2) + n * 32);
     }
-    // Step s, whose first D lines and J rows are in registers: reads the rest from
-    // its buffer (h*); once nothing of it is left to read, the first reads of step
-    // s + 1 from the other (t*) begin under the multiplications that remain, and
-    // step s + 2 starts travelling to h*.
-    template <bool LAST>
-    __device__ __forceinline__ void step(Frag *l, const Frag *r, Frag *next, LDS_AS char *ha,
-                                         LDS_AS char *hb, LDS_AS char *hw, LDS_AS char *ta,
-                                         LDS_AS char *tb, LDS_AS char *tw, uint32_t s) {
+    // One step from `here`; `there` is the next one, s + BUFFERS - 1 goes to `to`, which
+    // the barrier has just freed (its reads have all been multiplied).
+    __device__ __forceinline__ void step(u32x4 *l, const Step &r, Step &next, const LDS_AS char *here,
+                                         const LDS_AS char *there, LDS_AS char *to, uint32_t s) {
+        // the next step has landed; newer are the loads of those behind it
+        wait<(BUFFERS - 3) * LOADS>();
+        // not where they are read, which would wait for them
+        int sj[F], si[F];
 #pragma unroll
-        for (int x = 0; x < FI; x++) {
-            if (x + D < FI) l[(x + D) % RING] = line(ha, hw, x + D);
-            if (!LAST && x + D == FI) {
-                landed();
-                rows(next, tb, tw);
+        for (int y = 0; y < F; y++) {
+            sj[y] = static_cast<int>(r.sj[y] >> shift);
+            si[y] = static_cast<int>(r.si[y] >> shift);
+        }
+#pragma unroll
+        for (int n = 0; n < LINES; n++) {
+            l[(n + D) % RING] = n + D < LINES ? frag(here, wi, n + D) : frag(there, wi, n + D - LINES);
+            next.j[n] = frag(there + TILE, wj, n);
+            if (n < F) scales(next, there, n);
+            const int x = n % F, k = n / F;
+#pragma unroll
+            for (int y = 0; y < F; y++) {
+                if (k == 0)
+                    acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        wide(r.j[y]), wide(l[n % RING]), acc[x][y], 4, 4, 0, sj[y], 0, si[x]);
+                else
+                    acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        wide(r.j[F + y]), wide(l[n % RING]), acc[x][y], 4, 4, 2, sj[y], 2, si[x]);
+                if (y == 0) {
+#pragma unroll
+                    for (int q = n * LOADS / LINES; q < (n + 1) * LOADS / LINES; q++)
+                        load(to, s + BUFFERS - 1, q);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            if (!LAST && x + D >= FI) l[(x + D) % RING] = line(ta, tw, x + D - FI);
-            if (!LAST && x < SLOTS - 1) fetch(ta, tb, tw, s + 1, x + 1);
-            multiply(x, l[x % RING], r);
-            if (!LAST && x == FI - 1) fetch(ha, hb, hw, s + 2, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __device__ __forceinline__ void run(LDS_AS char *__restrict__ a0, LDS_AS char *__restrict__ a1,
-                                        LDS_AS char *__restrict__ b0, LDS_AS char *__restrict__ b1,
-                                        LDS_AS char *__restrict__ w0, LDS_AS char *__restrict__ w1,
-                                        uint32_t s0, uint32_t s1) {
+    __device__ __forceinline__ void run(LDS_AS char *lds, uint32_t s0, uint32_t s1) {
 #pragma unroll
-        for (int q = 0; q < SLOTS; q++) fetch(a0, b0, w0, s0, q);
-        fetch(a1, b1, w1, s0 + 1, 0);
-        landed();
-        Frag l[RING], r0[FJ], r1[FJ];
-        rows(r0, b0, w0);
+        for (int b = 0; b < BUFFERS - 1; b++)
 #pragma unroll
-        for (int x = 0; x < D; x++) l[x] = line(a0, w0, x);
-        uint32_t s = s0;
-        // What lies past the last step is fetched and read as well (in bounds by
-        // the descriptors, used by nothing), which keeps branches out of the loop.
+            for (int q = 0; q < LOADS; q++) load(lds + b * BUFFER, s0 + b, q);
+        wait<(BUFFERS - 2) * LOADS>();
+        u32x4 l[RING];
+        Step r0, r1;
+#pragma unroll
+        for (int n = 0; n < LINES; n++) r0.j[n] = frag(lds + TILE, wj, n);
+#pragma unroll
+        for (int n = 0; n < F; n++) scales(r0, lds, n);
+#pragma unroll
+        for (int n = 0; n < D; n++) l[n] = frag(lds, wi, n);
+        // What lies past the last step is fetched and read as well (in bounds by the
+        // descriptors, used by nothing), which keeps branches out of the loop.
+        uint32_t here = 0, to = (BUFFERS - 1) * BUFFER, s = s0;
+        auto after = [](uint32_t b) { return b == (BUFFERS - 1) * BUFFER ? 0 : b + BUFFER; };
         for (; s + 1 < s1; s += 2) {
-            step<false>(l, r0, r1, a0, b0, w0, a1, b1, w1, s);
-            step<false>(l, r1, r0, a1, b1, w1, a0, b0, w0, s + 1);
+            const uint32_t there = after(here), to2 = after(to);
+            step(l, r0, r1, lds + here, lds + there, lds + to, s);
+            here = after(there);
+            step(l, r1, r0, lds + there, lds + here, lds + to2, s + 1);
+            to = after(to2);
         }
-        if (s < s1) step<true>(l, r0, r1, a0, b0, w0, a1, b1, w1, s);
-        landed();                // no load may still be on its way to LDS at the end
+        if (s < s1) step(l, r0, r1, lds + here, lds + after(here), lds + to, s);
+        arrived();               // no load may still be on its way to LDS at the end,
+        __syncthreads();         // nor a read of what the sums will overwrite
     }
 };
 
-template <int T, int WI, int WJ>
-__global__ __launch_bounds__(WI * WJ * 64, 1) void tiles_kernel(MmLaunch p) {
-    typedef Tiles<T, WI, WJ> E;
+// An operand's codes [rows, steps, 64 bytes] -> [steps, rows, 64 bytes] and scales
+// [rows, steps, 4] -> [steps, rows, 4]: a workgroup takes 64 rows of 4 steps, a lane 16
+// bytes of codes in each.
+__global__ __launch_bounds__(256) void turn_kernel(const char *__restrict__ codes,
+                                                   const char *__restrict__ scales, int64_t rows,
+                                                   uint32_t steps, char *__restrict__ to,
+                                                   char *__restrict__ sto) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x >> 2);
+    const int c = threadIdx.x & 3;
+    const uint32_t s0 = blockIdx.y * 4;
+    if (row >= rows) return;
+    const u32x4 *in = reinterpret_cast<const u32x4 *>(codes + row * steps * 64) + c;
+    u32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (s0 + k < steps) v[k] = in[(s0 + k) * 4];
+    if (s0 + c < steps)
+        *reinterpret_cast<uint32_t *>(sto + ((s0 + c) * rows + row) * 4) =
+            *reinterpret_cast<const uint32_t *>(scales + (row * steps + s0 + c) * 4);
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (s0 + k < steps) *(reinterpret_cast<u32x4 *>(to + ((s0 + k) * rows + row) * 64) + c) = v[k];
+}
+
+// x [rows, cols] -> turned 4-bit blocks, as tide_mx_quant and turn_kernel make them.  16
+// lanes a unit of 128 columns, 8 values each; a workgroup takes 16 rows of 4 units.
+template <int ET>
+__global__ __launch_bounds__(256) void quant_turned_kernel(const char *__restrict__ x, int64_t rows,
+                                                           int64_t cols, char *__restrict__ to,
+                                                           char *__restrict__ sto, int vec) {
+    constexpr int ES = ET == kElemF32 ? 4 : 2;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 15;
+    const int64_t unit0 = static_cast<int64_t>(blockIdx.y) * 4, units = (cols + 127) / 128;
+    float v[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const int64_t c = (unit0 + k) * 128 + lane * 8;
+        const int n = row < rows ? static_cast<int>(max(min(cols - c, static_cast<int64_t>(8)), static_cast<int64_t>(0))) : 0;
+        load8<ET>(x + (row * cols + c) * ES, n, vec != 0, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        uint32_t scale;
+        const uint32_t c = encode4(v[k], &scale);
+        if (row >= rows || unit0 + k >= units) continue;
+        const int64_t at = (unit0 + k) * rows + row;
+        *reinterpret_cast<uint32_t *>(to + at * 64 + lane * 4) = c;
+        if (lane % 4 == 0) sto[at * 4 + lane / 4] = static_cast<char>(scale);
+    }
+}
+
+// The sums of a wave go through its part of LDS, 32 rows at a time: a lane holds 4
+// neighbours of a row at a distance of 8, and leaves with 8.
+template <int T>
+__device__ __forceinline__ void store_sums(const MmLaunch &p, const Work &w, const Tiles<T> &e,
+                                           LDS_AS char *lds) {
+    constexpr int W = T / 2, PITCH = W * 4 + 16, F = Tiles<T>::F, PER = W / 8;
+    static_assert(32 * PITCH <= Tiles<T>::LDS / 4, "a wave's part of LDS");
+    lds += e.wave * (Tiles<T>::LDS / 4);
+#pragma unroll
+    for (int c = 0; c < F; c++) {
+#pragma unroll
+        for (int y = 0; y < F; y++)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                *reinterpret_cast<LDS_AS f32x4 *>(lds + (e.lane & 31) * PITCH + y * 128 + q * 32 +
+                                                  (e.lane >> 5) * 16) =
+                    f32x4{e.acc[c][y][4 * q], e.acc[c][y][4 * q + 1], e.acc[c][y][4 * q + 2],
+                          e.acc[c][y][4 * q + 3]};
+#pragma unroll
+        for (int q = 0; q < 32 * PER / 64; q++) {
+            const int row = q * (64 / PER) + e.lane / PER, col = e.lane % PER * 8;
+            const LDS_AS f32x4 *v = reinterpret_cast<const LDS_AS f32x4 *>(lds + row * PITCH + col * 4);
+            const f32x4 a = v[0], b = v[1];
+            const int li = e.wi * W + c * 32 + row, lj = e.wj * W + col;
+            const int64_t i = static_cast<int64_t>(w.r) * T + li, j = static_cast<int64_t>(w.c) * T + lj;
+            if (w.part) {
+                if (i < p.rows && j < p.cols) {
+                    f32x4 *o = reinterpret_cast<f32x4 *>(w.part + li * T + lj);
+                    o[0] = a;
+                    o[1] = b;
+                }
+            } else if (p.out_bf16 && i < p.rows && p.cols - j >= 8) {
+                *reinterpret_cast<half_u32x4 *>(p.out + (i * p.cols + j) * 2) =
+                    half_u32x4{pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
+            } else {
+                store4(p, i, j, a);
+                store4(p, i, j + 4, b);
+            }
+        }
+    }
+}
+
+template <int T>
+__global__ __launch_bounds__(kTileThreads, T == 256 ? 1 : 2) void tiles_kernel(TilesLaunch p) {
+    typedef Tiles<T> E;
     __shared__ __attribute__((aligned(1024))) char lds[E::LDS];
     const int t = threadIdx.x, lane = t & 63;
-    const int r16 = lane & 15, g = lane >> 4;
-    const Work work = work_of<T>(p, (p.sum + 255) / 256);
+    const int64_t steps = (p.sum + 127) / 128;
+    const Work work = work_of<T>(p, steps);
     const int64_t i0 = static_cast<int64_t>(work.r) * T, j0 = static_cast<int64_t>(work.c) * T;
-    const uint32_t s0 = uniform(work.s0), s1 = uniform(work.s1);
-    const uint32_t ni = uniform(min(p.rows - i0, static_cast<int64_t>(T)));
-    const uint32_t nj = uniform(min(p.cols - j0, static_cast<int64_t>(T)));
 
+    // A buffer from the tile's first row on: as it lies to the tile's last row, turned
+    // (below 2^31 bytes) to the last step's, with rows that are not the tile's own,
+    // whose products nothing stores.
+    const auto from = [&](const Way &w, int64_t first, int64_t all, uint32_t bytes, uint32_t v) {
+        const int64_t n = w.turned ? (steps * all - first) * bytes
+                                   : min(all - first, static_cast<int64_t>(T)) * w.row;
+        return typename E::From{buffer_of(scalar(w.at + first * w.row), uniform(n)), v, 64 * w.row, w.step};
+    };
+    // A wave's load of codes fills 16 rows of 4 chunks: LDS chunk c of row r is chunk
+    // c ^ (r >> 3 & 3) of memory.
+    const uint32_t chunk = ((t & 3) ^ (t >> 5 & 3)) * 16;
     E e;
-    e.pitch = static_cast<uint32_t>(p.a_pitch);
-    e.spitch = static_cast<uint32_t>(p.as_pitch);
+    e.lane = lane;
     e.wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wi = e.wave / WJ, wj = e.wave % WJ;
-    e.ra = buffer_of(p.a + i0 * e.pitch, ni * e.pitch);
-    e.rb = buffer_of(p.b + j0 * e.pitch, nj * e.pitch);
-    e.rsa = buffer_of(p.as + i0 * e.spitch, ni * e.spitch);
-    e.rsb = buffer_of(p.bs + j0 * e.spitch, nj * e.spitch);
-    // A wave's load fills 8 rows of 8 chunks: LDS chunk c of row r is chunk
-    // c ^ (r & 7) of memory.  A row ends inside a step if its 128-column units are
-    // odd in number: the step's second half is then fetched as zeros.
-    const int chunk = (t & 7) ^ (t >> 3 & 7);
-    e.vc = (t >> 3) * e.pitch + chunk * 16;
-    e.vc_half = chunk < 4 ? e.vc : E::OUTSIDE;
-    e.vs = (lane >> 1) * e.spitch + (lane & 1) * 4;
-    e.vs_half = (lane & 1) ? E::OUTSIDE : e.vs;
-    e.half_step = e.pitch % 128 ? e.pitch / 128 : 0xffffffffu;
-    e.fa = (wi * (T / WI) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
-    e.fb = (wj * (T / WJ) + r16) * 128 + ((g ^ (r16 & 7)) << 4);
-    e.sa = (wi * (T / WI) + r16) * 8;
-    e.sb = (T + wj * (T / WJ) + r16) * 8;
+    e.wi = e.wave / 2;
+    e.wj = e.wave % 2;
+    e.ci = from(p.ci, i0, p.rows, 64, (t >> 2) * p.ci.row + chunk);
+    e.cj = from(p.cj, j0, p.cols, 64, (t >> 2) * p.cj.row + chunk);
+    e.si = from(p.si, i0, p.rows, 4, lane * p.si.row);
+    e.sj = from(p.sj, j0, p.cols, 4, lane * p.sj.row);
+    const int r = lane & 31, g = lane >> 5;
+    e.fa = r * 64 + ((g ^ (r >> 3 & 3)) << 4);
     e.shift = 8 * g;
 #pragma unroll
-    for (int x = 0; x < E::FI; x++)
+    for (int x = 0; x < E::F; x++)
 #pragma unroll
-        for (int y = 0; y < E::FJ; y++) e.acc[x][y] = f32x4{0, 0, 0, 0};
-    LDS_AS char *const b = (LDS_AS char *)lds, *const w = b + 4 * E::TILE;
-    e.run(b, b + E::TILE, b + 2 * E::TILE, b + 3 * E::TILE, w, w + E::SCALES, s0, s1);
-    store_tile<T>(p, work, wi * (T / WI) + r16, wj * (T / WJ) + g * 4, e.acc);
+        for (int y = 0; y < E::F; y++)
+#pragma unroll
+            for (int n = 0; n < 16; n++) e.acc[x][y][n] = 0.0f;
+    e.run((LDS_AS char *)lds, uniform(work.s0), uniform(work.s1));
+    store_sums<T>(p, work, e, (LDS_AS char *)lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -462,7 +594,7 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
         else
             launch_few<4>(p, s);
     } else {
-        if (quant) {
+        if (quant && c.x_turned < 0) {
             if (a.workspace_bytes < c.x)
                 return fail(TIDE_E_INVALID, std::string(name) + ": the workspace holds " +
                                                 std::to_string(a.workspace_bytes) +
@@ -472,6 +604,36 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
             if (st != TIDE_OK) return st;
             p.a = ws;
             p.as = ws + c.x_scales;
+        }
+        TilesLaunch q = {};
+        if (c.kernel == kFp4Tiles) {
+            // as they lie, or turned
+            const int64_t steps = block_count(a.K);
+            const unsigned fours = static_cast<unsigned>((steps + 3) / 4);
+            auto ways = [&](const char *codes, const char *scales, int64_t rows, int64_t at, Way &cw, Way &sw) {
+                cw = Way{codes, static_cast<uint32_t>(p.b_pitch), 64, 0};
+                sw = Way{scales, static_cast<uint32_t>(p.bs_pitch), 4, 0};
+                if (at < 0) return;
+                char *const to = ws + at, *const sto = to + steps * rows * 64;
+                if (quant && at == c.x_turned) {
+                    const dim3 g(static_cast<unsigned>((rows + 15) / 16), fours), b(256);
+                    const int vec = a.K % 8 == 0;
+                    switch (in) {
+                        case kElemBf16: quant_turned_kernel<kElemBf16><<<g, b, 0, s>>>(x, rows, a.K, to, sto, vec); break;
+                        case kElemF16: quant_turned_kernel<kElemF16><<<g, b, 0, s>>>(x, rows, a.K, to, sto, vec); break;
+                        case kElemF32: quant_turned_kernel<kElemF32><<<g, b, 0, s>>>(x, rows, a.K, to, sto, vec); break;
+                    }
+                } else {
+                    turn_kernel<<<dim3(static_cast<unsigned>((rows + 63) / 64), fours), dim3(256), 0, s>>>(
+                        codes, scales, rows, static_cast<uint32_t>(steps), to, sto);
+                }
+                cw = Way{to, 64, static_cast<uint32_t>(rows * 64), 1};
+                sw = Way{sto, 4, static_cast<uint32_t>(rows * 4), 1};
+            };
+            ways(p.a, p.as, a.M, c.x_turned, q.ci, q.si);
+            ways(p.b, p.bs, a.N, c.w_turned, q.cj, q.sj);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return hip_fail((std::string(name) + ": kernel launch").c_str(), e);
         }
         const int T = c.mm.tile;
         const int64_t tr = (p.rows + T - 1) / T, tc = (p.cols + T - 1) / T;
@@ -483,10 +645,13 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
         p.tr = static_cast<uint32_t>(tr);
         p.tc = static_cast<uint32_t>(tc);
         const dim3 grid(static_cast<unsigned>(c.mm.direct + cut));
+        static_cast<MmLaunch &>(q) = p;
         if (c.kernel == kFp4Tiles && T == 256)
-            tiles_kernel<256, 2, 4><<<grid, dim3(512), 0, s>>>(p);
+            tiles_kernel<256><<<grid, dim3(kTileThreads), 0, s>>>(q);
+        else if (c.kernel == kFp4Tiles && T == 128)
+            tiles_kernel<128><<<grid, dim3(kTileThreads), 0, s>>>(q);
         else if (c.kernel == kFp4Tiles)
-            tiles_kernel<128, 2, 2><<<grid, dim3(256), 0, s>>>(p);
+            tiles_kernel<64><<<grid, dim3(kTileThreads), 0, s>>>(q);
         else if (op == kFp4Dx)
             launch_wide<kBf16Along, kFoursAcross>(p, T, grid, s);
         else

@@ -42,6 +42,14 @@ __device__ __forceinline__ uint32_t uniform(int64_t v) {
     return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
 }
 
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const char *scalar(const char *p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    return reinterpret_cast<const char *>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // What a workgroup computes: a tile of the output and a piece of its sum.
 struct Work {
     uint32_t r, c;               // tile

@@ -178,14 +178,6 @@ constexpr int kStep = 32;
 // Steps in LDS: 160 KB of it for one workgroup a unit, 80 KB for two.
 __host__ __device__ constexpr int buffers(int T) { return T == 64 ? 10 : 5; }
 
-// A pointer that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ const char *scalar(const char *p) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
-    return reinterpret_cast<const char *>(static_cast<uint64_t>(hi) << 32 | lo);
-}
-
 __device__ __forceinline__ int key(int r) { return r >> 3 & 3; }
 
 template <bool ACROSS, int T>

@@ -72,7 +72,7 @@ void choices(std::mt19937_64 &g) {
             continue;
         }
         const int64_t sum = op == tide::kFp4Dx ? N : K, cols = op == tide::kFp4Dx ? K : N;
-        const int64_t step = c.kernel == tide::kFp4Tiles ? 256 : 64, steps = (sum + step - 1) / step;
+        const int64_t step = c.kernel == tide::kFp4Tiles ? 128 : 64, steps = (sum + step - 1) / step;
         const int64_t T = c.mm.tile, tiles = ((M + T - 1) / T) * ((cols + T - 1) / T);
         EXPECT(c.mm.direct >= 0 && c.mm.direct <= tiles && c.mm.splits >= 1);
         EXPECT(c.mm.chunk * c.mm.splits >= steps && c.mm.chunk * (c.mm.splits - 1) < steps);
