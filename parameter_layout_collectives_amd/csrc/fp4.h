@@ -26,9 +26,11 @@ struct Fp4Args {
     uint32_t flags;
 };
 
+constexpr int64_t kStripWaves = 4, kStripRows = kStripWaves * 32;   // rows of W in a strip
 enum Fp4Kernel {
     kFp4Tiles,        // 4-bit instruction, both operands in 4-bit blocks
     kFp4Wide,         // bf16 instruction, W widened on its way into LDS
+    kFp4Strips,       // bf16 instruction, W widened in registers, x through LDS; some rows
     kFp4Skinny,       // bf16 instruction, W widened in registers; few rows
     kFp4SkinnyInOne,  // the same, x (rounded) in LDS in the same launch
 };

@@ -42,8 +42,28 @@ tide_status check_product(const char *name, Fp4Op op, int64_t M, int64_t N, int6
     return TIDE_OK;
 }
 
-// Rows that the skinny kernel takes.
+// The skinny kernel's workgroups, one for 16 rows of W, each read all of x; the
+// strips' share it among 128 and cost a second launch, in which the sum's pieces meet.
+// So the skinny kernel takes up to 16 rows, of few multiplications or where a compute
+// unit has one workgroup and x is small (rows x N x K, us, skinny against strips):
+// 1 x 14336 x 4096 10.8 : 13.5, 2 12.6 : 13.5, 4 15.7 : 13.5, 16 21.9 : 13.9;
+// 3 x 8192 x 8192 16.1 : 14.8; 1 x 28672 x 8192 34 : 33; 16 x 4096 x 4096 7.9 : 11.1,
+// 8 x 4096 x 14336 14.4 : 15.4, 16 19.5 : 15.6.
 constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewSum = int64_t(1) << 27;
+constexpr int64_t kFewX = int64_t(1) << 17;
+// The strips take matrices from a size on (x N x K, us, strips against tiles of 64:
+// 17 x 256 x 8192 8.3 : 9.1, 64 x 300 x 2000 11.7 : 7.7, 20 x 1000 x 1000 10.2 : 6.9),
+// and rows, of bf16 x up to 64 (64 x 4096 x 4096 13.8 : 16.2, 64 x 8192 x 8192 19.7 :
+// 28); against the 4-bit tiles, whose operand x lies ready, larger matrices and up to 32
+// (32 x 4096 x 4096 13.1 : 12.2, 17 x 14336 x 4096 16.8 : 19.3, 64 x 4096 x 4096 16 : 13.4).
+constexpr int64_t kStripMost = 64, kStripMost4 = 32;
+constexpr int64_t kStripLeast = int64_t(1) << 21, kStripLeast4 = int64_t(1) << 25;
+// Workgroups that fill the card, one per compute unit (with two, 64 x 28672 x 8192
+// takes 52 us for 48, 32 x 8192 x 28672 41 for 40.7), and least units of 128 columns in a
+// piece of a sum (40 x 1024 x 4096 8.7 us, with 8 units 11.1).
+constexpr int64_t kStripGroups = kCus;
+constexpr int64_t kStripUnits = 4;
 // Least rows of the other operand, and columns, of an operand that is turned; and
 // least rows of an x that is made so.
 constexpr int64_t kTurnRows = 4096;
@@ -64,16 +84,31 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     const int64_t cols = op == kFp4Dx ? K : N, sum = op == kFp4Dx ? N : K;
     const bool quant = op == kFp4Linear && (flags & TIDE_F_QUANT_X);
     const int64_t padded = M * block_cols(K) * 2;       // x as bf16 rows of whole units
-    if (op != kFp4Dx && M <= kFewRows) {
-        if (op == kFp4Linear && M * (block_cols(K) * 2 + 16) <= kInOneBytesFp4) {
-            c.kernel = kFp4SkinnyInOne;
-            return c;
+    const bool few = M <= kFewRows && (M * N * K <= kFewSum || (N <= 16 * kCus && M * K <= kFewX));
+    const bool strips = M <= (op == kFp4Mm || quant ? kStripMost4 : kStripMost) &&
+                        N * K >= (op == kFp4Mm ? kStripLeast4 : kStripLeast);
+    const bool room = op != kFp4Dx && workspace_bytes >= rounded(padded);
+    if (op == kFp4Linear && M <= kFewRows && M * (block_cols(K) * 2 + 16) <= kInOneBytesFp4 &&
+        (few || !strips || !room)) {
+        c.kernel = kFp4SkinnyInOne;
+        return c;
+    }
+    if (room && (few || strips)) {
+        c.kernel = few ? kFp4Skinny : kFp4Strips;
+        c.x = rounded(padded);
+        if (few) return c;
+        const int64_t units = std::max<int64_t>(1, block_count(K));
+        const int64_t groups = std::max<int64_t>(1, (N + kStripRows - 1) / kStripRows);
+        const int64_t pieces = std::max<int64_t>(1, std::min(kStripGroups / groups, units / kStripUnits));
+        c.mm.splits = 1;
+        c.mm.chunk = units;
+        const int64_t chunk = (units + pieces * 4 - 1) / (pieces * 4) * 4, n = (units + chunk - 1) / chunk;
+        if (n > 1 && c.x + n * M * N * 4 <= workspace_bytes) {
+            c.mm.splits = static_cast<int>(n);
+            c.mm.chunk = chunk;
+            c.mm.workspace = n * M * N * 4;
         }
-        if (workspace_bytes >= rounded(padded)) {
-            c.kernel = kFp4Skinny;
-            c.x = rounded(padded);
-            return c;
-        }
+        return c;
     }
     c.kernel = op == kFp4Mm || quant ? kFp4Tiles : kFp4Wide;
     if (quant) {

@@ -340,8 +340,7 @@ __global__ __launch_bounds__(kTileThreads, T == 256 ? 1 : 2) void tiles_kernel(T
 // Y = x W^T for few rows of x
 // ---------------------------------------------------------------------------
 //
-// W's bytes bound it.  Each workgroup takes 16 rows of W and all rows of x (MT
-// groups of 16); its waves cut the sum into groups of GB units of 128 columns and
+// W's bytes bound it.  Each workgroup takes 16 rows of W and all of x's, up to 16; its waves cut the sum into groups of GB units of 128 columns and
 // join through LDS in wave order.  Codes go from memory to registers as 16-byte
 // loads, one block each, become bf16 there (exactly) and enter the bf16 instruction;
 // the k-order inside a load is the same on both sides.
@@ -365,12 +364,14 @@ __device__ __forceinline__ bf16x8 plain8(const float *v) {
     return r;
 }
 
-template <int MT, int SRC, bool QUANT>
+typedef u32x4 word_u32x4 __attribute__((aligned(4)));
+
+template <int SRC, bool QUANT>
 __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
     constexpr bool MADE = SRC != kPadded;
     constexpr int GB = 4;                            // units in a group
     extern __shared__ __attribute__((aligned(16))) char made[];
-    __shared__ __attribute__((aligned(16))) f32x4 part[kFewWaves][MT][64];
+    __shared__ __attribute__((aligned(16))) f32x4 part[kFewWaves][64];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int r16 = lane & 15, g = lane >> 4;
     const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
@@ -378,26 +379,26 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
     const int64_t wrow = min(j0 + r16, p.cols - 1);
     const char *w = p.b + wrow * p.b_pitch + g * 16;
     const char *ws = p.bs + wrow * p.bs_pitch;
-    u32x4 wv[GB];
-    uint32_t wsc[GB];
+    u32x4 wv[GB], wsc;
+    // A whole group's scales in one load: each takes a line of the cache per row.
     auto load_w = [&](int b, int n) {
+        if (n == GB) {
+            wsc = *reinterpret_cast<const word_u32x4 *>(ws + b * 4);
+        } else {
+#pragma unroll
+            for (int q = 0; q < GB; q++)
+                if (q < n) wsc[q] = *reinterpret_cast<const uint32_t *>(ws + (b + q) * 4);
+        }
 #pragma unroll
         for (int q = 0; q < GB; q++)
-            if (q < n) {
-                wsc[q] = *reinterpret_cast<const uint32_t *>(ws + (b + q) * 4);
-                wv[q] = *reinterpret_cast<const u32x4 *>(w + (b + q) * 64);
-            }
+            if (q < n) wv[q] = *reinterpret_cast<const u32x4 *>(w + (b + q) * 64);
     };
     int b = wave * GB;
     if (b < nb) load_w(b, min(nb - b, GB));
 
-    const char *x[MT];
+    const char *x;
     if (!MADE) {
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-            const int64_t row = min(static_cast<int64_t>(m * 16 + r16), p.rows - 1);
-            x[m] = p.a + row * p.a_pitch + g * 64;
-        }
+        x = p.a + min(static_cast<int64_t>(r16), p.rows - 1) * p.a_pitch + g * 64;
     } else {
         // a pitch of 16 bytes more than a row, so that 16 rows' pieces lie in
         // different banks
@@ -413,14 +414,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
             if (u < units) *reinterpret_cast<bf16x8 *>(made + row * pitch + c * 2) = h;
         }
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < MT; m++)
-            x[m] = made + min(m * 16 + r16, rows - 1) * pitch + g * 64;
+        x = made + min(r16, rows - 1) * pitch + g * 64;
     }
 
-    f32x4 acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; m++) acc[m] = f32x4{0, 0, 0, 0};
+    f32x4 acc = {0, 0, 0, 0};
     // Units b .. b + n - 1, n = GB with FULL.
     auto group = [&](auto full, int n) {
         constexpr bool FULL = decltype(full)::value;
@@ -429,14 +426,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
             if (!FULL && q >= n) break;
             const float s = __uint_as_float((wsc[q] >> (8 * g) & 0xffu) << 23);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const bf16x8 wf = widen4(wv[q][e], s);
-#pragma unroll
-                for (int m = 0; m < MT; m++)
-                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        wf, *reinterpret_cast<const bf16x8 *>(x[m] + (b + q) * 256 + e * 16), acc[m],
-                        0, 0, 0);
-            }
+            for (int e = 0; e < 4; e++)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    widen4(wv[q][e], s),
+                    *reinterpret_cast<const bf16x8 *>(x + (b + q) * 256 + e * 16), acc, 0, 0, 0);
         }
     };
     for (; b < nb; b += kFewWaves * GB) {
@@ -448,16 +441,214 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
         const int next = b + kFewWaves * GB;
         if (next < nb) load_w(next, min(nb - next, GB));
     }
-#pragma unroll
-    for (int m = 0; m < MT; m++) part[wave][m][lane] = acc[m];
+    part[wave][lane] = acc;
     __syncthreads();
-    for (int i = t; i < MT * 64; i += kFewWaves * 64) {
-        const int m = i / 64, l = i % 64;
-        f32x4 s = part[0][m][l];
+    if (wave > 0) return;
+    f32x4 sum = part[0][lane];
 #pragma unroll
-        for (int q = 1; q < kFewWaves; q++) s += part[q][m][l];
-        store4(p, m * 16 + (l & 15), j0 + (l >> 4) * 4, s);
+    for (int q = 1; q < kFewWaves; q++) sum += part[q][lane];
+    store4(p, r16, j0 + g * 4, sum);
+}
+
+// ---------------------------------------------------------------------------
+// Y = x W^T for some rows of x
+// ---------------------------------------------------------------------------
+//
+// W's bytes should still bound it, but x, which every row of W meets, is too large to
+// be read again for each 16 of them.  A workgroup takes 32 rows of W per wave and a
+// piece of the sum.  x's rows (16 MT) go through registers into LDS, GU units of 128
+// columns (16 KB, a group) at a time, and every wave multiplies by them; W's codes go
+// from memory to registers, become bf16 there and are multiplied at once.  Both are
+// asked for two groups ahead (four ahead, or two workgroups on a compute unit, are no
+// faster).  The pieces' sums meet in the workspace.  32 x 8192 x 28672: 32.7 us, of which
+// the second launch takes 4; W's 125 MB come at 4.4 TB/s, which a copy of as many also
+// reaches.  Alone, without x, products and scales, the loads of W take 24 to 27.
+//
+// LDS: a row's unit is 16 chunks of 16 bytes, chunk c of row r at c ^ strip_key(r), so
+// that the lanes that a read takes at a time fall into different banks.
+struct StripLaunch : MmLaunch {
+    int64_t units;               // of 128 columns
+    uint32_t groups;             // workgroups along W's rows
+};
+
+__device__ __forceinline__ int strip_key(int r) { return (r & 3) | ((r & 8) ? 12 : 0); }
+
+template <int MT>
+__global__ __launch_bounds__(kStripWaves * 64, 2) void strip_kernel(StripLaunch p) {
+    constexpr int GU = 4 / MT, BUFFER = 16384;
+    constexpr int SLOTS = BUFFER / (kStripWaves * 1024);   // of 16 bytes of x, per thread
+    struct Rows {                // of x, in one group
+        u32x4 v[SLOTS];
+    };
+    constexpr int AHEAD = 2;     // groups of W
+    constexpr int PITCH = 80;    // of a row's scales in LDS
+    struct Codes {               // a wave's 2 x 16 rows of W in one group
+        u32x4 v[GU][2];
+    };
+    __shared__ __attribute__((aligned(1024))) char mem[2 * BUFFER + kStripRows * PITCH];
+    LDS_AS char *const lds = (LDS_AS char *)mem;
+    const int t = threadIdx.x, lane = t & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t group = uniform(blockIdx.x % p.groups), piece = uniform(blockIdx.x / p.groups);
+    const int64_t j0 = static_cast<int64_t>(uniform(group * kStripWaves + wave)) * 32;
+    const int u0 = static_cast<int>(uniform(piece * p.chunk));
+    const int u1 = static_cast<int>(uniform(min((piece + 1) * p.chunk, p.units)));
+
+    // x: a wave's slot is 4 rows of one unit; rows and columns past the end are zeros
+    const __amdgpu_buffer_rsrc_t rx = buffer_of(scalar(p.a), uniform(p.rows * p.a_pitch));
+    auto ask_x = [&](Rows &x, int it) {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++) {
+            const int k = q * static_cast<int>(kStripWaves) + wave;
+            const int u = u0 + it * GU + k / (4 * MT), row = k % (4 * MT) * 4 + g;
+            const int c = u * 128 + (r16 ^ strip_key(row)) * 8;
+            const uint32_t at = static_cast<uint32_t>(row * p.a_pitch) + c * 2;
+            x.v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   rx, u < u1 && row < p.rows ? at : 0x80000000u, 0, 0));
+        }
+    };
+    auto put_x = [&](const Rows &x, int buffer) {
+#pragma unroll
+        for (int q = 0; q < SLOTS; q++)
+            *reinterpret_cast<LDS_AS u32x4 *>(lds + buffer * BUFFER + (q * kStripWaves + wave) * 1024 +
+                                              lane * 16) = x.v[q];
+    };
+    // W: rows past the last one are zeros; units past the row's end are the next
+    // row's, which nothing multiplies
+    const int64_t there = max(min(p.cols - j0, static_cast<int64_t>(32)), static_cast<int64_t>(0));
+    const __amdgpu_buffer_rsrc_t rw = buffer_of(scalar(p.b + j0 * p.b_pitch), uniform(there * p.b_pitch));
+    const __amdgpu_buffer_rsrc_t rs = buffer_of(scalar(p.bs + j0 * p.bs_pitch), uniform(there * p.bs_pitch));
+    uint32_t wat[2], sat[2];
+#pragma unroll
+    for (int f = 0; f < 2; f++) {
+        wat[f] = (f * 16 + r16) * static_cast<uint32_t>(p.b_pitch) + g * 16;
+        sat[f] = (f * 16 + r16) * static_cast<uint32_t>(p.bs_pitch) + g * 16;
     }
+    auto ask_w = [&](Codes &c, int it) {
+        const uint32_t u = u0 + it * GU;
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+#pragma unroll
+            for (int q = 0; q < GU; q++)
+                c.v[q][f] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wat[f], (u + q) * 64, 0));
+    };
+    // Scales of 16 units at a time, which a row's 4 lanes share out and each wave reads
+    // back by bytes from its own part of LDS: a load per group would take a line of the
+    // cache for each row and 4 or 8 bytes.
+    u32x4 sc[2];
+    LDS_AS char *const sto = lds + 2 * BUFFER + (wave * 32 + r16) * PITCH;
+    auto ask_scales = [&](int u) {
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+            sc[f] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, sat[f], (u0 + u) * 4, 0));
+    };
+    auto put_scales = [&] {
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+            *reinterpret_cast<LDS_AS u32x4 *>(sto + f * 16 * PITCH + g * 16) = sc[f];
+    };
+    f32x4 acc[2][MT];
+#pragma unroll
+    for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) acc[f][m] = f32x4{0, 0, 0, 0};
+    const int key = strip_key(r16);
+    auto multiply = [&](auto full, const Codes &c, int it, int buffer) {
+        const LDS_AS char *const x = lds + buffer * BUFFER + r16 * 256;
+#pragma unroll
+        for (int q = 0; q < GU; q++) {
+            if (!decltype(full)::value && u0 + it * GU + q >= u1) break;
+            float s[2];
+#pragma unroll
+            for (int f = 0; f < 2; f++)
+                s[f] = __uint_as_float(
+                    static_cast<uint32_t>(*reinterpret_cast<const LDS_AS uint8_t *>(
+                        sto + f * 16 * PITCH + (it * GU + q) % 16 * 4 + g)) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                bf16x8 xf[MT];
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+                    xf[m] = *reinterpret_cast<const LDS_AS bf16x8 *>(x + (q * MT + m) * 4096 +
+                                                                     (((g * 4 + e) ^ key) << 4));
+#pragma unroll
+                for (int f = 0; f < 2; f++) {
+                    const bf16x8 wf = widen4(c.v[q][f][e], s[f]);
+#pragma unroll
+                    for (int m = 0; m < MT; m++)
+                        acc[f][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m], acc[f][m], 0, 0, 0);
+                }
+            }
+        }
+    };
+    Rows x[2];
+    Codes c[AHEAD];
+    ask_x(x[0], 0);
+    ask_scales(0);
+    ask_w(c[0], 0);
+    ask_x(x[1], 1);
+#pragma unroll
+    for (int k = 1; k < AHEAD; k++) ask_w(c[k], k);
+    put_x(x[0], 0);
+    ask_x(x[0], 2);
+    // Group `it` of x is in LDS, and every wave has read the buffer that is filled next.
+    auto turns = [&](auto full, int it) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++) {
+            __syncthreads();
+            if (k == 0 && it * GU % 16 == 0) {
+                put_scales();
+                ask_scales(it * GU + 16);
+            }
+            put_x(x[(k + 1) % 2], (k + 1) % 2);
+            ask_x(x[(k + 1) % 2], it + k + 3);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(full, c[k], it + k, k % 2);
+            ask_w(c[k], it + k + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int it = 0;
+    for (; u0 + (it + AHEAD) * GU <= u1; it += AHEAD) turns(std::true_type{}, it);
+    if (u0 + it * GU < u1) turns(std::false_type{}, it);
+
+    float *const part = p.splits > 1 ? p.partial + piece * p.rows * p.cols : nullptr;
+#pragma unroll
+    for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            const int64_t row = m * 16 + r16, col = j0 + f * 16 + g * 4;
+            if (!part) {
+                store4(p, row, col, acc[f][m]);
+            } else if (row < p.rows) {
+                float *o = part + row * p.cols + col;
+                if (p.cols - col >= 4)
+                    *reinterpret_cast<row_f32x4 *>(o) = acc[f][m];
+                else
+                    for (int k = 0; k < 4; k++)
+                        if (col + k < p.cols) o[k] = acc[f][m][k];
+            }
+        }
+}
+
+// Adds the pieces' sums [splits, rows, cols] in their order.
+__global__ __launch_bounds__(256) void strip_join_kernel(MmLaunch p) {
+    const int64_t all = p.rows * p.cols;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= all) return;
+    f32x4 sum = {0, 0, 0, 0};
+    if (all - at >= 4) {
+#pragma unroll 8
+        for (int q = 0; q < p.splits; q++)
+            sum += *reinterpret_cast<const row_f32x4 *>(p.partial + q * all + at);
+    } else {
+        for (int q = 0; q < p.splits; q++)
+            for (int k = 0; k < all - at; k++) sum[k] += p.partial[q * all + at + k];
+    }
+    p.rows = 1;                  // the output as one row
+    p.cols = all;
+    store4(p, 0, at, sum);
 }
 
 // x [rows, cols] -> bf16 rows of whole units of 128 columns, zeros past the last
@@ -501,10 +692,22 @@ void launch_wide(const MmLaunch &p, int tile, dim3 grid, hipStream_t s) {
         wide_kernel<MI, MJ, 64, 2, 2, false><<<grid, dim3(256), 0, s>>>(p);
 }
 
-template <int MT>
-void launch_few(const MmLaunch &p, hipStream_t s) {
-    const dim3 g(static_cast<unsigned>((p.cols + 15) / 16)), b(kFewWaves * 64);
-    few_kernel<MT, kPadded, false><<<g, b, 0, s>>>(p);
+// x in bf16 rows of whole units.
+void launch_strips(const MmLaunch &mm, const MmChoice &c, char *partial, hipStream_t s) {
+    StripLaunch p = {mm, block_count(mm.sum), static_cast<uint32_t>((mm.cols + kStripRows - 1) / kStripRows)};
+    p.sum = p.units * 128;
+    p.chunk = c.chunk;
+    p.splits = c.splits;
+    p.partial = reinterpret_cast<float *>(partial);
+    const dim3 g(p.groups * c.splits), b(kStripWaves * 64);
+    if (p.rows <= 16)
+        strip_kernel<1><<<g, b, 0, s>>>(p);
+    else if (p.rows <= 32)
+        strip_kernel<2><<<g, b, 0, s>>>(p);
+    else
+        strip_kernel<4><<<g, b, 0, s>>>(p);
+    if (c.splits > 1)
+        strip_join_kernel<<<dim3(static_cast<unsigned>((p.rows * p.cols + 1023) / 1024)), dim3(256), 0, s>>>(p);
 }
 
 template <int ET>
@@ -521,9 +724,9 @@ void launch_in_one(const MmLaunch &p, bool quant, hipStream_t s) {
     const dim3 g(static_cast<unsigned>((p.cols + 15) / 16)), b(kFewWaves * 64);
     const unsigned lds = static_cast<unsigned>(p.rows * (2 * block_cols(p.sum) + 16));
     if (quant)
-        few_kernel<1, ET, true><<<g, b, lds, s>>>(p);
+        few_kernel<ET, true><<<g, b, lds, s>>>(p);
     else
-        few_kernel<1, ET, false><<<g, b, lds, s>>>(p);
+        few_kernel<ET, false><<<g, b, lds, s>>>(p);
 }
 
 tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) {
@@ -572,7 +775,7 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
             case kElemF16: launch_in_one<kElemF16>(p, quant, s); break;
             case kElemF32: launch_in_one<kElemF32>(p, quant, s); break;
         }
-    } else if (c.kernel == kFp4Skinny) {
+    } else if (c.kernel == kFp4Skinny || c.kernel == kFp4Strips) {
         p.a_pitch = block_cols(a.K) * 2;
         if (op == kFp4Mm) {
             const int64_t blocks = a.M * block_cols(a.K) / 32;
@@ -587,12 +790,11 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
             }
             p.a = ws;
         }
-        if (a.M <= 16)
-            launch_few<1>(p, s);
-        else if (a.M <= 32)
-            launch_few<2>(p, s);
+        if (c.kernel == kFp4Skinny)
+            few_kernel<kPadded, false><<<dim3(static_cast<unsigned>((p.cols + 15) / 16)),
+                                         dim3(kFewWaves * 64), 0, s>>>(p);
         else
-            launch_few<4>(p, s);
+            launch_strips(p, c.mm, ws + c.x, s);
     } else {
         if (quant && c.x_turned < 0) {
             if (a.workspace_bytes < c.x)

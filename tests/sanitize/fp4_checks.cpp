@@ -71,6 +71,14 @@ void choices(std::mt19937_64 &g) {
             EXPECT(c.x <= given && c.x >= M * tide::block_cols(K) * 2);
             continue;
         }
+        if (c.kernel == tide::kFp4Strips) {
+            EXPECT(M <= 64 && c.x <= given && c.x >= M * tide::block_cols(K) * 2);
+            const int64_t units = tide::block_count(K);
+            EXPECT(c.mm.chunk * c.mm.splits >= units && c.mm.chunk * (c.mm.splits - 1) < units);
+            EXPECT(c.mm.workspace == (c.mm.splits > 1 ? c.mm.splits * M * N * 4 : 0));
+            EXPECT(c.x + c.mm.workspace <= given);
+            continue;
+        }
         const int64_t sum = op == tide::kFp4Dx ? N : K, cols = op == tide::kFp4Dx ? K : N;
         const int64_t step = c.kernel == tide::kFp4Tiles ? 128 : 64, steps = (sum + step - 1) / step;
         const int64_t T = c.mm.tile, tiles = ((M + T - 1) / T) * ((cols + T - 1) / T);

@@ -236,6 +236,36 @@ def test_products_over_large_tiles(shape):
     check_products(*shape)
 
 
+# one to 64 rows of x by matrices of 2^21 numbers and more: sums in one piece and in
+# several, units of 128 columns that end inside a group, rows that end inside a strip
+STRIPS = [(17, 2000, 1100), (1, 33000, 4100), (5, 20000, 4100), (16, 5000, 28700), (20, 1030, 2100),
+          (33, 4099, 520), (48, 129, 20000), (64, 70, 30001), (32, 300, 7040), (32, 1300, 26000),
+          (18, 33000, 1050), (9, 40000, 900)]
+
+
+@pytest.mark.parametrize("shape", STRIPS)
+def test_products_of_some_rows(shape):
+    check_products(*shape)
+
+
+@pytest.mark.parametrize("shape", STRIPS)
+def test_some_rows_between_nans(shape):
+    """Nothing past a row's end or a matrix' end enters a sum: rows in turn NaN."""
+    note(f"fp4 some rows between NaNs {shape}")
+    m, n, k = shape
+    x, xq, w, _ = operands(m, n, k, 51)
+    y, y4 = tide.fp4_linear(x, w, dtype=FP), tide.fp4_mm(xq, w, dtype=FP)
+    c, s = w.codes.clone(), w.scales.clone()
+    s[::2] = 255
+    odd = tide.Fp4Blocks(c, s, k)
+    for got, want in ((tide.fp4_linear(x, odd, dtype=FP), y), (tide.fp4_mm(xq, odd, dtype=FP), y4)):
+        assert torch.equal(got[:, 1::2], want[:, 1::2])
+        assert bool(torch.isnan(got[:, ::2]).all())
+    x[m // 2, k - 1] = float("nan")
+    bad = torch.isnan(tide.fp4_linear(x, w, dtype=FP))
+    assert bool(bad[m // 2].all()) and int(bad.sum()) == n
+
+
 def test_products_without_elements():
     note("fp4 products without elements")
     for m, n, k in [(0, 5, 40), (5, 0, 40), (5, 6, 0), (0, 0, 0), (40, 6, 0)]:
@@ -248,7 +278,8 @@ def test_products_without_elements():
         assert dx.shape == (m, k) and not bool(dx.any())
 
 
-@pytest.mark.parametrize("shape", [(40, 130, 1000), (300, 257, 5000), (2, 40, 700)])
+@pytest.mark.parametrize("shape", [(40, 130, 1000), (300, 257, 5000), (2, 40, 700), (2, 33000, 4100),
+                                   (40, 1030, 2100)])
 def test_without_workspace(shape):
     """A call without workspace runs another way, where it can."""
     note(f"fp4 products without workspace {shape}")
