@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
     }
     _Float16 *X = reinterpret_cast<_Float16 *>(s.base + g.base + m * g.stride) + panel_at(g.nrp, row, col);
     *reinterpret_cast<f16x8 *>(X) = h;
-    *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
+    if (ET == kElemF32 || g.both()) *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
 }
 
 // ------------------------------------------------------- the products
@@ -379,6 +379,7 @@ struct ProductArgs {
     float ca, cb, cc;            // the step's coefficients (kPoly)
     int from;                    // which of the two X is read
     int first, last;             // of the steps
+    int short_g;                 // G is in 16 bits
     uint32_t total;              // workgroups
 };
 
@@ -494,6 +495,15 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     constexpr int PARTS = STAGE == kGram ? 0 : STAGE == kPoly ? 1 : 2;
     constexpr int KEEP = K::F < 2 ? 1 : 2;
     f16x8 held[KEEP][U::PASSES][PARTS ? PARTS : 1];
+    // A G in 16 bits is hi alone in the first step (down to 2^-25 of X's elements'
+    // mean).  Without lo in the last one, a matrix of low rank would be off by more than
+    // its rounding to bf16.
+    const bool lows = g.both() || !p.first || !p.short_g;
+    if (PARTS == 2)
+#pragma unroll
+        for (int c = 0; c < KEEP; c++)
+#pragma unroll
+            for (int q = 0; q < U::PASSES; q++) held[c][q][1] = f16x8{0, 0, 0, 0, 0, 0, 0, 0};
     auto ask = [&](int c) {
 #pragma unroll
         for (int q = 0; q < U::PASSES; q++) {
@@ -502,7 +512,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                 const char *from = old + panel_at(orows, i, j) * 2;
 #pragma unroll
                 for (int h = 0; h < PARTS; h++)
-                    held[c % KEEP][q][h] = *reinterpret_cast<const f16x8 *>(from + h * 2 * g.lo());
+                    if (h == 0 || lows)
+                        held[c % KEEP][q][h] = *reinterpret_cast<const f16x8 *>(from + h * 2 * g.lo());
             }
         }
     };
@@ -537,30 +548,33 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                 if (i < rp && j < rp) {                  // X's padding makes zeros of A's and P's
                     if (STAGE == kGram) {
 #pragma unroll
-                        for (int n = 0; n < 8; n++) {
-                            v[n] *= f;
-                            if (diagonal && i == j + n) {
-                                ad[i] = v[n];
-                                v[n] = 0.0f;
-                            }
-                            h[n] = static_cast<_Float16>(v[n] * kScaleA);
-                        }
+                        for (int n = 0; n < 8; n++) h[n] = static_cast<_Float16>(v[n] * (f * kScaleA));
+                        if (diagonal)
+#pragma unroll
+                            for (int n = 0; n < 8; n++)
+                                if (i == j + n) {
+                                    ad[i] = v[n] * f;
+                                    h[n] = 0;
+                                }
                     } else {
-                        const float di = ad[i];
+                        // O_ij (b + c d_i + c d_j) + c (O^2)_ij, in the scales of O and R
+                        const float cs = p.cc * (kScaleP / kScaleA), co = p.cc * f * kScaleP;
+                        const float di = ad[i], bi = p.cb * (kScaleP / kScaleA) + cs * di;
                         const f32x4 dl = *reinterpret_cast<const f32x4 *>(ad + j);
                         const f32x4 dh = *reinterpret_cast<const f32x4 *>(ad + j + 4);
                         const f16x8 o = held[c % KEEP][q][0];
 #pragma unroll
-                        for (int n = 0; n < 8; n++) {
-                            const float oij = static_cast<float>(o[n]) * (1.0f / kScaleA);
-                            const float oo = v[n] * f;
-                            v[n] = p.cb * oij + p.cc * ((di + (n < 4 ? dl[n] : dh[n - 4])) * oij + oo);
-                            if (diagonal && i == j + n) {
-                                pd[i] = i < r ? p.ca + p.cb * di + p.cc * (di * di + oo) : 0.0f;
-                                v[n] = 0.0f;
-                            }
-                            h[n] = static_cast<_Float16>(v[n] * kScaleP);
-                        }
+                        for (int n = 0; n < 8; n++)
+                            h[n] = static_cast<_Float16>(
+                                __builtin_fmaf(static_cast<float>(o[n]),
+                                               __builtin_fmaf(cs, n < 4 ? dl[n] : dh[n - 4], bi), v[n] * co));
+                        if (diagonal)
+#pragma unroll
+                            for (int n = 0; n < 8; n++)
+                                if (i == j + n) {
+                                    pd[i] = i < r ? p.ca + p.cb * di + p.cc * (di * di + v[n] * f) : 0.0f;
+                                    h[n] = 0;
+                                }
                     }
                     *reinterpret_cast<f16x8 *>(to + panel_at(rp, i, j)) = h;
                 }
@@ -595,23 +609,28 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
             const f16x8 h = held[c % KEEP][q][0], l = held[c % KEEP][q][PARTS - 1];
             f32x4 ql, qh;
             if (tall) {
-                ql = *reinterpret_cast<const f32x4 *>(pd + j);
-                qh = *reinterpret_cast<const f32x4 *>(pd + j + 4);
+                ql = *reinterpret_cast<const f32x4 *>(pd + j) * f;
+                qh = *reinterpret_cast<const f32x4 *>(pd + j + 4) * f;
             } else {
-                const float qi = pd[i];
+                const float qi = pd[i] * f;
                 ql = qh = f32x4{qi, qi, qi, qi};
             }
+            // in instructions that take fp16 factors as they are: 5 or 6 an element,
+            // where the conversions apart would be 12, and this is what a short sum's
+            // tile spends as much time on as on its products
 #pragma unroll
-            for (int n = 0; n < 8; n++)
-                v[n] = (v[n] * (1.0f / kScaleP) +
-                        (n < 4 ? ql[n] : qh[n - 4]) * (static_cast<float>(h[n]) + static_cast<float>(l[n]))) * f;
+            for (int n = 0; n < 8; n++) {
+                const float qn = n < 4 ? ql[n] : qh[n - 4];
+                v[n] = __builtin_fmaf(static_cast<float>(h[n]), qn, v[n] * (f / kScaleP));
+                v[n] = __builtin_fmaf(static_cast<float>(l[n]), qn, v[n]);
+            }
             if (!p.last) {
                 const int64_t at = panel_at(g.nrp, i, j);
                 f16x8 nh, nl;
 #pragma unroll
                 for (int n = 0; n < 8; n++) {
                     nh[n] = static_cast<_Float16>(v[n]);
-                    nl[n] = static_cast<_Float16>(v[n] - static_cast<float>(nh[n]));
+                    nl[n] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(nh[n]), -1.0f, v[n]));
                 }
                 *reinterpret_cast<f16x8 *>(to + at) = nh;
                 *reinterpret_cast<f16x8 *>(to + at + g.lo()) = nl;
@@ -701,8 +720,12 @@ tide_status over_groups(const OrthoPlan &plan, Wgs wgs, Launch launch) {
     return TIDE_OK;
 }
 
-// Large tiles once they fill three quarters of the card, small ones while middle
-// ones would leave half of it idle (the blocked products' rule).
+// Small tiles while middle ones would leave half of the card idle.  Else by whole
+// rounds of the card, 256 large tiles or 512 middle ones (half the work, 0.55 of the
+// time).  48 x [768, 2048]: X X^T and P, 2 rounds of each, 120 and 74 us with large
+// tiles, 91 and 46 with middle ones; P X, 5 rounds against 9, 220 against 200.  [4096,
+// 4096]: X X^T and P, 1 round against 2, 94 and 100 against 91 and 96, but P X, 1
+// against 2, 135 against 149, and all steps 1555 against 1650.
 int tile_for(const OrthoPlan &plan, int stage) {
     auto tiles = [&](uint32_t T) {
         int64_t n = 0;
@@ -710,7 +733,10 @@ int tile_for(const OrthoPlan &plan, int stage) {
             n += static_cast<int64_t>(g.count) * tiles_of(g, stage, T);
         return n;
     };
-    return tiles(256) >= kCus * 3 / 4 ? 256 : tiles(128) < kCus / 2 ? 64 : 128;
+    const int64_t middle = tiles(128);
+    if (middle < kCus / 2) return 64;
+    const int64_t large = (tiles(256) + kCus - 1) / kCus, half = (middle + 2 * kCus - 1) / (2 * kCus);
+    return large * 20 <= half * 11 ? 256 : 128;
 }
 
 template <int STAGE>
@@ -785,6 +811,7 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         p.from = i % 2;
         p.first = i == 0;
         p.last = i == a.steps - 1;
+        p.short_g = in_type(a.flags) != kElemF32;
         st = run_product<kGram>(plan, p, s);
         if (st == TIDE_OK) st = run_product<kPoly>(plan, p, s);
         if (st == TIDE_OK) st = run_product<kApply>(plan, p, s);
