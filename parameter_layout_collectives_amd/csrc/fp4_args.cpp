@@ -64,6 +64,8 @@ constexpr int64_t kStripLeast = int64_t(1) << 21, kStripLeast4 = int64_t(1) << 2
 // piece of a sum (40 x 1024 x 4096 8.7 us, with 8 units 11.1).
 constexpr int64_t kStripGroups = kCus;
 constexpr int64_t kStripUnits = 4;
+// Least steps that a cut has to save.
+constexpr int64_t kCutSaves = 24;
 // Least rows of the other operand, and columns, of an operand that is turned; and
 // least rows of an x that is made so.
 constexpr int64_t kTurnRows = 4096;
@@ -132,7 +134,12 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     const bool four = c.kernel == kFp4Tiles;
     c.mm.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256 : tiles(128) < kCus / 2 ? 64 : 128;
     // The 4-bit tiles' step is 128 columns, and two of them cost what cut_sums takes for
-    // one: cut by single steps, 777 x 1000 over 1111 takes 16.7 us, whole 13.4.
+    // one.  A cut that leaves no whole set has to save more than its second launch costs,
+    // kCutSaves steps, and of the 4-bit tiles, whose steps are short, also its traffic
+    // (M x N x K, us, cut / whole): bf16 x 300 x 2048 x 1024 12.5 / 7.8, 500 x 2048 x 2048 18.6 / 13.9,
+    // 4096 26.4 / 34, 100 x 512 x 2048 8.1 / 11.4, 200 x 1024 x 2048 12.5 / 11.6, 4096 15.1 /
+    // 20.3; 4 bits 200 x 1024 x 4096 15.0 / 12.5, 8192 20.3 / 19.0, 16384 23.2 / 29.7,
+    // 100 x 512 x 8192 15.2 / 21.5, 500 x 2048 x 16384 40 / 33.
     const int64_t step = four ? 256 : 64, per = four ? 2 : 1;
     c.mm.direct = tiles(c.mm.tile);
     c.mm.splits = 1;
@@ -140,6 +147,8 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     c.mm.workspace = 0;
     MmChoice cut = c.mm;
     cut_sums(cut, c.mm.direct, c.mm.chunk);
+    const int64_t least = std::max(kCutSaves, four ? c.mm.direct * 3 / 4 : 0);
+    if (cut.direct == 0 && c.mm.chunk - cut.chunk < least) cut = c.mm;
     cut.chunk *= per;
     c.mm.chunk *= per;
     if (c.x + cut.workspace <= workspace_bytes) c.mm = cut;

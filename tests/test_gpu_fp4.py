@@ -226,7 +226,8 @@ def test_products_over_inputs(k):
 
 @pytest.mark.parametrize("shape", [(1, 14336, 4096), (16, 100, 28672), (1, 33, 30000), (4, 64, 7000),
                                    (200, 1000, 5000), (500, 300, 9000), (1500, 1510, 460),
-                                   (2050, 2056, 1100), (777, 1001, 1111), (131, 201, 392)])
+                                   (2050, 2056, 1100), (777, 1001, 1111), (131, 201, 392),
+                                   (100, 512, 8200), (130, 5000, 600)])
 def test_products_of_many_shapes(shape):
     check_products(*shape)
 
