@@ -29,6 +29,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <new>
+#include <vector>
 
 #include "block.h"
 #include "block_device.h"
@@ -687,19 +689,19 @@ __global__ __launch_bounds__(kThreads, T == 256 ? 1 : 2) void product_kernel(Pro
 
 constexpr int64_t kMaxWgs = 0xffffffffll / 512;
 
-// Calls launch(groups, workgroups) over the plan's groups, as many at a time as
+// Calls launch(groups, workgroups) over the groups in their order, as many at a time as
 // kernel arguments hold and a launch can count; wgs(g): workgroups of one matrix of
 // g, which are fewer than that (ortho_plan).
 template <class Wgs, class Launch>
-tide_status over_groups(const OrthoPlan &plan, Wgs wgs, Launch launch) {
+tide_status over_groups(const std::vector<OrthoGroup> &groups, Wgs wgs, Launch launch) {
     size_t at = 0;
     uint32_t done = 0;           // matrices of group `at` launched before
-    while (at < plan.groups.size()) {
+    while (at < groups.size()) {
         Groups a;
         a.n = 0;
         int64_t total = 0;
-        while (at < plan.groups.size() && a.n < kOrthoGroups) {
-            OrthoGroup g = plan.groups[at];
+        while (at < groups.size() && a.n < kOrthoGroups) {
+            OrthoGroup g = groups[at];
             const int64_t per = wgs(g);
             const int64_t n = std::min<int64_t>(g.count - done, (kMaxWgs - total) / per);
             if (n == 0) break;
@@ -726,10 +728,10 @@ tide_status over_groups(const OrthoPlan &plan, Wgs wgs, Launch launch) {
 // tiles, 91 and 46 with middle ones; P X, 5 rounds against 9, 220 against 200.  [4096,
 // 4096]: X X^T and P, 1 round against 2, 94 and 100 against 91 and 96, but P X, 1
 // against 2, 135 against 149, and all steps 1555 against 1650.
-int tile_for(const OrthoPlan &plan, int stage) {
+int tile_for(const std::vector<OrthoGroup> &groups, int stage) {
     auto tiles = [&](uint32_t T) {
         int64_t n = 0;
-        for (const OrthoGroup &g : plan.groups)
+        for (const OrthoGroup &g : groups)
             n += static_cast<int64_t>(g.count) * tiles_of(g, stage, T);
         return n;
     };
@@ -739,11 +741,23 @@ int tile_for(const OrthoPlan &plan, int stage) {
     return large * 20 <= half * 11 ? 256 : 128;
 }
 
+// For X X^T the groups with the longest sums first: else their tiles leave most of
+// the card idle at the launch's end (the 8B layer, sums of 14336 and 4096, 910 us, so
+// 830).  The other products' sums are up to r, and their order gains nothing (P X of
+// the same layer 1680 to 1700 us as they come, 1740 the longest first).
+std::vector<OrthoGroup> longest_first(const std::vector<OrthoGroup> &groups) {
+    std::vector<OrthoGroup> v = groups;
+    std::stable_sort(v.begin(), v.end(), [](const OrthoGroup &a, const OrthoGroup &b) {
+        return std::max(a.nrp, a.ncp) > std::max(b.nrp, b.ncp);
+    });
+    return v;
+}
+
 template <int STAGE>
-tide_status run_product(const OrthoPlan &plan, ProductArgs p, hipStream_t s) {
-    const int T = tile_for(plan, STAGE);
+tide_status run_product(const std::vector<OrthoGroup> &groups, ProductArgs p, hipStream_t s) {
+    const int T = tile_for(groups, STAGE);
     return over_groups(
-        plan, [&](const OrthoGroup &g) { return tiles_of(g, STAGE, static_cast<uint32_t>(T)); },
+        groups, [&](const OrthoGroup &g) { return tiles_of(g, STAGE, static_cast<uint32_t>(T)); },
         [&](const Groups &a, uint32_t total) {
             p.a = a;
             p.total = total;
@@ -759,13 +773,13 @@ tide_status run_product(const OrthoPlan &plan, ProductArgs p, hipStream_t s) {
 template <int ET>
 tide_status run_first(const OrthoPlan &plan, const Space &sp, hipStream_t s) {
     tide_status st = over_groups(
-        plan, [](const OrthoGroup &g) { return g.parts; },
+        plan.groups, [](const OrthoGroup &g) { return g.parts; },
         [&](const Groups &a, uint32_t total) {
             squares_kernel<ET><<<dim3(total), dim3(256), 0, s>>>(a, sp);
         });
     if (st != TIDE_OK) return st;
     return over_groups(
-        plan, [](const OrthoGroup &g) { return g.nrp / 16 * ((g.ncp + 127) / 128); },
+        plan.groups, [](const OrthoGroup &g) { return g.nrp / 16 * ((g.ncp + 127) / 128); },
         [&](const Groups &a, uint32_t total) {
             first_kernel<ET><<<dim3(total), dim3(256), 0, s>>>(a, sp);
         });
@@ -778,6 +792,12 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
     if (plan.order.empty()) {
         clear_error();
         return TIDE_OK;
+    }
+    std::vector<OrthoGroup> by_length;
+    try {
+        by_length = longest_first(plan.groups);
+    } catch (const std::bad_alloc &) {
+        return fail(TIDE_E_NOMEM, "tide_ortho: out of host memory");
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     Space sp;
@@ -812,9 +832,9 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         p.first = i == 0;
         p.last = i == a.steps - 1;
         p.short_g = in_type(a.flags) != kElemF32;
-        st = run_product<kGram>(plan, p, s);
-        if (st == TIDE_OK) st = run_product<kPoly>(plan, p, s);
-        if (st == TIDE_OK) st = run_product<kApply>(plan, p, s);
+        st = run_product<kGram>(by_length, p, s);
+        if (st == TIDE_OK) st = run_product<kPoly>(plan.groups, p, s);
+        if (st == TIDE_OK) st = run_product<kApply>(plan.groups, p, s);
     }
     if (st == TIDE_OK) clear_error();
     return st;
