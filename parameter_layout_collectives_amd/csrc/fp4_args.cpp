@@ -64,10 +64,16 @@ constexpr int64_t kStripLeast = int64_t(1) << 21, kStripLeast4 = int64_t(1) << 2
 // piece of a sum (40 x 1024 x 4096 8.7 us, with 8 units 11.1).
 constexpr int64_t kStripGroups = kCus;
 constexpr int64_t kStripUnits = 4;
+// Least steps in a piece of a large tile.
+constexpr int64_t kDeepSteps = 16;
 // Least steps that a cut has to save.
 constexpr int64_t kCutSaves = 24;
-// Least rows of the other operand, and columns, of an operand that is turned; and
-// least rows of an x that is made so.
+// An operand is turned if the other has so many rows and both so many columns; an x
+// that is quantised here is made so from fewer rows on, as it costs nothing more
+// (M x N x K, us, turned / as it lies).  x: 128 x 8192 x 8192 25.8 / 31.7, 512 41 / 50,
+// 8192 322 / 386, over 512 columns 10.5 / 10.5; given in blocks 512 x 8192 x 8192 38.7 /
+// 44.3, 512 x 4096 x 8192 32.3 / 31.6.  w: 2048 x 8192 x 8192 90.2 / 89.6, 4096 166 /
+// 170, 8192 306 / 322.
 constexpr int64_t kTurnRows = 4096;
 constexpr int64_t kTurnSum = 1024;
 constexpr int64_t kTurnMade = 128;
@@ -133,6 +139,15 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((cols + t - 1) / t); };
     const bool four = c.kernel == kFp4Tiles;
     c.mm.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256 : tiles(128) < kCus / 2 ? 64 : 128;
+    // In bf16, large tiles also where they have to be cut to fill the card, if most of
+    // each is used and the pieces are long (dX, M x N x K, us, large / middle tiles):
+    // 256 x 8192 x 8192 55 / 62, 1024 122 / 154, 2048 x 14336 x 4096 190 / 253, 1024 x 4096 x
+    // 4096 50 / 50; pieces of 8 steps, 2048 x 1024 x 4096 33 / 25.
+    const int64_t large = tiles(256), pieces = std::min(kCus / std::max<int64_t>(large, 1), kMaxSplits);
+    if (aligned && !four && pieces >= 2 && large >= kCus / 8 && tiles(128) >= 3 * large &&
+        sum >= pieces * kDeepSteps * 64 &&
+        c.x + large * pieces * 256 * 256 * 4 <= workspace_bytes)
+        c.mm.tile = 256;
     // The 4-bit tiles' step is 128 columns, and two of them cost what cut_sums takes for
     // one.  A cut that leaves no whole set has to save more than its second launch costs,
     // kCutSaves steps, and of the 4-bit tiles, whose steps are short, also its traffic

@@ -232,7 +232,8 @@ def test_products_of_many_shapes(shape):
     check_products(*shape)
 
 
-@pytest.mark.parametrize("shape", [(4000, 4104, 1100), (4100, 1104, 4000), (4200, 4400, 2210)])
+@pytest.mark.parametrize("shape", [(4000, 4104, 1100), (4100, 1104, 4000), (4200, 4400, 2210),
+                                   (250, 8200, 8200)])
 def test_products_over_large_tiles(shape):
     check_products(*shape)
 
