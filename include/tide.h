@@ -506,8 +506,9 @@ tide_status tide_mx_unshard(const tide_plan *plan, const void *gathered, void *c
  * An empty sum gives zeros.
  *   workspace  device memory of tide_mx_workspace() bytes, 16-byte aligned, used
  *              during the call only.  With fewer bytes (NULL and 0) a call may be
- *              slower and round differently; TIDE_F_QUANT_X with more than 16 rows
- *              needs what x's blocks take (TIDE_E_INVALID with less). */
+ *              slower and round differently; TIDE_F_QUANT_X with more than 16 rows,
+ *              or more of x than 56 KB in bf16, needs what x's blocks take
+ *              (TIDE_E_INVALID with less). */
 tide_status tide_mx_mm(const void *x_codes, const void *x_scales, int64_t m, const void *w_codes,
                         const void *w_scales, int64_t n, int64_t k, void *out, uint32_t flags,
                         void *workspace, int64_t workspace_bytes, void *stream);

@@ -151,10 +151,11 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     // The 4-bit tiles' step is 128 columns, and two of them cost what cut_sums takes for
     // one.  A cut that leaves no whole set has to save more than its second launch costs,
     // kCutSaves steps, and of the 4-bit tiles, whose steps are short, also its traffic
-    // (M x N x K, us, cut / whole): bf16 x 300 x 2048 x 1024 12.5 / 7.8, 500 x 2048 x 2048 18.6 / 13.9,
-    // 4096 26.4 / 34, 100 x 512 x 2048 8.1 / 11.4, 200 x 1024 x 2048 12.5 / 11.6, 4096 15.1 /
-    // 20.3; 4 bits 200 x 1024 x 4096 15.0 / 12.5, 8192 20.3 / 19.0, 16384 23.2 / 29.7,
-    // 100 x 512 x 8192 15.2 / 21.5, 500 x 2048 x 16384 40 / 33.
+    // (M x N x K, us, cut / whole): bf16 x 300 x 2048 x 1024 12.5 / 7.8, 500 x 2048 x 2048
+    // 18.6 / 13.9, 500 x 2048 x 4096 26.4 / 34, 100 x 512 x 2048 8.1 / 11.4, 200 x 1024 x 2048
+    // 12.5 / 11.6, 200 x 1024 x 4096 15.1 / 20.3; 4 bits 200 x 1024 x 4096 15.0 / 12.5, over
+    // 8192 20.3 / 19.0, over 16384 23.2 / 29.7, 100 x 512 x 8192 15.2 / 21.5, 500 x 2048 x 16384
+    // 40 / 33.
     const int64_t step = four ? 256 : 64, per = four ? 2 : 1;
     c.mm.direct = tiles(c.mm.tile);
     c.mm.splits = 1;

@@ -13,7 +13,10 @@
 // a weight's largest entries carry most of what a product sums.
 //
 // As for 8-bit blocks, HBM bounds all of them: 16 lanes share 128 columns, 8
-// elements each (4 lanes a block), four such units in flight.
+// elements each (4 lanes a block), four such units in flight.  A rank's eighth of an 8B
+// layer from fp32 shards 24.4 us, 5.1 TB/s; the gathered layer to bf16 78 us, 7.1 TB/s
+// (what was just written comes from the last-level cache); 14336 x 4096 fp32 into blocks
+// 54 us, 4.9 TB/s (a copy reaches 4.8 to 5.3).
 #include "cast_device.h"
 #include "fp4.h"
 

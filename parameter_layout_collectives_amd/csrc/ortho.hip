@@ -25,6 +25,12 @@
 // twice the length.
 // Powers of two keep the numbers in fp16's range: X by 2^ex, about sqrt(r c), O by
 // 2^12, R by 2^10.
+//
+// The products bound it, and where the sums are short X's traffic: P X reads X (hi for
+// the product, hi and lo for its join) and writes it, 8 bytes an element and step.  Five
+// steps of [4096, 4096] take 1.51 to 1.55 ms, 0.9 PFLOP/s of the multiplications above,
+// of an 8B layer's seven matrices 14.4 ms, 1.03 PFLOP/s (fp16's library product 1.58),
+// of 48 x [768, 2048] 1.8 ms: X X^T 90 us, P 46, P X 200 to 230 a step, at 3.3 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -139,7 +145,8 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
     float x[8];
     const int n = row < g.nr && col < g.nc ? static_cast<int>(min(g.nc - col, 8u)) : 0;
     load8<ET>(src + (static_cast<int64_t>(row) * g.nc + col) * ES, n, false, x);
-    const double norm = sqrt(sum256(threadIdx.x < g.parts ? s.sums[static_cast<int64_t>(id) * kOrthoParts + threadIdx.x] : 0.0, part));
+    const double *const sums = s.sums + static_cast<int64_t>(id) * kOrthoParts;
+    const double norm = sqrt(sum256(threadIdx.x < g.parts ? sums[threadIdx.x] : 0.0, part));
     const int ex = x_exponent(g.nr, g.nc);
     int k = 0;
     double frac = 1.0;
@@ -167,7 +174,8 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
 
 // out[i, j] = sum over c of I(i, c) J(c, j) for fp16 factors in panels, so that both
 // go straight into LDS, in runs of at least 1 KB: rows of 64 bytes each from a
-// row-major matrix, half lines of the cache, take 1.5 times as long.  A T x T tile of
+// row-major matrix are half lines of the cache (an 8B layer 17.9 ms, in panels, with
+// larger fragments and more steps in LDS, 15.4).  A T x T tile of
 // the output per workgroup of 4 waves, 2 x 2; one step of the sum is 32 values, 64 T
 // bytes of a factor:
 //   along   (the sum runs along the rows): T rows of one panel
@@ -429,8 +437,9 @@ struct Turn {
 #pragma unroll
         for (int n = 0; n < 4; n++) v[n] = a[n], v[4 + n] = b[n];
     }
-    // The 32 rows once more, as fp16 numbers, behind the sums, to be read down the columns: rows 8 g .. 8 g + 7 of column 16 q + r16 for lane
-    // (r16, g), a run of 1 KB in the matrix's other half.
+    // The 32 rows once more, as fp16 numbers, behind the sums, to be read down the
+    // columns: rows 8 g .. 8 g + 7 of column 16 q + r16 for lane (r16, g), a run of 1 KB in
+    // the matrix's other half.
     static constexpr int HALF = 32 * PITCH, HALF_PITCH = W * 2 + 16;
     static_assert(HALF + 32 * HALF_PITCH <= buffers(T) * 2 * T * 64 / 4, "a wave's part of LDS");
     __device__ __forceinline__ void set(int q, const f16x8 &h) const {
