@@ -30,7 +30,7 @@
 // the product, hi and lo for its join) and writes it, 8 bytes an element and step.  Five
 // steps of [4096, 4096] take 1.51 to 1.55 ms, 0.9 PFLOP/s of the multiplications above,
 // of an 8B layer's seven matrices 14.4 ms, 1.03 PFLOP/s (fp16's library product 1.58),
-// of 48 x [768, 2048] 1.8 ms: X X^T 90 us, P 46, P X 200 to 230 a step, at 3.3 TB/s.
+// of 48 x [768, 2048] 1.7 ms: X X^T 90 us, P 46, P X 190 to 210 a step, at 3.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -294,6 +294,11 @@ struct Half {
     static constexpr int LOADS = FI::SLOTS + FJ::SLOTS;
     static constexpr int PER_LINE = LOADS / LINES;         // loads issued with a line
     static constexpr int BUFFERS = buffers(T);
+    // Loads return in order, so the first steps would wait for any that set out before
+    // them; under the last steps, two workgroups a unit, 48 x [768, 2048] take 1706 us
+    // for 1784.  The large tiles, alone on their unit and in long sums, are as fast with
+    // them at the start (8B layer 14.2 ms for 14.35), behind the first steps' loads.
+    static constexpr uint32_t LATE = T == 256 ? 1u << 30 : 32;
     static constexpr int TILE = FI::BYTES, BUFFER = 2 * TILE, LDS = BUFFERS * BUFFER;
     static_assert(LINES % RING == 0 && LOADS % LINES == 0, "a step starts at ring entry 0");
 
@@ -349,7 +354,10 @@ struct Half {
         fi.next();
         fj.next();
     }
-    __device__ __forceinline__ void run(LDS_AS char *lds, uint32_t steps) {
+    // ask(c), c < ASKS: loads of the caller's own, which set out when LATE (c = 0) and
+    // LATE / 2 (c = 1) steps are left.
+    template <int ASKS, class Ask>
+    __device__ __forceinline__ void run(LDS_AS char *lds, uint32_t steps, Ask ask) {
         ai = FI::lane_at(lane);
         aj = FJ::lane_at(lane);
 #pragma unroll
@@ -369,13 +377,24 @@ struct Half {
         uint32_t here = 0, to = (BUFFERS - 1) * BUFFER;
         auto after = [](uint32_t b) { return b == (BUFFERS - 1) * BUFFER ? 0 : b + BUFFER; };
         // sums are of 64 values or a multiple: steps come in pairs
-        for (; steps; steps -= 2) {
-            const uint32_t there = after(here), to2 = after(to);
-            step(l, r0, r1, lds + here, lds + there, lds + to);
-            here = after(there);
-            step(l, r1, r0, lds + there, lds + here, lds + to2);
-            to = after(to2);
+        auto until = [&](uint32_t left) {
+            for (; steps > left; steps -= 2) {
+                const uint32_t there = after(here), to2 = after(to);
+                step(l, r0, r1, lds + here, lds + there, lds + to);
+                here = after(there);
+                step(l, r1, r0, lds + there, lds + here, lds + to2);
+                to = after(to2);
+            }
+        };
+        if (ASKS > 0) {
+            until(LATE);
+            ask(0);
         }
+        if (ASKS > 1) {
+            until(LATE / 2);
+            ask(1);
+        }
+        until(0);
         arrived();               // no load may still be on its way to LDS at the end,
         __syncthreads();         // nor a read of what the sums will overwrite
     }
@@ -499,8 +518,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     const U turn = {lds + k.wave * (K::LDS / 4), lane, STAGE == kApply && p.last ? U::W / 8 : 4};
     const uint32_t li = i0 + k.wi * U::W, lj = j0 + k.wj * U::W;       // the wave's first row and column
     // What the sums are joined with, 32 rows of the wave's tile at a time: asked for
-    // ahead, the first KEEP times before the products, so that its latency and (all
-    // workgroups come here together) its traffic lie under them.
+    // ahead, the first KEEP times under the products, so that its latency and (all
+    // workgroups come here together) its traffic lie under them; see LATE.
     const char *const __restrict__ old = STAGE == kPoly ? base + g.a_at() : x;
     const uint32_t orows = STAGE == kPoly ? rp : g.nrp, ocols = STAGE == kPoly ? rp : g.ncp;
     constexpr int PARTS = STAGE == kGram ? 0 : STAGE == kPoly ? 1 : 2;
@@ -518,21 +537,19 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     auto ask = [&](int c) {
 #pragma unroll
         for (int q = 0; q < U::PASSES; q++) {
-            const uint32_t i = li + c * 32 + turn.row(q), j = lj + turn.col(q);
-            if (i < orows && j < ocols) {
-                const char *from = old + panel_at(orows, i, j) * 2;
+            // Past the matrix its last row or columns, whose values nothing uses.  Not a
+            // branch by lanes: here, between the loops, the compiler (ROCm 7.2) has
+            // placed a register's copy before the lanes are joined again.
+            const uint32_t i = min(li + c * 32 + turn.row(q), orows - 1);
+            const uint32_t j = min(lj + turn.col(q), ocols - 8);
+            const char *from = old + panel_at(orows, i, j) * 2;
 #pragma unroll
-                for (int h = 0; h < PARTS; h++)
-                    if (h == 0 || lows)
-                        held[c % KEEP][q][h] = *reinterpret_cast<const f16x8 *>(from + h * 2 * g.lo());
-            }
+            for (int h = 0; h < PARTS; h++)
+                if (h == 0 || lows)
+                    held[c % KEEP][q][h] = *reinterpret_cast<const f16x8 *>(from + h * 2 * g.lo());
         }
     };
-    if (PARTS)
-#pragma unroll
-        for (int c = 0; c < KEEP; c++) ask(c);
-
-    k.run(lds, uniform(steps));
+    k.template run<PARTS ? KEEP : 0>(lds, uniform(steps), ask);
 
     const float2 t1 = p.first ? p.s.scales[g.first + m] : make_float2(1.0f, 1.0f);
     const int ex = x_exponent(g.nr, g.nc);
