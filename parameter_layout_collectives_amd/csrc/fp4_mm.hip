@@ -40,7 +40,7 @@ namespace {
 // that misses the L2 takes longer than two steps.
 // 8192 x 28672 x 8192: 0.86 to 0.91 ms, 4.2 to 4.5 PFLOP/s (bf16's library product reaches
 // 1.58), matrix units busy 56% of the cycles at a clock of 1.8 GHz; with x's and W's
-// turning 0.96 ms.  In steps of 256 columns, two of them in LDS, it took 2.3 ms; with 8
+// turning 0.94 ms.  In steps of 256 columns, two of them in LDS, it took 2.3 ms; with 8
 // waves in fragments of 16 x 16, 1.1.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -211,9 +211,10 @@ __global__ __launch_bounds__(256) void turn_kernel(const char *__restrict__ code
                                                    const char *__restrict__ scales, int64_t rows,
                                                    uint32_t steps, char *__restrict__ to,
                                                    char *__restrict__ sto) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x >> 2);
+    const uint32_t fours = (steps + 3) / 4;
+    const int64_t row = static_cast<int64_t>(blockIdx.x / fours) * 64 + (threadIdx.x >> 2);
     const int c = threadIdx.x & 3;
-    const uint32_t s0 = blockIdx.y * 4;
+    const uint32_t s0 = blockIdx.x % fours * 4;
     if (row >= rows) return;
     const u32x4 *in = reinterpret_cast<const u32x4 *>(codes + row * steps * 64) + c;
     u32x4 v[4];
@@ -229,15 +230,18 @@ __global__ __launch_bounds__(256) void turn_kernel(const char *__restrict__ code
 }
 
 // x [rows, cols] -> turned 4-bit blocks, as tide_mx_quant and turn_kernel make them.  16
-// lanes a unit of 128 columns, 8 values each; a workgroup takes 16 rows of 4 units.
+// lanes a unit of 128 columns, 8 values each; a workgroup takes 16 rows of 4 units, the
+// next one the next units: 8192 x 8192 bf16 36 us, 4.7 TB/s (down the rows first 48).
 template <int ET>
 __global__ __launch_bounds__(256) void quant_turned_kernel(const char *__restrict__ x, int64_t rows,
                                                            int64_t cols, char *__restrict__ to,
                                                            char *__restrict__ sto, int vec) {
     constexpr int ES = ET == kElemF32 ? 4 : 2;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    const int64_t units = (cols + 127) / 128;
+    const uint32_t fours = static_cast<uint32_t>((units + 3) / 4);
+    const int64_t row = static_cast<int64_t>(blockIdx.x / fours) * 16 + (threadIdx.x >> 4);
     const int lane = threadIdx.x & 15;
-    const int64_t unit0 = static_cast<int64_t>(blockIdx.y) * 4, units = (cols + 127) / 128;
+    const int64_t unit0 = static_cast<int64_t>(blockIdx.x % fours) * 4;
     float v[4][8];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
@@ -826,7 +830,7 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
                 if (at < 0) return;
                 char *const to = ws + at, *const sto = to + steps * rows * 64;
                 if (quant && at == c.x_turned) {
-                    const dim3 g(static_cast<unsigned>((rows + 15) / 16), fours), b(256);
+                    const dim3 g(static_cast<unsigned>((rows + 15) / 16) * fours), b(256);
                     const int vec = a.K % 8 == 0;
                     switch (in) {
                         case kElemBf16: quant_turned_kernel<kElemBf16><<<g, b, 0, s>>>(x, rows, a.K, to, sto, vec); break;
@@ -834,7 +838,7 @@ tide_status run_fp4(Fp4Op op, const char *name, const Fp4Args &a, void *stream) 
                         case kElemF32: quant_turned_kernel<kElemF32><<<g, b, 0, s>>>(x, rows, a.K, to, sto, vec); break;
                     }
                 } else {
-                    turn_kernel<<<dim3(static_cast<unsigned>((rows + 63) / 64), fours), dim3(256), 0, s>>>(
+                    turn_kernel<<<dim3(static_cast<unsigned>((rows + 63) / 64) * fours), dim3(256), 0, s>>>(
                         codes, scales, rows, static_cast<uint32_t>(steps), to, sto);
                 }
                 cw = Way{to, 64, static_cast<uint32_t>(rows * 64), 1};

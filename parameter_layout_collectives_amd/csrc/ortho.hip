@@ -28,7 +28,7 @@
 //
 // The products bound it, and where the sums are short X's traffic: P X reads X (hi for
 // the product, hi and lo for its join) and writes it, 8 bytes an element and step.  Five
-// steps of [4096, 4096] take 1.51 to 1.55 ms, 0.9 PFLOP/s of the multiplications above,
+// steps of [4096, 4096] take 1.50 to 1.54 ms, 0.9 PFLOP/s of the multiplications above,
 // of an 8B layer's seven matrices 14.4 ms, 1.03 PFLOP/s (fp16's library product 1.58),
 // of 48 x [768, 2048] 1.7 ms: X X^T 90 us, P 46, P X 190 to 210 a step, at 3.6 TB/s.
 #include <hip/hip_runtime.h>
@@ -107,7 +107,18 @@ __global__ __launch_bounds__(256) void squares_kernel(Groups a, Space s) {
     const int64_t chunk = ((numel + g.parts - 1) / g.parts + 7) / 8 * 8;
     const int64_t lo = q * chunk, hi = min(lo + chunk, numel);
     double v = 0;
-    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += 2048) {
+    int64_t i = lo + threadIdx.x * 8;
+    // four loads in flight: [4096, 4096] 11 us, one at a time 17 to 22
+    for (; i + 3 * 2048 + 8 <= hi; i += 4 * 2048) {
+        float x[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; u++) load8<ET>(src + (i + u * 2048) * ES, 8, false, x[u]);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int k = 0; k < 8; k++) v += static_cast<double>(x[u][k]) * x[u][k];
+    }
+    for (; i < hi; i += 2048) {
         float x[8];
         load8<ET>(src + i * ES, static_cast<int>(min(hi - i, static_cast<int64_t>(8))), false, x);
 #pragma unroll
