@@ -389,7 +389,8 @@ def test_operands_between_nans(shape):
 
 
 @pytest.mark.parametrize("shape", [(5, 61, 131), (50, 61, 131), (130, 200, 260), (16, 40, 256),
-                                   (9, 24, 20000)])
+                                   (9, 24, 20000), (20, 1030, 2100), (33, 2050, 1024), (13, 8200, 4096),
+                                   (250, 8200, 8200)])
 def test_x_and_dy_of_any_alignment(shape):
     note(f"fp4 products unaligned {shape}")
     m, n, k = shape
@@ -406,7 +407,8 @@ def test_x_and_dy_of_any_alignment(shape):
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
 @pytest.mark.parametrize("shape", [(1, 33, 4096), (1, 40, 28672), (1, 40, 28800), (16, 40, 1700),
-                                   (16, 40, 1900), (17, 64, 700), (200, 100, 4097)])
+                                   (16, 40, 1900), (17, 64, 700), (200, 100, 4097), (20, 1030, 2101),
+                                   (9, 20000, 900), (31, 2050, 1024)])
 def test_linear_rounds_x_as_quant_does(shape, dtype):
     note(f"fp4_linear quant_x {shape} {dtype}")
     m, n, k = shape
@@ -418,9 +420,10 @@ def test_linear_rounds_x_as_quant_does(shape, dtype):
         assert blocks_ref.off(y, want, mass, k) <= 1.0
 
 
-def test_same_call_same_bits_on_two_streams():
-    note("fp4 products on two streams")
-    sets = [operands(300, 200, 9000, 20 + 5 * i) for i in range(2)]
+@pytest.mark.parametrize("shape", [(300, 200, 9000), (50, 2050, 4100), (4200, 600, 4300)])
+def test_same_call_same_bits_on_two_streams(shape):
+    note(f"fp4 products on two streams {shape}")
+    sets = [operands(*shape, 20 + 5 * i) for i in range(2)]
 
     def both(x, xq, w, dy):
         return [tide.fp4_mm(xq, w), tide.fp4_linear(x, w), tide.fp4_linear(x, w, quant_x=True),
@@ -606,6 +609,38 @@ def test_captured(m):
         for i, x in enumerate(xs):
             x.copy_(rand((m, k), 50 + 2 * it + i))
         master.mul_(1.5)
+        torch.cuda.synchronize()
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        for i, x in enumerate(xs):
+            for got, want in zip(outs[i], step(x)):
+                assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("shape", [(40, 2050, 4100), (20, 2050, 1024), (4200, 700, 4200)])
+def test_captured_in_several_launches(shape):
+    """Sums in pieces, padded x and turned operands, in two graphs that replay in turn."""
+    note(f"fp4 captured launches {shape}")
+    m, n, k = shape
+    _, xq, w, dy = operands(m, n, k, 48)
+    xs = [rand((m, k), 60 + i) for i in range(2)]
+
+    def step(x):
+        return [tide.fp4_linear(x, w), tide.fp4_linear(x, w, quant_x=True),
+                tide.fp4_mm(tide.fp4_quant(x), w), tide.fp4_mm_dx(dy, w)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    outs, graphs = [], []
+    for x in xs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=side):
+            outs.append(step(x))
+        graphs.append(gr)
+    for it in range(3):
+        for i, x in enumerate(xs):
+            x.copy_(rand((m, k), 70 + 2 * it + i))
         torch.cuda.synchronize()
         for gr in graphs:
             gr.replay()
