@@ -23,6 +23,9 @@
 // eighth of r (an emulation in 64 bits).  With fewer rows R outweighs Q there (37 of
 // rank 4: 4e-3), so up to kOrthoBoth of them R X takes lo as well, as one sum of
 // twice the length.
+// Few rows average none of these roundings out (2 x 2: up to 8e-3), and cost next to
+// nothing: up to kOrthoSmall of them the steps run in fp64 on A alone, since P and A
+// commute: A <- P A P and M <- P M from M = I, and the result is M X, one pass over G.
 // Powers of two keep the numbers in fp16's range: X by 2^ex, about sqrt(r c), O by
 // 2^12, R by 2^10.
 //
@@ -179,6 +182,167 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
     _Float16 *X = reinterpret_cast<_Float16 *>(s.base + g.base + m * g.stride) + panel_at(g.nrp, row, col);
     *reinterpret_cast<f16x8 *>(X) = h;
     if (ET == kElemF32 || g.both()) *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
+}
+
+// ------------------------------------------------------- few rows
+//
+// Latency bounds these: three launches for all steps, where the products take three a
+// step.  A chunk of 256 columns is in LDS as [r][256]; G is read once, as an out may be
+// another matrix's src.
+constexpr int kSmallPitch = kOrthoSmallCols + 1;
+
+template <int ET>
+__device__ __forceinline__ float load1(const char *p, int64_t i) {
+    if (ET == kElemF32) return reinterpret_cast<const float *>(p)[i];
+    if (ET == kElemF16) return static_cast<float>(reinterpret_cast<const _Float16 *>(p)[i]);
+    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
+}
+
+// Calls each(offset in the matrix, row, column of the chunk) for this thread's elements
+// of columns [c0, c0 + n), in the order of memory.
+template <class Each>
+__device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int n, Each each) {
+    const int r = g.r();
+    for (int e = threadIdx.x; e < r * n; e += 256) {
+        const int i = g.tall() ? e % r : e / n, col = g.tall() ? e / r : e % n;
+        each(g.tall() ? c0 * r + e : static_cast<int64_t>(i) * g.nc + c0 + col, i, col);
+    }
+}
+
+// G G^T of a piece of the columns: a thread sums a 2 x 2 block (r = 1: 1 x 1) over some
+// of them.
+template <int ET>
+__global__ __launch_bounds__(256) void small_gram_kernel(Groups a, Space s) {
+    __shared__ float x[kOrthoSmall * kSmallPitch];
+    __shared__ double part[256][4];
+    const OrthoGroup g = group_of(a, blockIdx.x);
+    const uint32_t in = blockIdx.x - g.wg0, m = in / g.parts, q = in % g.parts;
+    const char *const src = reinterpret_cast<const char *>(s.pointers[g.first + m].src);
+    char *const base = s.base + g.base + m * g.stride;
+    const int r = g.r(), t = threadIdx.x;
+    const int64_t c = g.tall() ? g.nr : g.nc;
+    const int64_t chunks = (c + kOrthoSmallCols - 1) / kOrthoSmallCols, per = (chunks + g.parts - 1) / g.parts;
+    const int64_t c0 = q * per * kOrthoSmallCols, c1 = min(c0 + per * kOrthoSmallCols, c);
+    int side = 1;                                          // threads along a row of blocks
+    while (side * 2 < r) side *= 2;
+    const int B = r > 1 ? 2 : 1, per_set = side * side, sets = 256 / per_set;
+    const int pt = t % per_set, pi = pt / side * B, pj = pt % side * B;
+    const int pi1 = min(pi + B - 1, r - 1), pj1 = min(pj + B - 1, r - 1);
+    double v00 = 0, v01 = 0, v10 = 0, v11 = 0;
+    for (int64_t at = c0; at < c1; at += kOrthoSmallCols) {
+        const int n = static_cast<int>(min(kOrthoSmallCols, c1 - at));
+        __syncthreads();
+        over_chunk(g, at, n, [&](int64_t off, int i, int col) {
+            const float v = load1<ET>(src, off);
+            reinterpret_cast<float *>(base)[off] = v;
+            x[i * kSmallPitch + col] = v;
+        });
+        __syncthreads();
+        if (pi < r && pj < r)
+            for (int col = t / per_set; col < n; col += sets) {
+                const double i0 = x[pi * kSmallPitch + col], i1 = x[pi1 * kSmallPitch + col];
+                const double j0 = x[pj * kSmallPitch + col], j1 = x[pj1 * kSmallPitch + col];
+                v00 += i0 * j0;
+                v01 += i0 * j1;
+                v10 += i1 * j0;
+                v11 += i1 * j1;
+            }
+    }
+    part[t][0] = v00;
+    part[t][1] = v01;
+    part[t][2] = v10;
+    part[t][3] = v11;
+    __syncthreads();
+    double *const to = reinterpret_cast<double *>(base + g.gram_at()) + static_cast<int64_t>(q) * r * r;
+    for (int e = t; e < r * r; e += 256) {
+        const int i = e / r, j = e % r, p = i / B * side + j / B, k = i % B * 2 + j % B;
+        double v = 0;
+        for (int u = 0; u < sets; u++) v += part[u * per_set + p][k];
+        to[e] = v;
+    }
+}
+
+struct SmallArgs {
+    Groups a;
+    Space s;
+    float coefficients[192];
+    int steps;
+};
+
+// All steps on A, one workgroup a matrix; what G 2^-k is multiplied by, and k.
+__global__ __launch_bounds__(256) void small_steps_kernel(SmallArgs p) {
+    constexpr int R = kOrthoSmall;
+    __shared__ double A[R * R], P[R * R], M[R * R], T[R * R], U[R * R];
+    const OrthoGroup g = group_of(p.a, blockIdx.x);
+    char *const base = p.s.base + g.base + (blockIdx.x - g.wg0) * g.stride;
+    const double *const gram = reinterpret_cast<const double *>(base + g.gram_at());
+    const int r = g.r(), n = r * r, t = threadIdx.x;
+    for (int e = t; e < n; e += 256) {
+        double v = 0;
+        for (uint32_t q = 0; q < g.parts; q++) v += gram[static_cast<int64_t>(q) * n + e];
+        A[e] = v;
+        M[e] = e / r == e % r;
+    }
+    __syncthreads();
+    double sum = 0;
+    for (int i = 0; i < r; i++) sum += A[i * r + i];
+    __syncthreads();
+    const double norm = sqrt(sum);
+    const bool finite = norm < __builtin_inf();
+    for (int e = t; e < n; e += 256) A[e] = norm > 0 ? A[e] / sum : 0.0;
+    int k = 0;
+    const double frac = finite && norm > 0 ? frexp(norm, &k) : 1.0;
+    __syncthreads();
+    auto times = [&](double *out, const double *x, const double *y) {
+        for (int e = t; e < n; e += 256) {
+            double v = 0;
+            for (int j = 0; j < r; j++) v += x[e / r * r + j] * y[j * r + e % r];
+            out[e] = v;
+        }
+    };
+    for (int q = 0; q < p.steps; q++) {
+        const double ca = p.coefficients[3 * q], cb = p.coefficients[3 * q + 1], cc = p.coefficients[3 * q + 2];
+        times(T, A, A);
+        __syncthreads();
+        for (int e = t; e < n; e += 256) P[e] = (e / r == e % r ? ca : 0.0) + cb * A[e] + cc * T[e];
+        __syncthreads();
+        times(T, P, M);
+        times(U, P, A);
+        __syncthreads();
+        for (int e = t; e < n; e += 256) M[e] = T[e];
+        times(A, U, P);
+        __syncthreads();
+    }
+    double *const map = reinterpret_cast<double *>(base + g.map_at());
+    for (int e = t; e < n; e += 256)
+        map[e] = !finite ? __builtin_nan("") : norm > 0 ? M[e] / frac : 0.0;
+    if (t == 0) map[n] = k;
+}
+
+// out = M (G 2^-k), 256 columns a workgroup.
+__global__ __launch_bounds__(256) void small_apply_kernel(Groups a, Space s) {
+    __shared__ float x[kOrthoSmall * kSmallPitch];
+    __shared__ double M[kOrthoSmall * kOrthoSmall];
+    const OrthoGroup g = group_of(a, blockIdx.x);
+    const int64_t c = g.tall() ? g.nr : g.nc;
+    const uint32_t per = static_cast<uint32_t>((c + kOrthoSmallCols - 1) / kOrthoSmallCols);
+    const uint32_t in = blockIdx.x - g.wg0, m = in / per;
+    const char *const base = s.base + g.base + m * g.stride;
+    const double *const map = reinterpret_cast<const double *>(base + g.map_at());
+    const int r = g.r(), k = -static_cast<int>(map[r * r]);
+    const int64_t c0 = static_cast<int64_t>(in % per) * kOrthoSmallCols;
+    const int n = static_cast<int>(min(kOrthoSmallCols, c - c0));
+    for (int e = threadIdx.x; e < r * r; e += 256) M[e] = map[e];
+    over_chunk(g, c0, n, [&](int64_t off, int i, int col) {
+        x[i * kSmallPitch + col] = ldexpf(reinterpret_cast<const float *>(base)[off], k);
+    });
+    __syncthreads();
+    __bf16 *const out = reinterpret_cast<__bf16 *>(s.pointers[g.first + m].out);
+    over_chunk(g, c0, n, [&](int64_t off, int i, int col) {
+        double v = 0;
+        for (int j = 0; j < r; j++) v += M[i * r + j] * x[j * kSmallPitch + col];
+        out[off] = static_cast<__bf16>(static_cast<float>(v));
+    });
 }
 
 // ------------------------------------------------------- the products
@@ -807,16 +971,24 @@ tide_status run_product(const std::vector<OrthoGroup> &groups, ProductArgs p, hi
         });
 }
 
+// What reads the matrices: of the large ones, and of the small ones.
 template <int ET>
-tide_status run_first(const OrthoPlan &plan, const Space &sp, hipStream_t s) {
+tide_status run_first(const std::vector<OrthoGroup> &groups, const std::vector<OrthoGroup> &small,
+                      const Space &sp, hipStream_t s) {
     tide_status st = over_groups(
-        plan.groups, [](const OrthoGroup &g) { return g.parts; },
+        groups, [](const OrthoGroup &g) { return g.parts; },
         [&](const Groups &a, uint32_t total) {
             squares_kernel<ET><<<dim3(total), dim3(256), 0, s>>>(a, sp);
         });
+    if (st == TIDE_OK)
+        st = over_groups(
+            small, [](const OrthoGroup &g) { return g.parts; },
+            [&](const Groups &a, uint32_t total) {
+                small_gram_kernel<ET><<<dim3(total), dim3(256), 0, s>>>(a, sp);
+            });
     if (st != TIDE_OK) return st;
     return over_groups(
-        plan.groups, [](const OrthoGroup &g) { return g.nrp / 16 * ((g.ncp + 127) / 128); },
+        groups, [](const OrthoGroup &g) { return g.nrp / 16 * ((g.ncp + 127) / 128); },
         [&](const Groups &a, uint32_t total) {
             first_kernel<ET><<<dim3(total), dim3(256), 0, s>>>(a, sp);
         });
@@ -830,9 +1002,10 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         clear_error();
         return TIDE_OK;
     }
-    std::vector<OrthoGroup> by_length;
+    std::vector<OrthoGroup> groups, small, by_length;
     try {
-        by_length = longest_first(plan.groups);
+        for (const OrthoGroup &g : plan.groups) (g.small() ? small : groups).push_back(g);
+        by_length = longest_first(groups);
     } catch (const std::bad_alloc &) {
         return fail(TIDE_E_NOMEM, "tide_ortho: out of host memory");
     }
@@ -855,11 +1028,31 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         if (e != hipSuccess) return hip_fail("tide_ortho: kernel launch", e);
     }
     switch (in_type(a.flags)) {
-        case kElemBf16: st = run_first<kElemBf16>(plan, sp, s); break;
-        case kElemF16: st = run_first<kElemF16>(plan, sp, s); break;
-        case kElemF32: st = run_first<kElemF32>(plan, sp, s); break;
+        case kElemBf16: st = run_first<kElemBf16>(groups, small, sp, s); break;
+        case kElemF16: st = run_first<kElemF16>(groups, small, sp, s); break;
+        case kElemF32: st = run_first<kElemF32>(groups, small, sp, s); break;
     }
-    for (int i = 0; i < a.steps && st == TIDE_OK; i++) {
+    if (st == TIDE_OK)
+        st = over_groups(
+            small, [](const OrthoGroup &) { return 1; },
+            [&](const Groups &g, uint32_t total) {
+                SmallArgs p;
+                p.a = g;
+                p.s = sp;
+                p.steps = a.steps;
+                for (int i = 0; i < 3 * a.steps; i++) p.coefficients[i] = a.coefficients[i];
+                small_steps_kernel<<<dim3(total), dim3(256), 0, s>>>(p);
+            });
+    if (st == TIDE_OK)
+        st = over_groups(
+            small,
+            [](const OrthoGroup &g) {
+                return (std::max(g.nr, g.nc) + kOrthoSmallCols - 1) / kOrthoSmallCols;
+            },
+            [&](const Groups &g, uint32_t total) {
+                small_apply_kernel<<<dim3(total), dim3(256), 0, s>>>(g, sp);
+            });
+    for (int i = 0; i < a.steps && st == TIDE_OK && !groups.empty(); i++) {
         ProductArgs p;
         p.s = sp;
         p.ca = a.coefficients[3 * i];
@@ -870,8 +1063,8 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         p.last = i == a.steps - 1;
         p.short_g = in_type(a.flags) != kElemF32;
         st = run_product<kGram>(by_length, p, s);
-        if (st == TIDE_OK) st = run_product<kPoly>(plan.groups, p, s);
-        if (st == TIDE_OK) st = run_product<kApply>(plan.groups, p, s);
+        if (st == TIDE_OK) st = run_product<kPoly>(groups, p, s);
+        if (st == TIDE_OK) st = run_product<kApply>(groups, p, s);
     }
     if (st == TIDE_OK) clear_error();
     return st;

@@ -52,7 +52,8 @@ tide_status ortho_plan(const char *name, int32_t n, const int64_t *rows, const i
                 g.nrp = static_cast<uint32_t>(up(nr, 64));
                 g.ncp = static_cast<uint32_t>(up(nc, 64));
                 g.first = static_cast<uint32_t>(i);
-                const int64_t pieces = up(static_cast<int64_t>(nr) * nc, kOrthoPiece) / kOrthoPiece;
+                const int64_t pieces = g.small() ? up(std::max(nr, nc), kOrthoSmallCols) / kOrthoSmallCols
+                                                 : up(static_cast<int64_t>(nr) * nc, kOrthoPiece) / kOrthoPiece;
                 g.parts = static_cast<uint32_t>(std::min<int64_t>(pieces, kOrthoParts));
                 g.base = plan->bytes;
                 g.stride = up(g.bytes(), 256);

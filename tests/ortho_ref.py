@@ -37,6 +37,8 @@ def emulated(g, steps=5, coefficients=QUINTIC, both=256):
     if x.shape[0] > x.shape[1]:
         return emulated(x.t().contiguous(), steps, coefficients, both).t().contiguous()
     r, c = x.shape
+    if r <= 32:
+        return exact(g, steps, coefficients)
     norm = float(torch.sqrt((x * x).sum()))
     if norm == 0:
         return torch.zeros_like(x)

@@ -49,6 +49,77 @@ def test_is_the_definition(shape, dtype):
         assert bool((buf[:32] == 7.0).all()) and bool((buf[-32:] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 2), (2, 1), (2, 2), (2, 3), (3, 2), (29, 2), (3, 259), (4, 4),
+                                   (5, 1000), (7, 255), (256, 8), (257, 9), (16, 16), (17, 513), (31, 70),
+                                   (32, 32), (32, 4000), (100000, 3), (1, 70000), (70000, 32)])
+def test_few_rows_are_exact(shape, dtype):
+    """Up to 32 rows the steps run in fp64, and G enters as it is: what is left is the
+    result's half step of bf16, 2^-8 of each entry, and fp32's on the way, 2^-24; 2^-20 of
+    the largest entry covers fp64's through 5 steps that raise it by up to 500."""
+    note(f"ortho few rows {shape} {dtype}")
+    for seed in range(6 if shape[0] * shape[1] < 5000 else 2):
+        for kind in ("full", "heavy", "low"):
+            g = ref.gradient(*shape, seed, kind, dtype, "cuda")
+            n = g.numel()
+            buf = torch.full((n + 64,), 7.0, dtype=BF, device="cuda")
+            out = buf[32:32 + n].view(shape)
+            tide.ortho(g, out=out)
+            want = ref.exact(g)
+            room = 2.0 ** -8 * want.abs() + 2.0 ** -20 * want.abs().max()
+            assert bool(((out.double() - want).abs() <= room).all()), (seed, kind)
+            assert bool((buf[:32] == 7.0).all()) and bool((buf[-32:] == 7.0).all())
+
+
+@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e30, 3e38])
+def test_few_rows_of_any_size_of_numbers(scale):
+    note(f"ortho few rows scale {scale}")
+    for shape in ((7, 300), (300, 7)):
+        g = ref.gradient(*shape, 2, "full", FP, "cuda")
+        g = ((g / g.abs().max()).double() * scale).float()
+        check(g, tide.ortho(g), (shape, scale))
+
+
+def test_few_rows_beside_many():
+    """Small matrices in a list with large ones: each as alone, zeros, NaNs and
+    infinities in their own matrix only, outs that are other matrices' srcs, other
+    steps, captured and replayed."""
+    note("ortho few rows beside many")
+    shapes = [(3, 400), (70, 200), (3, 400), (400, 3), (400, 3), (33, 40), (32, 40), (1, 1)]
+    gs = [ref.gradient(*s, i, "heavy", BF, "cuda") for i, s in enumerate(shapes)]
+    alone = [tide.ortho(g) for g in gs]
+    assert all(torch.equal(a, b) for a, b in zip(tide.ortho(gs), alone))
+    x = [g.clone() for g in gs]
+    tide.ortho(x, out=[x[2], x[1], x[0], x[4], x[3], *x[5:]])
+    got = [x[2], x[1], x[0], x[4], x[3], *x[5:]]
+    assert all(torch.equal(a, b) for a, b in zip(got, alone))
+    bad = [g.clone() for g in gs]
+    bad[0].zero_()
+    bad[2][1, 7], bad[3][399, 2] = float("nan"), float("inf")
+    outs = tide.ortho(bad)
+    assert not bool(outs[0].any())
+    assert bool(torch.isnan(outs[2]).all()) and bool(torch.isnan(outs[3]).all())
+    for i in (1, 4, 5, 6, 7):
+        assert torch.equal(outs[i], alone[i])
+    for co, steps in (((1.5, -0.5, 0.0), 64), ((3.4445, -4.775, 2.0315), 1),
+                      ([(3.0, -3.0, 1.0), (2.0, -1.5, 0.5)], 2)):
+        for g in gs[:1] + gs[3:4]:
+            check(g, tide.ortho(g, steps=steps, coefficients=co), steps, co, steps)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=side):
+        held = tide.ortho(gs)
+    for it in range(3):
+        for i, g in enumerate(gs):
+            g.copy_(ref.gradient(*shapes[i], 20 + 8 * it + i, "full", BF, "cuda"))
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, tide.ortho(gs)))
+
+
 @pytest.mark.parametrize("shape", [(2050, 4100), (4100, 2050), (3000, 3100)])
 def test_large_tiles(shape):
     note(f"ortho large {shape}")
