@@ -11,7 +11,7 @@ namespace tide {
 // P X takes X's lo as well up to this many rows (the smaller side), and up to
 // kOrthoSmall the steps run on X X^T alone, in 64 bits: see ortho.hip.
 constexpr uint32_t kOrthoBoth = 256, kOrthoSmall = 32;
-constexpr int64_t kOrthoSmallCols = 256;       // columns of a small matrix in LDS
+constexpr int64_t kOrthoSmallCols = 128;       // columns of a small matrix in LDS
 
 // Equal matrices [nr, nc] of one call, as the kernels see them.  r is the smaller
 // side; the padded sizes are multiples of 64, zeros in between.

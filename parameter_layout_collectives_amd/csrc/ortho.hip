@@ -187,8 +187,8 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
 // ------------------------------------------------------- few rows
 //
 // Latency bounds these: three launches for all steps, where the products take three a
-// step.  A chunk of 256 columns is in LDS as [r][256]; G is read once, as an out may be
-// another matrix's src.
+// step.  A chunk of kOrthoSmallCols columns is in LDS, a row after the other; G is read
+// once, as an out may be another matrix's src.
 constexpr int kSmallPitch = kOrthoSmallCols + 1;
 
 template <int ET>
@@ -198,14 +198,29 @@ __device__ __forceinline__ float load1(const char *p, int64_t i) {
     return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
 }
 
-// Calls each(offset in the matrix, row, column of the chunk) for this thread's elements
-// of columns [c0, c0 + n), in the order of memory.
-template <class Each>
-__device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int n, Each each) {
-    const int r = g.r();
-    for (int e = threadIdx.x; e < r * n; e += 256) {
-        const int i = g.tall() ? e % r : e / n, col = g.tall() ? e / r : e % n;
-        each(g.tall() ? c0 * r + e : static_cast<int64_t>(i) * g.nc + c0 + col, i, col);
+// Columns [c0, c0 + n) of a small matrix, its elements in the order of memory: load(offset
+// in the matrix) of eight a thread, then store(offset, place in the chunk, value) of them.
+template <class Load, class Store>
+__device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int n, Load load, Store store) {
+    const int r = g.r(), all = r * n, d = g.tall() ? r : n;
+    const float inverse = 1.0f / d;
+    auto row_of = [&](int e) {                             // e / d: e < 2^13, d <= 2^8
+        return static_cast<int>((e + 0.5f) * inverse);
+    };
+    for (int e0 = threadIdx.x; e0 < all; e0 += 2048) {
+        float v[8];
+        int64_t off[8];
+        int at[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            const int e = min(e0 + u * 256, all - 1), q = row_of(e), rest = e - q * d;
+            off[u] = g.tall() ? c0 * r + e : static_cast<int64_t>(q) * g.nc + c0 + rest;
+            at[u] = g.tall() ? rest * kSmallPitch + q : q * kSmallPitch + rest;
+            v[u] = load(off[u], at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+            if (e0 + u * 256 < all) store(off[u], at[u], v[u]);
     }
 }
 
@@ -232,13 +247,15 @@ __global__ __launch_bounds__(256) void small_gram_kernel(Groups a, Space s) {
     for (int64_t at = c0; at < c1; at += kOrthoSmallCols) {
         const int n = static_cast<int>(min(kOrthoSmallCols, c1 - at));
         __syncthreads();
-        over_chunk(g, at, n, [&](int64_t off, int i, int col) {
-            const float v = load1<ET>(src, off);
-            reinterpret_cast<float *>(base)[off] = v;
-            x[i * kSmallPitch + col] = v;
-        });
+        over_chunk(
+            g, at, n, [&](int64_t off, int) { return load1<ET>(src, off); },
+            [&](int64_t off, int place, float v) {
+                reinterpret_cast<float *>(base)[off] = v;
+                x[place] = v;
+            });
         __syncthreads();
         if (pi < r && pj < r)
+#pragma unroll 4
             for (int col = t / per_set; col < n; col += sets) {
                 const double i0 = x[pi * kSmallPitch + col], i1 = x[pi1 * kSmallPitch + col];
                 const double j0 = x[pj * kSmallPitch + col], j1 = x[pj1 * kSmallPitch + col];
@@ -271,78 +288,128 @@ struct SmallArgs {
 
 // All steps on A, one workgroup a matrix; what G 2^-k is multiplied by, and k.
 __global__ __launch_bounds__(256) void small_steps_kernel(SmallArgs p) {
-    constexpr int R = kOrthoSmall;
-    __shared__ double A[R * R], P[R * R], M[R * R], T[R * R], U[R * R];
+    constexpr int R = kOrthoSmall, W = R + 2;              // zeros past r
+    __shared__ __attribute__((aligned(16))) double A[R * W], P[R * W], M[R * W], T[R * W], U[R * W];
     const OrthoGroup g = group_of(p.a, blockIdx.x);
     char *const base = p.s.base + g.base + (blockIdx.x - g.wg0) * g.stride;
     const double *const gram = reinterpret_cast<const double *>(base + g.gram_at());
     const int r = g.r(), n = r * r, t = threadIdx.x;
-    for (int e = t; e < n; e += 256) {
-        double v = 0;
-        for (uint32_t q = 0; q < g.parts; q++) v += gram[static_cast<int64_t>(q) * n + e];
-        A[e] = v;
-        M[e] = e / r == e % r;
+    // a thread's 2 x 2 block of every matrix
+    const int bi = t / 16 * 2, bj = t % 16 * 2;
+    int at[4], from[4];
+    double v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int i = bi + u / 2, j = bj + u % 2;
+        at[u] = i * W + j;
+        from[u] = min(i, r - 1) * r + min(j, r - 1);
+    }
+#pragma unroll 4
+    for (uint32_t q = 0; q < g.parts; q++)
+#pragma unroll
+        for (int u = 0; u < 4; u++) v[u] += gram[static_cast<int64_t>(q) * n + from[u]];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int i = bi + u / 2, j = bj + u % 2;
+        A[at[u]] = i < r && j < r ? v[u] : 0.0;
+        M[at[u]] = i == j && i < r;
     }
     __syncthreads();
     double sum = 0;
-    for (int i = 0; i < r; i++) sum += A[i * r + i];
+    for (int i = 0; i < r; i++) sum += A[i * W + i];
     __syncthreads();
     const double norm = sqrt(sum);
     const bool finite = norm < __builtin_inf();
-    for (int e = t; e < n; e += 256) A[e] = norm > 0 ? A[e] / sum : 0.0;
+#pragma unroll
+    for (int u = 0; u < 4; u++) A[at[u]] = norm > 0 ? A[at[u]] / sum : 0.0;
     int k = 0;
     const double frac = finite && norm > 0 ? frexp(norm, &k) : 1.0;
     __syncthreads();
     auto times = [&](double *out, const double *x, const double *y) {
-        for (int e = t; e < n; e += 256) {
-            double v = 0;
-            for (int j = 0; j < r; j++) v += x[e / r * r + j] * y[j * r + e % r];
-            out[e] = v;
+        double o[4] = {0, 0, 0, 0};
+#pragma unroll 8
+        for (int j = 0; j < r; j++) {
+            const double a = x[bi * W + j], b = x[bi * W + W + j], c = y[j * W + bj], d = y[j * W + bj + 1];
+            o[0] += a * c;
+            o[1] += a * d;
+            o[2] += b * c;
+            o[3] += b * d;
         }
+#pragma unroll
+        for (int u = 0; u < 4; u++) out[at[u]] = o[u];
     };
     for (int q = 0; q < p.steps; q++) {
         const double ca = p.coefficients[3 * q], cb = p.coefficients[3 * q + 1], cc = p.coefficients[3 * q + 2];
         times(T, A, A);
         __syncthreads();
-        for (int e = t; e < n; e += 256) P[e] = (e / r == e % r ? ca : 0.0) + cb * A[e] + cc * T[e];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int i = bi + u / 2, j = bj + u % 2;
+            P[at[u]] = (i == j && i < r ? ca : 0.0) + cb * A[at[u]] + cc * T[at[u]];
+        }
         __syncthreads();
         times(T, P, M);
         times(U, P, A);
         __syncthreads();
-        for (int e = t; e < n; e += 256) M[e] = T[e];
+#pragma unroll
+        for (int u = 0; u < 4; u++) M[at[u]] = T[at[u]];
         times(A, U, P);
         __syncthreads();
     }
     double *const map = reinterpret_cast<double *>(base + g.map_at());
-    for (int e = t; e < n; e += 256)
-        map[e] = !finite ? __builtin_nan("") : norm > 0 ? M[e] / frac : 0.0;
+    for (int e = t; e < n; e += 256) {
+        const double o = M[e / r * W + e % r];
+        map[e] = !finite ? __builtin_nan("") : norm > 0 ? o / frac : 0.0;
+    }
     if (t == 0) map[n] = k;
 }
 
-// out = M (G 2^-k), 256 columns a workgroup.
+// out = M (G 2^-k), a chunk a workgroup.
 __global__ __launch_bounds__(256) void small_apply_kernel(Groups a, Space s) {
-    __shared__ float x[kOrthoSmall * kSmallPitch];
-    __shared__ double M[kOrthoSmall * kOrthoSmall];
+    constexpr int R = kOrthoSmall;
+    __shared__ float x[R * kSmallPitch];
+    __shared__ __attribute__((aligned(16))) double M[R * R];
     const OrthoGroup g = group_of(a, blockIdx.x);
     const int64_t c = g.tall() ? g.nr : g.nc;
     const uint32_t per = static_cast<uint32_t>((c + kOrthoSmallCols - 1) / kOrthoSmallCols);
     const uint32_t in = blockIdx.x - g.wg0, m = in / per;
     const char *const base = s.base + g.base + m * g.stride;
     const double *const map = reinterpret_cast<const double *>(base + g.map_at());
-    const int r = g.r(), k = -static_cast<int>(map[r * r]);
+    const int r = g.r(), k = -static_cast<int>(map[r * r]), t = threadIdx.x;
     const int64_t c0 = static_cast<int64_t>(in % per) * kOrthoSmallCols;
     const int n = static_cast<int>(min(kOrthoSmallCols, c - c0));
-    for (int e = threadIdx.x; e < r * r; e += 256) M[e] = map[e];
-    over_chunk(g, c0, n, [&](int64_t off, int i, int col) {
-        x[i * kSmallPitch + col] = ldexpf(reinterpret_cast<const float *>(base)[off], k);
-    });
+    for (int e = t; e < R * R; e += 256) M[e] = e / R < r && e % R < r ? map[e / R * r + e % R] : 0.0;
+    for (int e = t; e < (R - r) * kSmallPitch; e += 256) x[r * kSmallPitch + e] = 0.0f;
+    over_chunk(
+        g, c0, n, [&](int64_t off, int) { return ldexpf(reinterpret_cast<const float *>(base)[off], k); },
+        [&](int64_t, int place, float v) { x[place] = v; });
+    __syncthreads();
+    // a column's rows by 2 threads
+    constexpr int COLS = static_cast<int>(kOrthoSmallCols), SHARE = 256 / COLS;
+    const int col = t % COLS;
+    float v[R];
+#pragma unroll
+    for (int j = 0; j < R; j++) v[j] = x[j * kSmallPitch + col];
+    __syncthreads();
+    if (col < n)
+        for (int i = t / COLS; i < r; i += SHARE) {
+            double even = 0, odd = 0;
+#pragma unroll
+            for (int j8 = 0; j8 < R; j8 += 8) {
+                if (j8 >= r) break;
+#pragma unroll
+                for (int j = j8; j < j8 + 8; j += 2) {
+                    even += M[i * R + j] * v[j];
+                    odd += M[i * R + j + 1] * v[j + 1];
+                }
+            }
+            x[i * kSmallPitch + col] = static_cast<float>(even + odd);
+        }
     __syncthreads();
     __bf16 *const out = reinterpret_cast<__bf16 *>(s.pointers[g.first + m].out);
-    over_chunk(g, c0, n, [&](int64_t off, int i, int col) {
-        double v = 0;
-        for (int j = 0; j < r; j++) v += M[i * r + j] * x[j * kSmallPitch + col];
-        out[off] = static_cast<__bf16>(static_cast<float>(v));
-    });
+    over_chunk(
+        g, c0, n, [&](int64_t, int place) { return x[place]; },
+        [&](int64_t off, int, float v) { out[off] = static_cast<__bf16>(v); });
 }
 
 // ------------------------------------------------------- the products
