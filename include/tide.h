@@ -542,9 +542,11 @@ int64_t tide_mx_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t 
  * fp32 diagonal and a rest in fp16, and the products' factors are fp16 numbers.
  * Against 64 bits X is off by 3e-4 to 1e-3 of its norm, 1.6e-3 for matrices of a low
  * rank, where its rounding to bf16 is 1.7e-3.  With a smaller side of up to 32 the
- * steps run in fp64 throughout and only that rounding is left.  fp16's range asks for singular values
- * of every step's X up to 3.9 and |b x^2 + c x^4| there up to 63; beyond that the
- * result holds infinities or NaNs.
+ * steps run in fp64 throughout and only that rounding is left, and in many steps fp64's
+ * own, which every step raises by up to a where X has nothing else: 2^-52 a^steps.
+ * For larger matrices fp16's range asks for singular values of every step's X up to
+ * 3.9 and |b x^2 + c x^4| there up to 63; beyond that the result holds infinities or
+ * NaNs.
  *
  *   src, out      host arrays of n device pointers, element-aligned (NULL allowed
  *                 for a matrix without elements).  An out may be its or another

@@ -9,9 +9,11 @@
 namespace tide {
 
 // P X takes X's lo as well up to this many rows (the smaller side), and up to
-// kOrthoSmall the steps run on X X^T alone, in 64 bits: see ortho.hip.
+// kOrthoSmall the steps run on X X^T alone, in 64 bits, until they have raised what is
+// near zero by kOrthoRaised: see ortho.hip.
 constexpr uint32_t kOrthoBoth = 256, kOrthoSmall = 32;
 constexpr int64_t kOrthoSmallCols = 128;       // columns of a small matrix in LDS
+constexpr double kOrthoRaised = 32768.0;
 
 // Equal matrices [nr, nc] of one call, as the kernels see them.  r is the smaller
 // side; the padded sizes are multiples of 64, zeros in between.
@@ -41,10 +43,11 @@ struct OrthoGroup {
     }
     __host__ __device__ int64_t a_diag() const { return p_at() + 2 * static_cast<int64_t>(rp()) * rp(); }
     __host__ __device__ int64_t p_diag() const { return a_diag() + 4 * rp(); }
-    // A small matrix: G in fp32, `parts` sums of G G^T, and the matrix that G is
-    // multiplied by, followed by the exponent of 2 that G is divided by (fp64).
+    // A small matrix: G in fp32, a later X in fp64, `parts` sums of X X^T, and the matrix
+    // that X is multiplied by, followed by the exponent of 2 that it is divided by (fp64).
     __host__ __device__ bool small() const { return r() <= kOrthoSmall; }
-    __host__ __device__ int64_t gram_at() const { return (4 * static_cast<int64_t>(nr) * nc + 15) / 16 * 16; }
+    __host__ __device__ int64_t later_at() const { return (4 * static_cast<int64_t>(nr) * nc + 15) / 16 * 16; }
+    __host__ __device__ int64_t gram_at() const { return later_at() + 8 * static_cast<int64_t>(nr) * nc; }
     __host__ __device__ int64_t map_at() const { return gram_at() + 8 * static_cast<int64_t>(parts) * r() * r(); }
     __host__ __device__ int64_t bytes() const {
         return small() ? map_at() + 8 * (static_cast<int64_t>(r()) * r() + 1) : p_diag() + 4 * rp();

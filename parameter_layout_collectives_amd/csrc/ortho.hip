@@ -26,6 +26,11 @@
 // Few rows average none of these roundings out (2 x 2: up to 8e-3), and cost next to
 // nothing: up to kOrthoSmall of them the steps run in fp64 on A alone, since P and A
 // commute: A <- P A P and M <- P M from M = I, and the result is M X, one pass over G.
+// A's rounding, 1e-16 of its norm, makes eigenvalues at zero negative, which X X^T never
+// is, and P A P raises them by a^2 a step until the polynomial, unbounded below zero, runs
+// away with them (16 x 64 of rank 4: 1.4e-3 off at 14 steps, NaN at 30).  So before steps
+// have raised them by kOrthoRaised^2 = 2^30, that is to 1e-7, where P is still a to 1e-6, X
+// <- M X is formed in fp64 and A from it anew: 8 of the usual steps.
 // Powers of two keep the numbers in fp16's range: X by 2^ex, about sqrt(r c), O by
 // 2^12, R by 2^10.
 //
@@ -39,6 +44,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "block.h"
@@ -187,12 +193,17 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
 // ------------------------------------------------------- few rows
 //
 // Latency bounds these: three launches for all steps, where the products take three a
-// step.  A chunk of kOrthoSmallCols columns is in LDS, a row after the other; G is read
-// once, as an out may be another matrix's src.
+// step (after every 8 of them three more).  A chunk of kOrthoSmallCols columns is in LDS,
+// a row after the other; G is read once, as an out may be another matrix's src.
 constexpr int kSmallPitch = kOrthoSmallCols + 1;
+constexpr int kLater = -1;       // in place of an element type: X in the workspace, fp64
 
 template <int ET>
-__device__ __forceinline__ float load1(const char *p, int64_t i) {
+using small_t = std::conditional_t<ET == kLater, double, float>;
+
+template <int ET>
+__device__ __forceinline__ small_t<ET> load1(const char *p, int64_t i) {
+    if constexpr (ET == kLater) return reinterpret_cast<const double *>(p)[i];
     if (ET == kElemF32) return reinterpret_cast<const float *>(p)[i];
     if (ET == kElemF16) return static_cast<float>(reinterpret_cast<const _Float16 *>(p)[i]);
     return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
@@ -200,7 +211,7 @@ __device__ __forceinline__ float load1(const char *p, int64_t i) {
 
 // Columns [c0, c0 + n) of a small matrix, its elements in the order of memory: load(offset
 // in the matrix) of eight a thread, then store(offset, place in the chunk, value) of them.
-template <class Load, class Store>
+template <class T, class Load, class Store>
 __device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int n, Load load, Store store) {
     const int r = g.r(), all = r * n, d = g.tall() ? r : n;
     const float inverse = 1.0f / d;
@@ -208,7 +219,7 @@ __device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int 
         return static_cast<int>((e + 0.5f) * inverse);
     };
     for (int e0 = threadIdx.x; e0 < all; e0 += 2048) {
-        float v[8];
+        T v[8];
         int64_t off[8];
         int at[8];
 #pragma unroll
@@ -224,16 +235,18 @@ __device__ __forceinline__ void over_chunk(const OrthoGroup &g, int64_t c0, int 
     }
 }
 
-// G G^T of a piece of the columns: a thread sums a 2 x 2 block (r = 1: 1 x 1) over some
-// of them.
+// X X^T (at first of X = G) of a piece of the columns: a thread sums a 2 x 2 block (r = 1:
+// 1 x 1) over some of them.
 template <int ET>
 __global__ __launch_bounds__(256) void small_gram_kernel(Groups a, Space s) {
-    __shared__ float x[kOrthoSmall * kSmallPitch];
+    typedef small_t<ET> T;
+    __shared__ T x[kOrthoSmall * kSmallPitch];
     __shared__ double part[256][4];
     const OrthoGroup g = group_of(a, blockIdx.x);
     const uint32_t in = blockIdx.x - g.wg0, m = in / g.parts, q = in % g.parts;
-    const char *const src = reinterpret_cast<const char *>(s.pointers[g.first + m].src);
     char *const base = s.base + g.base + m * g.stride;
+    const char *const src = ET == kLater ? base + g.later_at()
+                                         : reinterpret_cast<const char *>(s.pointers[g.first + m].src);
     const int r = g.r(), t = threadIdx.x;
     const int64_t c = g.tall() ? g.nr : g.nc;
     const int64_t chunks = (c + kOrthoSmallCols - 1) / kOrthoSmallCols, per = (chunks + g.parts - 1) / g.parts;
@@ -247,10 +260,10 @@ __global__ __launch_bounds__(256) void small_gram_kernel(Groups a, Space s) {
     for (int64_t at = c0; at < c1; at += kOrthoSmallCols) {
         const int n = static_cast<int>(min(kOrthoSmallCols, c1 - at));
         __syncthreads();
-        over_chunk(
+        over_chunk<T>(
             g, at, n, [&](int64_t off, int) { return load1<ET>(src, off); },
-            [&](int64_t off, int place, float v) {
-                reinterpret_cast<float *>(base)[off] = v;
+            [&](int64_t off, int place, T v) {
+                if constexpr (ET != kLater) reinterpret_cast<float *>(base)[off] = v;
                 x[place] = v;
             });
         __syncthreads();
@@ -284,9 +297,11 @@ struct SmallArgs {
     Space s;
     float coefficients[192];
     int steps;
+    int later;                   // not the first steps
 };
 
-// All steps on A, one workgroup a matrix; what G 2^-k is multiplied by, and k.
+// The steps on A, one workgroup a matrix; what X 2^-k is multiplied by, and k.  At first
+// X = G, whose norm is divided by; later k = 0.
 __global__ __launch_bounds__(256) void small_steps_kernel(SmallArgs p) {
     constexpr int R = kOrthoSmall, W = R + 2;              // zeros past r
     __shared__ __attribute__((aligned(16))) double A[R * W], P[R * W], M[R * W], T[R * W], U[R * W];
@@ -318,12 +333,13 @@ __global__ __launch_bounds__(256) void small_steps_kernel(SmallArgs p) {
     double sum = 0;
     for (int i = 0; i < r; i++) sum += A[i * W + i];
     __syncthreads();
-    const double norm = sqrt(sum);
+    const double norm = p.later ? 1.0 : sqrt(sum);
     const bool finite = norm < __builtin_inf();
+    if (!p.later)
 #pragma unroll
-    for (int u = 0; u < 4; u++) A[at[u]] = norm > 0 ? A[at[u]] / sum : 0.0;
+        for (int u = 0; u < 4; u++) A[at[u]] = norm > 0 ? A[at[u]] / sum : 0.0;
     int k = 0;
-    const double frac = finite && norm > 0 ? frexp(norm, &k) : 1.0;
+    const double frac = !p.later && finite && norm > 0 ? frexp(norm, &k) : 1.0;
     __syncthreads();
     auto times = [&](double *out, const double *x, const double *y) {
         double o[4] = {0, 0, 0, 0};
@@ -364,30 +380,38 @@ __global__ __launch_bounds__(256) void small_steps_kernel(SmallArgs p) {
     if (t == 0) map[n] = k;
 }
 
-// out = M (G 2^-k), a chunk a workgroup.
+// M (X 2^-k), a chunk a workgroup: X = G or (FROM) a later one; to out or (TO) to the later
+// X, in its place.
+template <bool FROM, bool TO>
 __global__ __launch_bounds__(256) void small_apply_kernel(Groups a, Space s) {
     constexpr int R = kOrthoSmall;
-    __shared__ float x[R * kSmallPitch];
+    typedef std::conditional_t<FROM || TO, double, float> T;
+    __shared__ T x[R * kSmallPitch];
     __shared__ __attribute__((aligned(16))) double M[R * R];
     const OrthoGroup g = group_of(a, blockIdx.x);
     const int64_t c = g.tall() ? g.nr : g.nc;
     const uint32_t per = static_cast<uint32_t>((c + kOrthoSmallCols - 1) / kOrthoSmallCols);
     const uint32_t in = blockIdx.x - g.wg0, m = in / per;
-    const char *const base = s.base + g.base + m * g.stride;
+    char *const base = s.base + g.base + m * g.stride;
+    double *const later = reinterpret_cast<double *>(base + g.later_at());
     const double *const map = reinterpret_cast<const double *>(base + g.map_at());
     const int r = g.r(), k = -static_cast<int>(map[r * r]), t = threadIdx.x;
     const int64_t c0 = static_cast<int64_t>(in % per) * kOrthoSmallCols;
     const int n = static_cast<int>(min(kOrthoSmallCols, c - c0));
     for (int e = t; e < R * R; e += 256) M[e] = e / R < r && e % R < r ? map[e / R * r + e % R] : 0.0;
-    for (int e = t; e < (R - r) * kSmallPitch; e += 256) x[r * kSmallPitch + e] = 0.0f;
-    over_chunk(
-        g, c0, n, [&](int64_t off, int) { return ldexpf(reinterpret_cast<const float *>(base)[off], k); },
-        [&](int64_t, int place, float v) { x[place] = v; });
+    for (int e = t; e < (R - r) * kSmallPitch; e += 256) x[r * kSmallPitch + e] = 0;
+    over_chunk<T>(
+        g, c0, n,
+        [&](int64_t off, int) -> T {
+            if constexpr (FROM) return later[off];
+            return ldexpf(reinterpret_cast<const float *>(base)[off], k);
+        },
+        [&](int64_t, int place, T v) { x[place] = v; });
     __syncthreads();
     // a column's rows by 2 threads
     constexpr int COLS = static_cast<int>(kOrthoSmallCols), SHARE = 256 / COLS;
     const int col = t % COLS;
-    float v[R];
+    T v[R];
 #pragma unroll
     for (int j = 0; j < R; j++) v[j] = x[j * kSmallPitch + col];
     __syncthreads();
@@ -403,13 +427,18 @@ __global__ __launch_bounds__(256) void small_apply_kernel(Groups a, Space s) {
                     odd += M[i * R + j + 1] * v[j + 1];
                 }
             }
-            x[i * kSmallPitch + col] = static_cast<float>(even + odd);
+            x[i * kSmallPitch + col] = static_cast<T>(even + odd);
         }
     __syncthreads();
     __bf16 *const out = reinterpret_cast<__bf16 *>(s.pointers[g.first + m].out);
-    over_chunk(
+    over_chunk<T>(
         g, c0, n, [&](int64_t, int place) { return x[place]; },
-        [&](int64_t off, int, float v) { out[off] = static_cast<__bf16>(v); });
+        [&](int64_t off, int, T v) {
+            if constexpr (TO)
+                later[off] = v;
+            else
+                out[off] = static_cast<__bf16>(static_cast<float>(v));
+        });
 }
 
 // ------------------------------------------------------- the products
@@ -1061,6 +1090,55 @@ tide_status run_first(const std::vector<OrthoGroup> &groups, const std::vector<O
         });
 }
 
+// The steps of small matrices whose G G^T is known.
+tide_status run_small(const std::vector<OrthoGroup> &small, const OrthoArgs &a, const Space &sp,
+                      hipStream_t s) {
+    SmallArgs p;
+    p.s = sp;
+    for (int from = 0, to = 0; from < a.steps; from = to) {
+        // as many steps as raise by less than kOrthoRaised, one at least
+        auto raises = [&](int i) { return std::max(1.0, std::fabs(static_cast<double>(a.coefficients[3 * i]))); };
+        double raised = raises(to++);
+        for (; to < a.steps && raised * raises(to) <= kOrthoRaised; to++) raised *= raises(to);
+        p.later = from > 0;
+        p.steps = to - from;
+        std::copy(a.coefficients + 3 * from, a.coefficients + 3 * to, p.coefficients);
+        tide_status st = TIDE_OK;
+        if (p.later)
+            st = over_groups(
+                small, [](const OrthoGroup &g) { return g.parts; },
+                [&](const Groups &g, uint32_t total) {
+                    small_gram_kernel<kLater><<<dim3(total), dim3(256), 0, s>>>(g, sp);
+                });
+        if (st == TIDE_OK)
+            st = over_groups(
+                small, [](const OrthoGroup &) { return 1; },
+                [&](const Groups &g, uint32_t total) {
+                    p.a = g;
+                    small_steps_kernel<<<dim3(total), dim3(256), 0, s>>>(p);
+                });
+        if (st == TIDE_OK)
+            st = over_groups(
+                small,
+                [](const OrthoGroup &g) {
+                    return (std::max(g.nr, g.nc) + kOrthoSmallCols - 1) / kOrthoSmallCols;
+                },
+                [&](const Groups &g, uint32_t total) {
+                    const dim3 n(total), b(256);
+                    if (from == 0 && to == a.steps)
+                        small_apply_kernel<false, false><<<n, b, 0, s>>>(g, sp);
+                    else if (from == 0)
+                        small_apply_kernel<false, true><<<n, b, 0, s>>>(g, sp);
+                    else if (to < a.steps)
+                        small_apply_kernel<true, true><<<n, b, 0, s>>>(g, sp);
+                    else
+                        small_apply_kernel<true, false><<<n, b, 0, s>>>(g, sp);
+                });
+        if (st != TIDE_OK) return st;
+    }
+    return TIDE_OK;
+}
+
 tide_status run_ortho(const OrthoArgs &a, void *stream) {
     OrthoPlan plan;
     tide_status st = check_ortho(a, &plan);
@@ -1099,26 +1177,7 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
         case kElemF16: st = run_first<kElemF16>(groups, small, sp, s); break;
         case kElemF32: st = run_first<kElemF32>(groups, small, sp, s); break;
     }
-    if (st == TIDE_OK)
-        st = over_groups(
-            small, [](const OrthoGroup &) { return 1; },
-            [&](const Groups &g, uint32_t total) {
-                SmallArgs p;
-                p.a = g;
-                p.s = sp;
-                p.steps = a.steps;
-                for (int i = 0; i < 3 * a.steps; i++) p.coefficients[i] = a.coefficients[i];
-                small_steps_kernel<<<dim3(total), dim3(256), 0, s>>>(p);
-            });
-    if (st == TIDE_OK)
-        st = over_groups(
-            small,
-            [](const OrthoGroup &g) {
-                return (std::max(g.nr, g.nc) + kOrthoSmallCols - 1) / kOrthoSmallCols;
-            },
-            [&](const Groups &g, uint32_t total) {
-                small_apply_kernel<<<dim3(total), dim3(256), 0, s>>>(g, sp);
-            });
+    if (st == TIDE_OK && !small.empty()) st = run_small(small, a, sp, s);
     for (int i = 0; i < a.steps && st == TIDE_OK && !groups.empty(); i++) {
         ProductArgs p;
         p.s = sp;
