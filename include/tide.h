@@ -537,16 +537,20 @@ int64_t tide_mx_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t 
  * matrix with orthonormal rows (or columns, if it has more rows), roughly.  A zero
  * matrix gives zeros, one that holds an infinity or a NaN gives NaNs.
  *
- * Exactness.  ||G||_F is summed in fp64, products in fp32.  Between products X is
- * held in pairs of fp16 numbers (22 bits), X X^T and the polynomial's matrix as an
- * fp32 diagonal and a rest in fp16, and the products' factors are fp16 numbers.
- * Against 64 bits X is off by 3e-4 to 1e-3 of its norm, 1.6e-3 for matrices of a low
- * rank, where its rounding to bf16 is 1.7e-3.  With a smaller side of up to 32 the
- * steps run in fp64 throughout and only that rounding is left, and in many steps fp64's
- * own, which every step raises by up to a where X has nothing else: 2^-52 a^steps.
- * For larger matrices fp16's range asks for singular values of every step's X up to
- * 3.9 and |b x^2 + c x^4| there up to 63; beyond that the result holds infinities or
- * NaNs.
+ * Exactness.  ||G||_F is summed in fp64, products in fp32.
+ *   A smaller side of up to 32: the steps run in fp64 throughout, and X's rounding to
+ * bf16 is left (1.7e-3 of its norm).  Where X has nothing but fp64's own rounding, 2^-52,
+ * every step raises that by up to a.
+ *   Larger matrices: between products X is held in pairs of fp16 numbers (22 bits), X X^T
+ * and the polynomial's matrix as an fp32 diagonal and a rest in fp16, and the products'
+ * factors are fp16 numbers.  Before the rounding to bf16 X is off by 3e-4 to 1e-3 of its
+ * norm in 5 such steps, up to 2e-3 for matrices of a low rank.  In more of them, or in
+ * steps whose |a| multiplied exceed 512, the product with X takes both of its numbers,
+ * half as long again, and X is off by 1e-3 to 2e-3.  Where X has nothing but its own
+ * rounding, 2^-23, every step raises that by up to a, as it does in fp32: a low rank is
+ * 2e-3 to 1e-2 off after 10 such steps and a full one after about 13.
+ * fp16's range asks for singular values of every step's X up to 3.9 and |b x^2 + c x^4|
+ * there up to 63; beyond that the result holds infinities or NaNs.
  *
  *   src, out      host arrays of n device pointers, element-aligned (NULL allowed
  *                 for a matrix without elements).  An out may be its or another

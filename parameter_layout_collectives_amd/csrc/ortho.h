@@ -8,10 +8,12 @@
 
 namespace tide {
 
-// P X takes X's lo as well up to this many rows (the smaller side), and up to
-// kOrthoSmall the steps run on X X^T alone, in 64 bits, until they have raised what is
-// near zero by kOrthoRaised: see ortho.hip.
+// P X takes X's lo as well up to this many rows (the smaller side), and for any where the
+// steps raise what is near zero by more than kOrthoRaisedHi; up to kOrthoSmall rows the
+// steps run on X X^T alone, in 64 bits, until they have raised it by kOrthoRaised: see
+// ortho.hip.
 constexpr uint32_t kOrthoBoth = 256, kOrthoSmall = 32;
+constexpr double kOrthoRaisedHi = 512.0;
 constexpr int64_t kOrthoSmallCols = 128;       // columns of a small matrix in LDS
 constexpr double kOrthoRaised = 32768.0;
 
@@ -34,7 +36,7 @@ struct OrthoGroup {
     // as a matrix hi and behind it lo.
     __host__ __device__ int64_t x_bytes() const { return 4 * static_cast<int64_t>(nrp) * ncp; }
     __host__ __device__ int64_t lo() const { return static_cast<int64_t>(nrp) * ncp; }
-    // Whether lo enters P X, too.
+    // Whether lo enters P X, too, by the rows alone.
     __host__ __device__ bool both() const { return r() <= kOrthoBoth; }
     // Then A = X X^T and P [rp, rp] without their diagonals, and these in fp32 [rp].
     __host__ __device__ int64_t a_at() const { return 2 * x_bytes(); }

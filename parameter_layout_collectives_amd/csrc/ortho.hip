@@ -22,7 +22,11 @@
 // it is rounded to bf16 (1.7e-3), by up to 1.6e-3 for matrices whose rank is an
 // eighth of r (an emulation in 64 bits).  With fewer rows R outweighs Q there (37 of
 // rank 4: 4e-3), so up to kOrthoBoth of them R X takes lo as well, as one sum of
-// twice the length.
+// twice the length.  What hi alone loses in directions where X has little is raised by a
+// in every later step: with 5 of the usual ones (3.4445^5 = 485) [300, 420] of rank 37 is
+// 1.5e-3 off, with 6 4e-3, with 8 5e-2; with lo 7e-4, 7e-4, 9e-4.  So above kOrthoRaisedHi
+// lo enters for any number of rows, in all steps (the first alone, or all but the last
+// five, would leave 4e-3 to 2e-2; [4096, 4096] 425 us a step for 270).
 // Few rows average none of these roundings out (2 x 2: up to 8e-3), and cost next to
 // nothing: up to kOrthoSmall of them the steps run in fp64 on A alone, since P and A
 // commute: A <- P A P and M <- P M from M = I, and the result is M X, one pass over G.
@@ -91,6 +95,7 @@ struct Space {
     const Pointers *pointers;
     double *sums;
     float2 *scales;
+    int lo;                      // X's lo enters P X whatever the rows
 };
 
 // ------------------------------------------------------- ||G||_F and X's first pair
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(256) void first_kernel(Groups a, Space s) {
     }
     _Float16 *X = reinterpret_cast<_Float16 *>(s.base + g.base + m * g.stride) + panel_at(g.nrp, row, col);
     *reinterpret_cast<f16x8 *>(X) = h;
-    if (ET == kElemF32 || g.both()) *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
+    if (ET == kElemF32 || g.both() || s.lo) *reinterpret_cast<f16x8 *>(X + g.lo()) = l;
 }
 
 // ------------------------------------------------------- few rows
@@ -760,9 +765,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     k.lane = lane;
     k.wi = k.wave / 2;
     k.wj = k.wave % 2;
-    // with both(), hi's sum goes on with lo, and P's from its start again
+    // with both, hi's sum goes on with lo, and P's from its start again
     const uint32_t once = (STAGE == kGram ? max(g.nrp, g.ncp) : rp) / kStep;
-    const bool twice = STAGE == kApply && g.both();
+    const bool both = g.both() || p.s.lo, twice = STAGE == kApply && both;
     const uint32_t steps = twice ? 2 * once : once, half = twice ? once : ~0u;
     const int64_t lo = twice ? 2 * g.lo() : 0;
     if (STAGE == kGram) {
@@ -799,7 +804,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
     // A G in 16 bits is hi alone in the first step (down to 2^-25 of X's elements'
     // mean).  Without lo in the last one, a matrix of low rank would be off by more than
     // its rounding to bf16.
-    const bool lows = g.both() || !p.first || !p.short_g;
+    const bool lows = both || !p.first || !p.short_g;
     if (PARTS == 2)
 #pragma unroll
         for (int c = 0; c < KEEP; c++)
@@ -1090,6 +1095,11 @@ tide_status run_first(const std::vector<OrthoGroup> &groups, const std::vector<O
         });
 }
 
+// By how much step i raises what is near zero.
+double raises(const OrthoArgs &a, int i) {
+    return std::max(1.0, std::fabs(static_cast<double>(a.coefficients[3 * i])));
+}
+
 // The steps of small matrices whose G G^T is known.
 tide_status run_small(const std::vector<OrthoGroup> &small, const OrthoArgs &a, const Space &sp,
                       hipStream_t s) {
@@ -1097,9 +1107,8 @@ tide_status run_small(const std::vector<OrthoGroup> &small, const OrthoArgs &a, 
     p.s = sp;
     for (int from = 0, to = 0; from < a.steps; from = to) {
         // as many steps as raise by less than kOrthoRaised, one at least
-        auto raises = [&](int i) { return std::max(1.0, std::fabs(static_cast<double>(a.coefficients[3 * i]))); };
-        double raised = raises(to++);
-        for (; to < a.steps && raised * raises(to) <= kOrthoRaised; to++) raised *= raises(to);
+        double raised = raises(a, to++);
+        for (; to < a.steps && raised * raises(a, to) <= kOrthoRaised; to++) raised *= raises(a, to);
         p.later = from > 0;
         p.steps = to - from;
         std::copy(a.coefficients + 3 * from, a.coefficients + 3 * to, p.coefficients);
@@ -1160,6 +1169,9 @@ tide_status run_ortho(const OrthoArgs &a, void *stream) {
     sp.pointers = reinterpret_cast<const Pointers *>(sp.base);
     sp.sums = reinterpret_cast<double *>(sp.base + plan.sums);
     sp.scales = reinterpret_cast<float2 *>(sp.base + plan.scales);
+    double raised = 1.0;
+    for (int i = 0; i < a.steps; i++) raised *= raises(a, i);
+    sp.lo = raised > kOrthoRaisedHi;
     const int n = static_cast<int>(plan.order.size());
     for (int at = 0; at < n; at += kPointersPerLaunch) {
         PointerArgs args;
