@@ -688,6 +688,13 @@ struct ProductArgs {
     uint32_t total;              // workgroups
 };
 
+// A sum rounded to fp32 and then to fp16.  Left to itself the compiler takes an
+// instruction that adds and rounds once, to fp16, for some of a row's entries.
+__device__ __forceinline__ _Float16 rounded_twice(float v) {
+    asm("" : "+v"(v));
+    return static_cast<_Float16>(v);
+}
+
 // Tiles of a matrix's A or P: on and below the diagonal; of its X: all.
 __host__ __device__ inline uint32_t tiles_of(const OrthoGroup &g, int stage, uint32_t T) {
     if (stage == kApply) return (g.nrp + T - 1) / T * ((g.ncp + T - 1) / T);
@@ -852,7 +859,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                 if (i < rp && j < rp) {                  // X's padding makes zeros of A's and P's
                     if (STAGE == kGram) {
 #pragma unroll
-                        for (int n = 0; n < 8; n++) h[n] = static_cast<_Float16>(v[n] * (f * kScaleA));
+                        for (int n = 0; n < 8; n++) h[n] = rounded_twice(v[n] * (f * kScaleA));
                         if (diagonal)
 #pragma unroll
                             for (int n = 0; n < 8; n++)
@@ -861,17 +868,20 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, const OrthoGr
                                     h[n] = 0;
                                 }
                     } else {
-                        // O_ij (b + c d_i + c d_j) + c (O^2)_ij, in the scales of O and R
+                        // O_ij (b + c (d_i + d_j)) + c (O^2)_ij, in the scales of O and R:
+                        // rounded alike for (i, j) and (j, i), as it depends on the tiles'
+                        // size whether an entry is mirrored or computed on both sides
                         const float cs = p.cc * (kScaleP / kScaleA), co = p.cc * f * kScaleP;
-                        const float di = ad[i], bi = p.cb * (kScaleP / kScaleA) + cs * di;
+                        const float di = ad[i], bs = p.cb * (kScaleP / kScaleA);
                         const f32x4 dl = *reinterpret_cast<const f32x4 *>(ad + j);
                         const f32x4 dh = *reinterpret_cast<const f32x4 *>(ad + j + 4);
                         const f16x8 o = held[c % KEEP][q][0];
 #pragma unroll
                         for (int n = 0; n < 8; n++)
-                            h[n] = static_cast<_Float16>(
+                            h[n] = rounded_twice(
                                 __builtin_fmaf(static_cast<float>(o[n]),
-                                               __builtin_fmaf(cs, n < 4 ? dl[n] : dh[n - 4], bi), v[n] * co));
+                                               __builtin_fmaf(cs, di + (n < 4 ? dl[n] : dh[n - 4]), bs),
+                                               v[n] * co));
                         if (diagonal)
 #pragma unroll
                             for (int n = 0; n < 8; n++)
