@@ -685,7 +685,6 @@ struct ProductArgs {
     int from;                    // which of the two X is read
     int first, last;             // of the steps
     int short_g;                 // G is in 16 bits
-    uint32_t total;              // workgroups
 };
 
 // A sum rounded to fp32 and then to fp16.  Left to itself the compiler takes an
@@ -1072,7 +1071,6 @@ tide_status run_product(const std::vector<OrthoGroup> &groups, ProductArgs p, hi
         groups, [&](const OrthoGroup &g) { return tiles_of(g, STAGE, static_cast<uint32_t>(T)); },
         [&](const Groups &a, uint32_t total) {
             p.a = a;
-            p.total = total;
             if (T == 256)
                 product_kernel<STAGE, 256><<<dim3(total), dim3(kThreads), 0, s>>>(p);
             else if (T == 128)
