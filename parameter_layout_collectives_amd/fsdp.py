@@ -154,6 +154,8 @@ class TideUnit:
         elif self._muon[0] != select:
             raise ValueError(f"earlier steps updated parameters {self._muon[0]}, not {select}")
         plan, device = self._muon[1], self.master.device
+        if not plan.S:           # matrices without elements only
+            return
         u = torch.zeros(self.world, plan.S, dtype=torch.bfloat16, device=device)
         for j, i in enumerate(select):
             src, _, seg = self.plan.param(i)
@@ -163,8 +165,7 @@ class TideUnit:
             u[:, dst:dst + seg].copy_(torch.add(g, buf, alpha=momentum) if nesterov else buf)
         full = [torch.empty(self.shapes[i], dtype=torch.bfloat16, device=device) for i in select]
         ag(plan, u.view(-1), full)
-        mats = [t.view(t.shape[0], -1) if t.dim() else t.view(1, 1) for t in full]
-        mats = [m for m in mats if m.numel()]
+        mats = [t.view(t.shape[0] if t.dim() else 1, -1) for t in full if t.numel()]
         ortho(mats, out=mats, steps=steps, coefficients=coefficients)
         pack(plan, full, u.view(-1))
         for j, i in enumerate(select):
