@@ -41,7 +41,7 @@ import torch
 
 from . import (BlockPlan, Fp4Plan, Plan, ag, block_linear, block_shard, fp4_linear, fp4_shard,
                grad_table, ortho, pack, rs)
-from .ortho import COEFFICIENTS
+from .ortho import COEFFICIENTS, check_steps
 
 
 class TideUnit:
@@ -142,17 +142,24 @@ class TideUnit:
         select: the parameters that are updated, by default all 2-D ones, the same in
         every call; others are left as they are, for another optimizer.  A parameter of
         more dimensions is taken as the matrix [dim0, inner].  scale: by default
-        sqrt(max(1, rows / cols)).  all_gather() then makes params of the new W."""
+        sqrt(max(1, rows / cols)).  all_gather() then makes params of the new W.  A call
+        that is refused leaves the unit as it was."""
         if select is None:
             select = [i for i, s in enumerate(self.shapes) if len(s) == 2]
         select = [int(i) for i in select]
         if not select:
             return
-        if self._muon is None:
-            self.momentum = torch.zeros_like(self.master)
-            self._muon = select, Plan([self.shapes[i] for i in select], self.world, self.plan.align)
-        elif self._muon[0] != select:
+        if not all(0 <= i < len(self.shapes) for i in select):
+            raise ValueError(f"select {select} holds an index out of range")
+        if self._muon is not None and self._muon[0] != select:
             raise ValueError(f"earlier steps updated parameters {self._muon[0]}, not {select}")
+        check_steps(steps, coefficients)
+        lr, momentum, weight_decay = float(lr), float(momentum), float(weight_decay)
+        factors = [self._muon_factor(i, lr, scale) for i in select]
+        if self._muon is None:
+            plan = Plan([self.shapes[i] for i in select], self.world, self.plan.align)
+            self.momentum = torch.zeros_like(self.master)
+            self._muon = select, plan
         plan, device = self._muon[1], self.master.device
         if not plan.S:           # matrices without elements only
             return
@@ -171,15 +178,20 @@ class TideUnit:
         for j, i in enumerate(select):
             src, _, seg = self.plan.param(i)
             dst, _, _ = plan.param(j)
-            rows = self.shapes[i][0] if self.shapes[i] else 1
-            cols = full[j].numel() // rows if rows else 0
-            if not seg or not cols:
+            if not seg:
                 continue
-            k = scale(rows, cols) if scale is not None else max(1.0, rows / cols) ** 0.5
             w = self.master[:, src:src + seg]
             if weight_decay:
                 w.mul_(1 - lr * weight_decay)
-            w.add_(u[:, dst:dst + seg], alpha=-lr * k)
+            w.add_(u[:, dst:dst + seg], alpha=factors[j])
+
+    def _muon_factor(self, i, lr, scale):
+        shape = self.shapes[i]
+        rows, cols = shape[0] if shape else 1, torch.Size(shape[1:]).numel()
+        if not rows or not cols:
+            return 0.0
+        k = scale(rows, cols) if scale is not None else max(1.0, rows / cols) ** 0.5
+        return -lr * float(k)
 
     def linear(self, i, x, grad=None, accumulate=False, dtype=None, short_sums=False,
                quant_x=False):

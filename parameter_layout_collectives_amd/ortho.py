@@ -14,6 +14,7 @@ import ctypes
 
 import torch
 
+from . import _check
 from ._lib import lib
 from .blocks import _IN_FLAG, _IN_TYPES, _call, _no_dual, _same_device
 
@@ -30,6 +31,23 @@ def _check_stack(t, what, dtypes):
         raise ValueError(f"{what} must be a contiguous 2-D or 3-D device tensor")
 
 
+def _steps(steps, coefficients):
+    """The steps' number and coefficients as the library takes them."""
+    flat = [float(v) for step in coefficients for v in step] \
+        if len(coefficients) and isinstance(coefficients[0], (tuple, list)) \
+        else [float(v) for v in coefficients] * int(steps)
+    steps = int(steps)
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coefficients: need (a, b, c), or {steps} triples of them")
+    return steps, (ctypes.c_float * max(1, len(flat)))(*flat)
+
+
+def check_steps(steps, coefficients):
+    """Refuses the steps that ortho() would refuse for any matrices."""
+    steps, flat = _steps(steps, coefficients)
+    _check(lib().tide_ortho(0, None, None, None, None, steps, flat, 0, None, 0, None))
+
+
 def ortho(g, out=None, steps=5, coefficients=COEFFICIENTS):
     """g orthogonalised, in bf16.
 
@@ -39,12 +57,7 @@ def ortho(g, out=None, steps=5, coefficients=COEFFICIENTS):
     every step, or one such triple per step.  Returns `out`, a list for a list."""
     one = isinstance(g, torch.Tensor)
     gs = [g] if one else list(g)
-    flat = [float(v) for step in coefficients for v in step] \
-        if len(coefficients) and isinstance(coefficients[0], (tuple, list)) \
-        else [float(v) for v in coefficients] * int(steps)
-    steps = int(steps)
-    if len(flat) != 3 * steps:
-        raise ValueError(f"coefficients: need (a, b, c), or {steps} triples of them")
+    steps, flat = _steps(steps, coefficients)
     if not gs:
         return []
     dtype, device = gs[0].dtype, gs[0].device
@@ -86,7 +99,7 @@ def ortho(g, out=None, steps=5, coefficients=COEFFICIENTS):
         # the allocator's blocks start at multiples of 512 bytes
         keep = torch.empty(size, dtype=torch.uint8, device=device) if size > 0 else None
         _call(device, lib().tide_ortho, n, (ctypes.c_void_p * n)(*src), (ctypes.c_void_p * n)(*dst),
-              rows, cols, steps, (ctypes.c_float * max(1, len(flat)))(*flat), _IN_FLAG[dtype],
+              rows, cols, steps, flat, _IN_FLAG[dtype],
               keep.data_ptr() if keep is not None else None, max(size, 0))
     return outs[0] if one else outs
 
