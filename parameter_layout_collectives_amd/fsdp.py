@@ -151,6 +151,8 @@ class TideUnit:
             return
         if not all(0 <= i < len(self.shapes) for i in select):
             raise ValueError(f"select {select} holds an index out of range")
+        if len(set(select)) != len(select):
+            raise ValueError(f"select {select} holds an index twice")
         if self._muon is not None and self._muon[0] != select:
             raise ValueError(f"earlier steps updated parameters {self._muon[0]}, not {select}")
         check_steps(steps, coefficients)

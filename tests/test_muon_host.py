@@ -19,6 +19,7 @@ def refused_scale(rows, cols):
     (dict(coefficients=[(3.0, -3.0, 1.0)] * 2), ValueError, "triples"),
     (dict(coefficients=(3.0, float("nan"), 1.0)), tide.TideError, "finite"),
     (dict(scale=refused_scale), ZeroDivisionError, "scale"),
+    (dict(select=[0, 0]), ValueError, "twice"),
     (dict(select=[-1]), ValueError, "out of range"),
     (dict(select=[3]), ValueError, "out of range"),
     (dict(momentum="much"), ValueError, "much"),
