@@ -23,7 +23,7 @@ def refused_scale(rows, cols):
     (dict(select=[-1]), ValueError, "out of range"),
     (dict(select=[3]), ValueError, "out of range"),
     (dict(momentum="much"), ValueError, "much"),
-    (dict(weight_decay=None), TypeError, ""),
+    (dict(weight_decay=None), TypeError, "float"),
 ])
 def test_refusals_leave_the_unit_as_it_was(kw, error, needle):
     unit = TideUnit(SHAPES, 2, device="cpu")
