@@ -138,16 +138,6 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     }
     auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((cols + t - 1) / t); };
     const bool four = c.kernel == kFp4Tiles;
-    c.mm.tile = aligned && tiles(256) >= kCus * 3 / 4 ? 256 : tiles(128) < kCus / 2 ? 64 : 128;
-    // In bf16, large tiles also where they have to be cut to fill the card, if most of
-    // each is used and the pieces are long (dX, M x N x K, us, large / middle tiles):
-    // 256 x 8192 x 8192 55 / 62, 1024 122 / 154, 2048 x 14336 x 4096 190 / 253, 1024 x 4096 x
-    // 4096 50 / 50; pieces of 8 steps, 2048 x 1024 x 4096 33 / 25.
-    const int64_t large = tiles(256), pieces = std::min(kCus / std::max<int64_t>(large, 1), kMaxSplits);
-    if (aligned && !four && pieces >= 2 && large >= kCus / 8 && tiles(128) >= 3 * large &&
-        sum >= pieces * kDeepSteps * 64 &&
-        c.x + large * pieces * 256 * 256 * 4 <= workspace_bytes)
-        c.mm.tile = 256;
     // The 4-bit tiles' step is 128 columns, and two of them cost what cut_sums takes for
     // one.  A cut that leaves no whole set has to save more than its second launch costs,
     // kCutSaves steps, and of the 4-bit tiles, whose steps are short, also its traffic
@@ -157,17 +147,32 @@ Fp4Choice fp4_choose(Fp4Op op, int64_t M, int64_t N, int64_t K, uint32_t flags, 
     // 8192 20.3 / 19.0, over 16384 23.2 / 29.7, 100 x 512 x 8192 15.2 / 21.5, 500 x 2048 x 16384
     // 40 / 33.
     const int64_t step = four ? 256 : 64, per = four ? 2 : 1;
-    c.mm.direct = tiles(c.mm.tile);
-    c.mm.splits = 1;
-    c.mm.chunk = (sum + step - 1) / step;
-    c.mm.workspace = 0;
-    MmChoice cut = c.mm;
-    cut_sums(cut, c.mm.direct, c.mm.chunk);
-    const int64_t least = std::max(kCutSaves, four ? c.mm.direct * 3 / 4 : 0);
-    if (cut.direct == 0 && c.mm.chunk - cut.chunk < least) cut = c.mm;
-    cut.chunk *= per;
-    c.mm.chunk *= per;
-    if (c.x + cut.workspace <= workspace_bytes) c.mm = cut;
+    auto tiled = [&](int T) {
+        MmChoice m = {};
+        m.tile = T;
+        m.direct = tiles(T);
+        m.splits = 1;
+        m.chunk = (sum + step - 1) / step;
+        MmChoice cut = m;
+        cut_sums(cut, m.direct, m.chunk);
+        const int64_t least = std::max(kCutSaves, four ? m.direct * 3 / 4 : 0);
+        if (cut.direct == 0 && m.chunk - cut.chunk < least) cut = m;
+        if (c.x + cut.workspace > workspace_bytes) cut = m;
+        cut.chunk *= per;
+        return cut;
+    };
+    // In bf16, large tiles also where they have to be cut to fill the card, if most of
+    // each is used and the pieces are long (dX, M x N x K, us, large / middle tiles):
+    // 256 x 8192 x 8192 55 / 62, 1024 122 / 154, 2048 x 14336 x 4096 190 / 253, 1024 x 4096 x
+    // 4096 50 / 50; pieces of 8 steps, 2048 x 1024 x 4096 33 / 25.  Uncut they leave most of
+    // it idle.
+    const int64_t large = tiles(256), pieces = std::min(kCus / std::max<int64_t>(large, 1), kMaxSplits);
+    if (aligned && !four && pieces >= 2 && large >= kCus / 8 && tiles(128) >= 3 * large &&
+        sum >= pieces * kDeepSteps * 64) {
+        c.mm = tiled(256);
+        if (c.mm.splits > 1) return c;
+    }
+    c.mm = tiled(aligned && large >= kCus * 3 / 4 ? 256 : tiles(128) < kCus / 2 ? 64 : 128);
     return c;
 }
 
