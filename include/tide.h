@@ -544,11 +544,14 @@ int64_t tide_mx_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32_t 
  *   Larger matrices: between products X is held in pairs of fp16 numbers (22 bits), X X^T
  * and the polynomial's matrix as an fp32 diagonal and a rest in fp16, and the products'
  * factors are fp16 numbers.  Before the rounding to bf16 X is off by 3e-4 to 1e-3 of its
- * norm in 5 such steps, up to 2e-3 for matrices of a low rank.  In more of them, or in
- * steps whose |a| multiplied exceed 512, the product with X takes both of its numbers,
- * half as long again, and X is off by 1e-3 to 2e-3.  Where X has nothing but its own
- * rounding, 2^-23, every step raises that by up to a, as it does in fp32: a low rank is
- * 2e-3 to 1e-2 off after 10 such steps and a full one after about 13.
+ * norm in 5 such steps, up to 2e-3 for matrices of a low rank, and up to 1e-2 for one of
+ * rank one whose entries have all one magnitude: all are then rounded alike, and nothing
+ * averages out.  In more steps, or steps whose |a| multiplied exceed 512, the product with
+ * X takes both of its numbers, half as long again, and X is off by 1e-3 to 2e-3, up to
+ * 9e-3 where the singular values are of two sizes, and 2e-2 for one magnitude.  Where X
+ * has nothing but its own rounding, 2^-23, every step raises that by up to a, as it does
+ * in fp32: a low rank is 2e-3 to 1e-2 off after 10 such steps and a full one after about
+ * 13.
  * fp16's range asks for singular values of every step's X up to 3.9 and |b x^2 + c x^4|
  * there up to 63; beyond that the result holds infinities or NaNs.
  *

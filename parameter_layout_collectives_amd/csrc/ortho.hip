@@ -20,13 +20,15 @@
 // Q X, and only O, R and, in X X^T and R X, hi are rounded to fp16.  So the products
 // run at fp16's full rate and the result is off by 3e-4 to 1e-3 of its norm before
 // it is rounded to bf16 (1.7e-3), by up to 1.6e-3 for matrices whose rank is an
-// eighth of r (an emulation in 64 bits).  With fewer rows R outweighs Q there (37 of
-// rank 4: 4e-3), so up to kOrthoBoth of them R X takes lo as well, as one sum of
-// twice the length.  What hi alone loses in directions where X has little is raised by a
-// in every later step: with 5 of the usual ones (3.4445^5 = 485) [300, 420] of rank 37 is
-// 1.5e-3 off, with 6 4e-3, with 8 5e-2; with lo 7e-4, 7e-4, 9e-4.  So above kOrthoRaisedHi
-// lo enters for any number of rows, in all steps (the first alone, or all but the last
-// five, would leave 4e-3 to 2e-2; [4096, 4096] 425 us a step for 270).
+// eighth of r (an emulation in 64 bits).  Only where a matrix of rank one has entries of
+// one magnitude are all rounded alike: there the result is off by up to 1e-2.
+// With fewer rows R outweighs Q in matrices of a low rank (37 rows of rank 4: 4e-3), so up
+// to kOrthoBoth of them R X takes lo as well, as one sum of twice the length.  What hi alone
+// loses in directions where X has little is raised by a in every later step: with 5 of the
+// usual ones (3.4445^5 = 485) [300, 420] of rank 37 is 1.5e-3 off, with 6 4e-3, with 8
+// 5e-2; with lo 7e-4, 7e-4, 9e-4.  So above kOrthoRaisedHi lo enters for any number of
+// rows, in all steps (the first alone, or all but the last five, would leave 4e-3 to 2e-2;
+// [4096, 4096] 425 us a step for 270).
 // Few rows average none of these roundings out (2 x 2: up to 8e-3), and cost next to
 // nothing: up to kOrthoSmall of them the steps run in fp64 on A alone, since P and A
 // commute: A <- P A P and M <- P M from M = I, and the result is M X, one pass over G.

@@ -10,7 +10,7 @@ import torch
 import ortho_ref as ref
 import parameter_layout_collectives_amd as tide
 from gpu_helpers import note
-from test_ortho_steps_host import CASES, SHAPES
+from test_ortho_steps_host import CASES, ONE_MAGNITUDE, ONE_MAGNITUDE_OFF, SHAPES, signs
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -44,3 +44,12 @@ def test_many_steps_stay_bounded():
         for kind in ("full", "low"):
             out = tide.ortho(ref.gradient(*shape, 3, kind, FP, "cuda"), steps=64)
             assert bool(torch.isfinite(out).all()) and float(out.abs().max()) <= 1.3
+
+
+@pytest.mark.parametrize("shape", ONE_MAGNITUDE + [(99, 71), (1504, 315)])
+def test_entries_of_one_magnitude(shape):
+    note(f"ortho, entries of one magnitude {shape}")
+    for dtype in (BF, FP):
+        g = signs(*shape).to(dtype).cuda()
+        err = ref.off(tide.ortho(g), ref.exact(g))
+        assert err <= 2.0 ** -8 + ONE_MAGNITUDE_OFF, (dtype, err)

@@ -40,3 +40,24 @@ def test_hi_alone_would_not_do():
     """Why: a low rank in 8 steps."""
     g = ref.gradient(300, 420, 7, "low")
     assert ref.off(ref.emulated(g, 8), ref.exact(g, 8)) > 3e-2
+
+
+# Of rank one, all entries of one magnitude: every rounding is the same, none averages out.
+ONE_MAGNITUDE = [(71, 99), (39, 370), (64, 64), (315, 1504), (512, 1024), (325, 600)]
+ONE_MAGNITUDE_OFF = 1.05e-2
+
+
+def signs(r, c, seed=1):
+    gen = torch.Generator().manual_seed(seed)
+    rows, cols = (torch.sign(torch.randn(n, generator=gen)) for n in (r, c))
+    return rows[:, None] * cols[None, :] * 0.25
+
+
+@pytest.mark.parametrize("shape", ONE_MAGNITUDE)
+def test_entries_of_one_magnitude(shape):
+    g = signs(*shape)
+    assert ref.off(ref.emulated(g), ref.exact(g)) < ONE_MAGNITUDE_OFF
+
+
+def test_entries_of_one_magnitude_are_the_worst_known():
+    assert ref.off(ref.emulated(signs(315, 1504)), ref.exact(signs(315, 1504))) > 9e-3
