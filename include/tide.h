@@ -467,7 +467,8 @@ int64_t tide_block_workspace(int32_t op, int64_t m, int64_t n, int64_t k, uint32
  * holds an infinity or a NaN has scale byte 255 and codes 0 and stands for NaNs.
  * Codes past column C are 0, scale bytes of blocks past it 127.  Every value of
  * the format is a bf16 number.  Operands given to the calls below hold scale bytes
- * of 2..252 or 255 and those zeros, as tide_mx_quant and tide_mx_shard write them.
+ * of 2..252 or 255 and those zeros, as tide_mx_quant and tide_mx_shard write them;
+ * that is not looked for.
  *
  * codes have to be 16-byte aligned and scales 4-byte aligned.  Sizes, graph
  * capture, errors and streams as for the 8-bit blocks. */

@@ -471,9 +471,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(MmLaunch p) {
 // columns (16 KB, a group) at a time, and every wave multiplies by them; W's codes go
 // from memory to registers, become bf16 there and are multiplied at once.  Both are
 // asked for two groups ahead (four ahead, or two workgroups on a compute unit, are no
-// faster).  The pieces' sums meet in the workspace.  32 x 8192 x 28672: 32.7 us, of which
-// the second launch takes 4; W's 125 MB come at 4.4 TB/s, which a copy of as many also
-// reaches.  Alone, without x, products and scales, the loads of W take 24 to 27.
+// faster).  The pieces' sums meet in the workspace.  32 x 8192 x 28672: 34.3 us, of which
+// the second launch takes 4 to 5; W's 125 MB come at 4.1 TB/s (a copy of 128 MiB: 5.3), and
+// x's 1.8 MB once for each 128 rows of W, 117 MB, through the L2.  Alone, without x,
+// products and scales, the loads of W take 24 to 27.
 //
 // LDS: a row's unit is 16 chunks of 16 bytes, chunk c of row r at c ^ strip_key(r), so
 // that the lanes that a read takes at a time fall into different banks.

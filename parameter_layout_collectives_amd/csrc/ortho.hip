@@ -42,9 +42,9 @@
 //
 // The products bound it, and where the sums are short X's traffic: P X reads X (hi for
 // the product, hi and lo for its join) and writes it, 8 bytes an element and step.  Five
-// steps of [4096, 4096] take 1.50 to 1.60 ms, 0.9 PFLOP/s of the multiplications above,
-// of an 8B layer's seven matrices 14.4 ms, 1.03 PFLOP/s (fp16's library product 1.58),
-// of 48 x [768, 2048] 1.7 ms: X X^T 90 us, P 46, P X 190 to 210 a step, at 3.6 TB/s.
+// steps of [4096, 4096] take 1.51 to 1.61 ms, 0.9 PFLOP/s of the multiplications above,
+// of an 8B layer's seven matrices 14.1 ms, 1.05 PFLOP/s (fp16's library product 1.58),
+// of 48 x [768, 2048] 1.7 ms: X X^T 85 us, P 40, P X 203 a step, at 3.7 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

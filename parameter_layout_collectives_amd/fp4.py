@@ -43,8 +43,10 @@ class Fp4Blocks(_Codes):
     even column of a pair in the low half of its byte.
     scales: [rows, cols rounded up to 128, / 32], uint8 or float8_e8m0fnu, 2 to 252,
     or 255 for a block of NaNs.  Codes past the last column are 0 and scales past the
-    last block 127, as fp4_quant, fp4_shard and ag() write them.  Either tensor may
-    be replaced, or its storage released and restored, as those of Blocks."""
+    last block 127, as fp4_quant, fp4_shard and ag() write them.  The calls do not
+    look for other scales or for codes behind the last column, which blocks made
+    elsewhere might hold: they would enter the sums.  Either tensor may be replaced,
+    or its storage released and restored, as those of Blocks."""
 
     __slots__ = ()
     _code_types = (torch.uint8, torch.float4_e2m1fn_x2)
